@@ -260,6 +260,113 @@ ink_status_t inkling_attn_kv_conv_write(const ink_attn_params_t* params, const v
                                         void* stream);
 
 /*
+ * Options of the masked attention entry points (a NULL pointer to this struct: none of them).
+ * Query token t of sequence b sits at position p as above and sees the keys
+ *     max(key_begin[t], p - window + 1 when window > 0, 0) <= k < min(key_end[t], L_b)
+ * so one pair of numbers per token expresses packed documents (key_begin = the document's first
+ * position), a bidirectional prefix or image block (key_end = its end), padding (an empty
+ * range), and windows.  The window bounds the past only.  The score of a visible key is
+ *     x   = sm_scale * <q[t,h,:], K[k,h/G,:]>
+ *     s_k = (softcap > 0 ? softcap * tanh(x / softcap) : x) - slopes[h] * |p - k|
+ */
+typedef struct {
+  float softcap;             /* > 0: scores capped by a tanh; 0: not capped */
+  const int32_t* key_begin;  /* device int32 [rows of q] first visible key, or NULL: 0 */
+  const int32_t* key_end;    /* device int32 [rows of q] last visible key + 1, or NULL: p + 1 */
+  const float* slopes;       /* device fp32 [Hq], or NULL: no distance bias */
+} ink_attn_mask_t;
+
+/*
+ * Bytes of device workspace a masked attention call (or, with is_decode == 0,
+ * inkling_attn_qk_norm_rope_write) needs; initialise it once with
+ * inkling_attn_workspace_init.  Returns 0 if the parameters are invalid.  It does not depend on
+ * the lengths.  Calls that share a workspace must not overlap on the GPU.
+ */
+size_t inkling_attn_masked_workspace_bytes(const ink_attn_params_t* params, int is_decode);
+
+/*
+ * Paged prefill without a per-token bias tensor: capped scores, distance bias and a visible key
+ * range per token (ink_attn_mask_t).  For models that take their positions from a rotation of q
+ * and k (inkling_attn_qk_norm_rope_write) or from the distance bias.
+ *   q, cu_q_lens, k_cache, v_cache, block_table, seq_lens, out: as for inkling_attn_prefill,
+ *              except that there is no max_q_len; out must not overlap q
+ *   total_q    rows of q and out; rows from cu_q_lens[B] on belong to no sequence and are
+ *              neither read nor written
+ *   lse        device, fp32 [total_q, Hq], or NULL: log of the sum of exp(s_k) over the visible
+ *              keys (natural units), with which outputs over parts of a history are joined
+ *   workspace  device, >= inkling_attn_masked_workspace_bytes(params, 0), initialised once
+ * A token that sees no key gets a zero output row and lse = -infinity.  params.rel_extent is
+ * not used (any valid value).  A sequence whose rows lie outside [0, total_q) is skipped
+ * (INK_DEVERR_BAD_ROWS); one with more new tokens than history gets zero rows
+ * (INK_DEVERR_QLEN_EXCEEDS_KV).
+ */
+ink_status_t inkling_attn_prefill_masked(const ink_attn_params_t* params, const ink_attn_mask_t* mask,
+                                         const void* q, const int32_t* cu_q_lens, int32_t total_q,
+                                         const void* k_cache, const void* v_cache,
+                                         const int32_t* block_table, const int32_t* seq_lens,
+                                         void* out, float* lse, void* workspace,
+                                         size_t workspace_bytes, void* stream);
+
+/*
+ * Paged decode without a per-token bias tensor: row b of q is sequence b at p = L_b - 1; the
+ * options, results and requirements are those of inkling_attn_prefill_masked
+ * (workspace: inkling_attn_masked_workspace_bytes(params, 1)).  A sequence with
+ * seq_lens[b] <= 0 gets a zero row and lse = -infinity.
+ */
+ink_status_t inkling_attn_decode_masked(const ink_attn_params_t* params, const ink_attn_mask_t* mask,
+                                        const void* q, const void* k_cache, const void* v_cache,
+                                        const int32_t* block_table, const int32_t* seq_lens, void* out,
+                                        float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Pairing of the channels that are rotated together.
+ */
+typedef enum {
+  INK_ROPE_HALF = 0,         /* channel i with channel i + rot_dim / 2 */
+  INK_ROPE_INTERLEAVED = 1   /* channel 2 i with channel 2 i + 1 */
+} ink_rope_layout_t;
+
+/* Norm and rotation of inkling_attn_qk_norm_rope_write. */
+typedef struct {
+  const float* w_q;          /* device fp32 [D], 16-byte aligned: weight of the RMS norm of q, or NULL: no norm */
+  const float* w_k;          /* the same for k */
+  float eps;                 /* added to the mean square; >= 0 */
+  const float* inv_freq;     /* device fp32 [rot_dim / 2]: angle per position of each pair (unused when rot_dim == 0) */
+  int32_t rot_dim;           /* 0 (no rotation) or a multiple of 16, at most D: the first channels, rotated */
+  int32_t layout;            /* ink_rope_layout_t */
+  float rot_scale;           /* multiplies cos and sin (1, or the attention factor of a long-context scaling) */
+} ink_norm_rope_t;
+
+/*
+ * The step's K/V write for models with normed or rotated heads: RMS norm of every query and key
+ * head, rotation by the token's position, and K and V into the paged caches, in one pass.
+ *   y = x * (mean(x^2) + eps)^(-1/2) * w          (fp32; without weights y = x)
+ *   pair (a, b) of channels with frequency f at position p, in fp32:
+ *     a' = rot_scale * (a cos(p f) - b sin(p f)),  b' = rot_scale * (b cos(p f) + a sin(p f))
+ * rounded to bf16 once.  The angle is reduced exactly enough that far positions (any int32) keep
+ * an error of a few fp32 roundings of one turn.  V is stored as it is.
+ *   q, k, v       device, bf16; row t of q holds Hq heads of D contiguous channels at
+ *                 q + t * q_stride elements (k, v: Hkv heads): parts of a fused projection's
+ *                 rows pass without a copy.  Strides are multiples of 8, 16-byte aligned bases.
+ *   cu_q_lens, seq_lens, block_table   as for inkling_attn_prefill: new row i of request b sits
+ *                 at p = L_b - n_b + i
+ *   q_out         device, bf16 [total_q, Hq, D]; may be q itself when q_stride == Hq * D
+ *   k_cache, v_cache  device, bf16 [num_pages, Hkv, P, D]; only the slots of the step's
+ *                 positions are written; must not overlap q, k or v
+ *   workspace     device, >= inkling_attn_masked_workspace_bytes(params, 0) (error word)
+ * Rows from cu_q_lens[B] on belong to no request and are left as they were.  A request with
+ * n_b > L_b (INK_DEVERR_QLEN_EXCEEDS_KV) has its rows skipped; a page id outside [0, num_pages)
+ * (INK_DEVERR_PAGE_OUT_OF_RANGE) has the K/V rows of its keys skipped.  Two rows that name the
+ * same slot (requests sharing a page they write to) race: either row may be kept.
+ */
+ink_status_t inkling_attn_qk_norm_rope_write(const ink_attn_params_t* params, const ink_norm_rope_t* rope,
+                                             const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                             const void* v, int64_t v_stride, const int32_t* cu_q_lens,
+                                             int32_t total_q, const int32_t* seq_lens, const int32_t* block_table,
+                                             void* q_out, void* k_cache, void* v_cache, void* workspace,
+                                             size_t workspace_bytes, void* stream);
+
+/*
  * Synchronise `stream`, copy the sticky device error word (INK_DEVERR_* bits) to
  * *err_out, and clear it when `clear` is non-zero.  This is the only entry point that
  * blocks the host.

@@ -31,6 +31,8 @@ EXPORTED_SYMBOLS = ("inkling_attn_workspace_bytes", "inkling_attn_workspace_init
                     "inkling_attn_prefill", "inkling_attn_prefill_bf16bias",
                     "inkling_attn_prefill_lowrank_bias", "inkling_attn_decode",
                     "inkling_attn_decode_noalloc", "inkling_attn_kv_conv_write",
+                    "inkling_attn_masked_workspace_bytes", "inkling_attn_prefill_masked",
+                    "inkling_attn_decode_masked", "inkling_attn_qk_norm_rope_write",
                     "inkling_attn_read_device_error", "inkling_attn_status_string",
                     "inkling_attn_version", "inkling_attn_set_wait_limit_ns")
 
@@ -47,6 +49,20 @@ class ink_attn_params_t(ctypes.Structure):
                 ("page_size", ctypes.c_int32), ("max_pages_per_seq", ctypes.c_int32),
                 ("num_pages", ctypes.c_int32), ("rel_extent", ctypes.c_int32),
                 ("window", ctypes.c_int32), ("sm_scale", ctypes.c_float)]
+
+
+class ink_attn_mask_t(ctypes.Structure):
+    _fields_ = [("softcap", ctypes.c_float), ("key_begin", ctypes.c_void_p), ("key_end", ctypes.c_void_p),
+                ("slopes", ctypes.c_void_p)]
+
+
+class ink_norm_rope_t(ctypes.Structure):
+    _fields_ = [("w_q", ctypes.c_void_p), ("w_k", ctypes.c_void_p), ("eps", ctypes.c_float),
+                ("inv_freq", ctypes.c_void_p), ("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("rot_scale", ctypes.c_float)]
+
+
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
 
 
 def library_path() -> str:
@@ -81,6 +97,15 @@ def load_library(path: Optional[str] = None):
     lib.inkling_attn_decode_noalloc.restype = ctypes.c_int
     lib.inkling_attn_kv_conv_write.argtypes = [PP, V, V, V, I32, V, V, V, V, I32, V, V, V, V, V, V, V, S, V]
     lib.inkling_attn_kv_conv_write.restype = ctypes.c_int
+    I64, MP, RP = ctypes.c_int64, ctypes.POINTER(ink_attn_mask_t), ctypes.POINTER(ink_norm_rope_t)
+    lib.inkling_attn_masked_workspace_bytes.argtypes = [PP, ctypes.c_int]
+    lib.inkling_attn_masked_workspace_bytes.restype = S
+    lib.inkling_attn_prefill_masked.argtypes = [PP, MP, V, V, I32, V, V, V, V, V, V, V, S, V]
+    lib.inkling_attn_prefill_masked.restype = ctypes.c_int
+    lib.inkling_attn_decode_masked.argtypes = [PP, MP, V, V, V, V, V, V, V, V, S, V]
+    lib.inkling_attn_decode_masked.restype = ctypes.c_int
+    lib.inkling_attn_qk_norm_rope_write.argtypes = [PP, RP, V, I64, V, I64, V, I64, V, I32, V, V, V, V, V, V, S, V]
+    lib.inkling_attn_qk_norm_rope_write.restype = ctypes.c_int
     lib.inkling_attn_read_device_error.argtypes = [V, S, V, ctypes.POINTER(ctypes.c_uint32), ctypes.c_int]
     lib.inkling_attn_read_device_error.restype = ctypes.c_int
     lib.inkling_attn_status_string.argtypes = [ctypes.c_int]
@@ -245,6 +270,146 @@ def inkling_attn_kv_conv_write(params, k_new, v_new, cu_q_lens, seq_lens, block_
         _dev(workspace, "workspace", torch.uint8), workspace.numel(), _stream_handle(stream))
     _check(code, "inkling_attn_kv_conv_write")
     return k_cache, v_cache
+
+
+def _shape(t, name, shape):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _opt_dev(t, name, dtype, shape):
+    if t is None:
+        return None
+    ptr = _dev(t, name, dtype)
+    _shape(t, name, shape)
+    return ptr
+
+
+def _one_device(*tensors):
+    """The device all the given tensors (None skipped) live on."""
+    devices = {t.device for t in tensors if t is not None}
+    if len(devices) != 1:
+        raise ValueError(f"tensors on different devices: {sorted(map(str, devices))}")
+    return devices.pop()
+
+
+def _check_pools(params, k_cache, v_cache, block_table, seq_lens):
+    pool = (params.num_pages, params.num_kv_heads, params.page_size, params.head_dim)
+    _shape(k_cache, "k_cache", pool)
+    _shape(v_cache, "v_cache", pool)
+    _shape(block_table, "block_table", (params.num_seqs, params.max_pages_per_seq))
+    _shape(seq_lens, "seq_lens", (params.num_seqs,))
+
+
+def inkling_attn_masked_workspace_bytes(params: ink_attn_params_t, is_decode: bool) -> int:
+    return int(load_library().inkling_attn_masked_workspace_bytes(ctypes.byref(params), int(bool(is_decode))))
+
+
+def alloc_masked_workspace(params: ink_attn_params_t, is_decode: bool = True, device="cuda") -> torch.Tensor:
+    """Allocate (through PyTorch) and initialise a workspace for the masked entry points."""
+    n = inkling_attn_masked_workspace_bytes(params, is_decode)
+    if n == 0:
+        raise InkError(2, "inkling_attn_masked_workspace_bytes")
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    with torch.cuda.device(ws.device):
+        inkling_attn_workspace_init(ws)
+    return ws
+
+
+def _mask_struct(params, rows, softcap, key_begin, key_end, slopes) -> ink_attn_mask_t:
+    return ink_attn_mask_t(float(softcap), _opt_dev(key_begin, "key_begin", torch.int32, (rows,)),
+                           _opt_dev(key_end, "key_end", torch.int32, (rows,)),
+                           _opt_dev(slopes, "slopes", torch.float32, (params.num_q_heads,)))
+
+
+def inkling_attn_prefill_masked(params, q, cu_q_lens, k_cache, v_cache, block_table, seq_lens, out, workspace, *,
+                                softcap: float = 0.0, key_begin=None, key_end=None, slopes=None, lse=None, stream=None):
+    """Paged prefill with capped scores, a distance bias and a visible key range per token."""
+    lib = load_library()
+    ptrs = [_dev(q, "q", torch.bfloat16), _dev(cu_q_lens, "cu_q_lens", torch.int32)]
+    T = int(q.shape[0])
+    _shape(q, "q", (T, params.num_q_heads, params.head_dim))
+    _shape(out, "out", q.shape)
+    _shape(cu_q_lens, "cu_q_lens", (params.num_seqs + 1,))
+    tail = [_dev(k_cache, "k_cache", torch.bfloat16), _dev(v_cache, "v_cache", torch.bfloat16),
+            _dev(block_table, "block_table", torch.int32), _dev(seq_lens, "seq_lens", torch.int32),
+            _dev(out, "out", torch.bfloat16), _opt_dev(lse, "lse", torch.float32, q.shape[:2]),
+            _dev(workspace, "workspace", torch.uint8), workspace.numel()]
+    _check_pools(params, k_cache, v_cache, block_table, seq_lens)
+    mask = _mask_struct(params, T, softcap, key_begin, key_end, slopes)
+    device = _one_device(q, cu_q_lens, k_cache, v_cache, block_table, seq_lens, out, lse, workspace, key_begin, key_end, slopes)
+    with torch.cuda.device(device):
+        code = lib.inkling_attn_prefill_masked(ctypes.byref(params), ctypes.byref(mask), *ptrs, T, *tail,
+                                               _stream_handle(stream))
+    _check(code, "inkling_attn_prefill_masked")
+    return out
+
+
+def inkling_attn_decode_masked(params, q, k_cache, v_cache, block_table, seq_lens, out, workspace, *,
+                               softcap: float = 0.0, key_begin=None, key_end=None, slopes=None, lse=None, stream=None):
+    """Paged decode with capped scores, a distance bias and a visible key range per sequence."""
+    lib = load_library()
+    ptrs = [_dev(q, "q", torch.bfloat16), _dev(k_cache, "k_cache", torch.bfloat16),
+            _dev(v_cache, "v_cache", torch.bfloat16), _dev(block_table, "block_table", torch.int32),
+            _dev(seq_lens, "seq_lens", torch.int32), _dev(out, "out", torch.bfloat16),
+            _opt_dev(lse, "lse", torch.float32, q.shape[:2]), _dev(workspace, "workspace", torch.uint8),
+            workspace.numel()]
+    _shape(q, "q", (params.num_seqs, params.num_q_heads, params.head_dim))
+    _shape(out, "out", q.shape)
+    _check_pools(params, k_cache, v_cache, block_table, seq_lens)
+    mask = _mask_struct(params, params.num_seqs, softcap, key_begin, key_end, slopes)
+    device = _one_device(q, k_cache, v_cache, block_table, seq_lens, out, lse, workspace, key_begin, key_end, slopes)
+    with torch.cuda.device(device):
+        code = lib.inkling_attn_decode_masked(ctypes.byref(params), ctypes.byref(mask), *ptrs, _stream_handle(stream))
+    _check(code, "inkling_attn_decode_masked")
+    return out
+
+
+def _rows_dev(t: torch.Tensor, name: str, shape):
+    """Pointer and token stride of [T, H, D] rows whose heads are contiguous (a view of a fused projection)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    _shape(t, name, shape)
+    T, H, D = shape
+    if t.stride(2) != 1 or (H > 1 and t.stride(1) != D):
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
+    return t.data_ptr(), (int(t.stride(0)) if T > 1 else H * D)
+
+
+def inkling_attn_qk_norm_rope_write(params, q, k, v, cu_q_lens, seq_lens, block_table, q_out, k_cache, v_cache,
+                                    workspace, *, w_q=None, w_k=None, eps: float = 1e-6, inv_freq=None,
+                                    layout: str = "half", rot_scale: float = 1.0, stream=None):
+    """Per-head RMS norm and rotation of q and k, and the write of k and v into the paged caches.
+
+    ``q``, ``k`` and ``v`` may be views of one fused projection; ``inv_freq`` (see ``rotary.inv_freq``)
+    has one frequency per rotated pair, None for no rotation."""
+    lib = load_library()
+    if layout not in ROPE_LAYOUTS:
+        raise ValueError(f"layout must be one of {sorted(ROPE_LAYOUTS)}, got {layout!r}")
+    T, D = int(q.shape[0]), params.head_dim
+    rows = [*_rows_dev(q, "q", (T, params.num_q_heads, D)), *_rows_dev(k, "k", (T, params.num_kv_heads, D)),
+            *_rows_dev(v, "v", (T, params.num_kv_heads, D))]
+    mid = [_dev(cu_q_lens, "cu_q_lens", torch.int32), T, _dev(seq_lens, "seq_lens", torch.int32),
+           _dev(block_table, "block_table", torch.int32), _dev(q_out, "q_out", torch.bfloat16),
+           _dev(k_cache, "k_cache", torch.bfloat16), _dev(v_cache, "v_cache", torch.bfloat16),
+           _dev(workspace, "workspace", torch.uint8), workspace.numel()]
+    _shape(q_out, "q_out", q.shape)
+    _shape(cu_q_lens, "cu_q_lens", (params.num_seqs + 1,))
+    _check_pools(params, k_cache, v_cache, block_table, seq_lens)
+    rot = 0 if inv_freq is None else 2 * int(inv_freq.numel())
+    rope = ink_norm_rope_t(_opt_dev(w_q, "w_q", torch.float32, (D,)), _opt_dev(w_k, "w_k", torch.float32, (D,)),
+                           float(eps), _opt_dev(inv_freq, "inv_freq", torch.float32, (rot // 2,)), rot,
+                           ROPE_LAYOUTS[layout], float(rot_scale))
+    device = _one_device(q, k, v, cu_q_lens, seq_lens, block_table, q_out, k_cache, v_cache, workspace, w_q, w_k, inv_freq)
+    with torch.cuda.device(device):
+        code = lib.inkling_attn_qk_norm_rope_write(ctypes.byref(params), ctypes.byref(rope), *rows, *mid,
+                                                   _stream_handle(stream))
+    _check(code, "inkling_attn_qk_norm_rope_write")
+    return q_out
 
 
 def inkling_attn_set_wait_limit_ns(limit_ns: int) -> None:

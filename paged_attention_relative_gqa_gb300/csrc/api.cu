@@ -529,3 +529,143 @@ ink_status_t inkling_attn_kv_conv_write(const ink_attn_params_t* params, const v
 }
 
 }  // extern "C"
+
+namespace {
+
+ink_status_t masked_impl(const ink_attn_params_t* params, const ink_attn_mask_t* mask, const void* q,
+                         const int32_t* cu_q_lens, int32_t total_q, const void* k_cache, const void* v_cache,
+                         const int32_t* block_table, const int32_t* seq_lens, void* out, float* lse,
+                         void* workspace, size_t workspace_bytes, void* stream, bool decode) {
+  ink_status_t st = validate(params);
+  if (st != INK_OK) return st;
+  static const ink_attn_mask_t kNone = {0.f, nullptr, nullptr, nullptr};
+  const ink_attn_mask_t& mk = mask ? *mask : kNone;
+  if (!q || !k_cache || !v_cache || !block_table || !seq_lens || !out || !workspace || (!decode && !cu_q_lens))
+    return INK_ERR_NULL_PTR;
+  if (total_q < 0 || !(mk.softcap >= 0.f) || mk.softcap > 1e30f) return INK_ERR_BAD_SHAPE;
+  if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) ||
+      !aligned(cu_q_lens, 4) || !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(lse, 4) ||
+      !aligned(mk.key_begin, 4) || !aligned(mk.key_end, 4) || !aligned(mk.slopes, 4) || !aligned(workspace, 256))
+    return INK_ERR_ALIGNMENT;
+  if ((long long)total_q * params->num_q_heads >= (1ll << 31)) return INK_ERR_TOO_LARGE;
+  if (workspace_bytes < inkling_attn_masked_workspace_bytes(params, decode ? 1 : 0)) return INK_ERR_WORKSPACE;
+  if (params->num_seqs == 0 || total_q == 0) return INK_OK;
+  ink::MaskedArgs a;
+  a.q = q;
+  a.cu_q = decode ? nullptr : cu_q_lens;
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.key_begin = mk.key_begin;
+  a.key_end = mk.key_end;
+  a.slopes = mk.slopes;
+  a.k = k_cache;
+  a.v = v_cache;
+  a.out = out;
+  a.lse = lse;
+  a.err = reinterpret_cast<uint32_t*>(workspace);
+  a.B = params->num_seqs;
+  a.T = total_q;
+  a.Hq = params->num_q_heads;
+  a.Hkv = params->num_kv_heads;
+  a.G = params->num_q_heads / params->num_kv_heads;
+  a.log2_page = ilog2(params->page_size);
+  a.max_pages = params->max_pages_per_seq;
+  a.num_pages = params->num_pages;
+  a.W = params->window;
+  a.sm_scale = params->sm_scale;
+  a.softcap = mk.softcap;
+  a.wait_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
+  if (ink::launch_masked_simple(a, params->head_dim, (cudaStream_t)stream) != cudaSuccess) return INK_ERR_CUDA;
+  return INK_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t inkling_attn_masked_workspace_bytes(const ink_attn_params_t* params, int is_decode) {
+  if (validate(params) != INK_OK) return 0;
+  (void)is_decode;
+  return kHeaderBytes;
+}
+
+ink_status_t inkling_attn_prefill_masked(const ink_attn_params_t* params, const ink_attn_mask_t* mask,
+                                         const void* q, const int32_t* cu_q_lens, int32_t total_q,
+                                         const void* k_cache, const void* v_cache,
+                                         const int32_t* block_table, const int32_t* seq_lens,
+                                         void* out, float* lse, void* workspace,
+                                         size_t workspace_bytes, void* stream) {
+  return masked_impl(params, mask, q, cu_q_lens, total_q, k_cache, v_cache, block_table, seq_lens, out, lse,
+                     workspace, workspace_bytes, stream, false);
+}
+
+ink_status_t inkling_attn_decode_masked(const ink_attn_params_t* params, const ink_attn_mask_t* mask,
+                                        const void* q, const void* k_cache, const void* v_cache,
+                                        const int32_t* block_table, const int32_t* seq_lens, void* out,
+                                        float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  return masked_impl(params, mask, q, nullptr, params ? params->num_seqs : 0, k_cache, v_cache, block_table,
+                     seq_lens, out, lse, workspace, workspace_bytes, stream, true);
+}
+
+ink_status_t inkling_attn_qk_norm_rope_write(const ink_attn_params_t* params, const ink_norm_rope_t* rope,
+                                             const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                             const void* v, int64_t v_stride, const int32_t* cu_q_lens,
+                                             int32_t total_q, const int32_t* seq_lens, const int32_t* block_table,
+                                             void* q_out, void* k_cache, void* v_cache, void* workspace,
+                                             size_t workspace_bytes, void* stream) {
+  ink_status_t st = validate(params);
+  if (st != INK_OK) return st;
+  if (!rope || !q || !k || !v || !cu_q_lens || !seq_lens || !block_table || !q_out || !k_cache || !v_cache ||
+      !workspace)
+    return INK_ERR_NULL_PTR;
+  const int D = params->head_dim, Hq = params->num_q_heads, Hkv = params->num_kv_heads;
+  if (rope->rot_dim < 0 || rope->rot_dim > D || rope->rot_dim % 16 != 0) return INK_ERR_BAD_SHAPE;
+  if (rope->rot_dim > 0 && !rope->inv_freq) return INK_ERR_NULL_PTR;
+  if (rope->layout != INK_ROPE_HALF && rope->layout != INK_ROPE_INTERLEAVED) return INK_ERR_BAD_SHAPE;
+  if (!(rope->eps >= 0.f) || !(rope->rot_scale == rope->rot_scale) || total_q < 0) return INK_ERR_BAD_SHAPE;
+  if (q_stride < (int64_t)Hq * D || k_stride < (int64_t)Hkv * D || v_stride < (int64_t)Hkv * D)
+    return INK_ERR_BAD_SHAPE;
+  if (q_stride % 8 != 0 || k_stride % 8 != 0 || v_stride % 8 != 0 || !aligned(q, 16) || !aligned(k, 16) ||
+      !aligned(v, 16) || !aligned(q_out, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+      !aligned(rope->w_q, 16) || !aligned(rope->w_k, 16) || !aligned(rope->inv_freq, 4) || !aligned(cu_q_lens, 4) ||
+      !aligned(seq_lens, 4) || !aligned(block_table, 4) || !aligned(workspace, 256))
+    return INK_ERR_ALIGNMENT;
+  if (q_out == q && q_stride != (int64_t)Hq * D) return INK_ERR_BAD_SHAPE;
+  if (workspace_bytes < kHeaderBytes) return INK_ERR_WORKSPACE;
+  if (params->num_seqs == 0 || total_q == 0) return INK_OK;
+  ink::NormRopeArgs a;
+  a.x[0] = static_cast<const uint16_t*>(q);
+  a.x[1] = static_cast<const uint16_t*>(k);
+  a.x[2] = static_cast<const uint16_t*>(v);
+  a.x_stride[0] = q_stride;
+  a.x_stride[1] = k_stride;
+  a.x_stride[2] = v_stride;
+  a.q_out = static_cast<uint16_t*>(q_out);
+  a.cache[0] = static_cast<uint16_t*>(k_cache);
+  a.cache[1] = static_cast<uint16_t*>(v_cache);
+  a.w[0] = rope->w_q;
+  a.w[1] = rope->w_k;
+  a.inv_freq = rope->inv_freq;
+  a.cu_q = cu_q_lens;
+  a.seq_lens = seq_lens;
+  a.block_table = block_table;
+  a.err = reinterpret_cast<uint32_t*>(workspace);
+  a.B = params->num_seqs;
+  a.T = total_q;
+  a.H[0] = Hq;
+  a.H[1] = a.H[2] = Hkv;
+  a.log2_page = ilog2(params->page_size);
+  a.max_pages = params->max_pages_per_seq;
+  a.num_pages = params->num_pages;
+  a.rot_dim = rope->rot_dim;
+  a.eps = rope->eps;
+  a.rot_scale = rope->rot_scale;
+  int dev = 0;
+  const int sms = ink::current_device_sms(&dev);
+  if (sms <= 0) return INK_ERR_CUDA;
+  if (ink::launch_qk_norm_rope(a, D, rope->layout == INK_ROPE_INTERLEAVED, sms, (cudaStream_t)stream) != cudaSuccess)
+    return INK_ERR_CUDA;
+  return INK_OK;
+}
+
+}  // extern "C"

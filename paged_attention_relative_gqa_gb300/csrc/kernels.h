@@ -146,4 +146,46 @@ size_t kv_staged_smem_bytes(int tile_tokens, int kernel_size, int nvec, int stag
 void kv_conv_plan(KvConvArgs& a, int kernel_size, int num_sms);
 cudaError_t launch_kv_conv(const KvConvArgs& a, int kernel_size, cudaStream_t stream);
 
+// One call of the per-head norm, rotation and paged K/V write (qk_norm_rope.cu).
+struct NormRopeArgs {
+  const uint16_t* x[3];        // q, k, v rows: bf16, token stride x_stride[s] elements
+  long long x_stride[3];
+  uint16_t* q_out;             // bf16 [T, Hq, D]
+  uint16_t* cache[2];          // K, V: bf16 [num_pages, Hkv, P, D]
+  const float* w[2];           // norm weights of q, k: fp32 [D] or null
+  const float* inv_freq;       // fp32 [rot_dim / 2]
+  const int32_t* cu_q;         // [B+1]
+  const int32_t* seq_lens;     // [B]
+  const int32_t* block_table;  // [B, max_pages]
+  uint32_t* err;
+  int B, T, H[3], log2_page, max_pages, num_pages;
+  int rot_dim;
+  float eps, rot_scale;
+  int passes;                  // passes of a warp over one token's rows: ceil(Hq / rows) + 2 ceil(Hkv / rows)
+  int chunk, nchunks;          // passes per warp, warps per token
+};
+
+cudaError_t launch_qk_norm_rope(NormRopeArgs& a, int head_dim, bool interleaved, int num_sms, cudaStream_t stream);
+
+// One call of the masked attention (no bias tensor; a visible key range per token).
+struct MaskedArgs {
+  const void* q;               // bf16 [total_q, Hq, D]
+  const int32_t* cu_q;         // [B+1] (null: decode, row b is sequence b)
+  const int32_t* block_table;  // [B, max_pages]
+  const int32_t* seq_lens;     // [B]
+  const int32_t* key_begin;    // [total_q] or null
+  const int32_t* key_end;      // [total_q] or null
+  const float* slopes;         // [Hq] or null
+  const void* k;               // bf16 [num_pages, Hkv, P, D]
+  const void* v;
+  void* out;                   // bf16 [total_q, Hq, D]
+  float* lse;                  // fp32 [total_q, Hq] or null
+  uint32_t* err;
+  int B, T, Hq, Hkv, G, log2_page, max_pages, num_pages, W;
+  float sm_scale, softcap;
+  unsigned long long wait_ns;  // limit of one pipeline wait (the drain waits keep 2 s)
+};
+
+cudaError_t launch_masked_simple(const MaskedArgs& a, int head_dim, cudaStream_t stream);
+
 }  // namespace ink

@@ -1,0 +1,252 @@
+// qk_norm_rope.cu -- RMS norm of every query and key head, rotation by the token's position, and
+// the write of K and V into the paged caches, in one pass over the rows of the projection.
+//
+// For a head x of D channels at position p:
+//     y = x * (mean(x^2) + eps)^(-1/2) * w
+//     a' = c (a cos(p f) - b sin(p f)),  b' = c (b cos(p f) + a sin(p f))
+// for each pair (a, b) of the first rot_dim channels with frequency f (halves: channels i and
+// i + rot_dim / 2; interleaved: 2 i and 2 i + 1), all in fp32, one rounding to bf16 at the store.
+//
+// Bytes bound it: every row is read once and written once.  A warp takes one token and runs over
+// its head rows, LPR = D / 8 lanes to a row (16 bytes a lane, 512 contiguous bytes a warp and
+// pass), NB passes loaded before the first is used.  The angles depend on the token and the lane's channels only, so a
+// warp takes their sine and cosine once and keeps them in registers over all heads.  A token's
+// passes are cut over several warps when there are few tokens (decode).  In the half layout the
+// partner channels sit rot_dim / 16 lanes away and come by shuffle as raw bf16 (4 registers for
+// 8 channels), normed with the partner's weights.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace ink {
+namespace {
+
+constexpr int NR_THREADS = 256;
+constexpr int NB = 4;   // passes whose loads are in flight together
+
+__device__ __forceinline__ void unpack_bf16x8(const uint4 r, float (&f)[8]) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(w[i] << 16);
+    f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+
+// cos and sin of p * f, p any non-negative int32.  In turns: g = f / (2 pi) as the sum of two
+// floats (48 bits), p as the sum of two floats of at most 16 bits, so that each product's
+// rounding error is had from one fma and whole turns drop out exactly.  The result is off by
+// about p f 2^-48 turns plus a rounding of one turn.
+__device__ __forceinline__ void turn(int p, float f, float scale, float& c, float& s) {
+  constexpr float INV_2PI_HI = 0.15915494309189535f;                                 // rounded to fp32
+  constexpr float INV_2PI_LO = (float)(0.15915494309189535 - (double)INV_2PI_HI);    // and what that lost
+  const float gh = f * INV_2PI_HI;
+  const float gl = fmaf(f, INV_2PI_HI, -gh) + f * INV_2PI_LO;
+  const float ph = (float)(p & 0x7FFF0000), pl = (float)(p & 0xFFFF);
+  const float a = ph * gh, b = pl * gh;
+  const float ea = fmaf(ph, gh, -a), eb = fmaf(pl, gh, -b);
+  float r = (a - rintf(a)) + (b - rintf(b));
+  r += (ea + eb) + (ph * gl + pl * gl);
+  r -= rintf(r);
+  float cs, sn;
+  sincospif(2.f * r, &sn, &cs);
+  c = cs * scale;
+  s = sn * scale;
+}
+
+// The last b with cu_q[b] <= t < cu_q[B] (-1: t lies outside), by a whole warp: 32 offsets a step.
+__device__ __forceinline__ int find_seq_warp(const int32_t* cu_q, int B, int t, int lane) {
+  if (t >= __ldg(cu_q + B) || t < __ldg(cu_q)) return -1;
+  int lo = 0, n = B;   // the answer is among lo .. lo + n - 1
+  while (n > 1) {
+    const int step = (n + 31) >> 5;
+    const int i = lo + lane * step;
+    const bool le = lane * step < n && __ldg(cu_q + i) <= t;
+    const uint32_t m = __ballot_sync(0xffffffffu, le);
+    const int k = m ? 31 - __clz(m) : 0;
+    const int end = lo + n;
+    lo += k * step;
+    n = min(step, end - lo);
+  }
+  return lo;
+}
+
+// LAYOUT 0: no rotation, 1: halves, 2: interleaved
+template <int D, int LAYOUT>
+__global__ void __launch_bounds__(NR_THREADS) qk_norm_rope_kernel(const NormRopeArgs a) {
+  constexpr int LPR = D / 8;          // lanes per row
+  constexpr int RPP = 32 / LPR;       // rows per pass
+  const int lane = threadIdx.x & 31;
+  const long long gw = (long long)blockIdx.x * (NR_THREADS / 32) + (threadIdx.x >> 5);
+  const int t = (int)(gw / a.nchunks);
+  if (t >= a.T) return;
+  const int pass0 = (int)(gw - (long long)t * a.nchunks) * a.chunk;
+  const int pass1 = min(pass0 + a.chunk, a.passes);
+  const int lr = lane % LPR, rip = lane / LPR;
+  const int d = lr * 8;
+
+  const int b = find_seq_warp(a.cu_q, a.B, t, lane);
+  if (b < 0) return;                  // a row of no request
+  const int c0 = __ldg(a.cu_q + b), n = __ldg(a.cu_q + b + 1) - c0, L = __ldg(a.seq_lens + b);
+  if (c0 < 0 || t - c0 >= n) return;  // offsets that do not increase
+  if (n > L) {
+    if (lane == 0) record_error(a.err, INK_DEVERR_QLEN_EXCEEDS_KV);
+    return;
+  }
+  const int p = L - n + (t - c0);     // in [0, L)
+
+  const int hl = a.rot_dim >> 4;      // halves: lanes of half the rotated channels
+  const bool turned = LAYOUT != 0 && d < a.rot_dim;
+  float cs[LAYOUT == 1 ? 8 : 4], sn[LAYOUT == 1 ? 8 : 4];
+  if constexpr (LAYOUT == 1) {
+    const int f0 = (lr < hl ? lr : lr - hl) * 8;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      cs[e] = 1.f;
+      sn[e] = 0.f;
+      if (turned) turn(p, __ldg(a.inv_freq + f0 + e), a.rot_scale, cs[e], sn[e]);
+      if (lr < hl) sn[e] = -sn[e];    // first half: a cos - b sin; second: b cos + a sin
+    }
+  } else if constexpr (LAYOUT == 2) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      cs[e] = 1.f;
+      sn[e] = 0.f;
+      if (turned) turn(p, __ldg(a.inv_freq + lr * 4 + e), a.rot_scale, cs[e], sn[e]);
+    }
+  }
+  const int partner = LAYOUT == 1 && turned ? (lr < hl ? lr + hl : lr - hl) : lr;
+
+  int base = 0;                       // first pass of the section
+#pragma unroll 1
+  for (int sec = 0; sec < 3; ++sec) {
+    const int H = a.H[sec];
+    const int np = (H + RPP - 1) / RPP;
+    const int q0 = max(pass0 - base, 0), q1 = min(pass1 - base, np);
+    base += np;
+    if (q0 >= q1) continue;
+    uint16_t* dst;                    // row h goes to dst + h * step
+    long long step;
+    if (sec == 0) {
+      dst = a.q_out + (size_t)t * H * D;
+      step = D;
+    } else {
+      const int pi = p >> a.log2_page;
+      const int page = pi < a.max_pages ? __ldg(a.block_table + (size_t)b * a.max_pages + pi) : -1;
+      if (page < 0 || page >= a.num_pages) {
+        if (lane == 0) record_error(a.err, INK_DEVERR_PAGE_OUT_OF_RANGE);
+        continue;
+      }
+      step = (long long)D << a.log2_page;
+      dst = a.cache[sec - 1] + (size_t)page * H * step + (size_t)(p & ((1 << a.log2_page) - 1)) * D;
+    }
+    const uint16_t* src = a.x[sec] + (size_t)t * a.x_stride[sec];
+    const float* wsrc = sec < 2 ? a.w[sec] : nullptr;
+    float w[8], wp[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = wp[e] = 1.f;
+    if (wsrc) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const float4 f = __ldg(reinterpret_cast<const float4*>(wsrc + d) + x);
+        w[4 * x] = f.x; w[4 * x + 1] = f.y; w[4 * x + 2] = f.z; w[4 * x + 3] = f.w;
+        if constexpr (LAYOUT == 1) {
+          const float4 g = __ldg(reinterpret_cast<const float4*>(wsrc + partner * 8) + x);
+          wp[4 * x] = g.x; wp[4 * x + 1] = g.y; wp[4 * x + 2] = g.z; wp[4 * x + 3] = g.w;
+        }
+      }
+    }
+#pragma unroll 1
+    for (int q = q0; q < q1; q += NB) {
+      uint4 raw[NB];
+#pragma unroll
+      for (int k = 0; k < NB; ++k) {
+        const int h = (q + k) * RPP + rip;
+        raw[k] = make_uint4(0, 0, 0, 0);
+        if (q + k < q1 && h < H) raw[k] = *reinterpret_cast<const uint4*>(src + (size_t)h * D + d);
+      }
+#pragma unroll
+      for (int k = 0; k < NB; ++k) {
+        if (q + k >= q1) break;       // the same for the whole warp
+        const int h = (q + k) * RPP + rip;
+        uint4 res = raw[k];
+        if (sec < 2) {
+          float x[8], y[8];
+          unpack_bf16x8(raw[k], x);
+          float r = 1.f;
+          if (wsrc) {
+            float ss = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+#pragma unroll
+            for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            r = rsqrtf(fmaf(ss, 1.f / D, a.eps));
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = x[e] * r * w[e];
+          if constexpr (LAYOUT == 1) {
+            const int from = rip * LPR + partner;
+            uint4 other;
+            other.x = __shfl_sync(0xffffffffu, raw[k].x, from);
+            other.y = __shfl_sync(0xffffffffu, raw[k].y, from);
+            other.z = __shfl_sync(0xffffffffu, raw[k].z, from);
+            other.w = __shfl_sync(0xffffffffu, raw[k].w, from);
+            float z[8];
+            unpack_bf16x8(other, z);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              z[e] = z[e] * r * wp[e];
+              y[e] = turned ? fmaf(z[e], sn[e], x[e] * cs[e]) : x[e];
+            }
+          } else if constexpr (LAYOUT == 2) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              y[2 * e] = turned ? fmaf(-x[2 * e + 1], sn[e], x[2 * e] * cs[e]) : x[2 * e];
+              y[2 * e + 1] = turned ? fmaf(x[2 * e], sn[e], x[2 * e + 1] * cs[e]) : x[2 * e + 1];
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = x[e];
+          }
+          res = make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
+        }
+        if (h < H) *reinterpret_cast<uint4*>(dst + (size_t)h * step + d) = res;
+      }
+    }
+  }
+}
+
+template <int D>
+cudaError_t launch_t(const NormRopeArgs& a, int layout, cudaStream_t stream) {
+  const long long warps = (long long)a.T * a.nchunks;
+  const long long blocks = (warps + NR_THREADS / 32 - 1) / (NR_THREADS / 32);
+  if (blocks >= (1ll << 31)) return cudaErrorInvalidConfiguration;
+  const int grid = (int)blocks;
+  if (layout == 0) qk_norm_rope_kernel<D, 0><<<grid, NR_THREADS, 0, stream>>>(a);
+  else if (layout == 1) qk_norm_rope_kernel<D, 1><<<grid, NR_THREADS, 0, stream>>>(a);
+  else qk_norm_rope_kernel<D, 2><<<grid, NR_THREADS, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_qk_norm_rope(NormRopeArgs& a, int head_dim, bool interleaved, int num_sms, cudaStream_t stream) {
+  const int rpp = 32 / (head_dim / 8);
+  a.passes = (a.H[0] + rpp - 1) / rpp + 2 * ((a.H[1] + rpp - 1) / rpp);
+  // One warp per token when that already fills the machine (about 32 warps an SM); with fewer
+  // tokens a token's passes are cut over more warps, down to one pass each.
+  const long long want = (long long)num_sms * 32;
+  long long cut = a.T > 0 ? (want + a.T - 1) / a.T : 1;
+  cut = std::max(1ll, std::min<long long>(cut, a.passes));
+  a.chunk = (int)((a.passes + cut - 1) / cut);
+  a.nchunks = (a.passes + a.chunk - 1) / a.chunk;
+  const int layout = a.rot_dim == 0 ? 0 : interleaved ? 2 : 1;
+  return head_dim == 128 ? launch_t<128>(a, layout, stream) : launch_t<64>(a, layout, stream);
+}
+
+}  // namespace ink

@@ -1,0 +1,259 @@
+"""Masked, capped paged attention on the GPU against the fp64 oracle, element by element."""
+import numpy as np
+import pytest
+import torch
+
+from paged_attention_relative_gqa_gb300 import binding
+from tests.masked_common import call, check, options, problem, reference
+
+pytestmark = pytest.mark.gpu
+
+
+def _opts(prob, kind, seed, decode):
+    rng = np.random.default_rng(seed)
+    T = prob.total_q
+    L = np.repeat(prob.seq_lens_list, prob.q_lens)
+    p = np.concatenate([np.arange(b - a, b) for a, b in zip(prob.q_lens, prob.seq_lens_list)]) if T else np.zeros(0, int)
+    kw = {}
+    if "cap" in kind:
+        kw["softcap"] = {"cap": 30.0, "cap_small": 1.5, "cap_large": 500.0}[[w for w in kind.split("+") if w.startswith("cap")][0]]
+    if "slopes" in kind:
+        kw["slopes"] = 2.0 ** -rng.uniform(0, 8, prob.num_q_heads)
+    if "documents" in kind:
+        cut = 13
+        kw["begin"] = p // cut * cut
+    if "prefix" in kind:
+        kw["end"] = np.maximum(p + 1, L // 2)
+    if "random" in kind:   # anything goes: negative, past the end, empty, reversed
+        kw["begin"] = rng.integers(-5, L + 5)
+        kw["end"] = rng.integers(-5, L + 40)
+    if "nothing" in kind:
+        kw["begin"] = np.full(T, 3)
+        kw["end"] = np.full(T, 3)
+    return options(prob, **kw)
+
+
+PREFILL = [
+    # heads, dim, page, q_lens, seq_lens, window, options
+    ((8, 2), 64, 16, [1, 0, 37, 130, 5], [1, 4, 37, 400, 300], -1, ""),
+    ((8, 2), 64, 16, [1, 0, 37, 130, 5], [1, 4, 37, 400, 300], -1, "cap+slopes+random"),
+    ((8, 8), 128, 64, [257, 3], [257, 700], -1, "cap+prefix"),
+    ((8, 8), 64, 8, [90, 300], [95, 300], 37, "slopes"),
+    ((3, 1), 128, 32, [129, 1, 2], [129, 515, 2], -1, "cap_small+documents"),
+    ((14, 2), 128, 128, [40, 200], [300, 200], 100, "cap"),
+    ((16, 1), 64, 256, [33, 9], [700, 9], -1, "slopes+prefix"),
+    ((20, 1), 128, 16, [50], [333], 1, "cap_large"),
+    ((40, 1), 64, 64, [21], [128], 5, "documents"),
+    ((8, 1), 128, 64, [160, 100], [160, 1000], -1, "random"),
+    ((4, 2), 128, 16, [64, 64, 64], [64, 65, 1029], 64, "cap+random"),
+    ((8, 2), 128, 64, [70], [70], -1, "nothing"),
+    ((2, 1), 64, 8, [512], [1100], 512, "cap_small+slopes+documents"),
+]
+
+
+@pytest.mark.parametrize("case", range(len(PREFILL)))
+def test_prefill_against_the_oracle(cuda_device, case):
+    heads, dim, page, q_lens, seq_lens, window, kind = PREFILL[case]
+    prob = problem(heads, dim, page, q_lens, seq_lens, 100 + case, cuda_device, window, q_std=3.0 if "cap" in kind else 1.0)
+    opts = _opts(prob, kind, case, False)
+    out, lse, ws = call(prob, opts, False)
+    torch.cuda.synchronize()
+    assert binding.inkling_attn_read_device_error(ws) == 0
+    check(out, lse, reference(prob, opts), f"case {case}")
+
+
+DECODE = [
+    ((8, 2), 64, 16, [1, 5, 64, 65, 700], -1, ""),
+    ((8, 8), 128, 64, [1, 129, 1000], -1, "cap"),
+    ((16, 1), 128, 8, [300, 17], -1, "cap_small+slopes"),
+    ((20, 1), 64, 32, [63, 640], 100, "slopes"),
+    ((40, 2), 128, 16, [333, 2], 1, "cap"),
+    ((64, 8), 128, 64, [5000, 1, 300, 2048], -1, "slopes+documents"),
+    ((8, 2), 64, 256, [255, 256, 257, 4000], 512, "random"),
+    ((14, 2), 128, 128, [900, 30, 31, 32, 33], -1, "random"),
+    ((8, 1), 64, 64, [100, 200], -1, "nothing"),
+    ((8, 1), 128, 64, [20000], -1, "cap_large"),
+]
+
+
+@pytest.mark.parametrize("case", range(len(DECODE)))
+def test_decode_against_the_oracle(cuda_device, case):
+    heads, dim, page, seq_lens, window, kind = DECODE[case]
+    prob = problem(heads, dim, page, [1] * len(seq_lens), seq_lens, 200 + case, cuda_device, window,
+                   q_std=3.0 if "cap" in kind else 1.0)
+    opts = _opts(prob, kind, case, True)
+    out, lse, ws = call(prob, opts, True)
+    torch.cuda.synchronize()
+    assert binding.inkling_attn_read_device_error(ws) == 0
+    check(out, lse, reference(prob, opts), f"case {case}")
+
+
+@pytest.mark.parametrize("decode", [False, True])
+def test_empty_sequences_and_rows_behind_the_last(cuda_device, decode):
+    q_lens, seq_lens = ([1, 1, 1], [5, 0, 40]) if decode else ([5, 0, 9], [5, 0, 40])
+    prob = problem((8, 2), 64, 16, [n if L else 0 for n, L in zip(q_lens, seq_lens)], seq_lens, 7, cuda_device)
+    rows = len(seq_lens) if decode else prob.total_q + 6
+    prob.q = torch.randn(rows, 8, 64, device=cuda_device).to(torch.bfloat16)
+    if decode:
+        prob.cu_q_lens = torch.arange(4, dtype=torch.int32, device=cuda_device)
+    opts = options(prob)
+    out, lse, ws = call(prob, opts, decode)
+    torch.cuda.synchronize()
+    assert binding.inkling_attn_read_device_error(ws) == 0
+    check(out, lse, reference(prob, opts), "rows behind the last sequence")
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf"), -3.3895e38])
+@pytest.mark.parametrize("decode", [False, True])
+def test_values_in_masked_places_do_not_reach_the_output(cuda_device, decode, bad):
+    """Keys past the visible range of a row, and keys that only other rows see, hold `bad` in K and V."""
+    seq_lens = [200, 97, 330]
+    q_lens = [1, 1, 1] if decode else [200, 60, 70]
+    prob = problem((8, 2), 128, 16, q_lens, seq_lens, 8, cuda_device)
+    p = np.concatenate([np.arange(b - a, b) for a, b in zip(q_lens, seq_lens)])
+    begin = np.where(p >= 60, 60, 0)          # two documents: [0, 60) and [60, L)
+    opts = options(prob, begin=begin)
+    clean = reference(prob, opts)
+    table = prob.block_table.cpu().numpy()
+    for b, L in enumerate(seq_lens):
+        for k in list(range(20, 40)) + list(range(L, (L + 15) // 16 * 16)):
+            prob.k_cache[int(table[b, k // 16]), :, k % 16] = bad
+            prob.v_cache[int(table[b, k // 16]), :, k % 16] = bad
+    out, lse, ws = call(prob, opts, decode)
+    torch.cuda.synchronize()
+    second = np.nonzero((p >= 60) | (p < 20))[0]   # rows that see none of the poisoned keys
+    check(out[second], lse[second], tuple(x[second] for x in clean), "poisoned keys")
+
+
+def test_non_finite_values_reach_the_rows_that_see_them(cuda_device):
+    prob = problem((8, 2), 64, 16, [150], [150], 9, cuda_device)
+    table = prob.block_table.cpu().numpy()
+    prob.v_cache[int(table[0, 70 // 16]), :, 70 % 16, 5] = float("inf")
+    prob.v_cache[int(table[0, 90 // 16]), :, 90 % 16, 6] = float("nan")
+    opts = options(prob)
+    out, lse, ws = call(prob, opts, False)
+    torch.cuda.synchronize()
+    got = out.float().cpu().numpy()
+    assert np.isfinite(got[:70]).all() and np.isfinite(lse.cpu().numpy()).all()
+    assert np.isposinf(got[70:, :, 5]).all() and np.isfinite(got[:, :, 7:]).all()
+    assert np.isfinite(got[:90, :, 6]).all() and np.isnan(got[90:, :, 6]).all()
+
+
+@pytest.mark.parametrize("decode", [False, True])
+def test_pages_outside_the_pool_are_masked_and_reported(cuda_device, decode):
+    seq_lens = [200, 90]
+    prob = problem((8, 2), 64, 16, [1, 1] if decode else [30, 90], seq_lens, 10, cuda_device)
+    prob.block_table[0, 3] = prob.num_pages
+    prob.block_table[1, 0] = -4
+    opts = options(prob, slopes=np.linspace(0, 0.1, 8))
+    out, lse, ws = call(prob, opts, decode)
+    torch.cuda.synchronize()
+    assert binding.inkling_attn_read_device_error(ws) == binding.DEVERR_PAGE_OUT_OF_RANGE
+    check(out, lse, reference(prob, opts), "bad pages")
+
+
+def test_lengths_that_contradict_are_reported(cuda_device):
+    prob = problem((8, 2), 64, 16, [8, 4, 6], [20, 9, 30], 11, cuda_device)
+    prob.seq_lens[1] = 3   # four new tokens, three keys
+    opts = options(prob)
+    out, lse, ws = call(prob, opts, False)
+    torch.cuda.synchronize()
+    assert binding.inkling_attn_read_device_error(ws) == binding.DEVERR_QLEN_EXCEEDS_KV
+    check(out, lse, reference(prob, opts), "contradicting lengths")
+
+
+@pytest.mark.parametrize("decode", [False, True])
+def test_offsets_past_32_bits(cuda_device, decode):
+    """Pages at the end of a pool of more than 2^31 elements, another sequence at its start."""
+    prob = problem((8, 8), 128, 64, [1, 1] if decode else [5, 40], [100, 150], 12, cuda_device)
+    n = (1 << 31) // (8 * 64 * 128) + 64
+    big = []
+    for c in (prob.k_cache, prob.v_cache):
+        pool = torch.zeros(n, 8, 64, 128, dtype=torch.bfloat16, device=cuda_device)
+        pool[:2] = c[prob.block_table[0, :2].long()]
+        pool[n - 3:] = c[prob.block_table[1, :3].long()]
+        big.append(pool)
+    small = prob.to("cpu")
+    opts = options(prob)
+    want = reference(small, options(small))
+    prob.k_cache, prob.v_cache = big
+    prob.block_table = torch.tensor([[0, 1, n + 7], [n - 3, n - 2, n - 1]], dtype=torch.int32, device=cuda_device)
+    out, lse, ws = call(prob, opts, decode)
+    torch.cuda.synchronize()
+    assert binding.inkling_attn_read_device_error(ws) == 0
+    check(out, lse, want, "large pool")
+
+
+@pytest.mark.parametrize("decode", [False, True])
+def test_repeats_bit_for_bit_and_from_a_graph_on_another_stream(cuda_device, decode):
+    seq_lens = [1500, 3, 700, 2222]
+    prob = problem((16, 2), 128, 64, [1] * 4 if decode else [300, 3, 1, 222], seq_lens, 13, cuda_device, q_std=2.0)
+    opts = options(prob, softcap=20.0, slopes=np.linspace(0.01, 0.3, 16))
+    out, lse, ws = call(prob, opts, decode)
+    torch.cuda.synchronize()
+    first = (out.clone(), lse.clone())
+    check(out, lse, reference(prob, opts), "eager")
+    params = binding.params_of(prob)
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    o2, l2 = torch.zeros_like(out), torch.zeros_like(lse)
+    ws2 = binding.alloc_masked_workspace(params, decode, cuda_device)
+    torch.cuda.synchronize()
+
+    def go():
+        if decode:
+            binding.inkling_attn_decode_masked(params, prob.q, prob.k_cache, prob.v_cache, prob.block_table,
+                                               prob.seq_lens, o2, ws2, lse=l2, **opts)
+        else:
+            binding.inkling_attn_prefill_masked(params, prob.q, prob.cu_q_lens, prob.k_cache, prob.v_cache,
+                                                prob.block_table, prob.seq_lens, o2, ws2, lse=l2, **opts)
+    with torch.cuda.stream(side):
+        go()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        go()
+    for _ in range(3):
+        o2.zero_()
+        l2.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o2, first[0]) and torch.equal(l2, first[1])
+    # new lengths and inputs in the captured buffers
+    prob.seq_lens.copy_(torch.tensor([1400, 3, 650, 2000], dtype=torch.int32))
+    prob.seq_lens_list = [1400, 3, 650, 2000]
+    prob.q.copy_(torch.randn_like(prob.q, dtype=torch.float32))
+    graph.replay()
+    torch.cuda.synchronize()
+    check(o2, l2, reference(prob, opts), "replayed with new lengths")
+
+
+def test_prefill_and_decode_agree_and_parts_join(cuda_device):
+    """One token as prefill and as decode, and the outputs over two halves of a history joined by lse."""
+    L = 1000
+    prob = problem((8, 2), 128, 64, [1], [L], 14, cuda_device)
+    whole, wl, _ = call(prob, options(prob), False)
+    dec, dl, _ = call(prob, options(prob), True)
+    ref = reference(prob, options(prob))
+    check(whole, wl, ref, "prefill")
+    check(dec, dl, ref, "decode")
+    parts = [call(prob, options(prob, begin=[a], end=[b]), True) for a, b in ((0, 450), (450, L))]
+    lse = torch.stack([x[1] for x in parts])
+    w = torch.softmax(lse, 0)[..., None]
+    joined = sum(wi * x[0].float() for wi, x in zip(w, parts))
+    # two more bf16 roundings of the parts
+    tol = 2.0 ** -7 * sum(wi * x[0].float().abs() for wi, x in zip(w, parts)) + torch.as_tensor(ref[2] * 2.0 ** -7).to(cuda_device)
+    assert ((joined - whole.float()).abs() <= tol).all()
+
+
+def test_calls_on_two_streams_with_their_own_workspaces(cuda_device):
+    probs = [problem((8, 2), 64, 16, [1] * 5, [300, 20, 777, 1, 64], 15 + i, cuda_device) for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in probs]
+    params = [binding.params_of(p) for p in probs]
+    ws = [binding.alloc_masked_workspace(p, True, cuda_device) for p in params]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(5):
+        got = [call(p, options(p), True, workspace=w, stream=s) for p, w, s in zip(probs, ws, streams)]
+        torch.cuda.synchronize()
+    for p, (out, lse, _) in zip(probs, got):
+        check(out, lse, reference(p, options(p)), "two streams")
