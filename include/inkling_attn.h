@@ -270,7 +270,7 @@ ink_status_t inkling_attn_kv_conv_write(const ink_attn_params_t* params, const v
  *     s_k = (softcap > 0 ? softcap * tanh(x / softcap) : x) - slopes[h] * |p - k|
  */
 typedef struct {
-  float softcap;             /* > 0: scores capped by a tanh; 0: not capped */
+  float softcap;             /* in [1e-6, 1e6]: scores capped by a tanh; 0: not capped */
   const int32_t* key_begin;  /* device int32 [rows of q] first visible key, or NULL: 0 */
   const int32_t* key_end;    /* device int32 [rows of q] last visible key + 1, or NULL: p + 1 */
   const float* slopes;       /* device fp32 [Hq], or NULL: no distance bias */

@@ -532,6 +532,21 @@ ink_status_t inkling_attn_kv_conv_write(const ink_attn_params_t* params, const v
 
 namespace {
 
+// q [total_q, Hq, D] as {D, Hq, total_q}, boxes of 64 channels x heads x tokens with the 128-byte
+// swizzle: the rows of an MMA operand, tokens outermost.  Rows outside the tensor read as zeros.
+bool make_token_map(CUtensorMap* map, const void* q, const ink_attn_params_t* p, int total_q, int heads, int tokens) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t row = (cuuint64_t)p->head_dim * 2;
+  cuuint64_t dims[3] = {(cuuint64_t)p->head_dim, (cuuint64_t)p->num_q_heads, (cuuint64_t)total_q};
+  cuuint64_t strides[2] = {row, row * p->num_q_heads};
+  cuuint32_t box[3] = {64, (cuuint32_t)heads, (cuuint32_t)tokens};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 ink_status_t masked_impl(const ink_attn_params_t* params, const ink_attn_mask_t* mask, const void* q,
                          const int32_t* cu_q_lens, int32_t total_q, const void* k_cache, const void* v_cache,
                          const int32_t* block_table, const int32_t* seq_lens, void* out, float* lse,
@@ -542,7 +557,7 @@ ink_status_t masked_impl(const ink_attn_params_t* params, const ink_attn_mask_t*
   const ink_attn_mask_t& mk = mask ? *mask : kNone;
   if (!q || !k_cache || !v_cache || !block_table || !seq_lens || !out || !workspace || (!decode && !cu_q_lens))
     return INK_ERR_NULL_PTR;
-  if (total_q < 0 || !(mk.softcap >= 0.f) || mk.softcap > 1e30f) return INK_ERR_BAD_SHAPE;
+  if (total_q < 0 || !(mk.softcap == 0.f || (mk.softcap >= 1e-6f && mk.softcap <= 1e6f))) return INK_ERR_BAD_SHAPE;
   if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) ||
       !aligned(cu_q_lens, 4) || !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(lse, 4) ||
       !aligned(mk.key_begin, 4) || !aligned(mk.key_end, 4) || !aligned(mk.slopes, 4) || !aligned(workspace, 256))
@@ -575,7 +590,26 @@ ink_status_t masked_impl(const ink_attn_params_t* params, const ink_attn_mask_t*
   a.sm_scale = params->sm_scale;
   a.softcap = mk.softcap;
   a.wait_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
-  if (ink::launch_masked_simple(a, params->head_dim, (cudaStream_t)stream) != cudaSuccess) return INK_ERR_CUDA;
+  a.scale_log2 = params->sm_scale * 1.4426950408889634f;
+  a.cap_log2 = mk.softcap * 1.4426950408889634f;
+  a.cap_k1 = mk.softcap > 0.f ? (float)(2.0 * 1.4426950408889634 * params->sm_scale / mk.softcap) : 0.f;
+  a.cap_inv = mk.softcap > 0.f ? params->sm_scale / mk.softcap : 0.f;
+  a.counters = reinterpret_cast<uint32_t*>(workspace) + 16;   // inside the header
+  // a row tile: the heads of a KV head (in equal chunks when there are more than 128) times as
+  // many tokens as fit
+  a.head_chunks = (a.G + ink::MASKED_ROWS - 1) / ink::MASKED_ROWS;
+  a.heads_per_tile = (a.G + a.head_chunks - 1) / a.head_chunks;
+  a.tok_per_tile = ink::MASKED_ROWS / a.heads_per_tile;
+  if (decode) {
+    if (ink::launch_masked_simple(a, params->head_dim, (cudaStream_t)stream) != cudaSuccess) return INK_ERR_CUDA;
+    return INK_OK;
+  }
+  ink::MaskedMaps maps;
+  if (!make_pool_map(&maps.k, k_cache, params, 128) || !make_pool_map(&maps.v, v_cache, params, 128) ||
+      !make_token_map(&maps.q, q, params, total_q, a.heads_per_tile, a.tok_per_tile))
+    return INK_ERR_CUDA;
+  if (ink::launch_prefill_masked(maps, a, params->head_dim, aligned(out, 32), (cudaStream_t)stream) != cudaSuccess)
+    return INK_ERR_CUDA;
   return INK_OK;
 }
 

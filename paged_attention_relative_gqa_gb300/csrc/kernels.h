@@ -183,9 +183,27 @@ struct MaskedArgs {
   uint32_t* err;
   int B, T, Hq, Hkv, G, log2_page, max_pages, num_pages, W;
   float sm_scale, softcap;
+  float scale_log2;            // sm_scale * log2(e)
+  float cap_k1;                // 2 * sm_scale * log2(e) / softcap
+  float cap_log2;              // softcap * log2(e)
+  float cap_inv;               // sm_scale / softcap
   unsigned long long wait_ns;  // limit of one pipeline wait (the drain waits keep 2 s)
+  // prefill: a row tile holds tok_per_tile tokens x heads_per_tile query heads of one KV head
+  int head_chunks, heads_per_tile, tok_per_tile;
+  uint32_t* counters;          // [0] items handed out, [1] CTAs done; zero between calls
 };
 
+// Caps up to this one take the plain formula of tanh (fewer instructions, off by 2^-23 of the cap).
+constexpr float SOFTCAP_PLAIN = 64.f;
+constexpr int MASKED_ROWS = 128;   // rows of a tile
+
+// TMA descriptors: the pools with boxes of min(P, 128) rows, q as {D, Hq, T} with boxes of
+// 64 channels x heads_per_tile x tok_per_tile.
+struct MaskedMaps {
+  CUtensorMap k, v, q;
+};
+
+cudaError_t launch_prefill_masked(const MaskedMaps& m, const MaskedArgs& a, int head_dim, bool io32, cudaStream_t stream);
 cudaError_t launch_masked_simple(const MaskedArgs& a, int head_dim, cudaStream_t stream);
 
 }  // namespace ink

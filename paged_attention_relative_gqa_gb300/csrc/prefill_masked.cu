@@ -1,0 +1,757 @@
+// prefill_masked.cu -- paged prefill without a bias tensor on the 5th-generation tensor cores:
+// scores capped by a tanh, a bias linear in the distance, and a visible key range per token.
+//
+//   x = sm_scale <q[t,h], K[k]>,  s = cap(x) - slope_h |p - k|,  out = softmax(s) V,  lse = log sum exp(s)
+//   over keys max(begin_t, p - W + 1, 0) <= k < min(end_t, L)
+//
+// Work item: up to 256 rows of one sequence and KV head in two row tiles of 128 (the M of an
+// MMA).  A row is a (token, query head) pair, tokens outermost, so that the heads of a group fill
+// a tile together: 16 tokens x 8 heads, 128 tokens x 1 head, 25 tokens x 5 heads (125 rows used).
+// Both tiles read the same K and V tiles of 128 keys, a short run of tokens keeps the masked part
+// of the diagonal small, and a few new tokens still fill the rows.
+//
+// Tensor memory (512 columns for D = 128): S of both tiles (128 fp32 columns each), with P, the
+// bf16 numerators, over the first 64 columns of its S once that is in registers, and O of both
+// tiles (D columns each).  Q, K and V sit in shared memory (two Q tiles and a ring of K and V
+// tiles, 224 KB of the 227 KB).
+//
+// Warps (384 threads; registers moved from the last warpgroup to the two that run the softmax):
+//   0-3, 4-7  softmax of row tile 0 and 1, a thread per row: reads its 128 scores, caps, masks, keeps
+//             the running maximum (moved only when it grows by more than 2^8) and sum, writes P;
+//             at the end O / l and lse.
+//   8   K and V producer: TMA boxes of whole pages or 128 rows, table entries 32 at a time in lanes.
+//   9   MMA issue, in the order P_0 V(j), Q_0 K(j+1), P_1 V(j), Q_1 K(j+1): while one tile's softmax
+//       runs, the tensor cores work for the other.
+//   10  scheduler: hands out items (a counter in the workspace, longest first within a sequence),
+//       finds their key ranges, publishes them in shared memory, and loads their Q tiles by TMA.
+//   11  V check: in a tile that not every row of the item sees whole, rows of V that nobody sees
+//       are zeroed, and so are rows with an infinity or NaN (0 * NaN would reach rows that do not
+//       see the key); rows that do see one get it back in the epilogue.
+// Every wait is bounded; after a timeout the CTA records it, stops issuing, waits for what is in
+// flight and exits.
+#include <algorithm>
+#include <climits>
+
+#include "prefill_common.cuh"
+
+namespace ink {
+namespace {
+
+using namespace pf;
+
+constexpr int PM_THREADS = 384;
+constexpr int PM_KEYS = 128;      // keys per K or V tile
+constexpr int PM_ITEMS = 4;       // published items in flight
+constexpr int PM_BAD = 8;         // tiles whose unreadable keys are remembered
+constexpr int PM_VOK = 4;         // V tiles checked ahead of their product (at most NS / 2 are in the ring)
+constexpr int PM_REGS_SOFTMAX = 208, PM_REGS_REST = 88;   // registers a thread after the split
+constexpr float LN2 = 0.6931471805599453f;
+constexpr float RESCALE_LOG2 = 8.f;
+
+template <int D>
+struct PMShape {
+  static constexpr int CB = D / 64;
+  static constexpr int SUB = PM_KEYS * 128;        // one 64-channel block of a tile
+  static constexpr int TILE = CB * SUB;            // K, V and Q tiles alike
+  static constexpr int NS = D == 128 ? 5 : 8;      // ring slots, K and V tiles in turn
+  static constexpr uint32_t TO = 256;              // S_h at 128 h, O_h at TO + D h
+};
+
+struct PMItem {
+  int b, kvh, h0, gh;        // sequence, KV head, first query head, heads of the item
+  int t0, ntok, pos0, L;     // first packed row, tokens, position of the first, length
+  int lo_min, hi_max;        // keys any row sees lie in [lo_min, hi_max)
+  int lo_max, hi_min;        // keys in [lo_max, hi_min) are seen by every row
+  int kt0, nt, nh, bad_len;  // first key tile, tiles (-1: no more items), row tiles
+};
+
+template <int D>
+struct PMSmem {
+  using S = PMShape<D>;
+  static constexpr size_t q = 0;
+  static constexpr size_t ring = 2 * (size_t)S::TILE;
+  static constexpr size_t bars = ring + (size_t)S::NS * S::TILE;
+  // full[NS], empty[NS], v_ok[VOK], s_full[2], p_full[2], o_full[2], q_full[2], q_empty[2],
+  // item_full[ITEMS], item_empty[ITEMS], drain
+  static constexpr int NBAR = 2 * S::NS + PM_VOK + 10 + 2 * PM_ITEMS + 1;
+  static constexpr size_t items = bars + (NBAR * 8 + 15) / 16 * 16;
+  static constexpr size_t kbad = items + PM_ITEMS * sizeof(PMItem);
+  static constexpr size_t poison = kbad + PM_BAD * 16;
+  static constexpr size_t misc = poison + PM_ITEMS * 4;
+  static constexpr size_t total = misc + 16;
+  static constexpr size_t alloc = total + 1024;
+  static_assert(alloc <= 227 * 1024, "shared memory budget");
+};
+
+// Visible keys [lo, hi) of token t at position p (hi <= lo: none).
+__device__ __forceinline__ void token_keys(const MaskedArgs& a, int t, int p, int L, int& lo, int& hi) {
+  lo = a.key_begin ? max(__ldg(a.key_begin + t), 0) : 0;
+  if (a.W > 0) lo = max(lo, p - a.W + 1);
+  hi = a.key_end ? __ldg(a.key_end + t) : p + 1;
+  hi = max(0, min(hi, (int)min((long long)L, (long long)a.max_pages << a.log2_page)));
+}
+
+// Bounded wait of a whole warp (inline: a call would keep the registers from being split).
+__device__ __forceinline__ bool pm_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, const MaskedArgs& a) {
+  bool ok = mbar_probe(bar, parity, a.wait_ns);
+  if (!ok && !*abort_flag) {
+    ok = mbar_wait_limit(bar, parity, a.wait_ns);
+    if (!ok) {
+      record_error(a.err, INK_DEVERR_WAIT_TIMEOUT);
+      *abort_flag = 1;
+    }
+  }
+  return __all_sync(0xffffffffu, ok);
+}
+
+__device__ __forceinline__ float fast_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// CAP 0: no cap.  1: s = C (1 - 2 / (1 + 2^(k1 x))), off by about 2^-23 C: for caps up to
+// SOFTCAP_PLAIN.  2: the same, and for |x| < C / 4 the odd series of tanh to the 7th power, whose
+// relative error stays below 2^-21: for caps so large that 2^-23 C would count.
+template <int D, int CAP, bool IO32>
+__global__ void __launch_bounds__(PM_THREADS, 1)
+prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                      const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ MaskedArgs a) {
+  using S = PMShape<D>;
+  using L_ = PMSmem<D>;
+  constexpr int NS = S::NS;
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_align1024(smem_raw);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L_::bars);
+  uint64_t* empty = full + NS;
+  uint64_t* v_ok = empty + NS;
+  uint64_t* s_full = v_ok + PM_VOK;     // [2] S_h in TMEM, every earlier product of h done
+  uint64_t* p_full = s_full + 2;        // [2] P_h written
+  uint64_t* o_full = p_full + 2;        // [2] the item's last O_h product done
+  uint64_t* q_full = o_full + 2;        // [2]
+  uint64_t* q_empty = q_full + 2;       // [2] the item's last S_h product done
+  uint64_t* item_full = q_empty + 2;    // [ITEMS]
+  uint64_t* item_empty = item_full + PM_ITEMS;
+  uint64_t* drain = item_empty + PM_ITEMS;
+  PMItem* items = reinterpret_cast<PMItem*>(smem + L_::items);
+  uint32_t* kbad = reinterpret_cast<uint32_t*>(smem + L_::kbad);      // [BAD][4] bit per unreadable key
+  volatile int* poison = reinterpret_cast<volatile int*>(smem + L_::poison);   // [ITEMS]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L_::misc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L_::misc + 4);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int P = 1 << a.log2_page;
+
+  if (tid == 0) {
+    for (int x = 0; x < NS; ++x) {
+      mbar_init(&full[x], 1);
+      mbar_init(&empty[x], 1);
+    }
+    for (int x = 0; x < PM_VOK; ++x) mbar_init(&v_ok[x], 1);
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&s_full[x], 1);
+      mbar_init(&p_full[x], 4);
+      mbar_init(&o_full[x], 1);
+      mbar_init(&q_full[x], 1);
+      mbar_init(&q_empty[x], 1);
+    }
+    for (int x = 0; x < PM_ITEMS; ++x) {
+      mbar_init(&item_full[x], 1);
+      mbar_init(&item_empty[x], 11);   // producer, MMA, V check, 8 softmax warps
+    }
+    mbar_init(drain, 1);
+    fence_mbar_init();
+    *abort_flag = 0;
+  }
+  // rows of a Q tile past the last (token, head) pair stay zero
+  for (int x = tid; x < 2 * S::TILE / 16; x += PM_THREADS)
+    *reinterpret_cast<uint4*>(smem + L_::q + (size_t)x * 16) = make_uint4(0u, 0u, 0u, 0u);
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  if (warp == 9) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
+                 "n"(512));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  // The k-th item of this CTA into `it`; false when there is none (or after a timeout).
+  auto next_item = [&](int k, PMItem& it) -> bool {
+    if (!pm_wait(&item_full[k % PM_ITEMS], (uint32_t)(k / PM_ITEMS) & 1u, abort_flag, a)) return false;
+    it = items[k % PM_ITEMS];
+    return it.nt >= 0;
+  };
+  auto done_item = [&](int k) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&item_empty[k % PM_ITEMS]);
+  };
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(PM_REGS_REST));
+    if (warp == 8) {
+      // ---------------------------------------------------------------- K and V producer
+      if (lane == 0) {
+        prefetch_tensormap(&tmK);
+        prefetch_tensormap(&tmV);
+      }
+      const int seg = min(P, PM_KEYS), nseg = PM_KEYS / seg;
+      int chunk_base = 0, chunk_val = -1;   // table entries chunk_base + lane
+      int f = 0;                            // fills issued
+      bool go = true;
+      PMItem it;
+      for (int k = 0; go && next_item(k, it); ++k) {
+        done_item(k);
+        for (int j = 0; j < it.nt && go; ++j) {
+          const int k0 = (it.kt0 + j) * PM_KEYS;
+          const int last_idx = (it.hi_max - 1) >> a.log2_page;
+          const int pfirst = k0 >> a.log2_page, plast = (k0 + PM_KEYS - 1) >> a.log2_page;
+          if (j == 0 || plast >= chunk_base + 32) {
+            chunk_base = pfirst;   // entries past the item's last key are not read
+            chunk_val = __ldg(a.block_table + (size_t)it.b * a.max_pages + min(chunk_base + lane, last_idx));
+          }
+          const int ks = k0 + lane * seg;                 // lane < nseg takes one segment
+          const bool want = lane < nseg && ks < it.hi_max && ks + seg > it.lo_min;
+          const int page = __shfl_sync(0xffffffffu, chunk_val, min(max((ks >> a.log2_page) - chunk_base, 0), 31));
+          const bool bad_seg = want && (page < 0 || page >= a.num_pages);
+          const bool load = want && !bad_seg;
+          const uint32_t nload = __popc(__ballot_sync(0xffffffffu, load));
+          const uint32_t bmask = __ballot_sync(0xffffffffu, bad_seg);
+          const int row = load ? ((page * a.Hkv + it.kvh) << a.log2_page) + (ks & (P - 1)) : 0;
+#pragma unroll 1
+          for (int kv = 0; kv < 2; ++kv, ++f) {
+            const int st = f % NS;
+            if (f >= NS && !pm_wait(&empty[st], (uint32_t)((f / NS) - 1) & 1u, abort_flag, a)) {
+              go = false;
+              break;
+            }
+            if (kv == 0 && lane < 4) {   // keys of this tile whose page is outside the pool
+              uint32_t bad = 0;
+              for (uint32_t mm = bmask; mm; mm &= mm - 1) {
+                const int x0 = (__ffs(mm) - 1) * seg - 32 * lane, x1 = x0 + seg;   // bits [x0, x1) of this word
+                const int y0 = max(x0, 0), y1 = min(x1, 32);
+                if (y1 > y0) bad |= (0xffffffffu >> (32 - (y1 - y0))) << y0;
+              }
+              kbad[((f >> 1) % PM_BAD) * 4 + lane] = bad;
+              if (bmask && lane == 0) record_error(a.err, INK_DEVERR_PAGE_OUT_OF_RANGE);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive_expect_tx(&full[st], nload * (uint32_t)(seg * D * 2));
+            __syncwarp();
+            if (load) {
+              uint8_t* dst = smem + L_::ring + (size_t)st * S::TILE + lane * seg * 128;
+#pragma unroll
+              for (int cb = 0; cb < S::CB; ++cb)
+                tma_load_2d(dst + cb * S::SUB, kv ? &tmV : &tmK, cb * 64, row, &full[st]);
+            }
+          }
+        }
+      }
+      if (lane == 0) pp_drain_ring(full, NS, f, a.err);
+    } else if (warp == 9) {
+      // ---------------------------------------------------------------- MMA issue
+      constexpr uint32_t IDESC_S = umma_idesc_bf16(128, PM_KEYS, false, false);
+      constexpr uint32_t IDESC_PV = umma_idesc_bf16(128, D, false, true);
+      const uint32_t qaddr = smem_u32(smem + L_::q), raddr = smem_u32(smem + L_::ring);
+      int g = 0;                       // tiles walked: K of tile g is fill 2 g, V fill 2 g + 1
+      uint32_t qn0 = 0, qn1 = 0, pn0 = 0, pn1 = 0;
+      bool go = true;
+      auto slot = [&](int f) { return f % NS; };
+      auto par = [&](int f) { return (uint32_t)(f / NS) & 1u; };
+      auto issue_s = [&](int h, int f) {
+        const uint64_t ad = umma_desc_sw128(qaddr + h * S::TILE, 16, 1024);
+        const uint64_t bd = umma_desc_sw128(raddr + slot(f) * S::TILE, 16, 1024);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint64_t off = (uint64_t)(((kk >> 2) * S::SUB + (kk & 3) * 32) >> 4);
+          umma_ss_warp(tmem + 128u * h, ad + off, bd + off, IDESC_S, kk > 0 ? 1u : 0u);
+        }
+      };
+      auto issue_pv = [&](int h, int f, bool acc) {
+        const uint64_t bd = umma_desc_sw128(raddr + slot(f) * S::TILE, S::SUB, 1024);
+#pragma unroll
+        for (int ks = 0; ks < PM_KEYS / 16; ++ks)
+          umma_ts_warp(tmem + S::TO + (uint32_t)(D * h), tmem + 128u * h + ks * 8, bd + (uint64_t)((ks * 16 * 128) >> 4),
+                       IDESC_PV, (acc || ks > 0) ? 1u : 0u);
+      };
+      PMItem it;
+      for (int k = 0; go && next_item(k, it); ++k) {
+        done_item(k);
+        if (it.nt <= 0) continue;
+        go = pm_wait(&full[slot(2 * g)], par(2 * g), abort_flag, a);
+        for (int h = 0; h < it.nh && go; ++h) {
+          uint32_t& qn = h ? qn1 : qn0;
+          go = pm_wait(&q_full[h], qn & 1u, abort_flag, a);
+          ++qn;
+          if (!go) break;
+          tc_fence_after();
+          issue_s(h, 2 * g);
+          umma_commit_warp(&s_full[h]);
+          if (it.nt == 1) umma_commit_warp(&q_empty[h]);
+          __syncwarp();
+        }
+        if (!go) break;
+        umma_commit_warp(&empty[slot(2 * g)]);
+        for (int j = 0; j < it.nt && go; ++j, ++g) {
+          const int vf = 2 * g + 1, kf = 2 * g + 2;
+          const bool more = j + 1 < it.nt;
+          go = pm_wait(&full[slot(vf)], par(vf), abort_flag, a) && pm_wait(&v_ok[g % PM_VOK], (uint32_t)(g / PM_VOK) & 1u, abort_flag, a);
+          for (int h = 0; h < it.nh && go; ++h) {
+            uint32_t& pn = h ? pn1 : pn0;
+            go = pm_wait(&p_full[h], pn & 1u, abort_flag, a);
+            ++pn;
+            if (!go) break;
+            tc_fence_after();
+            issue_pv(h, vf, j > 0);
+            if (more) {
+              if (h == 0) go = pm_wait(&full[slot(kf)], par(kf), abort_flag, a);
+              if (!go) break;
+              issue_s(h, kf);
+              umma_commit_warp(&s_full[h]);
+              if (j + 2 == it.nt) umma_commit_warp(&q_empty[h]);
+            } else {
+              umma_commit_warp(&o_full[h]);
+            }
+            __syncwarp();
+          }
+          if (!go) break;
+          umma_commit_warp(&empty[slot(vf)]);
+          if (more) umma_commit_warp(&empty[slot(kf)]);
+          __syncwarp();
+        }
+      }
+      umma_commit_warp(drain);
+      __syncwarp();
+      if (!mbar_wait_bounded(drain, 0)) record_error(a.err, INK_DEVERR_WAIT_TIMEOUT);
+    } else if (warp == 10) {
+      // ---------------------------------------------------------------- scheduler and Q loads
+      if (lane == 0) prefetch_tensormap(&tmQ);
+      const int per = a.Hkv * a.head_chunks, tpi = 2 * a.tok_per_tile;
+      int cb = 0, base = 0, cnt = 0, incl = 0, total = 0;
+      auto load_chunk = [&]() {   // items of sequences cb + lane
+        const int b = cb + lane;
+        cnt = 0;
+        if (b < a.B) {
+          const int c0 = __ldg(a.cu_q + b), c1 = __ldg(a.cu_q + b + 1);
+          if (c0 < 0 || c1 > a.T || c1 < c0) {
+            if (blockIdx.x == 0) record_error(a.err, INK_DEVERR_BAD_ROWS);
+          } else {
+            cnt = (c1 - c0 + tpi - 1) / tpi * per;
+          }
+        }
+        incl = cnt;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += v;
+        }
+        total = __shfl_sync(0xffffffffu, incl, 31);
+      };
+      load_chunk();
+      int idx = blockIdx.x, qn0 = 0, qn1 = 0;
+      for (int k = 0;; ++k) {
+        int next = 0;
+        if (lane == 0) next = (int)atomicAdd(a.counters, 1u) + (int)gridDim.x;
+        while (cb < a.B && idx >= base + total) {
+          base += total;
+          cb += 32;
+          if (cb < a.B) load_chunk();
+        }
+        const int sl = k % PM_ITEMS;
+        if (k >= PM_ITEMS && !pm_wait(&item_empty[sl], (uint32_t)((k / PM_ITEMS) - 1) & 1u, abort_flag, a)) break;
+        if (cb >= a.B) {
+          if (lane == 0) {
+            items[sl].nt = -1;
+            mbar_arrive(&item_full[sl]);
+          }
+          break;
+        }
+        const int src = __ffs(__ballot_sync(0xffffffffu, idx < base + incl)) - 1;
+        const int li = idx - base - __shfl_sync(0xffffffffu, incl - cnt, src);
+        const int nq = __shfl_sync(0xffffffffu, cnt, src) / per;
+        PMItem it;
+        it.b = cb + src;
+        const int qrev = li / per, r = li - qrev * per;
+        const int qt = nq - 1 - qrev;
+        it.kvh = r / a.head_chunks;
+        const int hc = r - it.kvh * a.head_chunks;
+        it.h0 = it.kvh * a.G + hc * a.heads_per_tile;
+        it.gh = min(a.heads_per_tile, a.G - hc * a.heads_per_tile);
+        const int c0 = __ldg(a.cu_q + it.b), n = __ldg(a.cu_q + it.b + 1) - c0;
+        it.L = __ldg(a.seq_lens + it.b);
+        it.t0 = c0 + qt * tpi;
+        it.ntok = min(tpi, n - qt * tpi);
+        it.pos0 = it.L - n + qt * tpi;
+        it.nh = it.ntok > a.tok_per_tile ? 2 : 1;
+        it.bad_len = n > it.L;
+        it.lo_min = INT_MAX;
+        it.hi_max = 0;
+        it.lo_max = 0;
+        it.hi_min = INT_MAX;
+        if (!it.bad_len) {
+          for (int i = lane; i < it.ntok; i += 32) {
+            int lo, hi;
+            token_keys(a, it.t0 + i, it.pos0 + i, it.L, lo, hi);
+            if (lo < hi) {
+              it.lo_min = min(it.lo_min, lo);
+              it.hi_max = max(it.hi_max, hi);
+              it.lo_max = max(it.lo_max, lo);
+              it.hi_min = min(it.hi_min, hi);
+            } else {
+              it.lo_max = INT_MAX;
+            }
+          }
+          it.lo_min = __reduce_min_sync(0xffffffffu, it.lo_min);
+          it.hi_max = __reduce_max_sync(0xffffffffu, it.hi_max);
+          it.lo_max = __reduce_max_sync(0xffffffffu, it.lo_max);
+          it.hi_min = __reduce_min_sync(0xffffffffu, it.hi_min);
+        }
+        it.kt0 = it.lo_min / PM_KEYS;
+        it.nt = it.hi_max > it.lo_min ? (it.hi_max - 1) / PM_KEYS - it.kt0 + 1 : 0;
+        if (lane == 0) {
+          if (it.bad_len) record_error(a.err, INK_DEVERR_QLEN_EXCEEDS_KV);
+          else if ((long long)it.L > ((long long)a.max_pages << a.log2_page)) record_error(a.err, INK_DEVERR_PAGE_OUT_OF_RANGE);
+          items[sl] = it;
+          poison[sl] = 0;
+          mbar_arrive(&item_full[sl]);
+        }
+        __syncwarp();
+        bool go = true;
+        for (int h = 0; h < it.nh && it.nt > 0 && go; ++h) {
+          int& qn = h ? qn1 : qn0;
+          if (qn > 0) go = pm_wait(&q_empty[h], (uint32_t)(qn - 1) & 1u, abort_flag, a);
+          if (!go) break;
+          ++qn;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&q_full[h], (uint32_t)(S::CB * a.heads_per_tile * a.tok_per_tile * 128));
+#pragma unroll
+            for (int c = 0; c < S::CB; ++c)
+              tma_load_3d(smem + L_::q + h * S::TILE + c * S::SUB, &tmQ, c * 64, it.h0, it.t0 + h * a.tok_per_tile,
+                          &q_full[h]);
+          }
+          __syncwarp();
+        }
+        if (!go) break;
+        idx = __shfl_sync(0xffffffffu, next, 0);
+      }
+      if (lane == 0) {
+        for (int h = 0; h < 2; ++h) {
+          const int n = h ? qn1 : qn0;
+          if (n > 0 && !mbar_wait_bounded(&q_full[h], (uint32_t)(n - 1) & 1u)) record_error(a.err, INK_DEVERR_WAIT_TIMEOUT);
+        }
+        // the last CTA to stop taking items leaves the counters at zero for the next call
+        __threadfence();
+        if (atomicAdd(a.counters + 1, 1u) == gridDim.x - 1) {
+          a.counters[0] = 0u;
+          a.counters[1] = 0u;
+        }
+      }
+    } else {
+      // ---------------------------------------------------------------- V check
+      int g = 0;
+      bool go = true;
+      PMItem it;
+      for (int k = 0; go && next_item(k, it); ++k) {
+        bool found = false;
+        for (int j = 0; j < it.nt; ++j, ++g) {
+          const int f = 2 * g + 1, st = f % NS;
+          go = pm_wait(&full[st], (uint32_t)(f / NS) & 1u, abort_flag, a);
+          if (!go) break;
+          const int k0 = (it.kt0 + j) * PM_KEYS;
+          const uint4 bad = *reinterpret_cast<const uint4*>(kbad + (g % PM_BAD) * 4);
+          if (k0 < it.lo_max || k0 + PM_KEYS > it.hi_min || (bad.x | bad.y | bad.z | bad.w)) {
+            const uint32_t badw[4] = {bad.x, bad.y, bad.z, bad.w};
+            uint8_t* vt = smem + L_::ring + (size_t)st * S::TILE;
+#pragma unroll 1
+            for (int x = 0; x < 4; ++x) {
+              const int kk = k0 + 32 * x + lane;
+              uint4* row = reinterpret_cast<uint4*>(vt + (32 * x + lane) * 128);
+              bool zero = kk < it.lo_min || kk >= it.hi_max || ((badw[x] >> lane) & 1u);
+              if (!zero) {   // exponents all ones carry into the sign places
+                uint32_t odd = 0;
+#pragma unroll
+                for (int c = 0; c < S::CB; ++c)
+#pragma unroll
+                  for (int y = 0; y < 8; ++y) {
+                    const uint4 w = row[c * (S::SUB / 16) + (y ^ (lane & 7))];
+                    odd |= ((w.x & 0x7F807F80u) + 0x00800080u) | ((w.y & 0x7F807F80u) + 0x00800080u) |
+                           ((w.z & 0x7F807F80u) + 0x00800080u) | ((w.w & 0x7F807F80u) + 0x00800080u);
+                  }
+                if (odd & 0x80008000u) zero = found = true;
+              }
+              if (zero) {
+#pragma unroll
+                for (int c = 0; c < S::CB; ++c)
+#pragma unroll
+                  for (int y = 0; y < 8; ++y) row[c * (S::SUB / 16) + (y ^ (lane & 7))] = make_uint4(0u, 0u, 0u, 0u);
+              }
+            }
+            if (found) poison[k % PM_ITEMS] = 1;
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&v_ok[g % PM_VOK]);
+        }
+        done_item(k);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------------ softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(PM_REGS_SOFTMAX));
+    const int h = warp >> 2, r = tid & 127;
+    const uint32_t tlane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t tm_s = tlane + 128u * h, tm_o = tlane + S::TO + (uint32_t)(D * h);
+    const int my_i = r / a.heads_per_tile, my_g = r - my_i * a.heads_per_tile;
+    __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out);
+    const bool scaled = CAP != 0 || a.slopes != nullptr || !(a.scale_log2 > 0.f);
+    const float mul = scaled ? 1.f : a.scale_log2;
+    uint32_t sn = 0, on = 0;
+    int g = 0;
+    bool go = true;
+    PMItem it;
+    for (int k = 0; go && next_item(k, it); ++k) {
+      if (h >= it.nh) {
+        g += max(it.nt, 0);
+        done_item(k);
+        continue;
+      }
+      const int ti = h * a.tok_per_tile + my_i;
+      const bool rv = my_i < a.tok_per_tile && ti < it.ntok && my_g < it.gh;
+      const int t = it.t0 + (rv ? ti : 0), head = it.h0 + (rv ? my_g : 0), p = it.pos0 + ti;
+      int lo = 0, hi = 0;
+      if (rv && !it.bad_len) token_keys(a, t, p, it.L, lo, hi);
+      const size_t orow = (size_t)t * a.Hq + head;
+      if (it.nt == 0) {   // no row sees a key
+        if (rv) {
+          uint4* o = reinterpret_cast<uint4*>(out + orow * D);
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c) o[c] = make_uint4(0u, 0u, 0u, 0u);
+          if (a.lse) a.lse[orow] = -INFINITY;
+        }
+        done_item(k);
+        continue;
+      }
+      const float slope2 = a.slopes ? __ldg(a.slopes + head) * LOG2E : 0.f;
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < it.nt; ++j, ++g) {
+        const int k0 = (it.kt0 + j) * PM_KEYS;
+        go = pm_wait(&s_full[h], sn & 1u, abort_flag, a);
+        if (!go) break;
+        ++sn;
+        tc_fence_after();
+        uint32_t sr[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(tm_s + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&sr[32 * c]));
+        tmem_wait_ld();
+        const uint4 bad = *reinterpret_cast<const uint4*>(kbad + (g % PM_BAD) * 4);
+        // ---- scores
+        if constexpr (CAP != 0) {
+          const uint64_t k12 = f2_pack(a.cap_k1, a.cap_k1), one2 = f2_pack(1.f, 1.f);
+          const uint64_t c2 = f2_pack(a.cap_log2, a.cap_log2), cn2 = f2_pack(-2.f * a.cap_log2, -2.f * a.cap_log2);
+#pragma unroll
+          for (int c = 0; c < 128; c += 2) {
+            const uint64_t raw = f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
+            float x, y;
+            f2_unpack(f2_mul(raw, k12), x, y);
+            f2_unpack(f2_add(f2_pack(fast_exp2(x), fast_exp2(y)), one2), x, y);
+            uint64_t s = f2_fma(f2_pack(fast_rcp(x), fast_rcp(y)), cn2, c2);
+            if constexpr (CAP == 2) {
+              const uint64_t u = f2_mul(raw, f2_pack(a.cap_inv, a.cap_inv)), u2 = f2_mul(u, u);
+              uint64_t w = f2_fma(u2, f2_pack(-17.f / 315.f, -17.f / 315.f), f2_pack(2.f / 15.f, 2.f / 15.f));
+              w = f2_fma(w, u2, f2_pack(-1.f / 3.f, -1.f / 3.f));
+              w = f2_fma(w, u2, one2);
+              float u0, u1, w0, w1, s0, s1;
+              f2_unpack(u, u0, u1);
+              f2_unpack(f2_mul(f2_mul(w, u), c2), w0, w1);
+              f2_unpack(s, s0, s1);
+              s = f2_pack(fabsf(u0) < 0.25f ? w0 : s0, fabsf(u1) < 0.25f ? w1 : s1);
+            }
+            f2_unpack(s, x, y);
+            sr[c] = __float_as_uint(x);
+            sr[c + 1] = __float_as_uint(y);
+          }
+        } else if (scaled) {
+#pragma unroll
+          for (int c = 0; c < 128; ++c) sr[c] = __float_as_uint(__uint_as_float(sr[c]) * a.scale_log2);
+        }
+        if (a.slopes) {
+          const float d0 = (float)(p - k0);
+#pragma unroll
+          for (int c = 0; c < 128; ++c)
+            sr[c] = __float_as_uint(fmaf(-slope2, fabsf(d0 - (float)c), __uint_as_float(sr[c])));
+        }
+        if (k0 < it.lo_max || k0 + PM_KEYS > it.hi_min || (bad.x | bad.y | bad.z | bad.w)) {
+          const uint32_t badw[4] = {bad.x, bad.y, bad.z, bad.w};
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const int x0 = max(lo - k0 - 32 * w, 0), x1 = min(hi - k0 - 32 * w, 32);   // visible bits [x0, x1)
+            uint32_t vis = x1 > x0 ? (0xffffffffu >> (32 - (x1 - x0))) << x0 : 0u;
+            vis &= ~badw[w];
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (!((vis >> c) & 1u)) sr[32 * w + c] = 0xff800000u;   // -infinity
+          }
+        }
+        // ---- running maximum
+        float mxv[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int c = 0; c < 128; c += 2)
+          mxv[(c >> 1) & 3] = fmax3(mxv[(c >> 1) & 3], __uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
+        const float mx = fmaxf(fmaxf(mxv[0], mxv[1]), fmaxf(mxv[2], mxv[3])) * mul;
+        const bool mine = mx > m + RESCALE_LOG2;
+        if (__any_sync(0xffffffffu, mine)) {
+          if (j > 0) {   // every earlier product into O_h is done: s_full came after it
+            const float fr = mine ? fast_exp2(m - mx) : 1.f;
+#pragma unroll 1
+            for (int c2 = 0; c2 < D / 16; ++c2) {
+              uint32_t ov[16];
+              tmem_ld16(tm_o + c2 * 16, ov);
+              tmem_wait_ld();
+#pragma unroll
+              for (int x = 0; x < 16; ++x) ov[x] = __float_as_uint(__uint_as_float(ov[x]) * fr);
+              tmem_st16(tm_o + c2 * 16, ov);
+            }
+            l *= fr;
+          }
+          if (mine) m = mx;
+        }
+        // ---- numerators
+        const float nm = m == -INFINITY ? 0.f : -m;
+        const uint64_t mul2 = f2_pack(mul, mul), nm2 = f2_pack(nm, nm);
+        uint64_t ls2[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+        for (int quarter = 0; quarter < 4; ++quarter) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            const int e = 32 * quarter + 2 * c;
+            float t0, t1;
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[e]), __uint_as_float(sr[e + 1])), mul2, nm2), t0, t1);
+            const float p0 = fast_exp2(t0), p1 = fast_exp2(t1);
+            ls2[c & 3] = f2_add(ls2[c & 3], f2_pack(p0, p1));
+            pk[c] = pack_bf16(p0, p1);
+          }
+          tmem_st16(tm_s + 16 * quarter, pk);
+        }
+        {
+          float x0, x1, y0, y1;
+          f2_unpack(f2_add(ls2[0], ls2[1]), x0, x1);
+          f2_unpack(f2_add(ls2[2], ls2[3]), y0, y1);
+          l += (x0 + y0) + (x1 + y1);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[h]);
+      }
+      if (!go) break;
+      // ---- epilogue
+      go = pm_wait(&o_full[h], on & 1u, abort_flag, a);
+      if (!go) break;
+      ++on;
+      tc_fence_after();
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const bool nothing = l == 0.f;
+      const bool poisoned = poison[k % PM_ITEMS] != 0;
+#pragma unroll 1
+      for (int c2 = 0; c2 < D / 32; ++c2) {
+        uint32_t ov[32];
+        tmem_ld32(tm_o + c2 * 32, ov);
+        tmem_wait_ld();
+#pragma unroll
+        for (int x = 0; x < 32; ++x) ov[x] = nothing ? 0u : __float_as_uint(__uint_as_float(ov[x]) * (l == l ? inv : l));
+        if (poisoned && rv) {
+          // infinities and NaN of the keys this row sees
+#pragma unroll 1
+          for (int kk = lo; kk < hi; ++kk) {
+            const int page = __ldg(a.block_table + (size_t)it.b * a.max_pages + (kk >> a.log2_page));
+            if (page < 0 || page >= a.num_pages) continue;
+            const size_t vrow = ((((size_t)page * a.Hkv + it.kvh) << a.log2_page) + (kk & (P - 1))) * D + c2 * 32;
+            const uint16_t* vp = static_cast<const uint16_t*>(a.v) + vrow;
+#pragma unroll
+            for (int x = 0; x < 32; ++x) {
+              const uint32_t w = (uint32_t)__ldg(vp + x) << 16;
+              if ((w & 0x7F800000u) == 0x7F800000u) ov[x] = __float_as_uint(__uint_as_float(ov[x]) + __uint_as_float(w));
+            }
+          }
+        }
+        if (rv) {
+          uint4* o = reinterpret_cast<uint4*>(out + orow * D) + c2 * 4;
+#pragma unroll
+          for (int q8 = 0; q8 < 2; ++q8) {
+            uint32_t w[8];
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+              w[x] = pack_bf16(__uint_as_float(ov[16 * q8 + 2 * x]), __uint_as_float(ov[16 * q8 + 2 * x + 1]));
+            if constexpr (IO32) {
+              asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(o + 2 * q8), "r"(w[0]), "r"(w[1]),
+                           "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                           : "memory");
+            } else {
+              o[2 * q8] = make_uint4(w[0], w[1], w[2], w[3]);
+              o[2 * q8 + 1] = make_uint4(w[4], w[5], w[6], w[7]);
+            }
+          }
+        }
+      }
+      if (rv && a.lse) a.lse[orow] = nothing ? -INFINITY : (m == -INFINITY ? 0.f : m) * LN2 + logf(l);
+      tc_fence_before();
+      done_item(k);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(512));
+  }
+}
+
+template <int D, int CAP, bool IO32>
+cudaError_t launch_t(const MaskedMaps& m, const MaskedArgs& a, int grid, cudaStream_t stream) {
+  static std::atomic<unsigned long long> opted{0};
+  cudaError_t e = smem_opt_in_once(prefill_masked_kernel<D, CAP, IO32>, (int)PMSmem<D>::alloc, opted);
+  if (e != cudaSuccess) return e;
+  // The softmax warps' extra registers come out of what the block is launched with: a build with
+  // fewer would wait for them without end.
+  static const bool enough = [] {
+    cudaFuncAttributes at;
+    return cudaFuncGetAttributes(&at, prefill_masked_kernel<D, CAP, IO32>) == cudaSuccess &&
+           at.numRegs * PM_THREADS >= 128 * (2 * PM_REGS_SOFTMAX + PM_REGS_REST);
+  }();
+  if (!enough) return cudaErrorInvalidConfiguration;
+  prefill_masked_kernel<D, CAP, IO32><<<grid, PM_THREADS, PMSmem<D>::alloc, stream>>>(m.k, m.v, m.q, a);
+  return cudaGetLastError();
+}
+
+template <int D, bool IO32>
+cudaError_t launch_cap(const MaskedMaps& m, const MaskedArgs& a, int grid, cudaStream_t stream) {
+  if (a.softcap == 0.f) return launch_t<D, 0, IO32>(m, a, grid, stream);
+  return a.softcap <= SOFTCAP_PLAIN ? launch_t<D, 1, IO32>(m, a, grid, stream) : launch_t<D, 2, IO32>(m, a, grid, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_prefill_masked(const MaskedMaps& m, const MaskedArgs& a, int head_dim, bool io32, cudaStream_t stream) {
+  int dev = 0;
+  const int sms = current_device_sms(&dev);
+  if (sms <= 0) return cudaErrorInvalidDevice;
+  // no more CTAs than items there can be: every sequence adds at most one unfilled item per head
+  const long long tpi = 2ll * a.tok_per_tile, per = (long long)a.Hkv * a.head_chunks;
+  const long long most = (a.T / tpi + a.B) * per;
+  const int grid = (int)std::max(1ll, std::min<long long>(most, sms));
+  if (head_dim == 128)
+    return io32 ? launch_cap<128, true>(m, a, grid, stream) : launch_cap<128, false>(m, a, grid, stream);
+  return io32 ? launch_cap<64, true>(m, a, grid, stream) : launch_cap<64, false>(m, a, grid, stream);
+}
+
+}  // namespace ink

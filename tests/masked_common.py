@@ -70,5 +70,5 @@ def check(out, lse, ref, label=""):
     excess = (np.abs(got - want) - tol)[rows]
     assert excess.size == 0 or excess.max() <= 0, f"{label}: out off by {excess.max():.3e} over its bound"
     tol_l = (d + 2.0 ** -20 * (1.0 + np.abs(want_lse)))[rows]
-    ex = np.abs(got_lse - want_lse)[rows] - tol_l
+    ex = np.abs(got_lse[rows] - want_lse[rows]) - tol_l
     assert ex.size == 0 or ex.max() <= 0, f"{label}: lse off by {ex.max():.3e} over its bound"
