@@ -223,6 +223,24 @@ bool make_lowrank_maps(ink::PrefillMaps* m, const void* r, const void* proj_t, c
   return e == CUDA_SUCCESS;
 }
 
+bool make_decode_maps(ink::DecodeMaps* m, const void* q, const void* k_cache, const void* v_cache,
+                      const ink_attn_params_t* params) {
+  const int D = params->head_dim;
+  if (!make_pool_map(&m->k_seg, k_cache, params, 16) || !make_pool_map(&m->v_seg, v_cache, params, 16) ||
+      !make_rows_map3(&m->q3, q, (uint64_t)params->num_seqs * params->num_q_heads, D, D / 64, 16))
+    return false;
+  std::memset(&m->k_tile, 0, sizeof m->k_tile);
+  std::memset(&m->v_tile, 0, sizeof m->v_tile);
+  std::memset(&m->k_grp, 0, sizeof m->k_grp);
+  std::memset(&m->v_grp, 0, sizeof m->v_grp);
+  if (params->page_size >= 16 && (!make_group_map(&m->k_grp, k_cache, pool_rows(params), D, 1) ||
+                                  !make_group_map(&m->v_grp, v_cache, pool_rows(params), D, 1)))
+    return false;
+  return params->page_size < ink::TILE_KEYS ||
+         (make_group_map(&m->k_tile, k_cache, pool_rows(params), D, ink::TILE_KEYS / 16) &&
+          make_group_map(&m->v_tile, v_cache, pool_rows(params), D, ink::TILE_KEYS / 16));
+}
+
 }  // namespace
 
 extern "C" {
@@ -295,23 +313,7 @@ ink_status_t inkling_attn_decode(const ink_attn_params_t* params, const void* q,
   if (workspace_bytes < lay.total) return INK_ERR_WORKSPACE;
   if (params->num_seqs == 0) return INK_OK;
   ink::DecodeMaps maps;
-  const int cblocks = params->head_dim / 64;
-  if (!make_pool_map(&maps.k_seg, k_cache, params, 16) ||
-      !make_pool_map(&maps.v_seg, v_cache, params, 16) ||
-      !make_rows_map3(&maps.q3, q, (uint64_t)params->num_seqs * params->num_q_heads, params->head_dim, cblocks, 16))
-    return INK_ERR_CUDA;
-  std::memset(&maps.k_tile, 0, sizeof maps.k_tile);
-  std::memset(&maps.v_tile, 0, sizeof maps.v_tile);
-  std::memset(&maps.k_grp, 0, sizeof maps.k_grp);
-  std::memset(&maps.v_grp, 0, sizeof maps.v_grp);
-  if (params->page_size >= 16 &&
-      (!make_group_map(&maps.k_grp, k_cache, pool_rows(params), params->head_dim, 1) ||
-       !make_group_map(&maps.v_grp, v_cache, pool_rows(params), params->head_dim, 1)))
-    return INK_ERR_CUDA;
-  if (params->page_size >= ink::TILE_KEYS &&
-      (!make_group_map(&maps.k_tile, k_cache, pool_rows(params), params->head_dim, ink::TILE_KEYS / 16) ||
-       !make_group_map(&maps.v_tile, v_cache, pool_rows(params), params->head_dim, ink::TILE_KEYS / 16)))
-    return INK_ERR_CUDA;
+  if (!make_decode_maps(&maps, q, k_cache, v_cache, params)) return INK_ERR_CUDA;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   DecodeArgs a;
   a.q = q;
@@ -532,6 +534,22 @@ ink_status_t inkling_attn_kv_conv_write(const ink_attn_params_t* params, const v
 
 namespace {
 
+struct MaskedDecodeLayout {
+  size_t tickets_off, part_o_off, part_ml_off, total;
+};
+
+MaskedDecodeLayout masked_decode_layout(const ink_attn_params_t* p) {
+  MaskedDecodeLayout l;
+  const size_t B = (size_t)(p->num_seqs > 0 ? p->num_seqs : 1);
+  const size_t G = (size_t)(p->num_q_heads / p->num_kv_heads), rows = G <= 8 ? 8 : 16;
+  const size_t places = 2 * (size_t)ink::MASKED_DECODE_CTAS * rows;
+  l.tickets_off = kHeaderBytes;
+  l.part_o_off = align_up(l.tickets_off + B * p->num_kv_heads * ((G + 15) / 16) * sizeof(int32_t), 256);
+  l.part_ml_off = l.part_o_off + places * p->head_dim * sizeof(float);
+  l.total = align_up(l.part_ml_off + places * 2 * sizeof(float), 256);
+  return l;
+}
+
 // q [total_q, Hq, D] as {D, Hq, total_q}, boxes of 64 channels x heads x tokens with the 128-byte
 // swizzle: the rows of an MMA operand, tokens outermost.  Rows outside the tensor read as zeros.
 bool make_token_map(CUtensorMap* map, const void* q, const ink_attn_params_t* p, int total_q, int heads, int tokens) {
@@ -601,7 +619,15 @@ ink_status_t masked_impl(const ink_attn_params_t* params, const ink_attn_mask_t*
   a.heads_per_tile = (a.G + a.head_chunks - 1) / a.head_chunks;
   a.tok_per_tile = ink::MASKED_ROWS / a.heads_per_tile;
   if (decode) {
-    if (ink::launch_masked_simple(a, params->head_dim, (cudaStream_t)stream) != cudaSuccess) return INK_ERR_CUDA;
+    a.head_chunks = (a.G + 15) / 16;
+    const MaskedDecodeLayout lay = masked_decode_layout(params);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    a.tickets = reinterpret_cast<int32_t*>(ws + lay.tickets_off);
+    a.part_o = reinterpret_cast<float*>(ws + lay.part_o_off);
+    a.part_ml = reinterpret_cast<float*>(ws + lay.part_ml_off);
+    ink::DecodeMaps maps;
+    if (!make_decode_maps(&maps, q, k_cache, v_cache, params)) return INK_ERR_CUDA;
+    if (ink::launch_decode_masked(maps, a, params->head_dim, (cudaStream_t)stream) != cudaSuccess) return INK_ERR_CUDA;
     return INK_OK;
   }
   ink::MaskedMaps maps;
@@ -619,8 +645,7 @@ extern "C" {
 
 size_t inkling_attn_masked_workspace_bytes(const ink_attn_params_t* params, int is_decode) {
   if (validate(params) != INK_OK) return 0;
-  (void)is_decode;
-  return kHeaderBytes;
+  return is_decode ? masked_decode_layout(params).total : kHeaderBytes;
 }
 
 ink_status_t inkling_attn_prefill_masked(const ink_attn_params_t* params, const ink_attn_mask_t* mask,

@@ -191,7 +191,14 @@ struct MaskedArgs {
   // prefill: a row tile holds tok_per_tile tokens x heads_per_tile query heads of one KV head
   int head_chunks, heads_per_tile, tok_per_tile;
   uint32_t* counters;          // [0] items handed out, [1] CTAs done; zero between calls
+  // decode: partials of cut groups, two places per CTA of `rows` heads (8 or 16), and a ticket
+  // per (sequence, KV head, chunk of 16 query heads), zero between calls
+  float* part_o;               // [2 * CTAs, rows, D]
+  float* part_ml;              // [2 * CTAs, rows, 2] (running max in log2 units, sum)
+  int32_t* tickets;
 };
+
+constexpr int MASKED_DECODE_CTAS = 320;   // most CTAs of a masked decode (bounds its partials)
 
 // Caps up to this one take the plain formula of tanh (fewer instructions, off by 2^-23 of the cap).
 constexpr float SOFTCAP_PLAIN = 64.f;
@@ -204,6 +211,6 @@ struct MaskedMaps {
 };
 
 cudaError_t launch_prefill_masked(const MaskedMaps& m, const MaskedArgs& a, int head_dim, bool io32, cudaStream_t stream);
-cudaError_t launch_masked_simple(const MaskedArgs& a, int head_dim, cudaStream_t stream);
+cudaError_t launch_decode_masked(const DecodeMaps& m, const MaskedArgs& a, int head_dim, cudaStream_t stream);
 
 }  // namespace ink

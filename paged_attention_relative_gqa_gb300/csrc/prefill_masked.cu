@@ -32,6 +32,7 @@
 #include <algorithm>
 #include <climits>
 
+#include "masked_common.cuh"
 #include "prefill_common.cuh"
 
 namespace ink {
@@ -45,7 +46,6 @@ constexpr int PM_ITEMS = 4;       // published items in flight
 constexpr int PM_BAD = 8;         // tiles whose unreadable keys are remembered
 constexpr int PM_VOK = 4;         // V tiles checked ahead of their product (at most NS / 2 are in the ring)
 constexpr int PM_REGS_SOFTMAX = 208, PM_REGS_REST = 88;   // registers a thread after the split
-constexpr float LN2 = 0.6931471805599453f;
 constexpr float RESCALE_LOG2 = 8.f;
 
 template <int D>
@@ -83,14 +83,6 @@ struct PMSmem {
   static_assert(alloc <= 227 * 1024, "shared memory budget");
 };
 
-// Visible keys [lo, hi) of token t at position p (hi <= lo: none).
-__device__ __forceinline__ void token_keys(const MaskedArgs& a, int t, int p, int L, int& lo, int& hi) {
-  lo = a.key_begin ? max(__ldg(a.key_begin + t), 0) : 0;
-  if (a.W > 0) lo = max(lo, p - a.W + 1);
-  hi = a.key_end ? __ldg(a.key_end + t) : p + 1;
-  hi = max(0, min(hi, (int)min((long long)L, (long long)a.max_pages << a.log2_page)));
-}
-
 // Bounded wait of a whole warp (inline: a call would keep the registers from being split).
 __device__ __forceinline__ bool pm_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, const MaskedArgs& a) {
   bool ok = mbar_probe(bar, parity, a.wait_ns);
@@ -104,21 +96,13 @@ __device__ __forceinline__ bool pm_wait(uint64_t* bar, uint32_t parity, volatile
   return __all_sync(0xffffffffu, ok);
 }
 
-__device__ __forceinline__ float fast_rcp(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
 
-// CAP 0: no cap.  1: s = C (1 - 2 / (1 + 2^(k1 x))), off by about 2^-23 C: for caps up to
-// SOFTCAP_PLAIN.  2: the same, and for |x| < C / 4 the odd series of tanh to the 7th power, whose
-// relative error stays below 2^-21: for caps so large that 2^-23 C would count.
+// CAP: the formulas of score_log2 (masked_common.cuh), two scores at a time.
 template <int D, int CAP, bool IO32>
 __global__ void __launch_bounds__(PM_THREADS, 1)
 prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
