@@ -272,33 +272,59 @@ def inkling_attn_kv_conv_write(params, k_new, v_new, cu_q_lens, seq_lens, block_
     return k_cache, v_cache
 
 
-def _shape(t, name, shape):
-    if tuple(t.shape) != tuple(shape):
+def _refuse(t, name, dtype, shape, device):
+    """Say what is wrong with a tensor that ``_arg`` did not take."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, q on cuda:{device}")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _opt_dev(t, name, dtype, shape):
+def _arg(t, name, dtype, shape, device):
+    """Device pointer of a contiguous tensor of this dtype, shape (None: any) and device; None stays None.
+    (One pass of cheap checks: a decode step makes this call for a dozen tensors.)"""
     if t is None:
         return None
-    ptr = _dev(t, name, dtype)
-    _shape(t, name, shape)
-    return ptr
+    try:
+        if t.dtype is dtype and t.get_device() == device and (shape is None or t.shape == shape) and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, name, dtype, shape, device)
 
 
-def _one_device(*tensors):
-    """The device all the given tensors (None skipped) live on."""
-    devices = {t.device for t in tensors if t is not None}
-    if len(devices) != 1:
-        raise ValueError(f"tensors on different devices: {sorted(map(str, devices))}")
-    return devices.pop()
+def _need(**tensors):
+    """Required tensors are there; the device of the first one."""
+    for name, t in tensors.items():
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+    name, t = next(iter(tensors.items()))
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.get_device()
 
 
-def _check_pools(params, k_cache, v_cache, block_table, seq_lens):
-    pool = (params.num_pages, params.num_kv_heads, params.page_size, params.head_dim)
-    _shape(k_cache, "k_cache", pool)
-    _shape(v_cache, "v_cache", pool)
-    _shape(block_table, "block_table", (params.num_seqs, params.max_pages_per_seq))
-    _shape(seq_lens, "seq_lens", (params.num_seqs,))
+# The current stream's handle without a Stream object around it (a few microseconds less per call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _launch(fn, device, stream, *args):
+    """fn(*args, stream) with `device` current; None means that device's current stream."""
+    if stream is None:
+        handle = _raw_stream(device) if _raw_stream is not None else torch.cuda.current_stream(device).cuda_stream
+    else:
+        handle = _stream_handle(stream)
+    if torch.cuda.current_device() == device:
+        return fn(*args, handle)
+    with torch.cuda.device(device):
+        return fn(*args, handle)
 
 
 def inkling_attn_masked_workspace_bytes(params: ink_attn_params_t, is_decode: bool) -> int:
@@ -316,68 +342,55 @@ def alloc_masked_workspace(params: ink_attn_params_t, is_decode: bool = True, de
     return ws
 
 
-def _mask_struct(params, rows, softcap, key_begin, key_end, slopes) -> ink_attn_mask_t:
-    return ink_attn_mask_t(float(softcap), _opt_dev(key_begin, "key_begin", torch.int32, (rows,)),
-                           _opt_dev(key_end, "key_end", torch.int32, (rows,)),
-                           _opt_dev(slopes, "slopes", torch.float32, (params.num_q_heads,)))
+def _masked_call(name, params, q, cu_q_lens, k_cache, v_cache, block_table, seq_lens, out, workspace, softcap, key_begin,
+                 key_end, slopes, lse, stream):
+    lib = load_library()
+    prefill = name == "inkling_attn_prefill_masked"
+    dev = _need(q=q, k_cache=k_cache, v_cache=v_cache, block_table=block_table, seq_lens=seq_lens, out=out,
+                workspace=workspace)
+    B, Hq, D = params.num_seqs, params.num_q_heads, params.head_dim
+    T = int(q.shape[0]) if prefill else B
+    bf, i32, rows = torch.bfloat16, torch.int32, (T, Hq, D)
+    pool = (params.num_pages, params.num_kv_heads, params.page_size, D)
+    mask = ink_attn_mask_t(softcap, _arg(key_begin, "key_begin", i32, (T,), dev), _arg(key_end, "key_end", i32, (T,), dev),
+                           _arg(slopes, "slopes", torch.float32, (Hq,), dev))
+    head = [ctypes.byref(params), ctypes.byref(mask), _arg(q, "q", bf, rows, dev)]
+    if prefill:
+        _need(cu_q_lens=cu_q_lens)
+        head += [_arg(cu_q_lens, "cu_q_lens", i32, (B + 1,), dev), T]
+    code = _launch(getattr(lib, name), dev, stream, *head, _arg(k_cache, "k_cache", bf, pool, dev),
+                   _arg(v_cache, "v_cache", bf, pool, dev),
+                   _arg(block_table, "block_table", i32, (B, params.max_pages_per_seq), dev),
+                   _arg(seq_lens, "seq_lens", i32, (B,), dev), _arg(out, "out", bf, rows, dev),
+                   _arg(lse, "lse", torch.float32, (T, Hq), dev),
+                   _arg(workspace, "workspace", torch.uint8, None, dev), workspace.numel())
+    _check(code, name)
+    return out
 
 
 def inkling_attn_prefill_masked(params, q, cu_q_lens, k_cache, v_cache, block_table, seq_lens, out, workspace, *,
                                 softcap: float = 0.0, key_begin=None, key_end=None, slopes=None, lse=None, stream=None):
     """Paged prefill with capped scores, a distance bias and a visible key range per token."""
-    lib = load_library()
-    ptrs = [_dev(q, "q", torch.bfloat16), _dev(cu_q_lens, "cu_q_lens", torch.int32)]
-    T = int(q.shape[0])
-    _shape(q, "q", (T, params.num_q_heads, params.head_dim))
-    _shape(out, "out", q.shape)
-    _shape(cu_q_lens, "cu_q_lens", (params.num_seqs + 1,))
-    tail = [_dev(k_cache, "k_cache", torch.bfloat16), _dev(v_cache, "v_cache", torch.bfloat16),
-            _dev(block_table, "block_table", torch.int32), _dev(seq_lens, "seq_lens", torch.int32),
-            _dev(out, "out", torch.bfloat16), _opt_dev(lse, "lse", torch.float32, q.shape[:2]),
-            _dev(workspace, "workspace", torch.uint8), workspace.numel()]
-    _check_pools(params, k_cache, v_cache, block_table, seq_lens)
-    mask = _mask_struct(params, T, softcap, key_begin, key_end, slopes)
-    device = _one_device(q, cu_q_lens, k_cache, v_cache, block_table, seq_lens, out, lse, workspace, key_begin, key_end, slopes)
-    with torch.cuda.device(device):
-        code = lib.inkling_attn_prefill_masked(ctypes.byref(params), ctypes.byref(mask), *ptrs, T, *tail,
-                                               _stream_handle(stream))
-    _check(code, "inkling_attn_prefill_masked")
-    return out
+    return _masked_call("inkling_attn_prefill_masked", params, q, cu_q_lens, k_cache, v_cache, block_table, seq_lens, out,
+                        workspace, softcap, key_begin, key_end, slopes, lse, stream)
 
 
 def inkling_attn_decode_masked(params, q, k_cache, v_cache, block_table, seq_lens, out, workspace, *,
                                softcap: float = 0.0, key_begin=None, key_end=None, slopes=None, lse=None, stream=None):
     """Paged decode with capped scores, a distance bias and a visible key range per sequence."""
-    lib = load_library()
-    ptrs = [_dev(q, "q", torch.bfloat16), _dev(k_cache, "k_cache", torch.bfloat16),
-            _dev(v_cache, "v_cache", torch.bfloat16), _dev(block_table, "block_table", torch.int32),
-            _dev(seq_lens, "seq_lens", torch.int32), _dev(out, "out", torch.bfloat16),
-            _opt_dev(lse, "lse", torch.float32, q.shape[:2]), _dev(workspace, "workspace", torch.uint8),
-            workspace.numel()]
-    _shape(q, "q", (params.num_seqs, params.num_q_heads, params.head_dim))
-    _shape(out, "out", q.shape)
-    _check_pools(params, k_cache, v_cache, block_table, seq_lens)
-    mask = _mask_struct(params, params.num_seqs, softcap, key_begin, key_end, slopes)
-    device = _one_device(q, k_cache, v_cache, block_table, seq_lens, out, lse, workspace, key_begin, key_end, slopes)
-    with torch.cuda.device(device):
-        code = lib.inkling_attn_decode_masked(ctypes.byref(params), ctypes.byref(mask), *ptrs, _stream_handle(stream))
-    _check(code, "inkling_attn_decode_masked")
-    return out
+    return _masked_call("inkling_attn_decode_masked", params, q, None, k_cache, v_cache, block_table, seq_lens, out,
+                        workspace, softcap, key_begin, key_end, slopes, lse, stream)
 
 
-def _rows_dev(t: torch.Tensor, name: str, shape):
+def _rows_arg(t, name, shape, device):
     """Pointer and token stride of [T, H, D] rows whose heads are contiguous (a view of a fused projection)."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    _shape(t, name, shape)
+    if not (t.dtype is torch.bfloat16 and t.get_device() == device and t.shape == shape):
+        _refuse(t, name, torch.bfloat16, shape, device)
     T, H, D = shape
-    if t.stride(2) != 1 or (H > 1 and t.stride(1) != D):
+    st = t.stride()
+    if st[2] != 1 or (H > 1 and st[1] != D):
         raise ValueError(f"{name}: the heads of a row must be contiguous")
-    return t.data_ptr(), (int(t.stride(0)) if T > 1 else H * D)
+    return t.data_ptr(), (st[0] if T > 1 else H * D)
 
 
 def inkling_attn_qk_norm_rope_write(params, q, k, v, cu_q_lens, seq_lens, block_table, q_out, k_cache, v_cache,
@@ -390,24 +403,23 @@ def inkling_attn_qk_norm_rope_write(params, q, k, v, cu_q_lens, seq_lens, block_
     lib = load_library()
     if layout not in ROPE_LAYOUTS:
         raise ValueError(f"layout must be one of {sorted(ROPE_LAYOUTS)}, got {layout!r}")
-    T, D = int(q.shape[0]), params.head_dim
-    rows = [*_rows_dev(q, "q", (T, params.num_q_heads, D)), *_rows_dev(k, "k", (T, params.num_kv_heads, D)),
-            *_rows_dev(v, "v", (T, params.num_kv_heads, D))]
-    mid = [_dev(cu_q_lens, "cu_q_lens", torch.int32), T, _dev(seq_lens, "seq_lens", torch.int32),
-           _dev(block_table, "block_table", torch.int32), _dev(q_out, "q_out", torch.bfloat16),
-           _dev(k_cache, "k_cache", torch.bfloat16), _dev(v_cache, "v_cache", torch.bfloat16),
-           _dev(workspace, "workspace", torch.uint8), workspace.numel()]
-    _shape(q_out, "q_out", q.shape)
-    _shape(cu_q_lens, "cu_q_lens", (params.num_seqs + 1,))
-    _check_pools(params, k_cache, v_cache, block_table, seq_lens)
-    rot = 0 if inv_freq is None else 2 * int(inv_freq.numel())
-    rope = ink_norm_rope_t(_opt_dev(w_q, "w_q", torch.float32, (D,)), _opt_dev(w_k, "w_k", torch.float32, (D,)),
-                           float(eps), _opt_dev(inv_freq, "inv_freq", torch.float32, (rot // 2,)), rot,
-                           ROPE_LAYOUTS[layout], float(rot_scale))
-    device = _one_device(q, k, v, cu_q_lens, seq_lens, block_table, q_out, k_cache, v_cache, workspace, w_q, w_k, inv_freq)
-    with torch.cuda.device(device):
-        code = lib.inkling_attn_qk_norm_rope_write(ctypes.byref(params), ctypes.byref(rope), *rows, *mid,
-                                                   _stream_handle(stream))
+    dev = _need(q=q, k=k, v=v, cu_q_lens=cu_q_lens, seq_lens=seq_lens, block_table=block_table, q_out=q_out,
+                k_cache=k_cache, v_cache=v_cache, workspace=workspace)
+    B, Hq, Hkv, D = params.num_seqs, params.num_q_heads, params.num_kv_heads, params.head_dim
+    T = int(q.shape[0])
+    bf, i32, f32 = torch.bfloat16, torch.int32, torch.float32
+    pool = (params.num_pages, Hkv, params.page_size, D)
+    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+    rope = ink_norm_rope_t(_arg(w_q, "w_q", f32, (D,), dev), _arg(w_k, "w_k", f32, (D,), dev), eps,
+                           _arg(inv_freq, "inv_freq", f32, (rot // 2,), dev), rot, ROPE_LAYOUTS[layout], rot_scale)
+    code = _launch(lib.inkling_attn_qk_norm_rope_write, dev, stream, ctypes.byref(params), ctypes.byref(rope),
+                   *_rows_arg(q, "q", (T, Hq, D), dev), *_rows_arg(k, "k", (T, Hkv, D), dev),
+                   *_rows_arg(v, "v", (T, Hkv, D), dev), _arg(cu_q_lens, "cu_q_lens", i32, (B + 1,), dev), T,
+                   _arg(seq_lens, "seq_lens", i32, (B,), dev),
+                   _arg(block_table, "block_table", i32, (B, params.max_pages_per_seq), dev),
+                   _arg(q_out, "q_out", bf, (T, Hq, D), dev), _arg(k_cache, "k_cache", bf, pool, dev),
+                   _arg(v_cache, "v_cache", bf, pool, dev), _arg(workspace, "workspace", torch.uint8, None, dev),
+                   workspace.numel())
     _check(code, "inkling_attn_qk_norm_rope_write")
     return q_out
 

@@ -226,15 +226,12 @@ bool make_lowrank_maps(ink::PrefillMaps* m, const void* r, const void* proj_t, c
 bool make_decode_maps(ink::DecodeMaps* m, const void* q, const void* k_cache, const void* v_cache,
                       const ink_attn_params_t* params) {
   const int D = params->head_dim;
-  if (!make_pool_map(&m->k_seg, k_cache, params, 16) || !make_pool_map(&m->v_seg, v_cache, params, 16) ||
-      !make_rows_map3(&m->q3, q, (uint64_t)params->num_seqs * params->num_q_heads, D, D / 64, 16))
-    return false;
-  std::memset(&m->k_tile, 0, sizeof m->k_tile);
-  std::memset(&m->v_tile, 0, sizeof m->v_tile);
-  std::memset(&m->k_grp, 0, sizeof m->k_grp);
-  std::memset(&m->v_grp, 0, sizeof m->v_grp);
-  if (params->page_size >= 16 && (!make_group_map(&m->k_grp, k_cache, pool_rows(params), D, 1) ||
-                                  !make_group_map(&m->v_grp, v_cache, pool_rows(params), D, 1)))
+  std::memset(m, 0, sizeof *m);
+  if (!make_rows_map3(&m->q3, q, (uint64_t)params->num_seqs * params->num_q_heads, D, D / 64, 16)) return false;
+  if (params->page_size < 16)   // the only page size whose tiles come in 8-key boxes
+    return make_pool_map(&m->k_seg, k_cache, params, 16) && make_pool_map(&m->v_seg, v_cache, params, 16);
+  if (!make_group_map(&m->k_grp, k_cache, pool_rows(params), D, 1) ||
+      !make_group_map(&m->v_grp, v_cache, pool_rows(params), D, 1))
     return false;
   return params->page_size < ink::TILE_KEYS ||
          (make_group_map(&m->k_tile, k_cache, pool_rows(params), D, ink::TILE_KEYS / 16) &&
