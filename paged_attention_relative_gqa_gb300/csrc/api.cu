@@ -609,6 +609,13 @@ ink_status_t masked_impl(const ink_attn_params_t* params, const ink_attn_mask_t*
   a.cap_log2 = mk.softcap * 1.4426950408889634f;
   a.cap_k1 = mk.softcap > 0.f ? (float)(2.0 * 1.4426950408889634 * params->sm_scale / mk.softcap) : 0.f;
   a.cap_inv = mk.softcap > 0.f ? params->sm_scale / mk.softcap : 0.f;
+  // tanh(y) / y for |y| <= 0.45 as a polynomial in y^2 of the least relative error (2^-22), in terms
+  // of the raw product; left out (a negative reach) where its coefficients would leave fp32's range
+  static const double kNear[4] = {0.9999997567401877, -0.3332946719023333, 0.13236369052154567, -0.04602819379882759};
+  const double inv = mk.softcap > 0.f ? (double)params->sm_scale / mk.softcap : 0.0, ainv = inv < 0 ? -inv : inv;
+  a.cap_near = ainv >= 1e-5 && ainv <= 1e3 ? (float)(0.45 / ainv) : -1.f;
+  double c = 1.4426950408889634 * params->sm_scale;
+  for (int i = 0; i < 4; ++i, c *= inv * inv) a.near[i] = a.cap_near > 0.f ? (float)(c * kNear[i]) : 0.f;
   a.counters = reinterpret_cast<uint32_t*>(workspace) + 16;   // inside the header
   // a row tile: the heads of a KV head (in equal chunks when there are more than 128) times as
   // many tokens as fit

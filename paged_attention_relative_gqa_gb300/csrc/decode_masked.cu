@@ -195,7 +195,7 @@ __device__ __noinline__ void join_pieces(const float* part_o, const float* part_
   if (tid == 0) *ticket = 0;   // ready for the next call
 }
 
-template <int D, int NSTAGE, int HB, int CAP>
+template <int D, int NSTAGE, int HB, bool CAP>
 __global__ void __launch_bounds__(DM_THREADS, HB == 8 ? 2 : 1)
 decode_masked_kernel(const __grid_constant__ DecodeMaps maps, const __grid_constant__ MaskedArgs a) {
   using S = DMShape<D>;
@@ -562,7 +562,7 @@ decode_masked_kernel(const __grid_constant__ DecodeMaps maps, const __grid_const
   }
 }
 
-template <int D, int NSTAGE, int HB, int CAP>
+template <int D, int NSTAGE, int HB, bool CAP>
 cudaError_t launch_t(const DecodeMaps& m, const MaskedArgs& a, int sms, cudaStream_t stream) {
   constexpr size_t smem = DMSmem<D, NSTAGE, HB>::alloc;
   constexpr int ctas = HB == 8 ? 2 : 1;
@@ -580,9 +580,8 @@ cudaError_t launch_t(const DecodeMaps& m, const MaskedArgs& a, int sms, cudaStre
 
 template <int D, int NSTAGE, int HB>
 cudaError_t launch_cap(const DecodeMaps& m, const MaskedArgs& a, int sms, cudaStream_t stream) {
-  if (a.softcap == 0.f) return launch_t<D, NSTAGE, HB, 0>(m, a, sms, stream);
-  if (a.softcap <= SOFTCAP_PLAIN) return launch_t<D, NSTAGE, HB, 1>(m, a, sms, stream);
-  return launch_t<D, NSTAGE, HB, 2>(m, a, sms, stream);
+  return a.softcap == 0.f ? launch_t<D, NSTAGE, HB, false>(m, a, sms, stream)
+                          : launch_t<D, NSTAGE, HB, true>(m, a, sms, stream);
 }
 
 }  // namespace

@@ -187,6 +187,8 @@ struct MaskedArgs {
   float cap_k1;                // 2 * sm_scale * log2(e) / softcap
   float cap_log2;              // softcap * log2(e)
   float cap_inv;               // sm_scale / softcap
+  // prefill: for |<q, K[k]>| <= cap_near the capped score is x (near[0] + near[1] x^2 + ...)
+  float cap_near, near[4];
   unsigned long long wait_ns;  // limit of one pipeline wait (the drain waits keep 2 s)
   // prefill: a row tile holds tok_per_tile tokens x heads_per_tile query heads of one KV head
   int head_chunks, heads_per_tile, tok_per_tile;
@@ -200,8 +202,6 @@ struct MaskedArgs {
 
 constexpr int MASKED_DECODE_CTAS = 320;   // most CTAs of a masked decode (bounds its partials)
 
-// Caps up to this one take the plain formula of tanh (fewer instructions, off by 2^-23 of the cap).
-constexpr float SOFTCAP_PLAIN = 64.f;
 constexpr int MASKED_ROWS = 128;   // rows of a tile
 
 // TMA descriptors: the pools with boxes of min(P, 128) rows, q as {D, Hq, T} with boxes of

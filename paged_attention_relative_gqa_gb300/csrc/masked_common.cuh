@@ -25,22 +25,27 @@ __device__ __forceinline__ float fast_rcp(float x) {
   return y;
 }
 
-// The score in units of log 2 from the raw product x = <q, K[k]>.  With C the cap:
-//   CAP 0: x scale.
-//   CAP 1: C tanh(x scale / C) = C (1 - 2 / (1 + 2^(k1 x))), off by about 2^-23 C: for caps up to
-//          SOFTCAP_PLAIN.
-//   CAP 2: the same, and below C / 4 the odd series of tanh up to the 7th power, whose relative
-//          error stays below 2^-21 there: for caps so large that 2^-23 C would count.
-template <int CAP>
+// The score in units of log 2 from the raw product x = <q, K[k]>: x scale, or with a cap C
+// C tanh(y), y = x scale / C:
+//   |y| <= 1   y T(y^2), T the polynomial of degree 6 with the least relative error against
+//              tanh(y) / y (an exchange iteration; 2^-24.2, 2^-22.6 when evaluated in fp32)
+//   beyond     1 - 2 / (1 + 2^(k1 x)), off by about 2^-23
+// (The prefill has a shorter way for tiles that stay within CAP_NEAR of the cap.)
+constexpr int CAP_TERMS = 7;
+__device__ __forceinline__ constexpr float cap_term(int i) {
+  return i == 0 ? 0.99999994f : i == 1 ? -0.3333284f : i == 2 ? 0.13325204f : i == 3 ? -0.05345703f
+       : i == 4 ? 0.02028998f : i == 5 ? -0.006203379f : 0.0010410226f;
+}
+
+template <bool CAP>
 __device__ __forceinline__ float score_log2(const MaskedArgs& a, float x) {
-  if constexpr (CAP == 0) return x * a.scale_log2;
-  float s = fmaf(fast_rcp(1.f + fast_exp2(x * a.cap_k1)), -2.f * a.cap_log2, a.cap_log2);
-  if constexpr (CAP == 2) {
-    const float u = x * a.cap_inv, u2 = u * u;
-    const float w = fmaf(fmaf(fmaf(u2, -17.f / 315.f, 2.f / 15.f), u2, -1.f / 3.f), u2, 1.f) * u * a.cap_log2;
-    s = fabsf(u) < 0.25f ? w : s;
-  }
-  return s;
+  if constexpr (!CAP) return x * a.scale_log2;
+  const float y = x * a.cap_inv, u = y * y;
+  float t = cap_term(CAP_TERMS - 1);
+#pragma unroll
+  for (int i = CAP_TERMS - 2; i >= 0; --i) t = fmaf(t, u, cap_term(i));
+  const float far = fmaf(fast_rcp(1.f + fast_exp2(x * a.cap_k1)), -2.f * a.cap_log2, a.cap_log2);
+  return fabsf(y) <= 1.f ? t * y * a.cap_log2 : far;
 }
 
 }  // namespace

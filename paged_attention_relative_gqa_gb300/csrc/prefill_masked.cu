@@ -47,6 +47,7 @@ constexpr int PM_BAD = 8;         // tiles whose unreadable keys are remembered
 constexpr int PM_VOK = 4;         // V tiles checked ahead of their product (at most NS / 2 are in the ring)
 constexpr int PM_REGS_SOFTMAX = 208, PM_REGS_REST = 88;   // registers a thread after the split
 constexpr float RESCALE_LOG2 = 8.f;
+constexpr float FIXED_MAX_LOG2 = 75.f;   // caps up to 52
 
 template <int D>
 struct PMShape {
@@ -102,8 +103,10 @@ __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
   return d;
 }
 
-// CAP: the formulas of score_log2 (masked_common.cuh), two scores at a time.
-template <int D, int CAP, bool IO32>
+// CAP: capped scores.  Models keep most scores well inside the cap: while no score of a warp's tile
+// passes CAP_NEAR of it, tanh is an odd polynomial of four terms in the raw product (relative error
+// 2^-21.8; five packed FMAs for two scores and no special function), else score_log2.
+template <int D, bool CAP, bool IO32>
 __global__ void __launch_bounds__(PM_THREADS, 1)
 prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                       const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ MaskedArgs a) {
@@ -495,8 +498,11 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
     const uint32_t tm_s = tlane + 128u * h, tm_o = tlane + S::TO + (uint32_t)(D * h);
     const int my_i = r / a.heads_per_tile, my_g = r - my_i * a.heads_per_tile;
     __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out);
-    const bool scaled = CAP != 0 || a.slopes != nullptr || !(a.scale_log2 > 0.f);
+    const bool scaled = CAP || a.slopes != nullptr || !(a.scale_log2 > 0.f);
     const float mul = scaled ? 1.f : a.scale_log2;
+    // A score lies within the cap, so where 2^cap is far from overflow and underflow no maximum is
+    // needed: numerators are taken against 0.
+    const bool fixed = CAP && a.slopes == nullptr && a.cap_log2 <= FIXED_MAX_LOG2;
     uint32_t sn = 0, on = 0;
     int g = 0;
     bool go = true;
@@ -537,30 +543,27 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
         tmem_wait_ld();
         const uint4 bad = *reinterpret_cast<const uint4*>(kbad + (g % PM_BAD) * 4);
         // ---- scores
-        if constexpr (CAP != 0) {
-          const uint64_t k12 = f2_pack(a.cap_k1, a.cap_k1), one2 = f2_pack(1.f, 1.f);
-          const uint64_t c2 = f2_pack(a.cap_log2, a.cap_log2), cn2 = f2_pack(-2.f * a.cap_log2, -2.f * a.cap_log2);
+        if constexpr (CAP) {
+          float far = 0.f;   // largest |<q, K[k]>| of the tile
 #pragma unroll
-          for (int c = 0; c < 128; c += 2) {
-            const uint64_t raw = f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
-            float x, y;
-            f2_unpack(f2_mul(raw, k12), x, y);
-            f2_unpack(f2_add(f2_pack(fast_exp2(x), fast_exp2(y)), one2), x, y);
-            uint64_t s = f2_fma(f2_pack(fast_rcp(x), fast_rcp(y)), cn2, c2);
-            if constexpr (CAP == 2) {
-              const uint64_t u = f2_mul(raw, f2_pack(a.cap_inv, a.cap_inv)), u2 = f2_mul(u, u);
-              uint64_t w = f2_fma(u2, f2_pack(-17.f / 315.f, -17.f / 315.f), f2_pack(2.f / 15.f, 2.f / 15.f));
-              w = f2_fma(w, u2, f2_pack(-1.f / 3.f, -1.f / 3.f));
-              w = f2_fma(w, u2, one2);
-              float u0, u1, w0, w1, s0, s1;
-              f2_unpack(u, u0, u1);
-              f2_unpack(f2_mul(f2_mul(w, u), c2), w0, w1);
-              f2_unpack(s, s0, s1);
-              s = f2_pack(fabsf(u0) < 0.25f ? w0 : s0, fabsf(u1) < 0.25f ? w1 : s1);
+          for (int c = 0; c < 128; c += 2)
+            far = fmax3(far, fabsf(__uint_as_float(sr[c])), fabsf(__uint_as_float(sr[c + 1])));
+          if (__any_sync(0xffffffffu, !(far <= a.cap_near))) {
+#pragma unroll
+            for (int c = 0; c < 128; ++c) sr[c] = __float_as_uint(score_log2<true>(a, __uint_as_float(sr[c])));
+          } else {
+            const uint64_t t0 = f2_pack(a.near[0], a.near[0]), t1 = f2_pack(a.near[1], a.near[1]);
+            const uint64_t t2 = f2_pack(a.near[2], a.near[2]), t3 = f2_pack(a.near[3], a.near[3]);
+#pragma unroll
+            for (int c = 0; c < 128; c += 2) {
+              const uint64_t x = f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
+              const uint64_t u = f2_mul(x, x);
+              const uint64_t t = f2_fma(f2_fma(f2_fma(t3, u, t2), u, t1), u, t0);
+              float s0, s1;
+              f2_unpack(f2_mul(t, x), s0, s1);
+              sr[c] = __float_as_uint(s0);
+              sr[c + 1] = __float_as_uint(s1);
             }
-            f2_unpack(s, x, y);
-            sr[c] = __float_as_uint(x);
-            sr[c + 1] = __float_as_uint(y);
           }
         } else if (scaled) {
 #pragma unroll
@@ -585,6 +588,9 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
           }
         }
         // ---- running maximum
+        if (fixed) {
+          m = 0.f;
+        } else {
         float mxv[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int c = 0; c < 128; c += 2)
@@ -607,24 +613,31 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
           }
           if (mine) m = mx;
         }
+        }
         // ---- numerators
         const float nm = m == -INFINITY ? 0.f : -m;
         const uint64_t mul2 = f2_pack(mul, mul), nm2 = f2_pack(nm, nm);
         uint64_t ls2[4] = {0ull, 0ull, 0ull, 0ull};
+        auto numerators = [&](auto against_zero) {
 #pragma unroll
-        for (int quarter = 0; quarter < 4; ++quarter) {
-          uint32_t pk[16];
+          for (int quarter = 0; quarter < 4; ++quarter) {
+            uint32_t pk[16];
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            const int e = 32 * quarter + 2 * c;
-            float t0, t1;
-            f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[e]), __uint_as_float(sr[e + 1])), mul2, nm2), t0, t1);
-            const float p0 = fast_exp2(t0), p1 = fast_exp2(t1);
-            ls2[c & 3] = f2_add(ls2[c & 3], f2_pack(p0, p1));
-            pk[c] = pack_bf16(p0, p1);
+            for (int c = 0; c < 16; ++c) {
+              const int e = 32 * quarter + 2 * c;
+              float t0 = __uint_as_float(sr[e]), t1 = __uint_as_float(sr[e + 1]);
+              if constexpr (!decltype(against_zero)::value) f2_unpack(f2_fma(f2_pack(t0, t1), mul2, nm2), t0, t1);
+              const float p0 = fast_exp2(t0), p1 = fast_exp2(t1);
+              ls2[c & 3] = f2_add(ls2[c & 3], f2_pack(p0, p1));
+              pk[c] = pack_bf16(p0, p1);
+            }
+            tmem_st16(tm_s + 16 * quarter, pk);
           }
-          tmem_st16(tm_s + 16 * quarter, pk);
-        }
+        };
+        if (CAP && fixed)
+          numerators(std::true_type{});
+        else
+          numerators(std::false_type{});
         {
           float x0, x1, y0, y1;
           f2_unpack(f2_add(ls2[0], ls2[1]), x0, x1);
@@ -700,7 +713,7 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
   }
 }
 
-template <int D, int CAP, bool IO32>
+template <int D, bool CAP, bool IO32>
 cudaError_t launch_t(const MaskedMaps& m, const MaskedArgs& a, int grid, cudaStream_t stream) {
   static std::atomic<unsigned long long> opted{0};
   cudaError_t e = smem_opt_in_once(prefill_masked_kernel<D, CAP, IO32>, (int)PMSmem<D>::alloc, opted);
@@ -719,8 +732,7 @@ cudaError_t launch_t(const MaskedMaps& m, const MaskedArgs& a, int grid, cudaStr
 
 template <int D, bool IO32>
 cudaError_t launch_cap(const MaskedMaps& m, const MaskedArgs& a, int grid, cudaStream_t stream) {
-  if (a.softcap == 0.f) return launch_t<D, 0, IO32>(m, a, grid, stream);
-  return a.softcap <= SOFTCAP_PLAIN ? launch_t<D, 1, IO32>(m, a, grid, stream) : launch_t<D, 2, IO32>(m, a, grid, stream);
+  return a.softcap == 0.f ? launch_t<D, false, IO32>(m, a, grid, stream) : launch_t<D, true, IO32>(m, a, grid, stream);
 }
 
 }  // namespace
