@@ -44,7 +44,11 @@ constexpr int PM_THREADS = 384;
 constexpr int PM_KEYS = 128;      // keys per K or V tile
 constexpr int PM_ITEMS = 4;       // published items in flight
 constexpr int PM_BAD = 8;         // tiles whose unreadable keys are remembered
-constexpr int PM_VOK = 4;         // V tiles checked ahead of their product (at most NS / 2 are in the ring)
+// Barriers of K and V tiles go by tile, not by slot: at most 4 tiles of a kind are in the ring, and
+// every waiter waits for every tile of a kind in order, so a barrier is never a phase off.  (By slot,
+// whose fills alternate between K and V and may land out of order, one who waits for V alone would
+// at times see the phase before.)
+constexpr int PM_TILES = 4;
 constexpr int PM_REGS_SOFTMAX = 208, PM_REGS_REST = 88;   // registers a thread after the split
 constexpr float RESCALE_LOG2 = 8.f;
 constexpr float FIXED_MAX_LOG2 = 75.f;   // caps up to 52
@@ -72,9 +76,9 @@ struct PMSmem {
   static constexpr size_t q = 0;
   static constexpr size_t ring = 2 * (size_t)S::TILE;
   static constexpr size_t bars = ring + (size_t)S::NS * S::TILE;
-  // full[NS], empty[NS], v_ok[VOK], s_full[2], p_full[2], o_full[2], q_full[2], q_empty[2],
+  // k_full[TILES], v_full[TILES], v_ok[TILES], empty[NS], s_full[2], p_full[2], o_full[2], q_full[2], q_empty[2],
   // item_full[ITEMS], item_empty[ITEMS], drain
-  static constexpr int NBAR = 2 * S::NS + PM_VOK + 10 + 2 * PM_ITEMS + 1;
+  static constexpr int NBAR = S::NS + 3 * PM_TILES + 10 + 2 * PM_ITEMS + 1;
   static constexpr size_t items = bars + (NBAR * 8 + 15) / 16 * 16;
   static constexpr size_t kbad = items + PM_ITEMS * sizeof(PMItem);
   static constexpr size_t poison = kbad + PM_BAD * 16;
@@ -116,10 +120,11 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_align1024(smem_raw);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L_::bars);
-  uint64_t* empty = full + NS;
-  uint64_t* v_ok = empty + NS;
-  uint64_t* s_full = v_ok + PM_VOK;     // [2] S_h in TMEM, every earlier product of h done
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + L_::bars);
+  uint64_t* v_full = k_full + PM_TILES;
+  uint64_t* v_ok = v_full + PM_TILES;   // V tile checked
+  uint64_t* empty = v_ok + PM_TILES;
+  uint64_t* s_full = empty + NS;        // [2] S_h in TMEM, every earlier product of h done
   uint64_t* p_full = s_full + 2;        // [2] P_h written
   uint64_t* o_full = p_full + 2;        // [2] the item's last O_h product done
   uint64_t* q_full = o_full + 2;        // [2]
@@ -137,11 +142,12 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
   const int P = 1 << a.log2_page;
 
   if (tid == 0) {
-    for (int x = 0; x < NS; ++x) {
-      mbar_init(&full[x], 1);
-      mbar_init(&empty[x], 1);
+    for (int x = 0; x < NS; ++x) mbar_init(&empty[x], 1);
+    for (int x = 0; x < PM_TILES; ++x) {
+      mbar_init(&k_full[x], 1);
+      mbar_init(&v_full[x], 1);
+      mbar_init(&v_ok[x], 1);
     }
-    for (int x = 0; x < PM_VOK; ++x) mbar_init(&v_ok[x], 1);
     for (int x = 0; x < 2; ++x) {
       mbar_init(&s_full[x], 1);
       mbar_init(&p_full[x], 4);
@@ -230,19 +236,23 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
               kbad[((f >> 1) % PM_BAD) * 4 + lane] = bad;
               if (bmask && lane == 0) record_error(a.err, INK_DEVERR_PAGE_OUT_OF_RANGE);
             }
+            uint64_t* full = (kv ? v_full : k_full) + (f >> 1) % PM_TILES;
             __syncwarp();
-            if (lane == 0) mbar_arrive_expect_tx(&full[st], nload * (uint32_t)(seg * D * 2));
+            if (lane == 0) mbar_arrive_expect_tx(full, nload * (uint32_t)(seg * D * 2));
             __syncwarp();
             if (load) {
               uint8_t* dst = smem + L_::ring + (size_t)st * S::TILE + lane * seg * 128;
 #pragma unroll
               for (int cb = 0; cb < S::CB; ++cb)
-                tma_load_2d(dst + cb * S::SUB, kv ? &tmV : &tmK, cb * 64, row, &full[st]);
+                tma_load_2d(dst + cb * S::SUB, kv ? &tmV : &tmK, cb * 64, row, full);
             }
           }
         }
       }
-      if (lane == 0) pp_drain_ring(full, NS, f, a.err);
+      if (lane == 0) {
+        pp_drain_ring(k_full, PM_TILES, (f + 1) >> 1, a.err);
+        pp_drain_ring(v_full, PM_TILES, f >> 1, a.err);
+      }
     } else if (warp == 9) {
       // ---------------------------------------------------------------- MMA issue
       constexpr uint32_t IDESC_S = umma_idesc_bf16(128, PM_KEYS, false, false);
@@ -252,7 +262,9 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
       uint32_t qn0 = 0, qn1 = 0, pn0 = 0, pn1 = 0;
       bool go = true;
       auto slot = [&](int f) { return f % NS; };
-      auto par = [&](int f) { return (uint32_t)(f / NS) & 1u; };
+      auto wait_tile = [&](uint64_t* bars, int tile) {
+        return pm_wait(&bars[tile % PM_TILES], (uint32_t)(tile / PM_TILES) & 1u, abort_flag, a);
+      };
       auto issue_s = [&](int h, int f) {
         const uint64_t ad = umma_desc_sw128(qaddr + h * S::TILE, 16, 1024);
         const uint64_t bd = umma_desc_sw128(raddr + slot(f) * S::TILE, 16, 1024);
@@ -273,7 +285,7 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
       for (int k = 0; go && next_item(k, it); ++k) {
         done_item(k);
         if (it.nt <= 0) continue;
-        go = pm_wait(&full[slot(2 * g)], par(2 * g), abort_flag, a);
+        go = wait_tile(k_full, g);
         for (int h = 0; h < it.nh && go; ++h) {
           uint32_t& qn = h ? qn1 : qn0;
           go = pm_wait(&q_full[h], qn & 1u, abort_flag, a);
@@ -290,7 +302,7 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
         for (int j = 0; j < it.nt && go; ++j, ++g) {
           const int vf = 2 * g + 1, kf = 2 * g + 2;
           const bool more = j + 1 < it.nt;
-          go = pm_wait(&full[slot(vf)], par(vf), abort_flag, a) && pm_wait(&v_ok[g % PM_VOK], (uint32_t)(g / PM_VOK) & 1u, abort_flag, a);
+          go = wait_tile(v_full, g) && wait_tile(v_ok, g);
           for (int h = 0; h < it.nh && go; ++h) {
             uint32_t& pn = h ? pn1 : pn0;
             go = pm_wait(&p_full[h], pn & 1u, abort_flag, a);
@@ -299,7 +311,7 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
             tc_fence_after();
             issue_pv(h, vf, j > 0);
             if (more) {
-              if (h == 0) go = pm_wait(&full[slot(kf)], par(kf), abort_flag, a);
+              if (h == 0) go = wait_tile(k_full, g + 1);
               if (!go) break;
               issue_s(h, kf);
               umma_commit_warp(&s_full[h]);
@@ -449,8 +461,8 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
       for (int k = 0; go && next_item(k, it); ++k) {
         bool found = false;
         for (int j = 0; j < it.nt; ++j, ++g) {
-          const int f = 2 * g + 1, st = f % NS;
-          go = pm_wait(&full[st], (uint32_t)(f / NS) & 1u, abort_flag, a);
+          const int st = (2 * g + 1) % NS;
+          go = pm_wait(&v_full[g % PM_TILES], (uint32_t)(g / PM_TILES) & 1u, abort_flag, a);
           if (!go) break;
           const int k0 = (it.kt0 + j) * PM_KEYS;
           const uint4 bad = *reinterpret_cast<const uint4*>(kbad + (g % PM_BAD) * 4);
@@ -485,7 +497,7 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(&v_ok[g % PM_VOK]);
+          if (lane == 0) mbar_arrive(&v_ok[g % PM_TILES]);
         }
         done_item(k);
       }
@@ -544,10 +556,11 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
         const uint4 bad = *reinterpret_cast<const uint4*>(kbad + (g % PM_BAD) * 4);
         // ---- scores
         if constexpr (CAP) {
-          float far = 0.f;   // largest |<q, K[k]>| of the tile
+          float fv[4] = {0.f, 0.f, 0.f, 0.f};   // largest |<q, K[k]>| of the tile
 #pragma unroll
           for (int c = 0; c < 128; c += 2)
-            far = fmax3(far, fabsf(__uint_as_float(sr[c])), fabsf(__uint_as_float(sr[c + 1])));
+            fv[(c >> 1) & 3] = fmax3(fv[(c >> 1) & 3], fabsf(__uint_as_float(sr[c])), fabsf(__uint_as_float(sr[c + 1])));
+          const float far = fmaxf(fmax3(fv[0], fv[1], fv[2]), fv[3]);
           if (__any_sync(0xffffffffu, !(far <= a.cap_near))) {
 #pragma unroll
             for (int c = 0; c < 128; ++c) sr[c] = __float_as_uint(score_log2<true>(a, __uint_as_float(sr[c])));
