@@ -531,12 +531,12 @@ ink_status_t inkling_attn_kv_conv_write(const ink_attn_params_t* params, const v
 
 namespace {
 
-struct MaskedDecodeLayout {
+struct MaskedLayout {
   size_t tickets_off, part_o_off, part_ml_off, total;
 };
 
-MaskedDecodeLayout masked_decode_layout(const ink_attn_params_t* p) {
-  MaskedDecodeLayout l;
+MaskedLayout masked_decode_layout(const ink_attn_params_t* p) {
+  MaskedLayout l;
   const size_t B = (size_t)(p->num_seqs > 0 ? p->num_seqs : 1);
   const size_t G = (size_t)(p->num_q_heads / p->num_kv_heads), rows = G <= 8 ? 8 : 16;
   const size_t places = 2 * (size_t)ink::MASKED_DECODE_CTAS * rows;
@@ -544,6 +544,16 @@ MaskedDecodeLayout masked_decode_layout(const ink_attn_params_t* p) {
   l.part_o_off = align_up(l.tickets_off + B * p->num_kv_heads * ((G + 15) / 16) * sizeof(int32_t), 256);
   l.part_ml_off = l.part_o_off + places * p->head_dim * sizeof(float);
   l.total = align_up(l.part_ml_off + places * 2 * sizeof(float), 256);
+  return l;
+}
+
+MaskedLayout masked_prefill_layout(const ink_attn_params_t* p) {
+  MaskedLayout l;
+  const size_t rows = (size_t)ink::MASKED_PIECES * 2 * ink::MASKED_ROWS;
+  l.tickets_off = kHeaderBytes;
+  l.part_o_off = align_up(l.tickets_off + (size_t)ink::MASKED_PIECES * 2 * sizeof(int32_t), 256);
+  l.part_ml_off = l.part_o_off + rows * p->head_dim * sizeof(float);
+  l.total = l.part_ml_off + rows * 4 * sizeof(float);
   return l;
 }
 
@@ -616,19 +626,21 @@ ink_status_t masked_impl(const ink_attn_params_t* params, const ink_attn_mask_t*
   a.cap_near = ainv >= 1e-5 && ainv <= 1e3 ? (float)(0.45 / ainv) : -1.f;
   double c = 1.4426950408889634 * params->sm_scale;
   for (int i = 0; i < 4; ++i, c *= inv * inv) a.near[i] = a.cap_near > 0.f ? (float)(c * kNear[i]) : 0.f;
-  a.counters = reinterpret_cast<uint32_t*>(workspace) + 16;   // inside the header
+  a.stale = reinterpret_cast<uint32_t*>(workspace) + 15;   // these three inside the header
+  a.counters = reinterpret_cast<uint32_t*>(workspace) + 16;
   // a row tile: the heads of a KV head (in equal chunks when there are more than 128) times as
   // many tokens as fit
   a.head_chunks = (a.G + ink::MASKED_ROWS - 1) / ink::MASKED_ROWS;
   a.heads_per_tile = (a.G + a.head_chunks - 1) / a.head_chunks;
   a.tok_per_tile = ink::MASKED_ROWS / a.heads_per_tile;
+  const MaskedLayout lay = decode ? masked_decode_layout(params) : masked_prefill_layout(params);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.tickets = reinterpret_cast<int32_t*>(ws + lay.tickets_off);
+  a.part_o = reinterpret_cast<float*>(ws + lay.part_o_off);
+  a.part_ml = reinterpret_cast<float*>(ws + lay.part_ml_off);
+  a.io32 = aligned(out, 32) ? 1 : 0;
   if (decode) {
     a.head_chunks = (a.G + 15) / 16;
-    const MaskedDecodeLayout lay = masked_decode_layout(params);
-    uint8_t* ws = static_cast<uint8_t*>(workspace);
-    a.tickets = reinterpret_cast<int32_t*>(ws + lay.tickets_off);
-    a.part_o = reinterpret_cast<float*>(ws + lay.part_o_off);
-    a.part_ml = reinterpret_cast<float*>(ws + lay.part_ml_off);
     ink::DecodeMaps maps;
     if (!make_decode_maps(&maps, q, k_cache, v_cache, params)) return INK_ERR_CUDA;
     if (ink::launch_decode_masked(maps, a, params->head_dim, (cudaStream_t)stream) != cudaSuccess) return INK_ERR_CUDA;
@@ -638,7 +650,7 @@ ink_status_t masked_impl(const ink_attn_params_t* params, const ink_attn_mask_t*
   if (!make_pool_map(&maps.k, k_cache, params, 128) || !make_pool_map(&maps.v, v_cache, params, 128) ||
       !make_token_map(&maps.q, q, params, total_q, a.heads_per_tile, a.tok_per_tile))
     return INK_ERR_CUDA;
-  if (ink::launch_prefill_masked(maps, a, params->head_dim, aligned(out, 32), (cudaStream_t)stream) != cudaSuccess)
+  if (ink::launch_prefill_masked(maps, a, params->head_dim, (cudaStream_t)stream) != cudaSuccess)
     return INK_ERR_CUDA;
   return INK_OK;
 }
@@ -649,7 +661,7 @@ extern "C" {
 
 size_t inkling_attn_masked_workspace_bytes(const ink_attn_params_t* params, int is_decode) {
   if (validate(params) != INK_OK) return 0;
-  return is_decode ? masked_decode_layout(params).total : kHeaderBytes;
+  return (is_decode ? masked_decode_layout(params) : masked_prefill_layout(params)).total;
 }
 
 ink_status_t inkling_attn_prefill_masked(const ink_attn_params_t* params, const ink_attn_mask_t* mask,

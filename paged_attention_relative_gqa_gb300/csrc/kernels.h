@@ -192,13 +192,17 @@ struct MaskedArgs {
   unsigned long long wait_ns;  // limit of one pipeline wait (the drain waits keep 2 s)
   // prefill: a row tile holds tok_per_tile tokens x heads_per_tile query heads of one KV head
   int head_chunks, heads_per_tile, tok_per_tile;
+  int io32;                    // out 32-byte aligned: its rows are stored 32 bytes at a time
+  uint32_t* stale;             // nonzero after a timeout of a prefill, until the workspace is initialised again
   uint32_t* counters;          // [0] items handed out, [1] CTAs done; zero between calls
   // decode: partials of cut groups, two places per CTA of `rows` heads (8 or 16), and a ticket
   // per (sequence, KV head, chunk of 16 query heads), zero between calls
-  float* part_o;               // [2 * CTAs, rows, D]
-  float* part_ml;              // [2 * CTAs, rows, 2] (running max in log2 units, sum)
-  int32_t* tickets;
+  float* part_o;               // [2 * CTAs, rows, D]; prefill: [pieces, 2, D / 4, 128 rows] float4
+  float* part_ml;              // [2 * CTAs, rows, 2] (running max in log2 units, sum); prefill: [pieces, 2, 128 rows] float4
+  int32_t* tickets;            // prefill: [pieces, 2]
 };
+
+constexpr int MASKED_PIECES = 320;        // most pieces of cut items in one masked prefill
 
 constexpr int MASKED_DECODE_CTAS = 320;   // most CTAs of a masked decode (bounds its partials)
 
@@ -210,7 +214,7 @@ struct MaskedMaps {
   CUtensorMap k, v, q;
 };
 
-cudaError_t launch_prefill_masked(const MaskedMaps& m, const MaskedArgs& a, int head_dim, bool io32, cudaStream_t stream);
+cudaError_t launch_prefill_masked(const MaskedMaps& m, const MaskedArgs& a, int head_dim, cudaStream_t stream);
 cudaError_t launch_decode_masked(const DecodeMaps& m, const MaskedArgs& a, int head_dim, cudaStream_t stream);
 
 }  // namespace ink

@@ -24,9 +24,13 @@
 //       runs, the tensor cores work for the other.
 //   10  scheduler: hands out items (a counter in the workspace, longest first within a sequence),
 //       finds their key ranges, publishes them in shared memory, and loads their Q tiles by TMA.
-//   11  V check: in a tile that not every row of the item sees whole, rows of V that nobody sees
+//   11  K and V check: in a V tile that not every row of the item sees whole, rows of V that nobody sees
 //       are zeroed, and so are rows with an infinity or NaN (0 * NaN would reach rows that do not
 //       see the key); rows that do see one get it back in the epilogue.
+// When there are fewer items than SMs (a chunk of a prompt or a few drafted tokens against a long
+// history), the key tiles of an item are cut into pieces of equal length, as many as make two rounds
+// over the SMs; a piece leaves O, maximum and sum in the workspace, and the last one to finish (an
+// atomic ticket, no waiting) joins them in order.
 // Every wait is bounded; after a timeout the CTA records it, stops issuing, waits for what is in
 // flight and exits.
 #include <algorithm>
@@ -50,6 +54,7 @@ constexpr int PM_BAD = 8;         // tiles whose unreadable keys are remembered
 // at times see the phase before.)
 constexpr int PM_TILES = 4;
 constexpr int PM_REGS_SOFTMAX = 208, PM_REGS_REST = 88;   // registers a thread after the split
+constexpr int PM_PIECE_TILES = 8; // least tiles of a piece of a cut item
 constexpr float RESCALE_LOG2 = 8.f;
 constexpr float FIXED_MAX_LOG2 = 75.f;   // caps up to 52
 
@@ -68,6 +73,7 @@ struct PMItem {
   int lo_min, hi_max;        // keys any row sees lie in [lo_min, hi_max)
   int lo_max, hi_min;        // keys in [lo_max, hi_min) are seen by every row
   int kt0, nt, nh, bad_len;  // first key tile, tiles (-1: no more items), row tiles
+  int ticket, slot, np, one; // of a cut item: its number, its first place in the partials, its pieces, this one
 };
 
 template <int D>
@@ -76,14 +82,14 @@ struct PMSmem {
   static constexpr size_t q = 0;
   static constexpr size_t ring = 2 * (size_t)S::TILE;
   static constexpr size_t bars = ring + (size_t)S::NS * S::TILE;
-  // k_full[TILES], v_full[TILES], v_ok[TILES], empty[NS], s_full[2], p_full[2], o_full[2], q_full[2], q_empty[2],
+  // k_full[TILES], v_full[TILES], v_ok[TILES], k_ok[TILES], empty[NS], s_full[2], p_full[2], o_full[2], q_full[2], q_empty[2],
   // item_full[ITEMS], item_empty[ITEMS], drain
-  static constexpr int NBAR = S::NS + 3 * PM_TILES + 10 + 2 * PM_ITEMS + 1;
+  static constexpr int NBAR = S::NS + 4 * PM_TILES + 10 + 2 * PM_ITEMS + 1;
   static constexpr size_t items = bars + (NBAR * 8 + 15) / 16 * 16;
   static constexpr size_t kbad = items + PM_ITEMS * sizeof(PMItem);
   static constexpr size_t poison = kbad + PM_BAD * 16;
   static constexpr size_t misc = poison + PM_ITEMS * 4;
-  static constexpr size_t total = misc + 16;
+  static constexpr size_t total = misc + 32;
   static constexpr size_t alloc = total + 1024;
   static_assert(alloc <= 227 * 1024, "shared memory budget");
 };
@@ -95,6 +101,7 @@ __device__ __forceinline__ bool pm_wait(uint64_t* bar, uint32_t parity, volatile
     ok = mbar_wait_limit(bar, parity, a.wait_ns);
     if (!ok) {
       record_error(a.err, INK_DEVERR_WAIT_TIMEOUT);
+      *a.stale = 1;   // tickets of cut items may be left over
       *abort_flag = 1;
     }
   }
@@ -110,7 +117,9 @@ __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
 // CAP: capped scores.  Models keep most scores well inside the cap: while no score of a warp's tile
 // passes CAP_NEAR of it, tanh is an odd polynomial of four terms in the raw product (relative error
 // 2^-21.8; five packed FMAs for two scores and no special function), else score_log2.
-template <int D, bool CAP, bool IO32>
+// SPLIT: items may be cut into pieces (a kernel of its own: the joining code would cost the others
+// registers).
+template <int D, bool CAP, bool SPLIT>
 __global__ void __launch_bounds__(PM_THREADS, 1)
 prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                       const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ MaskedArgs a) {
@@ -123,7 +132,8 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
   uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + L_::bars);
   uint64_t* v_full = k_full + PM_TILES;
   uint64_t* v_ok = v_full + PM_TILES;   // V tile checked
-  uint64_t* empty = v_ok + PM_TILES;
+  uint64_t* k_ok = v_ok + PM_TILES;     // K tile checked (capped scores)
+  uint64_t* empty = k_ok + PM_TILES;
   uint64_t* s_full = empty + NS;        // [2] S_h in TMEM, every earlier product of h done
   uint64_t* p_full = s_full + 2;        // [2] P_h written
   uint64_t* o_full = p_full + 2;        // [2] the item's last O_h product done
@@ -137,6 +147,7 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
   volatile int* poison = reinterpret_cast<volatile int*>(smem + L_::poison);   // [ITEMS]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L_::misc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L_::misc + 4);
+  volatile int* joins = reinterpret_cast<volatile int*>(smem + L_::misc + 8);   // [2] this piece joins its item
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int P = 1 << a.log2_page;
@@ -147,6 +158,7 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
       mbar_init(&k_full[x], 1);
       mbar_init(&v_full[x], 1);
       mbar_init(&v_ok[x], 1);
+      mbar_init(&k_ok[x], 1);
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(&s_full[x], 1);
@@ -285,7 +297,7 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
       for (int k = 0; go && next_item(k, it); ++k) {
         done_item(k);
         if (it.nt <= 0) continue;
-        go = wait_tile(k_full, g);
+        go = wait_tile(k_full, g) && (!CAP || wait_tile(k_ok, g));
         for (int h = 0; h < it.nh && go; ++h) {
           uint32_t& qn = h ? qn1 : qn0;
           go = pm_wait(&q_full[h], qn & 1u, abort_flag, a);
@@ -311,7 +323,7 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
             tc_fence_after();
             issue_pv(h, vf, j > 0);
             if (more) {
-              if (h == 0) go = wait_tile(k_full, g + 1);
+              if (h == 0) go = wait_tile(k_full, g + 1) && (!CAP || wait_tile(k_ok, g + 1));
               if (!go) break;
               issue_s(h, kf);
               umma_commit_warp(&s_full[h]);
@@ -335,11 +347,15 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
       if (lane == 0) prefetch_tensormap(&tmQ);
       const int per = a.Hkv * a.head_chunks, tpi = 2 * a.tok_per_tile;
       int cb = 0, base = 0, cnt = 0, incl = 0, total = 0;
+      int my_c0 = 0, my_n = 0, my_len = 0;   // of this lane's sequence
       auto load_chunk = [&]() {   // items of sequences cb + lane
         const int b = cb + lane;
-        cnt = 0;
+        cnt = my_len = 0;
         if (b < a.B) {
           const int c0 = __ldg(a.cu_q + b), c1 = __ldg(a.cu_q + b + 1);
+          my_len = __ldg(a.seq_lens + b);
+          my_c0 = c0;
+          my_n = c1 - c0;
           if (c0 < 0 || c1 > a.T || c1 < c0) {
             if (blockIdx.x == 0) record_error(a.err, INK_DEVERR_BAD_ROWS);
           } else {
@@ -355,11 +371,34 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
         total = __shfl_sync(0xffffffffu, incl, 31);
       };
       load_chunk();
+      // pieces of an item: enough for two rounds over the SMs when the items alone do not fill one, of
+      // PM_PIECE_TILES tiles at least
+      int splits = 1;
+      if constexpr (SPLIT) {
+        const uint32_t stale = *reinterpret_cast<volatile uint32_t*>(a.stale);
+        const int sms = (int)min(gridDim.x, (unsigned)MASKED_PIECES / 2);
+        int all = total, longest = my_len;
+        for (cb = 32; cb < a.B && all < sms; cb += 32) {
+          load_chunk();
+          all += total;
+          longest = max(longest, my_len);
+        }
+        longest = __reduce_max_sync(0xffffffffu, longest);
+        if (a.W > 0 && !a.key_end) longest = min(longest, a.W + tpi + PM_KEYS);
+        if (all > 0) splits = max(1, min(2 * sms / all, longest / (PM_KEYS * PM_PIECE_TILES)));
+        if (cb > 32) {
+          cb = 0;
+          load_chunk();
+        }
+        cb = stale ? a.B : 0;
+        if (stale && lane == 0) record_error(a.err, INK_DEVERR_WAIT_TIMEOUT);   // left unusable by a timeout
+      }
       int idx = blockIdx.x, qn0 = 0, qn1 = 0;
-      for (int k = 0;; ++k) {
+      for (int k = 0;;) {
         int next = 0;
         if (lane == 0) next = (int)atomicAdd(a.counters, 1u) + (int)gridDim.x;
-        while (cb < a.B && idx >= base + total) {
+        const int item = SPLIT ? idx / splits : idx, one = SPLIT ? idx - item * splits : 0;
+        while (cb < a.B && item >= base + total) {
           base += total;
           cb += 32;
           if (cb < a.B) load_chunk();
@@ -373,8 +412,8 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
           }
           break;
         }
-        const int src = __ffs(__ballot_sync(0xffffffffu, idx < base + incl)) - 1;
-        const int li = idx - base - __shfl_sync(0xffffffffu, incl - cnt, src);
+        const int src = __ffs(__ballot_sync(0xffffffffu, item < base + incl)) - 1;
+        const int li = item - base - __shfl_sync(0xffffffffu, incl - cnt, src);
         const int nq = __shfl_sync(0xffffffffu, cnt, src) / per;
         PMItem it;
         it.b = cb + src;
@@ -384,8 +423,8 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
         const int hc = r - it.kvh * a.head_chunks;
         it.h0 = it.kvh * a.G + hc * a.heads_per_tile;
         it.gh = min(a.heads_per_tile, a.G - hc * a.heads_per_tile);
-        const int c0 = __ldg(a.cu_q + it.b), n = __ldg(a.cu_q + it.b + 1) - c0;
-        it.L = __ldg(a.seq_lens + it.b);
+        const int c0 = __shfl_sync(0xffffffffu, my_c0, src), n = __shfl_sync(0xffffffffu, my_n, src);
+        it.L = __shfl_sync(0xffffffffu, my_len, src);
         it.t0 = c0 + qt * tpi;
         it.ntok = min(tpi, n - qt * tpi);
         it.pos0 = it.L - n + qt * tpi;
@@ -415,6 +454,22 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
         }
         it.kt0 = it.lo_min / PM_KEYS;
         it.nt = it.hi_max > it.lo_min ? (it.hi_max - 1) / PM_KEYS - it.kt0 + 1 : 0;
+        it.np = 1;
+        if constexpr (SPLIT) {
+          const int len = max(PM_PIECE_TILES, (it.nt + splits - 1) / splits);
+          it.np = max(1, (it.nt + len - 1) / len);
+          it.ticket = item;
+          it.slot = item * splits;
+          it.one = one;
+          if (it.np > 1) {
+            it.kt0 += one * len;
+            it.nt = min(len, it.nt - one * len);
+          }
+          if (one >= it.np) {   // no such piece
+            idx = __shfl_sync(0xffffffffu, next, 0);
+            continue;
+          }
+        }
         if (lane == 0) {
           if (it.bad_len) record_error(a.err, INK_DEVERR_QLEN_EXCEEDS_KV);
           else if ((long long)it.L > ((long long)a.max_pages << a.log2_page)) record_error(a.err, INK_DEVERR_PAGE_OUT_OF_RANGE);
@@ -440,6 +495,7 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
         }
         if (!go) break;
         idx = __shfl_sync(0xffffffffu, next, 0);
+        ++k;
       }
       if (lane == 0) {
         for (int h = 0; h < 2; ++h) {
@@ -462,6 +518,31 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
         bool found = false;
         for (int j = 0; j < it.nt; ++j, ++g) {
           const int st = (2 * g + 1) % NS;
+          if constexpr (CAP) {
+            // Rows of K that nobody sees are zeroed: how scores are capped goes by the largest score of a
+            // tile, which must not hang on what lies in a slot or a page by chance.
+            go = pm_wait(&k_full[g % PM_TILES], (uint32_t)(g / PM_TILES) & 1u, abort_flag, a);
+            if (!go) break;
+            const int kb = (it.kt0 + j) * PM_KEYS;
+            const uint4 kw = *reinterpret_cast<const uint4*>(kbad + (g % PM_BAD) * 4);
+            if (kb < it.lo_min || kb + PM_KEYS > it.hi_max || (kw.x | kw.y | kw.z | kw.w)) {
+              const uint32_t kbw[4] = {kw.x, kw.y, kw.z, kw.w};
+              uint8_t* kt = smem + L_::ring + (size_t)((2 * g) % NS) * S::TILE;
+#pragma unroll 1
+              for (int x = 0; x < 4; ++x) {
+                const int kk = kb + 32 * x + lane;
+                if (kk >= it.lo_min && kk < it.hi_max && !((kbw[x] >> lane) & 1u)) continue;
+                uint4* row = reinterpret_cast<uint4*>(kt + (32 * x + lane) * 128);
+#pragma unroll
+                for (int c = 0; c < S::CB; ++c)
+#pragma unroll
+                  for (int y = 0; y < 8; ++y) row[c * (S::SUB / 16) + (y ^ (lane & 7))] = make_uint4(0u, 0u, 0u, 0u);
+              }
+              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&k_ok[g % PM_TILES]);
+          }
           go = pm_wait(&v_full[g % PM_TILES], (uint32_t)(g / PM_TILES) & 1u, abort_flag, a);
           if (!go) break;
           const int k0 = (it.kt0 + j) * PM_KEYS;
@@ -518,10 +599,13 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
     uint32_t sn = 0, on = 0;
     int g = 0;
     bool go = true;
-    PMItem it;
-    for (int k = 0; go && next_item(k, it); ++k) {
+    for (int k = 0; go; ++k) {
+      // (read where it is needed, from shared memory: the tile loop has no registers to spare)
+      const PMItem& it = items[k % PM_ITEMS];
+      if (!pm_wait(&item_full[k % PM_ITEMS], (uint32_t)(k / PM_ITEMS) & 1u, abort_flag, a) || it.nt < 0) break;
+      const int nt = it.nt, kt0 = it.kt0, lo_max = it.lo_max, hi_min = it.hi_min;
       if (h >= it.nh) {
-        g += max(it.nt, 0);
+        g += nt;
         done_item(k);
         continue;
       }
@@ -531,7 +615,7 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
       int lo = 0, hi = 0;
       if (rv && !it.bad_len) token_keys(a, t, p, it.L, lo, hi);
       const size_t orow = (size_t)t * a.Hq + head;
-      if (it.nt == 0) {   // no row sees a key
+      if (nt == 0) {   // no row sees a key
         if (rv) {
           uint4* o = reinterpret_cast<uint4*>(out + orow * D);
 #pragma unroll
@@ -543,8 +627,8 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
       }
       const float slope2 = a.slopes ? __ldg(a.slopes + head) * LOG2E : 0.f;
       float m = -INFINITY, l = 0.f;
-      for (int j = 0; j < it.nt; ++j, ++g) {
-        const int k0 = (it.kt0 + j) * PM_KEYS;
+      for (int j = 0; j < nt; ++j, ++g) {
+        const int k0 = (kt0 + j) * PM_KEYS;
         go = pm_wait(&s_full[h], sn & 1u, abort_flag, a);
         if (!go) break;
         ++sn;
@@ -588,7 +672,8 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
           for (int c = 0; c < 128; ++c)
             sr[c] = __float_as_uint(fmaf(-slope2, fabsf(d0 - (float)c), __uint_as_float(sr[c])));
         }
-        if (k0 < it.lo_max || k0 + PM_KEYS > it.hi_min || (bad.x | bad.y | bad.z | bad.w)) {
+        // ---- keys that this row does not see
+        if (k0 < lo_max || k0 + PM_KEYS > hi_min || (bad.x | bad.y | bad.z | bad.w)) {
           const uint32_t badw[4] = {bad.x, bad.y, bad.z, bad.w};
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
@@ -668,14 +753,85 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
       if (!go) break;
       ++on;
       tc_fence_after();
+      bool poisoned = poison[k % PM_ITEMS] != 0;
+      // a piece of a cut item: its part into the workspace; who is last goes on with the joined row
+      float4* part_o = reinterpret_cast<float4*>(a.part_o) + (size_t)(it.slot * 2 + h) * (D / 4) * MASKED_ROWS + r;
+      float4* part_ml = reinterpret_cast<float4*>(a.part_ml) + (size_t)(it.slot * 2 + h) * MASKED_ROWS + r;
+      constexpr size_t PART = (size_t)2 * (D / 4) * MASKED_ROWS;   // from one piece to the next
+      if (SPLIT && it.np > 1) {
+#pragma unroll 1
+        for (int c2 = 0; c2 < D / 32; ++c2) {
+          uint32_t ov[32];
+          tmem_ld32(tm_o + c2 * 32, ov);
+          tmem_wait_ld();
+#pragma unroll
+          for (int x = 0; x < 8; ++x)
+            __stcg(part_o + it.one * PART + (size_t)(c2 * 8 + x) * MASKED_ROWS,
+                   make_float4(__uint_as_float(ov[4 * x]), __uint_as_float(ov[4 * x + 1]), __uint_as_float(ov[4 * x + 2]),
+                               __uint_as_float(ov[4 * x + 3])));
+        }
+        __stcg(part_ml + (size_t)it.one * 2 * MASKED_ROWS, make_float4(m, l, poisoned ? 1.f : 0.f, 0.f));
+        tc_fence_before();
+        // every thread's stores come before the barrier, the ticket's add releases them and acquires
+        // the other pieces'
+        named_barrier_sync(1 + h, 128);
+        if (r == 0) {
+          int prev;
+          asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;"
+                       : "=r"(prev)
+                       : "l"(a.tickets + 2 * it.ticket + h)
+                       : "memory");
+          joins[h] = prev == it.np - 1;
+          if (prev == it.np - 1) a.tickets[2 * it.ticket + h] = 0;   // ready for the next call
+        }
+        named_barrier_sync(1 + h, 128);
+        if (!joins[h]) {
+          done_item(k);
+          continue;
+        }
+        m = -INFINITY;
+#pragma unroll 4
+        for (int x = 0; x < it.np; ++x) m = fmaxf(m, __ldcg(part_ml + (size_t)x * 2 * MASKED_ROWS).x);
+        l = 0.f;
+#pragma unroll 4
+        for (int x = 0; x < it.np; ++x) {
+          const float4 ml = __ldcg(part_ml + (size_t)x * 2 * MASKED_ROWS);
+          l += ml.y * (ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - m));
+          poisoned = poisoned || ml.z != 0.f;
+        }
+      }
       const float inv = l > 0.f ? 1.f / l : 0.f;
       const bool nothing = l == 0.f;
-      const bool poisoned = poison[k % PM_ITEMS] != 0;
 #pragma unroll 1
       for (int c2 = 0; c2 < D / 32; ++c2) {
         uint32_t ov[32];
-        tmem_ld32(tm_o + c2 * 32, ov);
-        tmem_wait_ld();
+        if (SPLIT && it.np > 1) {
+          float acc[32];
+#pragma unroll
+          for (int x = 0; x < 32; ++x) acc[x] = 0.f;
+          // (two pieces at a time: 17 loads in flight a thread)
+#pragma unroll 2
+          for (int y = 0; y < it.np; ++y) {
+            const float my = __ldcg(part_ml + (size_t)y * 2 * MASKED_ROWS).x;
+            float4 vv[8];
+#pragma unroll
+            for (int x = 0; x < 8; ++x) vv[x] = __ldcg(part_o + y * PART + (size_t)(c2 * 8 + x) * MASKED_ROWS);
+            const float w = my == -INFINITY ? 0.f : fast_exp2(my - m);
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+              const float4 v = vv[x];
+              acc[4 * x] = fmaf(w, v.x, acc[4 * x]);
+              acc[4 * x + 1] = fmaf(w, v.y, acc[4 * x + 1]);
+              acc[4 * x + 2] = fmaf(w, v.z, acc[4 * x + 2]);
+              acc[4 * x + 3] = fmaf(w, v.w, acc[4 * x + 3]);
+            }
+          }
+#pragma unroll
+          for (int x = 0; x < 32; ++x) ov[x] = __float_as_uint(acc[x]);
+        } else {
+          tmem_ld32(tm_o + c2 * 32, ov);
+          tmem_wait_ld();
+        }
 #pragma unroll
         for (int x = 0; x < 32; ++x) ov[x] = nothing ? 0u : __float_as_uint(__uint_as_float(ov[x]) * (l == l ? inv : l));
         if (poisoned && rv) {
@@ -701,7 +857,7 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
 #pragma unroll
             for (int x = 0; x < 8; ++x)
               w[x] = pack_bf16(__uint_as_float(ov[16 * q8 + 2 * x]), __uint_as_float(ov[16 * q8 + 2 * x + 1]));
-            if constexpr (IO32) {
+            if (a.io32) {
               asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(o + 2 * q8), "r"(w[0]), "r"(w[1]),
                            "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
                            : "memory");
@@ -726,41 +882,46 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
   }
 }
 
-template <int D, bool CAP, bool IO32>
+template <int D, bool CAP, bool SPLIT>
 cudaError_t launch_t(const MaskedMaps& m, const MaskedArgs& a, int grid, cudaStream_t stream) {
   static std::atomic<unsigned long long> opted{0};
-  cudaError_t e = smem_opt_in_once(prefill_masked_kernel<D, CAP, IO32>, (int)PMSmem<D>::alloc, opted);
+  cudaError_t e = smem_opt_in_once(prefill_masked_kernel<D, CAP, SPLIT>, (int)PMSmem<D>::alloc, opted);
   if (e != cudaSuccess) return e;
   // The softmax warps' extra registers come out of what the block is launched with: a build with
   // fewer would wait for them without end.
   static const bool enough = [] {
     cudaFuncAttributes at;
-    return cudaFuncGetAttributes(&at, prefill_masked_kernel<D, CAP, IO32>) == cudaSuccess &&
+    return cudaFuncGetAttributes(&at, prefill_masked_kernel<D, CAP, SPLIT>) == cudaSuccess &&
            at.numRegs * PM_THREADS >= 128 * (2 * PM_REGS_SOFTMAX + PM_REGS_REST);
   }();
   if (!enough) return cudaErrorInvalidConfiguration;
-  prefill_masked_kernel<D, CAP, IO32><<<grid, PM_THREADS, PMSmem<D>::alloc, stream>>>(m.k, m.v, m.q, a);
+  prefill_masked_kernel<D, CAP, SPLIT><<<grid, PM_THREADS, PMSmem<D>::alloc, stream>>>(m.k, m.v, m.q, a);
   return cudaGetLastError();
 }
 
-template <int D, bool IO32>
-cudaError_t launch_cap(const MaskedMaps& m, const MaskedArgs& a, int grid, cudaStream_t stream) {
-  return a.softcap == 0.f ? launch_t<D, false, IO32>(m, a, grid, stream) : launch_t<D, true, IO32>(m, a, grid, stream);
+template <int D>
+cudaError_t launch_d(const MaskedMaps& m, const MaskedArgs& a, int grid, bool split, cudaStream_t stream) {
+  if (a.softcap == 0.f) return split ? launch_t<D, false, true>(m, a, grid, stream) : launch_t<D, false, false>(m, a, grid, stream);
+  return split ? launch_t<D, true, true>(m, a, grid, stream) : launch_t<D, true, false>(m, a, grid, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_prefill_masked(const MaskedMaps& m, const MaskedArgs& a, int head_dim, bool io32, cudaStream_t stream) {
+cudaError_t launch_prefill_masked(const MaskedMaps& m, const MaskedArgs& a, int head_dim, cudaStream_t stream) {
   int dev = 0;
   const int sms = current_device_sms(&dev);
   if (sms <= 0) return cudaErrorInvalidDevice;
-  // no more CTAs than items there can be: every sequence adds at most one unfilled item per head
+  // Every sequence adds at most one unfilled item per KV head.  Cutting pays when the items cannot fill
+  // the SMs and an item can have two pieces' tiles (a chunk of 50 tokens against 30 K keys: 437 us
+  // whole, 195 us cut; a prompt that fills the SMs loses 3 % to the joining code's registers).
   const long long tpi = 2ll * a.tok_per_tile, per = (long long)a.Hkv * a.head_chunks;
-  const long long most = (a.T / tpi + a.B) * per;
-  const int grid = (int)std::max(1ll, std::min<long long>(most, sms));
-  if (head_dim == 128)
-    return io32 ? launch_cap<128, true>(m, a, grid, stream) : launch_cap<128, false>(m, a, grid, stream);
-  return io32 ? launch_cap<64, true>(m, a, grid, stream) : launch_cap<64, false>(m, a, grid, stream);
+  const long long items = (a.T / tpi + a.B) * per;
+  long long reach = (long long)a.max_pages << a.log2_page;
+  if (a.W > 0 && !a.key_end) reach = std::min<long long>(reach, a.W + tpi + PM_KEYS);
+  const long long pieces = reach / (PM_KEYS * PM_PIECE_TILES);
+  const bool split = items < sms && pieces >= 2;
+  const int grid = (int)std::max(1ll, std::min<long long>(split ? items * pieces : items, sms));
+  return head_dim == 128 ? launch_d<128>(m, a, grid, split, stream) : launch_d<64>(m, a, grid, split, stream);
 }
 
 }  // namespace ink

@@ -274,3 +274,82 @@ def test_many_launches_of_a_long_prompt_agree_and_report_nothing(cuda_device):
                                                 prob.block_table, prob.seq_lens, out, ws, lse=lse, **opts)
         assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
     assert binding.inkling_attn_read_device_error(ws) == 0
+
+
+def test_long_stretches_of_tokens_that_see_nothing(cuda_device):
+    """Whole work items without a key between items with keys: padding inside packed rows, a sequence
+    whose lengths contradict, and sequences without new tokens."""
+    q_lens, seq_lens = [3000, 0, 900, 2500, 0], [3000, 7, 1000, 2600, 0]
+    prob = problem((4, 1), 64, 64, q_lens, seq_lens, 17, cuda_device)
+    prob.seq_lens[2] = 100   # 900 new tokens, 100 keys
+    p = np.concatenate([np.arange(b - a, b) for a, b in zip(q_lens, seq_lens)])
+    end = np.where((p % 1400) < 1300, 0, p + 1)
+    begin = np.maximum(p - 5, 0)
+    opts = options(prob, begin=begin, end=end)
+    out, lse, ws = call(prob, opts, False)
+    torch.cuda.synchronize()
+    assert binding.inkling_attn_read_device_error(ws) == binding.DEVERR_QLEN_EXCEEDS_KV
+    check(out, lse, reference(prob, opts), "stretches of nothing")
+
+
+SPLIT = [
+    # few new tokens against long histories: the key tiles of an item are cut into pieces
+    ((8, 1), 128, 64, [5, 40, 1], [6000, 9111, 700], -1, "cap"),
+    ((8, 2), 64, 16, [33, 2], [5000, 4097], -1, "slopes+documents"),
+    ((5, 1), 128, 128, [60], [8000], -1, "random"),
+    ((4, 4), 64, 64, [200, 1], [7000, 3], 2500, "cap_large+prefix"),
+    ((16, 1), 128, 8, [9], [3333], -1, "slopes+cap_small"),
+]
+
+
+@pytest.mark.parametrize("case", range(len(SPLIT)))
+def test_prefill_of_few_tokens_against_long_histories(cuda_device, case):
+    heads, dim, page, q_lens, seq_lens, window, kind = SPLIT[case]
+    prob = problem(heads, dim, page, q_lens, seq_lens, 400 + case, cuda_device, window, q_std=3.0 if "cap" in kind else 1.0)
+    opts = _opts(prob, kind, case, False)
+    out, lse, ws = call(prob, opts, False)
+    ref = reference(prob, opts)
+    check(out, lse, ref, f"case {case}")
+    again, lse2, _ = call(prob, opts, False, workspace=ws)
+    torch.cuda.synchronize()
+    assert binding.inkling_attn_read_device_error(ws) == 0
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
+def test_non_finite_values_in_one_piece_of_a_cut_item(cuda_device):
+    prob = problem((8, 1), 128, 64, [20], [6000], 18, cuda_device)
+    table = prob.block_table.cpu().numpy()
+    prob.v_cache[int(table[0, 5990 // 64]), :, 5990 % 64, 3] = float("-inf")
+    out, lse, ws = call(prob, options(prob), False)
+    torch.cuda.synchronize()
+    got = out.float().cpu().numpy()   # token i sits at 5980 + i
+    assert np.isfinite(got[:10]).all() and np.isneginf(got[10:, :, 3]).all()
+    assert np.isfinite(np.delete(got, 3, axis=2)).all() and np.isfinite(lse.cpu().numpy()).all()
+
+
+@pytest.mark.parametrize("decode", [False, True])
+def test_waits_that_run_out_report_a_timeout_and_later_calls_are_right(cuda_device, decode):
+    """A zero wait limit makes every wait for data that is not there yet give up.  A prefill workspace
+    then refuses further work, with the same error, until it is initialised again."""
+    seq_lens = [1500 + 97 * i for i in range(24)] if decode else [900, 5000]
+    prob = problem((8, 2), 128, 64, [1] * 24 if decode else [700, 20], seq_lens, 19, cuda_device)
+    opts = options(prob, softcap=20.0)
+    ws = binding.alloc_masked_workspace(binding.params_of(prob), decode, cuda_device)
+    try:
+        binding.inkling_attn_set_wait_limit_ns(0)
+        call(prob, opts, decode, workspace=ws)
+        torch.cuda.synchronize()
+        assert binding.inkling_attn_read_device_error(ws) & binding.DEVERR_WAIT_TIMEOUT
+    finally:
+        binding.inkling_attn_set_wait_limit_ns(2_000_000_000)
+    if not decode:
+        out, lse, _ = call(prob, opts, decode, workspace=ws)
+        torch.cuda.synchronize()
+        assert binding.inkling_attn_read_device_error(ws) == binding.DEVERR_WAIT_TIMEOUT
+        assert (out == 7.0).all() and (lse == 7.0).all()
+        binding.inkling_attn_workspace_init(ws)
+    for _ in range(2):
+        out, lse, _ = call(prob, opts, decode, workspace=ws)
+        torch.cuda.synchronize()
+        assert binding.inkling_attn_read_device_error(ws) == 0
+        check(out, lse, reference(prob, opts), "after a timeout")
