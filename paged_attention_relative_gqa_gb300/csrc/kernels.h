@@ -202,7 +202,7 @@ struct MaskedArgs {
   int32_t* tickets;            // prefill: [pieces, 2]
 };
 
-constexpr int MASKED_PIECES = 320;        // most pieces of cut items in one masked prefill
+constexpr int MASKED_PIECES = 480;        // most pieces of cut items in one masked prefill
 
 constexpr int MASKED_DECODE_CTAS = 320;   // most CTAs of a masked decode (bounds its partials)
 

@@ -28,8 +28,8 @@
 //       are zeroed, and so are rows with an infinity or NaN (0 * NaN would reach rows that do not
 //       see the key); rows that do see one get it back in the epilogue.
 // When there are fewer items than SMs (a chunk of a prompt or a few drafted tokens against a long
-// history), the key tiles of an item are cut into pieces of equal length, as many as make two rounds
-// over the SMs; a piece leaves O, maximum and sum in the workspace, and the last one to finish (an
+// history), the key tiles of an item are cut into pieces of one length, chosen on the device so that
+// the rounds over the SMs are full ones; a piece leaves O, maximum and sum in the workspace, and the last one to finish (an
 // atomic ticket, no waiting) joins them in order.
 // Every wait is bounded; after a timeout the CTA records it, stops issuing, waits for what is in
 // flight and exits.
@@ -73,7 +73,7 @@ struct PMItem {
   int lo_min, hi_max;        // keys any row sees lie in [lo_min, hi_max)
   int lo_max, hi_min;        // keys in [lo_max, hi_min) are seen by every row
   int kt0, nt, nh, bad_len;  // first key tile, tiles (-1: no more items), row tiles
-  int ticket, slot, np, one; // of a cut item: its number, its first place in the partials, its pieces, this one
+  int slot, np, one;         // of a cut item: its first place in the partials, its pieces, this one
 };
 
 template <int D>
@@ -348,7 +348,14 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
       const int per = a.Hkv * a.head_chunks, tpi = 2 * a.tok_per_tile;
       int cb = 0, base = 0, cnt = 0, incl = 0, total = 0;
       int my_c0 = 0, my_n = 0, my_len = 0;   // of this lane's sequence
-      auto load_chunk = [&]() {   // items of sequences cb + lane
+      int piece_tiles = INT_MAX, my_np = 1;  // tiles of a piece, pieces of an item of this lane's sequence
+      // most tiles of an item of a sequence of length len
+      auto tiles_of = [&](int len) {
+        int t = (max(len, 1) + PM_KEYS - 1) / PM_KEYS;
+        if (a.W > 0 && !a.key_end) t = min(t, (a.W + tpi) / PM_KEYS + 2);
+        return t;
+      };
+      auto load_chunk = [&]() {   // pieces of sequences cb + lane
         const int b = cb + lane;
         cnt = my_len = 0;
         if (b < a.B) {
@@ -360,6 +367,10 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
             if (blockIdx.x == 0) record_error(a.err, INK_DEVERR_BAD_ROWS);
           } else {
             cnt = (c1 - c0 + tpi - 1) / tpi * per;
+            if constexpr (SPLIT) {
+              my_np = piece_tiles == INT_MAX ? 1 : (tiles_of(my_len) + piece_tiles - 1) / piece_tiles;
+              cnt *= my_np;
+            }
           }
         }
         incl = cnt;
@@ -371,34 +382,51 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
         total = __shfl_sync(0xffffffffu, incl, 31);
       };
       load_chunk();
-      // pieces of an item: enough for two rounds over the SMs when the items alone do not fill one, of
-      // PM_PIECE_TILES tiles at least
-      int splits = 1;
       if constexpr (SPLIT) {
+        // Lane i tries pieces of 1 / (i + 1) of the longest item.  The cost in eighths of a tile: rounds
+        // over the SMs (with a sixteenth to spare: CTAs that join are late for their next piece) times
+        // the mean piece and 5 tiles for its partials, and the last join, 1.2 tiles per piece of an item.
         const uint32_t stale = *reinterpret_cast<volatile uint32_t*>(a.stale);
-        const int sms = (int)min(gridDim.x, (unsigned)MASKED_PIECES / 2);
-        int all = total, longest = my_len;
-        for (cb = 32; cb < a.B && all < sms; cb += 32) {
+        int longest = 0;
+        for (int c = 0;;) {
+          longest = max(longest, cnt > 0 ? tiles_of(my_len) : 0);
+          c += 32;
+          if (c >= a.B) break;
+          cb = c;
           load_chunk();
-          all += total;
-          longest = max(longest, my_len);
         }
         longest = __reduce_max_sync(0xffffffffu, longest);
-        if (a.W > 0 && !a.key_end) longest = min(longest, a.W + tpi + PM_KEYS);
-        if (all > 0) splits = max(1, min(2 * sms / all, longest / (PM_KEYS * PM_PIECE_TILES)));
-        if (cb > 32) {
-          cb = 0;
-          load_chunk();
+        const int mine = max(PM_PIECE_TILES, (longest + lane) / (lane + 1));
+        int pieces = 0;
+        long long tiles = 0;
+        for (int c = 0; c < a.B; c += 32) {
+          if (cb != c) {
+            cb = c;
+            load_chunk();
+          }
+          const int t = tiles_of(my_len);
+          for (int x = 0; x < min(32, a.B - c); ++x)
+          {
+            const int n = __shfl_sync(0xffffffffu, cnt, x), tx = __shfl_sync(0xffffffffu, t, x);
+            pieces += n * ((tx + mine - 1) / mine);
+            tiles += (long long)n * tx;
+          }
         }
+        const int sms = (int)gridDim.x;
+        const long long cost8 = (long long)((pieces + pieces / 16 + sms - 1) / sms) * (8 * tiles / max(pieces, 1) + 40) +
+                                10 * (longest / mine);
+        const uint32_t cost = pieces > MASKED_PIECES ? 0x7ffffffu : (uint32_t)min(cost8, 0x3ffffffll);
+        const uint32_t best = __reduce_min_sync(0xffffffffu, cost << 5 | (uint32_t)lane);
+        if ((best >> 5) != 0x7ffffffu) piece_tiles = __shfl_sync(0xffffffffu, mine, (int)(best & 31u));
         cb = stale ? a.B : 0;
+        if (cb < a.B) load_chunk();
         if (stale && lane == 0) record_error(a.err, INK_DEVERR_WAIT_TIMEOUT);   // left unusable by a timeout
       }
       int idx = blockIdx.x, qn0 = 0, qn1 = 0;
       for (int k = 0;;) {
         int next = 0;
         if (lane == 0) next = (int)atomicAdd(a.counters, 1u) + (int)gridDim.x;
-        const int item = SPLIT ? idx / splits : idx, one = SPLIT ? idx - item * splits : 0;
-        while (cb < a.B && item >= base + total) {
+        while (cb < a.B && idx >= base + total) {
           base += total;
           cb += 32;
           if (cb < a.B) load_chunk();
@@ -412,9 +440,15 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
           }
           break;
         }
-        const int src = __ffs(__ballot_sync(0xffffffffu, item < base + incl)) - 1;
-        const int li = item - base - __shfl_sync(0xffffffffu, incl - cnt, src);
-        const int nq = __shfl_sync(0xffffffffu, cnt, src) / per;
+        const int src = __ffs(__ballot_sync(0xffffffffu, idx < base + incl)) - 1;
+        int li = idx - base - __shfl_sync(0xffffffffu, incl - cnt, src);   // piece, then item of the sequence
+        int nq = __shfl_sync(0xffffffffu, cnt, src) / per, one = 0;
+        if constexpr (SPLIT) {
+          const int np = __shfl_sync(0xffffffffu, my_np, src);
+          one = li % np;
+          li /= np;
+          nq /= np;
+        }
         PMItem it;
         it.b = cb + src;
         const int qrev = li / per, r = li - qrev * per;
@@ -456,10 +490,9 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
         it.nt = it.hi_max > it.lo_min ? (it.hi_max - 1) / PM_KEYS - it.kt0 + 1 : 0;
         it.np = 1;
         if constexpr (SPLIT) {
-          const int len = max(PM_PIECE_TILES, (it.nt + splits - 1) / splits);
-          it.np = max(1, (it.nt + len - 1) / len);
-          it.ticket = item;
-          it.slot = item * splits;
+          it.np = max(1, (it.nt - 1) / piece_tiles + 1);
+          const int len = (it.nt + it.np - 1) / it.np;
+          it.slot = idx - one;
           it.one = one;
           if (it.np > 1) {
             it.kt0 += one * len;
@@ -765,7 +798,7 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
           tmem_ld32(tm_o + c2 * 32, ov);
           tmem_wait_ld();
 #pragma unroll
-          for (int x = 0; x < 8; ++x)
+          for (int x = 0; x < 8 && rv; ++x)
             __stcg(part_o + it.one * PART + (size_t)(c2 * 8 + x) * MASKED_ROWS,
                    make_float4(__uint_as_float(ov[4 * x]), __uint_as_float(ov[4 * x + 1]), __uint_as_float(ov[4 * x + 2]),
                                __uint_as_float(ov[4 * x + 3])));
@@ -779,10 +812,10 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
           int prev;
           asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;"
                        : "=r"(prev)
-                       : "l"(a.tickets + 2 * it.ticket + h)
+                       : "l"(a.tickets + 2 * it.slot + h)
                        : "memory");
           joins[h] = prev == it.np - 1;
-          if (prev == it.np - 1) a.tickets[2 * it.ticket + h] = 0;   // ready for the next call
+          if (prev == it.np - 1) a.tickets[2 * it.slot + h] = 0;   // ready for the next call
         }
         named_barrier_sync(1 + h, 128);
         if (!joins[h]) {
@@ -811,7 +844,7 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
           for (int x = 0; x < 32; ++x) acc[x] = 0.f;
           // (two pieces at a time: 17 loads in flight a thread)
 #pragma unroll 2
-          for (int y = 0; y < it.np; ++y) {
+          for (int y = 0; y < (rv ? it.np : 0); ++y) {
             const float my = __ldcg(part_ml + (size_t)y * 2 * MASKED_ROWS).x;
             float4 vv[8];
 #pragma unroll
@@ -912,8 +945,8 @@ cudaError_t launch_prefill_masked(const MaskedMaps& m, const MaskedArgs& a, int 
   const int sms = current_device_sms(&dev);
   if (sms <= 0) return cudaErrorInvalidDevice;
   // Every sequence adds at most one unfilled item per KV head.  Cutting pays when the items cannot fill
-  // the SMs and an item can have two pieces' tiles (a chunk of 50 tokens against 30 K keys: 437 us
-  // whole, 195 us cut; a prompt that fills the SMs loses 3 % to the joining code's registers).
+  // the SMs and an item can have two pieces' tiles (a chunk of 50 tokens against 30 K keys: 433 us
+  // whole, 200 us cut; a prompt that fills the SMs loses 3 % to the joining code's registers).
   const long long tpi = 2ll * a.tok_per_tile, per = (long long)a.Hkv * a.head_chunks;
   const long long items = (a.T / tpi + a.B) * per;
   long long reach = (long long)a.max_pages << a.log2_page;
