@@ -272,43 +272,32 @@ def inkling_attn_kv_conv_write(params, k_new, v_new, cu_q_lens, seq_lens, block_
     return k_cache, v_cache
 
 
-def _refuse(t, name, dtype, shape, device):
-    """Say what is wrong with a tensor that ``_arg`` did not take."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.get_device() != device:
-        raise ValueError(f"{name} is on {t.device}, q on cuda:{device}")
-    raise ValueError(f"{name} must be contiguous")
-
-
-def _arg(t, name, dtype, shape, device):
-    """Device pointer of a contiguous tensor of this dtype, shape (None: any) and device; None stays None.
-    (One pass of cheap checks: a decode step makes this call for a dozen tensors.)"""
-    if t is None:
-        return None
-    try:
-        if t.dtype is dtype and t.get_device() == device and (shape is None or t.shape == shape) and t.is_contiguous():
-            return t.data_ptr()
-    except AttributeError:
-        pass
-    _refuse(t, name, dtype, shape, device)
-
-
-def _need(**tensors):
-    """Required tensors are there; the device of the first one."""
-    for name, t in tensors.items():
+def _refuse(device, *args):
+    """Raise for the first (tensor, name, dtype, shape or None) that does not hold; a contiguous tensor of
+    that dtype, shape and device is asked for."""
+    for t, name, dtype, shape in args:
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
-    name, t = next(iter(tensors.items()))
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    return t.get_device()
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if shape is not None and tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        if t.get_device() != device:
+            raise ValueError(f"{name} is on {t.device}, others on cuda:{device}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+
+
+def _opt(t, name, dtype, shape, device):
+    """Device pointer of an optional tensor, checked; None stays None."""
+    if t is None:
+        return None
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == device and t.shape == shape
+            and t.is_contiguous()):
+        _refuse(device, (t, name, dtype, shape))
+    return t.data_ptr()
 
 
 # The current stream's handle without a Stream object around it (a few microseconds less per call).
@@ -342,55 +331,96 @@ def alloc_masked_workspace(params: ink_attn_params_t, is_decode: bool = True, de
     return ws
 
 
-def _masked_call(name, params, q, cu_q_lens, k_cache, v_cache, block_table, seq_lens, out, workspace, softcap, key_begin,
-                 key_end, slopes, lse, stream):
-    lib = load_library()
-    prefill = name == "inkling_attn_prefill_masked"
-    dev = _need(q=q, k_cache=k_cache, v_cache=v_cache, block_table=block_table, seq_lens=seq_lens, out=out,
-                workspace=workspace)
-    B, Hq, D = params.num_seqs, params.num_q_heads, params.head_dim
-    T = int(q.shape[0]) if prefill else B
-    bf, i32, rows = torch.bfloat16, torch.int32, (T, Hq, D)
-    pool = (params.num_pages, params.num_kv_heads, params.page_size, D)
-    mask = ink_attn_mask_t(softcap, _arg(key_begin, "key_begin", i32, (T,), dev), _arg(key_end, "key_end", i32, (T,), dev),
-                           _arg(slopes, "slopes", torch.float32, (Hq,), dev))
-    head = [ctypes.byref(params), ctypes.byref(mask), _arg(q, "q", bf, rows, dev)]
-    if prefill:
-        _need(cu_q_lens=cu_q_lens)
-        head += [_arg(cu_q_lens, "cu_q_lens", i32, (B + 1,), dev), T]
-    code = _launch(getattr(lib, name), dev, stream, *head, _arg(k_cache, "k_cache", bf, pool, dev),
-                   _arg(v_cache, "v_cache", bf, pool, dev),
-                   _arg(block_table, "block_table", i32, (B, params.max_pages_per_seq), dev),
-                   _arg(seq_lens, "seq_lens", i32, (B,), dev), _arg(out, "out", bf, rows, dev),
-                   _arg(lse, "lse", torch.float32, (T, Hq), dev),
-                   _arg(workspace, "workspace", torch.uint8, None, dev), workspace.numel())
-    _check(code, name)
-    return out
+_BF16, _I32, _F32, _U8 = torch.bfloat16, torch.int32, torch.float32, torch.uint8
+
+
+def _pools_hold(params, device, rows, q, out, k_cache, v_cache, block_table, seq_lens, workspace):
+    """The tensors that every call takes are what they have to be.  (One expression of cheap checks: a
+    serving step makes these calls for every layer, and each check costs a tenth of a microsecond.)"""
+    pool = (params.num_pages, params.num_kv_heads, params.page_size, params.head_dim)
+    B = params.num_seqs
+    try:
+        if (device >= 0 and out.dtype is _BF16 and k_cache.dtype is _BF16 and v_cache.dtype is _BF16
+                and block_table.dtype is _I32 and seq_lens.dtype is _I32 and workspace.dtype is _U8
+                and out.shape == rows and k_cache.shape == pool and v_cache.shape == pool and seq_lens.shape == (B,)
+                and block_table.shape == (B, params.max_pages_per_seq)
+                and out.get_device() == device and k_cache.get_device() == device and v_cache.get_device() == device
+                and block_table.get_device() == device and seq_lens.get_device() == device
+                and workspace.get_device() == device and out.is_contiguous() and k_cache.is_contiguous()
+                and v_cache.is_contiguous() and block_table.is_contiguous() and seq_lens.is_contiguous()
+                and workspace.is_contiguous()):
+            return
+    except AttributeError:
+        pass
+    _refuse(device, (q, "q", _BF16, None), (out, "out", _BF16, rows), (k_cache, "k_cache", _BF16, pool),
+            (v_cache, "v_cache", _BF16, pool), (block_table, "block_table", _I32, (B, params.max_pages_per_seq)),
+            (seq_lens, "seq_lens", _I32, (B,)), (workspace, "workspace", _U8, None))
+
+
+def _device_of(q) -> int:
+    if not isinstance(q, torch.Tensor):
+        raise TypeError("q must be a torch.Tensor")
+    device = q.get_device()
+    if device < 0:
+        raise ValueError("q must be a CUDA tensor")
+    return device
+
+
+def _mask_struct(softcap, key_begin, key_end, slopes, T, Hq, device) -> ink_attn_mask_t:
+    if key_begin is None and key_end is None and slopes is None:
+        return ink_attn_mask_t(softcap)
+    return ink_attn_mask_t(softcap, _opt(key_begin, "key_begin", _I32, (T,), device),
+                           _opt(key_end, "key_end", _I32, (T,), device), _opt(slopes, "slopes", _F32, (Hq,), device))
 
 
 def inkling_attn_prefill_masked(params, q, cu_q_lens, k_cache, v_cache, block_table, seq_lens, out, workspace, *,
                                 softcap: float = 0.0, key_begin=None, key_end=None, slopes=None, lse=None, stream=None):
     """Paged prefill with capped scores, a distance bias and a visible key range per token."""
-    return _masked_call("inkling_attn_prefill_masked", params, q, cu_q_lens, k_cache, v_cache, block_table, seq_lens, out,
-                        workspace, softcap, key_begin, key_end, slopes, lse, stream)
+    device = _device_of(q)
+    T, Hq = q.shape[0], params.num_q_heads
+    rows = (T, Hq, params.head_dim)
+    if q.dtype is not _BF16 or q.shape != rows or not q.is_contiguous():
+        _refuse(device, (q, "q", _BF16, rows))
+    _pools_hold(params, device, rows, q, out, k_cache, v_cache, block_table, seq_lens, workspace)
+    mask = _mask_struct(softcap, key_begin, key_end, slopes, T, Hq, device)
+    cu = _opt(cu_q_lens, "cu_q_lens", _I32, (params.num_seqs + 1,), device)
+    if cu is None:
+        _refuse(device, (cu_q_lens, "cu_q_lens", _I32, None))
+    code = _launch(load_library().inkling_attn_prefill_masked, device, stream, ctypes.byref(params), ctypes.byref(mask),
+                   q.data_ptr(), cu, T, k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
+                   seq_lens.data_ptr(), out.data_ptr(), _opt(lse, "lse", _F32, (T, Hq), device), workspace.data_ptr(),
+                   workspace.numel())
+    if code != INK_OK:
+        raise InkError(code, "inkling_attn_prefill_masked")
+    return out
 
 
 def inkling_attn_decode_masked(params, q, k_cache, v_cache, block_table, seq_lens, out, workspace, *,
                                softcap: float = 0.0, key_begin=None, key_end=None, slopes=None, lse=None, stream=None):
     """Paged decode with capped scores, a distance bias and a visible key range per sequence."""
-    return _masked_call("inkling_attn_decode_masked", params, q, None, k_cache, v_cache, block_table, seq_lens, out,
-                        workspace, softcap, key_begin, key_end, slopes, lse, stream)
+    device = _device_of(q)
+    B, Hq = params.num_seqs, params.num_q_heads
+    rows = (B, Hq, params.head_dim)
+    if q.dtype is not _BF16 or q.shape != rows or not q.is_contiguous():
+        _refuse(device, (q, "q", _BF16, rows))
+    _pools_hold(params, device, rows, q, out, k_cache, v_cache, block_table, seq_lens, workspace)
+    mask = _mask_struct(softcap, key_begin, key_end, slopes, B, Hq, device)
+    code = _launch(load_library().inkling_attn_decode_masked, device, stream, ctypes.byref(params), ctypes.byref(mask),
+                   q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
+                   out.data_ptr(), _opt(lse, "lse", _F32, (B, Hq), device), workspace.data_ptr(), workspace.numel())
+    if code != INK_OK:
+        raise InkError(code, "inkling_attn_decode_masked")
+    return out
 
 
-def _rows_arg(t, name, shape, device):
-    """Pointer and token stride of [T, H, D] rows whose heads are contiguous (a view of a fused projection)."""
-    if not (t.dtype is torch.bfloat16 and t.get_device() == device and t.shape == shape):
-        _refuse(t, name, torch.bfloat16, shape, device)
-    T, H, D = shape
-    st = t.stride()
-    if st[2] != 1 or (H > 1 and st[1] != D):
+def _token_stride(t, name, shape, device) -> int:
+    """Token stride of [T, H, D] rows whose heads are contiguous (a view of a fused projection)."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is _BF16 and t.get_device() == device and t.shape == shape):
+        _refuse(device, (t, name, _BF16, shape))
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (shape[1] > 1 and s1 != shape[2]):
         raise ValueError(f"{name}: the heads of a row must be contiguous")
-    return t.data_ptr(), (st[0] if T > 1 else H * D)
+    return s0 if shape[0] > 1 else shape[1] * shape[2]
 
 
 def inkling_attn_qk_norm_rope_write(params, q, k, v, cu_q_lens, seq_lens, block_table, q_out, k_cache, v_cache,
@@ -400,27 +430,26 @@ def inkling_attn_qk_norm_rope_write(params, q, k, v, cu_q_lens, seq_lens, block_
 
     ``q``, ``k`` and ``v`` may be views of one fused projection; ``inv_freq`` (see ``rotary.inv_freq``)
     has one frequency per rotated pair, None for no rotation."""
-    lib = load_library()
-    if layout not in ROPE_LAYOUTS:
+    pairing = ROPE_LAYOUTS.get(layout)
+    if pairing is None:
         raise ValueError(f"layout must be one of {sorted(ROPE_LAYOUTS)}, got {layout!r}")
-    dev = _need(q=q, k=k, v=v, cu_q_lens=cu_q_lens, seq_lens=seq_lens, block_table=block_table, q_out=q_out,
-                k_cache=k_cache, v_cache=v_cache, workspace=workspace)
-    B, Hq, Hkv, D = params.num_seqs, params.num_q_heads, params.num_kv_heads, params.head_dim
-    T = int(q.shape[0])
-    bf, i32, f32 = torch.bfloat16, torch.int32, torch.float32
-    pool = (params.num_pages, Hkv, params.page_size, D)
-    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
-    rope = ink_norm_rope_t(_arg(w_q, "w_q", f32, (D,), dev), _arg(w_k, "w_k", f32, (D,), dev), eps,
-                           _arg(inv_freq, "inv_freq", f32, (rot // 2,), dev), rot, ROPE_LAYOUTS[layout], rot_scale)
-    code = _launch(lib.inkling_attn_qk_norm_rope_write, dev, stream, ctypes.byref(params), ctypes.byref(rope),
-                   *_rows_arg(q, "q", (T, Hq, D), dev), *_rows_arg(k, "k", (T, Hkv, D), dev),
-                   *_rows_arg(v, "v", (T, Hkv, D), dev), _arg(cu_q_lens, "cu_q_lens", i32, (B + 1,), dev), T,
-                   _arg(seq_lens, "seq_lens", i32, (B,), dev),
-                   _arg(block_table, "block_table", i32, (B, params.max_pages_per_seq), dev),
-                   _arg(q_out, "q_out", bf, (T, Hq, D), dev), _arg(k_cache, "k_cache", bf, pool, dev),
-                   _arg(v_cache, "v_cache", bf, pool, dev), _arg(workspace, "workspace", torch.uint8, None, dev),
-                   workspace.numel())
-    _check(code, "inkling_attn_qk_norm_rope_write")
+    device = _device_of(q)
+    T, Hq, Hkv, D = q.shape[0], params.num_q_heads, params.num_kv_heads, params.head_dim
+    rows, kv_rows = (T, Hq, D), (T, Hkv, D)
+    strides = _token_stride(q, "q", rows, device), _token_stride(k, "k", kv_rows, device), _token_stride(v, "v", kv_rows, device)
+    _pools_hold(params, device, rows, q, q_out, k_cache, v_cache, block_table, seq_lens, workspace)
+    cu = _opt(cu_q_lens, "cu_q_lens", _I32, (params.num_seqs + 1,), device)
+    if cu is None:
+        _refuse(device, (cu_q_lens, "cu_q_lens", _I32, None))
+    pairs = 0 if inv_freq is None else inv_freq.numel()
+    rope = ink_norm_rope_t(_opt(w_q, "w_q", _F32, (D,), device), _opt(w_k, "w_k", _F32, (D,), device), eps,
+                           _opt(inv_freq, "inv_freq", _F32, (pairs,), device), 2 * pairs, pairing, rot_scale)
+    code = _launch(load_library().inkling_attn_qk_norm_rope_write, device, stream, ctypes.byref(params),
+                   ctypes.byref(rope), q.data_ptr(), strides[0], k.data_ptr(), strides[1], v.data_ptr(), strides[2], cu, T,
+                   seq_lens.data_ptr(), block_table.data_ptr(), q_out.data_ptr(), k_cache.data_ptr(),
+                   v_cache.data_ptr(), workspace.data_ptr(), workspace.numel())
+    if code != INK_OK:
+        raise InkError(code, "inkling_attn_qk_norm_rope_write")
     return q_out
 
 
