@@ -627,8 +627,9 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
     const bool scaled = CAP || a.slopes != nullptr || !(a.scale_log2 > 0.f);
     const float mul = scaled ? 1.f : a.scale_log2;
     // A score lies within the cap, so where 2^cap is far from overflow and underflow no maximum is
-    // needed: numerators are taken against 0.
-    const bool fixed = CAP && a.slopes == nullptr && a.cap_log2 <= FIXED_MAX_LOG2;
+    // needed: numerators are taken against 0.  (Not for an item of one tile: a row of one key has the
+    // numerator 1 against its maximum, which bf16 holds exactly.)
+    const bool bounded = CAP && a.slopes == nullptr && a.cap_log2 <= FIXED_MAX_LOG2;
     uint32_t sn = 0, on = 0;
     int g = 0;
     bool go = true;
@@ -636,6 +637,7 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
       // (read where it is needed, from shared memory: the tile loop has no registers to spare)
       const PMItem& it = items[k % PM_ITEMS];
       if (!pm_wait(&item_full[k % PM_ITEMS], (uint32_t)(k / PM_ITEMS) & 1u, abort_flag, a) || it.nt < 0) break;
+      const bool fixed = bounded && it.nt > 1;
       const int nt = it.nt, kt0 = it.kt0, lo_max = it.lo_max, hi_min = it.hi_min;
       if (h >= it.nh) {
         g += nt;

@@ -9,8 +9,9 @@
 //
 // Bytes bound it: every row is read once and written once.  A warp takes one token and runs over
 // its head rows, LPR = D / 8 lanes to a row (16 bytes a lane, 512 contiguous bytes a warp and
-// pass), NB passes loaded before the first is used.  The angles depend on the token and the lane's channels only, so a
-// warp takes their sine and cosine once and keeps them in registers over all heads.  A token's
+// pass), the next NB passes on their way while NB are worked on.  The angles depend on the token
+// alone: a warp takes the sine and cosine of each pair once (a pair a lane) and folds them and the
+// weights into two factors per channel, which stay in registers over all heads of q or k.  A token's
 // passes are cut over several warps when there are few tokens (decode).  In the half layout the
 // partner channels sit rot_dim / 16 lanes away and come by shuffle as raw bf16 (4 registers for
 // 8 channels), normed with the partner's weights.
@@ -27,7 +28,7 @@ namespace ink {
 namespace {
 
 constexpr int NR_THREADS = 256;
-constexpr int NB = 4;   // passes whose loads are in flight together
+constexpr int NR_BLOCKS = 3;   // blocks an SM has registers for
 
 __device__ __forceinline__ void unpack_bf16x8(const uint4 r, float (&f)[8]) {
   const uint32_t w[4] = {r.x, r.y, r.z, r.w};
@@ -78,9 +79,13 @@ __device__ __forceinline__ int find_seq_warp(const int32_t* cu_q, int B, int t, 
 
 // LAYOUT 0: no rotation, 1: halves, 2: interleaved
 template <int D, int LAYOUT>
-__global__ void __launch_bounds__(NR_THREADS) qk_norm_rope_kernel(const NormRopeArgs a) {
+__global__ void __launch_bounds__(NR_THREADS, NR_BLOCKS) qk_norm_rope_kernel(const NormRopeArgs a) {
   constexpr int LPR = D / 8;          // lanes per row
   constexpr int RPP = 32 / LPR;       // rows per pass
+  // Passes loaded together, the next as many on their way.  Four, but two where the rotation of halves
+  // needs the registers (20,000 tokens of 16 + 2 x 2 heads of 64: 43 against 36 us; norm alone, 34,500
+  // tokens of 64 + 2 x 8 heads of 128: 211 against 229 us).
+  constexpr int NB = LAYOUT == 1 ? 2 : 4;
   const int lane = threadIdx.x & 31;
   const long long gw = (long long)blockIdx.x * (NR_THREADS / 32) + (threadIdx.x >> 5);
   const int t = (int)(gw / a.nchunks);
@@ -89,6 +94,32 @@ __global__ void __launch_bounds__(NR_THREADS) qk_norm_rope_kernel(const NormRope
   const int pass1 = min(pass0 + a.chunk, a.passes);
   const int lr = lane % LPR, rip = lane / LPR;
   const int d = lr * 8;
+
+  uint4 ahead[NB];   // the next batch of passes
+  // passes q .. q + NB - 1 of section sec, up to its pass `end`
+  auto load = [&](int sec, int q, int end) {
+    const uint16_t* src = a.x[sec] + (size_t)t * a.x_stride[sec] + d;
+#pragma unroll
+    for (int k = 0; k < NB; ++k) {
+      const int h = (q + k) * RPP + rip;
+      ahead[k] = make_uint4(0, 0, 0, 0);
+      if (q + k < end && h < a.H[sec]) ahead[k] = *reinterpret_cast<const uint4*>(src + (size_t)h * D);
+    }
+  };
+  // this warp's passes of section sec
+  auto span = [&](int sec, int& q0, int& q1) {
+    const int nq = (a.H[0] + RPP - 1) / RPP, nkv = (a.H[1] + RPP - 1) / RPP;
+    const int base = sec == 0 ? 0 : sec == 1 ? nq : nq + nkv;
+    q0 = max(pass0 - base, 0);
+    q1 = min(pass1 - base, sec == 0 ? nq : nkv);
+  };
+  // the first rows need nothing but the token: they are on their way while its request is looked up
+  int first = 0;
+  {
+    int q0, q1;
+    for (span(0, q0, q1); q0 >= q1; span(++first, q0, q1)) {}
+    load(first, q0, q1);
+  }
 
   const int b = find_seq_warp(a.cu_q, a.B, t, lane);
   if (b < 0) return;                  // a row of no request
@@ -102,34 +133,26 @@ __global__ void __launch_bounds__(NR_THREADS) qk_norm_rope_kernel(const NormRope
 
   const int hl = a.rot_dim >> 4;      // halves: lanes of half the rotated channels
   const bool turned = LAYOUT != 0 && d < a.rot_dim;
-  float cs[LAYOUT == 1 ? 8 : 4], sn[LAYOUT == 1 ? 8 : 4];
-  if constexpr (LAYOUT == 1) {
-    const int f0 = (lr < hl ? lr : lr - hl) * 8;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      cs[e] = 1.f;
-      sn[e] = 0.f;
-      if (turned) turn(p, __ldg(a.inv_freq + f0 + e), a.rot_scale, cs[e], sn[e]);
-      if (lr < hl) sn[e] = -sn[e];    // first half: a cos - b sin; second: b cos + a sin
+  // cos and sin of every pair, each taken by one lane, in shared memory until a section needs them
+  __shared__ float2 turns[LAYOUT != 0 ? NR_THREADS / 32 : 1][LAYOUT != 0 ? D / 2 : 1];
+  float2* mine = turns[LAYOUT != 0 ? threadIdx.x >> 5 : 0];
+  if constexpr (LAYOUT != 0) {
+    for (int f = lane; f < a.rot_dim / 2; f += 32) {
+      float c, sn;
+      turn(p, __ldg(a.inv_freq + f), a.rot_scale, c, sn);
+      mine[f] = make_float2(c, sn);
     }
-  } else if constexpr (LAYOUT == 2) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      cs[e] = 1.f;
-      sn[e] = 0.f;
-      if (turned) turn(p, __ldg(a.inv_freq + lr * 4 + e), a.rot_scale, cs[e], sn[e]);
-    }
+    __syncwarp();
   }
   const int partner = LAYOUT == 1 && turned ? (lr < hl ? lr + hl : lr - hl) : lr;
 
-  int base = 0;                       // first pass of the section
 #pragma unroll 1
-  for (int sec = 0; sec < 3; ++sec) {
+  for (int sec = first; sec < 3; ++sec) {
     const int H = a.H[sec];
-    const int np = (H + RPP - 1) / RPP;
-    const int q0 = max(pass0 - base, 0), q1 = min(pass1 - base, np);
-    base += np;
+    int q0, q1;
+    span(sec, q0, q1);
     if (q0 >= q1) continue;
+    if (sec != first) load(sec, q0, q1);
     uint16_t* dst;                    // row h goes to dst + h * step
     long long step;
     if (sec == 0) {
@@ -145,31 +168,41 @@ __global__ void __launch_bounds__(NR_THREADS) qk_norm_rope_kernel(const NormRope
       step = (long long)D << a.log2_page;
       dst = a.cache[sec - 1] + (size_t)page * H * step + (size_t)(p & ((1 << a.log2_page) - 1)) * D;
     }
-    const uint16_t* src = a.x[sec] + (size_t)t * a.x_stride[sec];
     const float* wsrc = sec < 2 ? a.w[sec] : nullptr;
-    float w[8], wp[8];
+    // y = r (x A + x' B) with the mean square's r, the pair's other channel x' and
+    //   halves: A = w cos, B = w' (-+ sin);  interleaved: the same with x' in the same lane
+    float A[8], B[LAYOUT != 0 ? 8 : 1];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) w[e] = wp[e] = 1.f;
+    for (int e = 0; e < 8; ++e) A[e] = 1.f;
     if (wsrc) {
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const float4 f = __ldg(reinterpret_cast<const float4*>(wsrc + d) + x);
-        w[4 * x] = f.x; w[4 * x + 1] = f.y; w[4 * x + 2] = f.z; w[4 * x + 3] = f.w;
-        if constexpr (LAYOUT == 1) {
-          const float4 g = __ldg(reinterpret_cast<const float4*>(wsrc + partner * 8) + x);
-          wp[4 * x] = g.x; wp[4 * x + 1] = g.y; wp[4 * x + 2] = g.z; wp[4 * x + 3] = g.w;
+        A[4 * x] = f.x; A[4 * x + 1] = f.y; A[4 * x + 2] = f.z; A[4 * x + 3] = f.w;
+      }
+    }
+    if (LAYOUT != 0 && turned && sec < 2) {
+#pragma unroll
+      for (int e = 0; e < (LAYOUT == 1 ? 8 : 4); ++e) {
+        if constexpr (LAYOUT == 1) {   // first half: a cos - b sin; second: b cos + a sin
+          const float2 t2 = mine[(lr < hl ? lr : lr - hl) * 8 + e];
+          B[e] = (wsrc ? __ldg(wsrc + partner * 8 + e) : 1.f) * (lr < hl ? -t2.y : t2.y);
+          A[e] *= t2.x;
+        } else if constexpr (LAYOUT == 2) {
+          const float2 t2 = mine[lr * 4 + e];
+          B[2 * e] = -A[2 * e + 1] * t2.y;
+          B[2 * e + 1] = A[2 * e] * t2.y;
+          A[2 * e] *= t2.x;
+          A[2 * e + 1] *= t2.x;
         }
       }
     }
+    uint4 raw[NB];
 #pragma unroll 1
     for (int q = q0; q < q1; q += NB) {
-      uint4 raw[NB];
 #pragma unroll
-      for (int k = 0; k < NB; ++k) {
-        const int h = (q + k) * RPP + rip;
-        raw[k] = make_uint4(0, 0, 0, 0);
-        if (q + k < q1 && h < H) raw[k] = *reinterpret_cast<const uint4*>(src + (size_t)h * D + d);
-      }
+      for (int k = 0; k < NB; ++k) raw[k] = ahead[k];
+      if (q + NB < q1) load(sec, q + NB, q1);
 #pragma unroll
       for (int k = 0; k < NB; ++k) {
         if (q + k >= q1) break;       // the same for the whole warp
@@ -187,8 +220,6 @@ __global__ void __launch_bounds__(NR_THREADS) qk_norm_rope_kernel(const NormRope
             for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
             r = rsqrtf(fmaf(ss, 1.f / D, a.eps));
           }
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = x[e] * r * w[e];
           if constexpr (LAYOUT == 1) {
             const int from = rip * LPR + partner;
             uint4 other;
@@ -199,19 +230,13 @@ __global__ void __launch_bounds__(NR_THREADS) qk_norm_rope_kernel(const NormRope
             float z[8];
             unpack_bf16x8(other, z);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              z[e] = z[e] * r * wp[e];
-              y[e] = turned ? fmaf(z[e], sn[e], x[e] * cs[e]) : x[e];
-            }
+            for (int e = 0; e < 8; ++e) y[e] = r * (turned ? fmaf(z[e], B[e], x[e] * A[e]) : x[e] * A[e]);
           } else if constexpr (LAYOUT == 2) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              y[2 * e] = turned ? fmaf(-x[2 * e + 1], sn[e], x[2 * e] * cs[e]) : x[2 * e];
-              y[2 * e + 1] = turned ? fmaf(x[2 * e], sn[e], x[2 * e + 1] * cs[e]) : x[2 * e + 1];
-            }
+            for (int e = 0; e < 8; ++e) y[e] = r * (turned ? fmaf(x[e ^ 1], B[e], x[e] * A[e]) : x[e] * A[e]);
           } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = x[e];
+            for (int e = 0; e < 8; ++e) y[e] = r * (x[e] * A[e]);
           }
           res = make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
         }
