@@ -300,20 +300,11 @@ def _opt(t, name, dtype, shape, device):
     return t.data_ptr()
 
 
-# The current stream's handle without a Stream object around it (a few microseconds less per call).
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
-def _launch(fn, device, stream, *args):
-    """fn(*args, stream) with `device` current; None means that device's current stream."""
-    if stream is None:
-        handle = _raw_stream(device) if _raw_stream is not None else torch.cuda.current_stream(device).cuda_stream
-    else:
-        handle = _stream_handle(stream)
-    if torch.cuda.current_device() == device:
-        return fn(*args, handle)
-    with torch.cuda.device(device):
-        return fn(*args, handle)
+# The current stream's handle without a Stream object around it, and the current device without the
+# lazy-initialisation check (a few microseconds less per call); a tensor on the device is there already.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def inkling_attn_masked_workspace_bytes(params: ink_attn_params_t, is_decode: bool) -> int:
@@ -386,10 +377,15 @@ def inkling_attn_prefill_masked(params, q, cu_q_lens, k_cache, v_cache, block_ta
     cu = _opt(cu_q_lens, "cu_q_lens", _I32, (params.num_seqs + 1,), device)
     if cu is None:
         _refuse(device, (cu_q_lens, "cu_q_lens", _I32, None))
-    code = _launch(load_library().inkling_attn_prefill_masked, device, stream, ctypes.byref(params), ctypes.byref(mask),
-                   q.data_ptr(), cu, T, k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
-                   seq_lens.data_ptr(), out.data_ptr(), _opt(lse, "lse", _F32, (T, Hq), device), workspace.data_ptr(),
-                   workspace.numel())
+    args = (ctypes.byref(params), ctypes.byref(mask), q.data_ptr(), cu, T, k_cache.data_ptr(), v_cache.data_ptr(),
+            block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(), _opt(lse, "lse", _F32, (T, Hq), device),
+            workspace.data_ptr(), workspace.numel(), _raw_stream(device) if stream is None else _stream_handle(stream))
+    fn = (_lib or load_library()).inkling_attn_prefill_masked
+    if _current_device() == device:
+        code = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            code = fn(*args)
     if code != INK_OK:
         raise InkError(code, "inkling_attn_prefill_masked")
     return out
@@ -405,9 +401,15 @@ def inkling_attn_decode_masked(params, q, k_cache, v_cache, block_table, seq_len
         _refuse(device, (q, "q", _BF16, rows))
     _pools_hold(params, device, rows, q, out, k_cache, v_cache, block_table, seq_lens, workspace)
     mask = _mask_struct(softcap, key_begin, key_end, slopes, B, Hq, device)
-    code = _launch(load_library().inkling_attn_decode_masked, device, stream, ctypes.byref(params), ctypes.byref(mask),
-                   q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
-                   out.data_ptr(), _opt(lse, "lse", _F32, (B, Hq), device), workspace.data_ptr(), workspace.numel())
+    args = (ctypes.byref(params), ctypes.byref(mask), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+            block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(), _opt(lse, "lse", _F32, (B, Hq), device),
+            workspace.data_ptr(), workspace.numel(), _raw_stream(device) if stream is None else _stream_handle(stream))
+    fn = (_lib or load_library()).inkling_attn_decode_masked
+    if _current_device() == device:
+        code = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            code = fn(*args)
     if code != INK_OK:
         raise InkError(code, "inkling_attn_decode_masked")
     return out
@@ -444,10 +446,16 @@ def inkling_attn_qk_norm_rope_write(params, q, k, v, cu_q_lens, seq_lens, block_
     pairs = 0 if inv_freq is None else inv_freq.numel()
     rope = ink_norm_rope_t(_opt(w_q, "w_q", _F32, (D,), device), _opt(w_k, "w_k", _F32, (D,), device), eps,
                            _opt(inv_freq, "inv_freq", _F32, (pairs,), device), 2 * pairs, pairing, rot_scale)
-    code = _launch(load_library().inkling_attn_qk_norm_rope_write, device, stream, ctypes.byref(params),
-                   ctypes.byref(rope), q.data_ptr(), strides[0], k.data_ptr(), strides[1], v.data_ptr(), strides[2], cu, T,
-                   seq_lens.data_ptr(), block_table.data_ptr(), q_out.data_ptr(), k_cache.data_ptr(),
-                   v_cache.data_ptr(), workspace.data_ptr(), workspace.numel())
+    args = (ctypes.byref(params), ctypes.byref(rope), q.data_ptr(), strides[0], k.data_ptr(), strides[1],
+            v.data_ptr(), strides[2], cu, T, seq_lens.data_ptr(), block_table.data_ptr(), q_out.data_ptr(),
+            k_cache.data_ptr(), v_cache.data_ptr(), workspace.data_ptr(), workspace.numel(), _raw_stream(device) if stream
+            is None else _stream_handle(stream))
+    fn = (_lib or load_library()).inkling_attn_qk_norm_rope_write
+    if _current_device() == device:
+        code = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            code = fn(*args)
     if code != INK_OK:
         raise InkError(code, "inkling_attn_qk_norm_rope_write")
     return q_out
