@@ -571,7 +571,7 @@ cudaError_t launch_t(const DecodeMaps& m, const MaskedArgs& a, int sms, cudaStre
   cudaError_t e = smem_opt_in_once(decode_masked_kernel<D, NSTAGE, HB, CAP>, (int)smem, opted);
   if (e != cudaSuccess) return e;
   long long keys = (long long)a.max_pages << a.log2_page;
-  if (a.W > 0 && !a.key_end) keys = std::min<long long>(keys, a.W + TILE_KEYS);
+  if (a.W > 0 && !a.key_end) keys = std::min(keys, (long long)a.W + TILE_KEYS);
   const long long most = ((keys + TILE_KEYS - 1) / TILE_KEYS + 1) * a.B * a.Hkv * a.head_chunks;
   const int grid = (int)std::min<long long>(std::min<long long>(ctas * sms, MASKED_DECODE_CTAS), most);
   decode_masked_kernel<D, NSTAGE, HB, CAP><<<grid, DM_THREADS, smem, stream>>>(m, a);

@@ -351,8 +351,9 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
       int piece_tiles = INT_MAX, my_np = 1;  // tiles of a piece, pieces of an item of this lane's sequence
       // most tiles of an item of a sequence of length len
       auto tiles_of = [&](int len) {
-        int t = (max(len, 1) + PM_KEYS - 1) / PM_KEYS;
-        if (a.W > 0 && !a.key_end) t = min(t, (a.W + tpi) / PM_KEYS + 2);
+        const long long keys = min(max((long long)len, 1ll), (long long)a.max_pages << a.log2_page);
+        int t = (int)((keys + PM_KEYS - 1) / PM_KEYS);
+        if (a.W > 0 && !a.key_end) t = min(t, (int)(((uint32_t)a.W + tpi) / PM_KEYS) + 2);
         return t;
       };
       auto load_chunk = [&]() {   // pieces of sequences cb + lane

@@ -353,3 +353,32 @@ def test_waits_that_run_out_report_a_timeout_and_later_calls_are_right(cuda_devi
         torch.cuda.synchronize()
         assert binding.inkling_attn_read_device_error(ws) == 0
         check(out, lse, reference(prob, opts), "after a timeout")
+
+
+@pytest.mark.parametrize("decode", [False, True])
+@pytest.mark.parametrize("window", [2**31 - 1, 2**31 - 200, 1 << 30])
+def test_windows_beyond_every_history_are_no_windows(cuda_device, decode, window):
+    """Few rows against long histories, whose pieces are counted from the window and the lengths."""
+    prob = problem((8, 1), 128, 64, [1, 1] if decode else [5, 40], [6000, 9111], 20, cuda_device)
+    opts = options(prob)
+    want, want_lse, _ = call(prob, opts, decode)
+    prob.window = window
+    out, lse, ws = call(prob, opts, decode)
+    torch.cuda.synchronize()
+    assert binding.inkling_attn_read_device_error(ws) == 0
+    check(out, lse, reference(prob, opts), "window beyond the history")
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+@pytest.mark.parametrize("tokens,keys", [(20, 6016), (600, 640)])
+@pytest.mark.parametrize("length", [2**31 - 1, 2**31 - 100, 1 << 20])
+def test_a_length_past_the_block_table_is_reported(cuda_device, tokens, keys, length):
+    """Keys end with the table; the rows' positions are those of the length."""
+    prob = problem((8, 1), 128, 64, [tokens], [keys], 21, cuda_device, max_pages=keys // 64)
+    opts = options(prob, end=np.full(tokens, keys))
+    want = reference(prob, opts)
+    prob.seq_lens[0] = length
+    out, lse, ws = call(prob, options(prob), False)
+    torch.cuda.synchronize()
+    assert binding.inkling_attn_read_device_error(ws) == binding.DEVERR_PAGE_OUT_OF_RANGE
+    check(out, lse, want, "length past the table")
