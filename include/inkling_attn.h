@@ -277,10 +277,13 @@ typedef struct {
 } ink_attn_mask_t;
 
 /*
- * Bytes of device workspace a masked attention call (or, with is_decode == 0,
- * inkling_attn_qk_norm_rope_write) needs; initialise it once with
- * inkling_attn_workspace_init.  Returns 0 if the parameters are invalid.  It does not depend on
- * the lengths.  Calls that share a workspace must not overlap on the GPU.
+ * Bytes of device workspace a masked attention call needs; initialise it once with
+ * inkling_attn_workspace_init.  Returns 0 if the parameters are invalid.  It depends on the head
+ * counts and head_dim only (about 65 MB for a prefill at D = 128, 3 to 6 MB for a decode), and one workspace
+ * of the largest size serves masked prefills and decodes of any sizes, one after the other; the
+ * other entry points' workspaces are laid out differently.  Calls that share a workspace must not
+ * overlap on the GPU.  After INK_DEVERR_WAIT_TIMEOUT initialise it again: until then a prefill of
+ * few rows against long histories does nothing but report the timeout.
  */
 size_t inkling_attn_masked_workspace_bytes(const ink_attn_params_t* params, int is_decode);
 
@@ -290,8 +293,8 @@ size_t inkling_attn_masked_workspace_bytes(const ink_attn_params_t* params, int 
  * and k (inkling_attn_qk_norm_rope_write) or from the distance bias.
  *   q, cu_q_lens, k_cache, v_cache, block_table, seq_lens, out: as for inkling_attn_prefill,
  *              except that there is no max_q_len; out must not overlap q
- *   total_q    rows of q and out; rows from cu_q_lens[B] on belong to no sequence and are
- *              neither read nor written
+ *   total_q    rows of q and out; rows from cu_q_lens[B] on belong to no sequence: they are not
+ *              written, and what they hold changes nothing
  *   lse        device, fp32 [total_q, Hq], or NULL: log of the sum of exp(s_k) over the visible
  *              keys (natural units), with which outputs over parts of a history are joined
  *   workspace  device, >= inkling_attn_masked_workspace_bytes(params, 0), initialised once
@@ -353,7 +356,7 @@ typedef struct {
  *   q_out         device, bf16 [total_q, Hq, D]; may be q itself when q_stride == Hq * D
  *   k_cache, v_cache  device, bf16 [num_pages, Hkv, P, D]; only the slots of the step's
  *                 positions are written; must not overlap q, k or v
- *   workspace     device, >= inkling_attn_masked_workspace_bytes(params, 0) (error word)
+ *   workspace     device, initialised, of any entry point's size; only its error word is used
  * Rows from cu_q_lens[B] on belong to no request and are left as they were.  A request with
  * n_b > L_b (INK_DEVERR_QLEN_EXCEEDS_KV) has its rows skipped; a page id outside [0, num_pages)
  * (INK_DEVERR_PAGE_OUT_OF_RANGE) has the K/V rows of its keys skipped.  Two rows that name the

@@ -532,28 +532,22 @@ ink_status_t inkling_attn_kv_conv_write(const ink_attn_params_t* params, const v
 namespace {
 
 struct MaskedLayout {
-  size_t tickets_off, part_o_off, part_ml_off, total;
+  size_t prefill_tickets, decode_tickets, part_o_off, part_ml_off, total;
 };
 
-MaskedLayout masked_decode_layout(const ink_attn_params_t* p) {
+// Header, the tickets of both kinds (what has to be zero between calls, at the same place for every
+// shape), then partials, which carry nothing from one call to the next: one workspace serves prefills
+// and decodes of any sizes in turn.
+MaskedLayout masked_layout(const ink_attn_params_t* p, bool decode) {
   MaskedLayout l;
-  const size_t B = (size_t)(p->num_seqs > 0 ? p->num_seqs : 1);
-  const size_t G = (size_t)(p->num_q_heads / p->num_kv_heads), rows = G <= 8 ? 8 : 16;
-  const size_t places = 2 * (size_t)ink::MASKED_DECODE_CTAS * rows;
-  l.tickets_off = kHeaderBytes;
-  l.part_o_off = align_up(l.tickets_off + B * p->num_kv_heads * ((G + 15) / 16) * sizeof(int32_t), 256);
-  l.part_ml_off = l.part_o_off + places * p->head_dim * sizeof(float);
-  l.total = align_up(l.part_ml_off + places * 2 * sizeof(float), 256);
-  return l;
-}
-
-MaskedLayout masked_prefill_layout(const ink_attn_params_t* p) {
-  MaskedLayout l;
-  const size_t rows = (size_t)ink::MASKED_PIECES * 2 * ink::MASKED_ROWS;
-  l.tickets_off = kHeaderBytes;
-  l.part_o_off = align_up(l.tickets_off + (size_t)ink::MASKED_PIECES * 2 * sizeof(int32_t), 256);
+  const size_t G = (size_t)(p->num_q_heads / p->num_kv_heads);
+  const size_t rows = decode ? 2 * (size_t)ink::MASKED_DECODE_CTAS * (G <= 8 ? 8 : 16)
+                             : 2 * (size_t)ink::MASKED_PIECES * ink::MASKED_ROWS;
+  l.prefill_tickets = kHeaderBytes;
+  l.decode_tickets = l.prefill_tickets + 2 * ink::MASKED_PIECES * sizeof(int32_t);
+  l.part_o_off = align_up(l.decode_tickets + ink::MASKED_DECODE_CTAS * sizeof(int32_t), 256);
   l.part_ml_off = l.part_o_off + rows * p->head_dim * sizeof(float);
-  l.total = l.part_ml_off + rows * 4 * sizeof(float);
+  l.total = align_up(l.part_ml_off + rows * (decode ? 2 : 4) * sizeof(float), 256);
   return l;
 }
 
@@ -633,9 +627,9 @@ ink_status_t masked_impl(const ink_attn_params_t* params, const ink_attn_mask_t*
   a.head_chunks = (a.G + ink::MASKED_ROWS - 1) / ink::MASKED_ROWS;
   a.heads_per_tile = (a.G + a.head_chunks - 1) / a.head_chunks;
   a.tok_per_tile = ink::MASKED_ROWS / a.heads_per_tile;
-  const MaskedLayout lay = decode ? masked_decode_layout(params) : masked_prefill_layout(params);
+  const MaskedLayout lay = masked_layout(params, decode);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  a.tickets = reinterpret_cast<int32_t*>(ws + lay.tickets_off);
+  a.tickets = reinterpret_cast<int32_t*>(ws + (decode ? lay.decode_tickets : lay.prefill_tickets));
   a.part_o = reinterpret_cast<float*>(ws + lay.part_o_off);
   a.part_ml = reinterpret_cast<float*>(ws + lay.part_ml_off);
   a.io32 = aligned(out, 32) ? 1 : 0;
@@ -661,7 +655,7 @@ extern "C" {
 
 size_t inkling_attn_masked_workspace_bytes(const ink_attn_params_t* params, int is_decode) {
   if (validate(params) != INK_OK) return 0;
-  return (is_decode ? masked_decode_layout(params) : masked_prefill_layout(params)).total;
+  return masked_layout(params, is_decode != 0).total;
 }
 
 ink_status_t inkling_attn_prefill_masked(const ink_attn_params_t* params, const ink_attn_mask_t* mask,

@@ -57,7 +57,6 @@ struct DMSmem {
 struct Piece {
   int b, kvh, h0, nh, L, lo, hi;
   int tile, n;            // first tile (absolute), tiles
-  int group;              // (b * Hkv + kvh) * head_chunks + chunk
   int c0, parts;          // first CTA of the group, CTAs
 };
 
@@ -123,7 +122,6 @@ struct Walk {
     const int c = gi - w.kvh * a.head_chunks;
     w.h0 = w.kvh * a.G + c * DM_QROWS;
     w.nh = min(DM_QROWS, a.G - c * DM_QROWS);
-    w.group = w.b * per + gi;
     const long long g0 = pos - x0;
     w.c0 = (int)(g0 / chunk);
     w.parts = (int)((g0 + T - 1) / chunk) - w.c0 + 1;
@@ -139,8 +137,9 @@ __device__ __forceinline__ bool dm_wait(uint64_t* bar, uint32_t parity, volatile
   return false;
 }
 
-// The piece's partial is in the workspace: take the group's ticket; the last of its pieces joins
-// all of them, in order, and resets the ticket.  Every thread's partial stores come before the
+// The piece's partial is in the workspace: take the group's ticket (a CTA's run is the start of one cut
+// group at most, so it goes by the first CTA); the last of its pieces joins all of them, in order, and
+// resets the ticket.  Every thread's partial stores come before the
 // barrier, the ticket's add releases them and acquires the others'.
 template <int D, int HB>
 __device__ __noinline__ void join_pieces(const float* part_o, const float* part_ml, int32_t* ticket, __nv_bfloat16* out,
@@ -556,7 +555,7 @@ decode_masked_kernel(const __grid_constant__ DecodeMaps maps, const __grid_const
         *reinterpret_cast<float4*>(a.part_o + (place * HB + r) * D + d) = acc;
     }
     if (!single)
-      join_pieces<D, HB>(a.part_o, a.part_ml, a.tickets + w.group, out + rowbase * D, a.lse ? a.lse + rowbase : nullptr,
+      join_pieces<D, HB>(a.part_o, a.part_ml, a.tickets + w.c0, out + rowbase * D, a.lse ? a.lse + rowbase : nullptr,
                          w.nh, w.c0, w.parts, tid, flags, head_ml);
     named_barrier_sync(1, DM_WARPS * 32);   // red, obuf, head_ml and flags are reused
   }

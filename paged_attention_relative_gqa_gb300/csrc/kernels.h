@@ -195,8 +195,8 @@ struct MaskedArgs {
   int io32;                    // out 32-byte aligned: its rows are stored 32 bytes at a time
   uint32_t* stale;             // nonzero after a timeout of a prefill, until the workspace is initialised again
   uint32_t* counters;          // [0] items handed out, [1] CTAs done; zero between calls
-  // decode: partials of cut groups, two places per CTA of `rows` heads (8 or 16), and a ticket
-  // per (sequence, KV head, chunk of 16 query heads), zero between calls
+  // decode: partials of cut groups, two places per CTA of `rows` heads (8 or 16), and a ticket per
+  // CTA, for the group cut at its end; zero between calls
   float* part_o;               // [2 * CTAs, rows, D]; prefill: [pieces, 2, D / 4, 128 rows] float4
   float* part_ml;              // [2 * CTAs, rows, 2] (running max in log2 units, sum); prefill: [pieces, 2, 128 rows] float4
   int32_t* tickets;            // prefill: [pieces, 2]

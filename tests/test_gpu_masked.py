@@ -382,3 +382,26 @@ def test_a_length_past_the_block_table_is_reported(cuda_device, tokens, keys, le
     torch.cuda.synchronize()
     assert binding.inkling_attn_read_device_error(ws) == binding.DEVERR_PAGE_OUT_OF_RANGE
     check(out, lse, want, "length past the table")
+
+
+def test_one_workspace_serves_prefills_and_decodes_of_any_sizes(cuda_device):
+    """Initialised once, then used in turn by calls of other batch sizes, head counts and kinds."""
+    def make(decode, heads, dim, q_lens, seq_lens, seed):
+        prob = problem(heads, dim, 64, q_lens, seq_lens, seed, cuda_device)
+        opts = options(prob, softcap=40.0)
+        return decode, prob, opts, reference(prob, opts)
+
+    wide = [300 + 31 * i for i in range(96)]
+    jobs = [make(True, (64, 8), 64, [1] * 96, wide, 25), make(False, (8, 1), 128, [30], [6000], 26),
+            make(True, (8, 1), 128, [1, 1], [9000, 7], 27), make(True, (32, 1), 128, [1] * 5, [4000] * 5, 28),
+            make(False, (8, 2), 64, [3, 20], [5000, 4000], 29)]
+    sizes = [binding.inkling_attn_masked_workspace_bytes(binding.params_of(j[1]), j[0]) for j in jobs]
+    ws = torch.empty(max(sizes), dtype=torch.uint8, device=cuda_device)
+    ws.fill_(0x5A)
+    binding.inkling_attn_workspace_init(ws)
+    for order in ((0, 1, 2, 3, 4), (4, 0, 3, 1, 0, 2, 0)):
+        for i in order:
+            decode, prob, opts, ref = jobs[i]
+            out, lse, _ = call(prob, opts, decode, workspace=ws)
+            check(out, lse, ref, f"call {i} of {order}")
+    assert binding.inkling_attn_read_device_error(ws) == 0
