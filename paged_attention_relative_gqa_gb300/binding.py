@@ -380,6 +380,8 @@ def inkling_attn_prefill_masked(params, q, cu_q_lens, k_cache, v_cache, block_ta
     args = (ctypes.byref(params), ctypes.byref(mask), q.data_ptr(), cu, T, k_cache.data_ptr(), v_cache.data_ptr(),
             block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(), _opt(lse, "lse", _F32, (T, Hq), device),
             workspace.data_ptr(), workspace.numel(), _raw_stream(device) if stream is None else _stream_handle(stream))
+    if T == 0 or params.num_seqs == 0:   # (empty tensors have no address)
+        return out
     fn = (_lib or load_library()).inkling_attn_prefill_masked
     if _current_device() == device:
         code = fn(*args)
@@ -404,6 +406,8 @@ def inkling_attn_decode_masked(params, q, k_cache, v_cache, block_table, seq_len
     args = (ctypes.byref(params), ctypes.byref(mask), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
             block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(), _opt(lse, "lse", _F32, (B, Hq), device),
             workspace.data_ptr(), workspace.numel(), _raw_stream(device) if stream is None else _stream_handle(stream))
+    if B == 0:   # (empty tensors have no address)
+        return out
     fn = (_lib or load_library()).inkling_attn_decode_masked
     if _current_device() == device:
         code = fn(*args)
@@ -450,6 +454,8 @@ def inkling_attn_qk_norm_rope_write(params, q, k, v, cu_q_lens, seq_lens, block_
             v.data_ptr(), strides[2], cu, T, seq_lens.data_ptr(), block_table.data_ptr(), q_out.data_ptr(),
             k_cache.data_ptr(), v_cache.data_ptr(), workspace.data_ptr(), workspace.numel(), _raw_stream(device) if stream
             is None else _stream_handle(stream))
+    if T == 0 or params.num_seqs == 0:   # (empty tensors have no address)
+        return q_out
     fn = (_lib or load_library()).inkling_attn_qk_norm_rope_write
     if _current_device() == device:
         code = fn(*args)

@@ -405,3 +405,24 @@ def test_one_workspace_serves_prefills_and_decodes_of_any_sizes(cuda_device):
             out, lse, _ = call(prob, opts, decode, workspace=ws)
             check(out, lse, ref, f"call {i} of {order}")
     assert binding.inkling_attn_read_device_error(ws) == 0
+
+
+@pytest.mark.parametrize("decode", [False, True])
+def test_empty_batches_return_at_once(cuda_device, decode):
+    prob = problem((8, 2), 64, 16, [1, 1], [9, 30], 30, cuda_device)
+    params, ws = binding.params_of(prob), None
+    ws = binding.alloc_masked_workspace(params, decode, cuda_device)
+    none = lambda *s, t=torch.bfloat16: torch.empty(s, dtype=t, device=cuda_device)
+    if decode:
+        params.num_seqs = 0
+        out = none(0, 8, 64)
+        assert binding.inkling_attn_decode_masked(params, none(0, 8, 64), prob.k_cache, prob.v_cache,
+                                                  prob.block_table[:0], prob.seq_lens[:0], out, ws) is out
+        return
+    out = none(0, 8, 64)
+    cu = torch.zeros(3, dtype=torch.int32, device=cuda_device)
+    assert binding.inkling_attn_prefill_masked(params, none(0, 8, 64), cu, prob.k_cache, prob.v_cache, prob.block_table,
+                                               prob.seq_lens, out, ws) is out
+    kv = none(0, 2, 64)
+    assert binding.inkling_attn_qk_norm_rope_write(params, none(0, 8, 64), kv, kv, cu, prob.seq_lens, prob.block_table, out,
+                                                   prob.k_cache, prob.v_cache, ws) is out
