@@ -384,6 +384,52 @@ def test_a_length_past_the_block_table_is_reported(cuda_device, tokens, keys, le
     check(out, lse, want, "length past the table")
 
 
+@pytest.mark.parametrize("softcap", [10.0, 50.0, 300.0])
+@pytest.mark.parametrize("power", [-60, 70])
+def test_capped_scores_leave_the_range_of_v(cuda_device, softcap, power):
+    """V near the ends of its range, scores up to the cap."""
+    prob = problem((8, 2), 128, 64, [200, 30], [300, 3000], 22, cuda_device, q_std=30.0)
+    prob.v_cache *= 2.0 ** power
+    opts = options(prob, softcap=softcap)
+    out, lse, ws = call(prob, opts, False)
+    torch.cuda.synchronize()
+    assert binding.inkling_attn_read_device_error(ws) == 0
+    check(out, lse, reference(prob, opts), "range of V")
+
+
+@pytest.mark.parametrize("softcap", [0.0, 50.0, 1000.0])
+@pytest.mark.parametrize("sign", [-1.0, 1.0])
+def test_scores_far_to_one_side(cuda_device, softcap, sign):
+    """All scores of a row near -20 or near 20: the largest magnitude of a tile is not its largest score."""
+    prob = problem((4, 2), 64, 64, [150, 20], [400, 2900], 23, cuda_device)
+    prob.k_cache *= 0.1
+    prob.k_cache += 1.0
+    prob.q = (0.1 * prob.q.float() + sign * 20.0 / 8.0).to(torch.bfloat16)   # 64 products of 2.5 over sqrt(64)
+    opts = options(prob, softcap=softcap)
+    out, lse, ws = call(prob, opts, False)
+    torch.cuda.synchronize()
+    assert binding.inkling_attn_read_device_error(ws) == 0
+    check(out, lse, reference(prob, opts), "scores to one side")
+
+
+@pytest.mark.parametrize("fill", [float("nan"), 1e30])
+def test_rows_of_other_sequences_change_no_bit(cuda_device, fill):
+    """Rows of a tile past a sequence's own (the next one's, padding) have no say in how it is capped."""
+    prob = problem((8, 2), 128, 64, [5, 70, 9], [1000, 70, 40], 24, cuda_device, q_std=2.0)
+    opts = options(prob, softcap=50.0)
+    want, want_lse, _ = call(prob, opts, False)
+    T = prob.total_q
+    q = torch.full((T + 40, *prob.q.shape[1:]), fill, dtype=torch.bfloat16, device=cuda_device)
+    q[:5] = prob.q[:5]
+    q[5 + 70:T] = prob.q[5 + 70:T]
+    prob.q = q
+    out, lse, _ = call(prob, opts, False)
+    torch.cuda.synchronize()
+    for part in (slice(0, 5), slice(75, T)):
+        assert torch.equal(out[part], want[part]) and torch.equal(lse[part], want_lse[part])
+    assert (out[T:] == 7.0).all() and (lse[T:] == 7.0).all()
+
+
 def test_one_workspace_serves_prefills_and_decodes_of_any_sizes(cuda_device):
     """Initialised once, then used in turn by calls of other batch sizes, head counts and kinds."""
     def make(decode, heads, dim, q_lens, seq_lens, seed):
