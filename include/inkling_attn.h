@@ -298,8 +298,9 @@ size_t inkling_attn_masked_workspace_bytes(const ink_attn_params_t* params, int 
  *   lse        device, fp32 [total_q, Hq], or NULL: log of the sum of exp(s_k) over the visible
  *              keys (natural units), with which outputs over parts of a history are joined
  *   workspace  device, >= inkling_attn_masked_workspace_bytes(params, 0), initialised once
- * A token that sees no key gets a zero output row and lse = -infinity.  params.rel_extent is
- * not used (any valid value).  A sequence whose rows lie outside [0, total_q) is skipped
+ * A token that sees no key gets a zero output row and lse = -infinity.  Sums are held in fp32 and divided
+ * at the end: |V| up to 2^100 is safe (2^70 when scores are capped).  params.rel_extent is not used
+ * (any valid value).  A sequence whose rows lie outside [0, total_q) is skipped
  * (INK_DEVERR_BAD_ROWS); one with more new tokens than history gets zero rows
  * (INK_DEVERR_QLEN_EXCEEDS_KV).
  */

@@ -29,10 +29,20 @@
 //       see the key); rows that do see one get it back in the epilogue.
 // When there are fewer items than SMs (a chunk of a prompt or a few drafted tokens against a long
 // history), the key tiles of an item are cut into pieces of one length, chosen on the device so that
-// the rounds over the SMs are full ones; a piece leaves O, maximum and sum in the workspace, and the last one to finish (an
-// atomic ticket, no waiting) joins them in order.
+// the rounds over the SMs are full ones; a piece leaves O, maximum and sum in the workspace, and the
+// last one to finish (an atomic ticket, no waiting) joins them in order.
 // Every wait is bounded; after a timeout the CTA records it, stops issuing, waits for what is in
 // flight and exits.
+//
+// What bounds it: the softmax.  Two row tiles and 128 keys take 2048 clocks of the tensor cores at D = 128,
+// but about 2650 pass: a row tile's chain (128 scores from tensor memory, 1200 clocks of softmax, P V and the
+// next S, four hand-overs of about 100 clocks) is longer than half of that, and the exponentials of both
+// tiles alone keep the special function units busy for 1024.  Measured with 64 query and 8 KV heads of
+// 128, prompts of about 5,000 tokens: 1.36 PFLOP/s causal, 1.44 on whole histories, 1.12 capped, 1.02 with
+// slopes (which cost 3 operations a score); 0.86 at D = 64, where a score has half the products.  A window
+// of 512 keys: 0.83, since an item is 5 tiles long and its start, masks and output run in no tile's shadow.
+// Tried without gain: P V in two halves, numerators against the last tile's maximum, P beside S, 64-key
+// tiles with Q in tensor memory, a third Q tile, S read in halves, output rows staged in shared memory.
 #include <algorithm>
 #include <climits>
 
@@ -56,7 +66,7 @@ constexpr int PM_TILES = 4;
 constexpr int PM_REGS_SOFTMAX = 208, PM_REGS_REST = 88;   // registers a thread after the split
 constexpr int PM_PIECE_TILES = 8; // least tiles of a piece of a cut item
 constexpr float RESCALE_LOG2 = 8.f;
-constexpr float CALM_LOG2 = 32.f;
+constexpr float CALM_LOG2 = 40.f;
 
 template <int D>
 struct PMShape {
@@ -630,12 +640,13 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
     const bool scaled = CAP || a.slopes != nullptr || !(a.scale_log2 > 0.f);
     const float mul = scaled ? 1.f : a.scale_log2;
     // The largest magnitude of a tile, which decides how its scores are capped, bounds them from above
-    // and below.  As long as it is small (|s| <= 32 in log2 units) in every row of a warp, no maximum is looked
-    // for: the numerators are taken against 0 and lie within [2^-32, 2^32], far inside bf16's range (sums
-    // of 2^17 of them times V overflow past |V| = 2^78).  2 sequences of 5,000 tokens, 64 + 2 x 8 heads of
-    // 128, cap 50: 905 us with every tile's maximum, 778 without.  Not with slopes, whose scores have no lower
-    // bound, nor for an item of one tile: a row of one key has the numerator 1 against its maximum, which
-    // bf16 holds exactly.
+    // and below.  As long as it is small (|s| <= 40 in log2 units) in every row of a warp, no maximum is looked
+    // for: the numerators are taken against 0 and lie within [2^-40, 2^40], far inside bf16's range (sums
+    // of 2^17 of them times V overflow past |V| = 2^70).  2 sequences of 5,000 tokens, 64 + 2 x 8 heads of
+    // 128, cap 50: 905 us with every tile's maximum, 778 without.  A tile with larger scores goes the general
+    // way, whose maximum leaves 0 only when it has to.  Not with slopes, whose scores have no lower bound,
+    // nor for an item of one tile: a row of one key has the numerator 1 against its maximum, which bf16 holds
+    // exactly.
     const float reach = CAP && a.slopes == nullptr ? fminf(a.cap_near, CALM_LOG2 / fabsf(a.scale_log2)) : -1.f;
     uint32_t sn = 0, on = 0;
     int g = 0;
@@ -671,7 +682,8 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
       float m = calm >= 0.f ? 0.f : -INFINITY, l = 0.f;
       int j = 0;
       bool waited = false;   // for S of tile j
-      // From tile j on: in a calm stretch until a tile that is none (its scores are read again), else to the end.
+      // From tile j on: in a calm stretch until a tile that is none (its scores are read again); one tile between
+      // two calm stretches; else to the end.
       // Scores that are neither capped nor shifted have a loop of their own at D = 128 (window of 512 keys,
       // 7,949 tokens: 159 -> 155 us, whole history: 778 -> 763); at D = 64 two loops are slower than one (494 ->
       // 507 us).
@@ -751,10 +763,11 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
             for (int c = 0; c < 128; c += 2)
               mxv[(c >> 1) & 3] = fmax3(mxv[(c >> 1) & 3], __uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
             const float mx = fmaxf(fmaxf(mxv[0], mxv[1]), fmaxf(mxv[2], mxv[3])) * mul;
-            const bool mine = mx > m + RESCALE_LOG2;
+            const bool mine = mx > m + (calm >= 0.f ? CALM_LOG2 : RESCALE_LOG2);
+            const float to = calm >= 0.f && fabsf(mx) <= CALM_LOG2 ? 0.f : mx;   // (back to 0 where that will do)
             if (__any_sync(0xffffffffu, mine)) {
               if (j > 0) {   // every earlier product into O_h is done: s_full came after it
-                const float fr = mine ? fast_exp2(m - mx) : 1.f;
+                const float fr = mine ? fast_exp2(m - to) : 1.f;
 #pragma unroll 1
                 for (int c2 = 0; c2 < D / 16; ++c2) {
                   uint32_t ov[16];
@@ -766,7 +779,7 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
                 }
                 l *= fr;
               }
-              if (mine) m = mx;
+              if (mine) m = to;
             }
           }
           // ---- numerators
@@ -797,12 +810,21 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&p_full[h]);
+          if (CAP && !CALM && calm >= 0.f) {
+            ++j, ++g;
+            return;
+          }
         }
       };
       if (CAP) {
-        if (calm >= 0.f) tiles(std::integral_constant<Stretch, Calm>{});
-        if (l == 0.f) m = -INFINITY;   // nothing seen in a calm stretch
-        if (go) tiles(std::integral_constant<Stretch, General>{});
+        while (go && j < nt) {
+          if (calm >= 0.f && __all_sync(0xffffffffu, m == 0.f || l == 0.f)) {
+            m = 0.f;
+            tiles(std::integral_constant<Stretch, Calm>{});
+            if (l == 0.f) m = -INFINITY;   // (no key seen yet: any maximum will do)
+          }
+          if (go && j < nt) tiles(std::integral_constant<Stretch, General>{});
+        }
       } else if (D == 64 || scaled) {
         tiles(std::integral_constant<Stretch, General>{});
       } else {
