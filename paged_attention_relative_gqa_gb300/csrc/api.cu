@@ -620,6 +620,9 @@ ink_status_t masked_impl(const ink_attn_params_t* params, const ink_attn_mask_t*
   a.cap_near = ainv >= 1e-5 && ainv <= 1e3 ? (float)(0.45 / ainv) : -1.f;
   double c = 1.4426950408889634 * params->sm_scale;
   for (int i = 0; i < 4; ++i, c *= inv * inv) a.near[i] = a.cap_near > 0.f ? (float)(c * kNear[i]) : 0.f;
+  // the same for |y| <= 1, as in score_log2, the cap in log2 units folded in
+  a.cap_mid = (float)(1.0 / ainv);
+  for (int i = 0; i < ink::CAP_TERMS; ++i) a.mid[i] = a.cap_log2 * ink::cap_term(i);
   a.stale = reinterpret_cast<uint32_t*>(workspace) + 15;   // these three inside the header
   a.counters = reinterpret_cast<uint32_t*>(workspace) + 16;
   // a row tile: the heads of a KV head (in equal chunks when there are more than 128) times as

@@ -86,7 +86,7 @@ struct PMItem {
   int slot, np, one;         // of a cut item: its first place in the partials, its pieces, this one
 };
 
-enum Stretch { General, Calm, Plain };   // loops over an item's tiles
+enum Stretch { General, Calm, Mild, Plain };   // loops over an item's tiles
 
 template <int D>
 struct PMSmem {
@@ -127,8 +127,9 @@ __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
 }
 
 // CAP: capped scores.  Models keep most scores well inside the cap: while no score of a warp's tile
-// passes CAP_NEAR of it, tanh is an odd polynomial of four terms in the raw product (relative error
-// 2^-21.8; five packed FMAs for two scores and no special function), else score_log2.
+// passes 0.45 of it, tanh is an odd polynomial of four terms in the raw product (relative error
+// 2^-21.8; five packed operations for two scores and no special function), up to the cap one of seven
+// terms (nine packed operations), else score_log2.
 // SPLIT: items may be cut into pieces (a kernel of its own: the joining code would cost the others
 // registers).
 template <int D, bool CAP, bool SPLIT>
@@ -647,7 +648,7 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
     // way, whose maximum leaves 0 only when it has to.  Not with slopes, whose scores have no lower bound,
     // nor for an item of one tile: a row of one key has the numerator 1 against its maximum, which bf16 holds
     // exactly.
-    const float reach = CAP && a.slopes == nullptr ? fminf(a.cap_near, CALM_LOG2 / fabsf(a.scale_log2)) : -1.f;
+    const float reach = CAP && a.slopes == nullptr ? fminf(a.cap_mid, CALM_LOG2 / fabsf(a.scale_log2)) : -1.f;
     uint32_t sn = 0, on = 0;
     int g = 0;
     bool go = true;
@@ -678,17 +679,19 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
         continue;
       }
       const float slope2 = a.slopes ? __ldg(a.slopes + head) * LOG2E : 0.f;
-      const float calm = nt > 1 ? reach : -1.f;   // the largest magnitude that needs no maximum
-      float m = calm >= 0.f ? 0.f : -INFINITY, l = 0.f;
+      // the largest magnitudes that need no maximum, for the short polynomial and for the longer one
+      const float mild = nt > 1 ? reach : -1.f, calm = fminf(mild, a.cap_near);
+      float m = mild >= 0.f ? 0.f : -INFINITY, l = 0.f;
       int j = 0;
       bool waited = false;   // for S of tile j
-      // From tile j on: in a calm stretch until a tile that is none (its scores are read again); one tile between
-      // two calm stretches; else to the end.
+      // From tile j on: in a calm or mild stretch until a tile that is none (its scores are read again), in a
+      // mild one to a calm tile; one tile between two such stretches; else to the end.
       // Scores that are neither capped nor shifted have a loop of their own at D = 128 (window of 512 keys,
       // 7,949 tokens: 159 -> 155 us, whole history: 778 -> 763); at D = 64 two loops are slower than one (494 ->
       // 507 us).
       auto tiles = [&](auto stretch) {
-        constexpr bool CALM = decltype(stretch)::value == Calm, PLAIN = decltype(stretch)::value == Plain;
+        constexpr Stretch ST = decltype(stretch)::value;
+        constexpr bool CALM = ST == Calm || ST == Mild, PLAIN = ST == Plain;
         for (; j < nt; ++j, ++g) {
           const int k0 = (kt0 + j) * PM_KEYS;
           if (!waited) {
@@ -703,6 +706,7 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
           for (int c = 0; c < 4; ++c) tmem_ld32(tm_s + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&sr[32 * c]));
           tmem_wait_ld();
           const uint4 bad = *reinterpret_cast<const uint4*>(kbad + (g % PM_BAD) * 4);
+          bool over = false;   // a mild stretch has come to a calm tile
           // ---- scores
           if constexpr (CAP) {
             float fv[4] = {0.f, 0.f, 0.f, 0.f};   // largest |<q, K[k]>| of the tile
@@ -711,27 +715,44 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
               fv[(c >> 1) & 3] = fmax3(fv[(c >> 1) & 3], fabsf(__uint_as_float(sr[c])), fabsf(__uint_as_float(sr[c + 1])));
             // (rows of other sequences have no say)
             const float far = rv ? fmaxf(fmax3(fv[0], fv[1], fv[2]), fv[3]) : 0.f;
-            const bool wild = __any_sync(0xffffffffu, !(far <= (CALM ? calm : a.cap_near)));
-            if (CALM && wild) {
-              waited = true;
-              return;
-            }
-            if (!CALM && wild) {
+            auto polynomial = [&](auto terms) {
+              constexpr int TERMS = decltype(terms)::value;
+              uint64_t co[TERMS];
 #pragma unroll
-              for (int c = 0; c < 128; ++c) sr[c] = __float_as_uint(score_log2<true>(a, __uint_as_float(sr[c])));
-            } else {
-              const uint64_t t0 = f2_pack(a.near[0], a.near[0]), t1 = f2_pack(a.near[1], a.near[1]);
-              const uint64_t t2 = f2_pack(a.near[2], a.near[2]), t3 = f2_pack(a.near[3], a.near[3]);
+              for (int i = 0; i < TERMS; ++i) {
+                const float f = TERMS == 4 ? a.near[i] : a.mid[i];
+                co[i] = f2_pack(f, f);
+              }
+              const uint64_t inv2 = f2_pack(a.cap_inv, a.cap_inv);
 #pragma unroll
               for (int c = 0; c < 128; c += 2) {
-                const uint64_t x = f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
+                uint64_t x = f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
+                if (TERMS != 4) x = f2_mul(x, inv2);
                 const uint64_t u = f2_mul(x, x);
-                const uint64_t t = f2_fma(f2_fma(f2_fma(t3, u, t2), u, t1), u, t0);
+                uint64_t t = co[TERMS - 1];
+#pragma unroll
+                for (int i = TERMS - 2; i >= 0; --i) t = f2_fma(t, u, co[i]);
                 float s0, s1;
                 f2_unpack(f2_mul(t, x), s0, s1);
                 sr[c] = __float_as_uint(s0);
                 sr[c + 1] = __float_as_uint(s1);
               }
+            };
+            auto within = [&](float reach) { return __all_sync(0xffffffffu, far <= reach); };
+            if constexpr (CALM) {
+              if (!within(ST == Calm ? calm : mild)) {
+                waited = true;
+                return;
+              }
+              over = ST == Mild && within(calm);
+              polynomial(std::integral_constant<int, ST == Calm ? 4 : CAP_TERMS>{});
+            } else if (within(a.cap_near)) {
+              polynomial(std::integral_constant<int, 4>{});
+            } else if (within(a.cap_mid)) {
+              polynomial(std::integral_constant<int, CAP_TERMS>{});
+            } else {
+#pragma unroll
+              for (int c = 0; c < 128; ++c) sr[c] = __float_as_uint(score_log2<true>(a, __uint_as_float(sr[c])));
             }
           } else if (!PLAIN && scaled) {
 #pragma unroll
@@ -763,8 +784,8 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
             for (int c = 0; c < 128; c += 2)
               mxv[(c >> 1) & 3] = fmax3(mxv[(c >> 1) & 3], __uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
             const float mx = fmaxf(fmaxf(mxv[0], mxv[1]), fmaxf(mxv[2], mxv[3])) * mul;
-            const bool mine = mx > m + (calm >= 0.f ? CALM_LOG2 : RESCALE_LOG2);
-            const float to = calm >= 0.f && fabsf(mx) <= CALM_LOG2 ? 0.f : mx;   // (back to 0 where that will do)
+            const bool mine = mx > m + (mild >= 0.f ? CALM_LOG2 : RESCALE_LOG2);
+            const float to = mild >= 0.f && fabsf(mx) <= CALM_LOG2 ? 0.f : mx;   // (back to 0 where that will do)
             if (__any_sync(0xffffffffu, mine)) {
               if (j > 0) {   // every earlier product into O_h is done: s_full came after it
                 const float fr = mine ? fast_exp2(m - to) : 1.f;
@@ -810,18 +831,22 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&p_full[h]);
-          if (CAP && !CALM && calm >= 0.f) {
+          if (over || (CAP && !CALM && mild >= 0.f)) {
             ++j, ++g;
             return;
           }
         }
       };
       if (CAP) {
+        bool rough = false;   // the tile before was neither calm nor mild
         while (go && j < nt) {
-          if (calm >= 0.f && __all_sync(0xffffffffu, m == 0.f || l == 0.f)) {
+          if (mild >= 0.f && __all_sync(0xffffffffu, m == 0.f || l == 0.f)) {
             m = 0.f;
-            tiles(std::integral_constant<Stretch, Calm>{});
-            if (l == 0.f) m = -INFINITY;   // (no key seen yet: any maximum will do)
+            if (!rough) tiles(std::integral_constant<Stretch, Calm>{});
+            if (go && j < nt) tiles(std::integral_constant<Stretch, Mild>{});
+            rough = waited;
+            if (!rough) continue;
+            if (l == 0.f) m = -INFINITY;   // no key seen yet: any maximum will do
           }
           if (go && j < nt) tiles(std::integral_constant<Stretch, General>{});
         }
