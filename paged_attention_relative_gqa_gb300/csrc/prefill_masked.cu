@@ -38,7 +38,7 @@
 // but about 2650 pass: a row tile's chain (128 scores from tensor memory, 1200 clocks of softmax, P V and the
 // next S, four hand-overs of about 100 clocks) is longer than half of that, and the exponentials of both
 // tiles alone keep the special function units busy for 1024.  Measured with 64 query and 8 KV heads of
-// 128, prompts of about 5,000 tokens: 1.36 PFLOP/s causal, 1.44 on whole histories, 1.12 capped, 1.02 with
+// 128, prompts of about 5,000 tokens: 1.36 PFLOP/s causal, 1.44 on whole histories, 1.10 capped, 1.02 with
 // slopes (which cost 3 operations a score); 0.86 at D = 64, where a score has half the products.  A window
 // of 512 keys: 0.83, since an item is 5 tiles long and its start, masks and output run in no tile's shadow.
 // Tried without gain: P V in two halves, numerators against the last tile's maximum, P beside S, 64-key
