@@ -566,6 +566,11 @@ bool make_token_map(CUtensorMap* map, const void* q, const ink_attn_params_t* p,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool overlap(const void* a, size_t an, const void* b, size_t bn) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + bn && y < x + an;
+}
+
 ink_status_t masked_impl(const ink_attn_params_t* params, const ink_attn_mask_t* mask, const void* q,
                          const int32_t* cu_q_lens, int32_t total_q, const void* k_cache, const void* v_cache,
                          const int32_t* block_table, const int32_t* seq_lens, void* out, float* lse,
@@ -584,6 +589,8 @@ ink_status_t masked_impl(const ink_attn_params_t* params, const ink_attn_mask_t*
   if ((long long)total_q * params->num_q_heads >= (1ll << 31)) return INK_ERR_TOO_LARGE;
   if (workspace_bytes < inkling_attn_masked_workspace_bytes(params, decode ? 1 : 0)) return INK_ERR_WORKSPACE;
   if (params->num_seqs == 0 || total_q == 0) return INK_OK;
+  const size_t row_bytes = (size_t)params->num_q_heads * params->head_dim * 2;
+  if (overlap(q, total_q * row_bytes, out, total_q * row_bytes)) return INK_ERR_BAD_SHAPE;
   ink::MaskedArgs a;
   a.q = q;
   a.cu_q = decode ? nullptr : cu_q_lens;
@@ -705,6 +712,14 @@ ink_status_t inkling_attn_qk_norm_rope_write(const ink_attn_params_t* params, co
   if (q_out == q && q_stride != (int64_t)Hq * D) return INK_ERR_BAD_SHAPE;
   if (workspace_bytes < kHeaderBytes) return INK_ERR_WORKSPACE;
   if (params->num_seqs == 0 || total_q == 0) return INK_OK;
+  // what is written overlaps neither what is read (but for q in place) nor what else is written
+  auto span = [&](int64_t stride, int n) { return 2 * ((size_t)(total_q - 1) * (size_t)stride + (size_t)n * D); };
+  const void* at[6] = {q, k, v, q_out, k_cache, v_cache};
+  const size_t pool = 2 * (size_t)pool_rows(params) * D;
+  const size_t bytes[6] = {span(q_stride, Hq), span(k_stride, Hkv), span(v_stride, Hkv), span((int64_t)Hq * D, Hq), pool, pool};
+  for (int w = 3; w < 6; ++w)
+    for (int x = 0; x < w; ++x)
+      if (overlap(at[w], bytes[w], at[x], bytes[x]) && !(w == 3 && x == 0 && q_out == q)) return INK_ERR_BAD_SHAPE;
   ink::NormRopeArgs a;
   a.x[0] = static_cast<const uint16_t*>(q);
   a.x[1] = static_cast<const uint16_t*>(k);

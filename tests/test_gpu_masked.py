@@ -472,3 +472,60 @@ def test_empty_batches_return_at_once(cuda_device, decode):
     kv = none(0, 2, 64)
     assert binding.inkling_attn_qk_norm_rope_write(params, none(0, 8, 64), kv, kv, cu, prob.seq_lens, prob.block_table, out,
                                                    prob.k_cache, prob.v_cache, ws) is out
+
+
+MANY = [
+    # more query heads per KV head than a row tile holds; more sequences than lanes of a warp
+    (False, (200, 1), 128, 64, [3, 40], [900, 40], -1, "cap+documents"),
+    (False, (260, 2), 64, 16, [17, 1], [300, 3100], 33, "slopes"),
+    (False, (129, 1), 64, 64, [5], [4500], -1, "random"),
+    (False, (8, 1), 64, 16, [1 + i % 5 for i in range(70)], [2100 + 7 * i for i in range(70)], -1, "cap"),
+    (False, (4, 2), 128, 8, [(5 * i) % 7 for i in range(150)], [(5 * i) % 7 + i for i in range(150)], -1, "slopes"),
+    (False, (2, 2), 64, 16, [1], [1], -1, "cap"),
+    (True, (200, 1), 128, 64, [1] * 2, [900, 40], -1, "cap"),
+    (True, (4, 2), 64, 16, [1] * 300, [1 + (37 * i) % 90 for i in range(300)], 20, "slopes"),
+]
+
+
+@pytest.mark.parametrize("case", range(len(MANY)))
+def test_many_heads_and_many_sequences(cuda_device, case):
+    decode, heads, dim, page, q_lens, seq_lens, window, kind = MANY[case]
+    prob = problem(heads, dim, page, q_lens, seq_lens, 500 + case, cuda_device, window, q_std=3.0 if "cap" in kind else 1.0)
+    opts = _opts(prob, kind, case, decode)
+    out, lse, ws = call(prob, opts, decode)
+    torch.cuda.synchronize()
+    assert binding.inkling_attn_read_device_error(ws) == 0
+    check(out, lse, reference(prob, opts), f"case {case}")
+    again, lse2, _ = call(prob, opts, decode, workspace=ws)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
+def test_offsets_that_change_between_replays(cuda_device):
+    """A captured prefill of few rows against long histories, replayed with other splits of its rows over
+    the sequences, other lengths and other ranges."""
+    prob = problem((8, 1), 128, 64, [20, 20, 8], [6000, 3000, 500], 31, cuda_device)
+    opts = options(prob, softcap=40.0, begin=np.zeros(48), end=np.full(48, 1 << 30))
+    params = binding.params_of(prob)
+    ws = binding.alloc_masked_workspace(params, False, cuda_device)
+    out, lse = torch.empty_like(prob.q), torch.empty(48, 8, dtype=torch.float32, device=cuda_device)
+    run = lambda: binding.inkling_attn_prefill_masked(params, prob.q, prob.cu_q_lens, prob.k_cache, prob.v_cache,
+                                                      prob.block_table, prob.seq_lens, out, ws, lse=lse, **opts)
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        run()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        run()
+    for q_lens, seq_lens, first in (([20, 20, 8], [6000, 3000, 500], 0), ([1, 0, 40], [5999, 3000, 490], 100),
+                                    ([48, 0, 0], [4000, 0, 0], 3990), ([0, 0, 0], [6000, 3000, 500], 0)):
+        prob.cu_q_lens.copy_(torch.tensor([0, *np.cumsum(q_lens)], dtype=torch.int32))
+        prob.seq_lens.copy_(torch.tensor(seq_lens, dtype=torch.int32))
+        opts["key_begin"].fill_(first)
+        out.fill_(7.0)
+        lse.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert binding.inkling_attn_read_device_error(ws) == 0
+        check(out, lse, reference(prob, opts), f"replayed with {q_lens}")

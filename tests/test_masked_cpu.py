@@ -107,6 +107,29 @@ def test_norm_rope_refusals(lib):
     assert rope(lib, total=0, q_out=OK) == 0 and rope(lib, p=params(num_seqs=0)) == 0
 
 
+def test_buffers_that_overlap_are_refused(lib):
+    at = lambda n: ctypes.c_void_p((1 << 20) + n)
+    row, rows = 64 * 128 * 2, 64 * 64 * 128 * 2
+    for off in (0, 16, row, rows - 16):
+        assert prefill(lib, out=at(off)) == 2
+        assert prefill(lib, q=at(off), out=OK) == 2
+    assert decode(lib) == 2   # q and out are one buffer
+    # norm and write: q_out against k and v, the caches against everything
+    big = [ctypes.c_void_p((1 << 40) * i) for i in range(1, 7)]
+
+    def write(q=big[0], k=big[1], v=big[2], q_out=big[3], k_cache=big[4], v_cache=big[5], qs=64 * 128):
+        p, r = params(), rope_opts()
+        return lib.inkling_attn_qk_norm_rope_write(ctypes.byref(p), ctypes.byref(r), q, qs, k, 8 * 128, v, 8 * 128, OK, 64,
+                                                   OK, OK, q_out, k_cache, v_cache, OK, 1 << 30, None)
+
+    behind = ctypes.c_void_p(big[0].value + row)
+    assert write(q_out=behind) == 2 and write(q_out=behind, qs=80 * 128) == 2
+    assert write(k=big[3]) == 2 and write(v=behind, q_out=big[0]) == 2
+    for name in ("q", "k", "v", "q_out", "v_cache"):
+        assert write(**{name: ctypes.c_void_p(big[4].value + row)}) == 2
+    assert write(v_cache=big[0]) == 2
+
+
 def test_binding_checks_before_the_library(lib):
     p = params(num_seqs=1, num_q_heads=2, num_kv_heads=1, head_dim=64, page_size=16, max_pages_per_seq=2, num_pages=3)
     q = torch.zeros(1, 2, 64, dtype=torch.bfloat16)
