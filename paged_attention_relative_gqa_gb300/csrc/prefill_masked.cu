@@ -397,9 +397,10 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
       };
       load_chunk();
       if constexpr (SPLIT) {
-        // Lane i tries pieces of 1 / (i + 1) of the longest item.  The cost in eighths of a tile: rounds
-        // over the SMs (with a sixteenth to spare: CTAs that join are late for their next piece) times
-        // the mean piece and 5 tiles for its partials, and the last join, 1.2 tiles per piece of an item.
+        // Lane i tries pieces of 1 / (i + 1) and 2 / (2 i + 3) of the longest item.  The cost in eighths of a
+        // tile, with 5 tiles for a piece's partials: the longest piece, or the rounds over the SMs (with a
+        // sixteenth to spare: CTAs that join are late for their next piece) times the mean one; and the last
+        // join, 1.2 tiles per piece of an item.
         const uint32_t stale = *reinterpret_cast<volatile uint32_t*>(a.stale);
         int longest = 0;
         for (int c = 0;;) {
@@ -410,8 +411,8 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
           load_chunk();
         }
         longest = __reduce_max_sync(0xffffffffu, longest);
-        const int mine = max(PM_PIECE_TILES, (longest + lane) / (lane + 1));
-        int pieces = 0;
+        int mine[2], pieces[2] = {0, 0}, top[2] = {0, 0};
+        for (int y = 0; y < 2; ++y) mine[y] = max(PM_PIECE_TILES, (2 * longest - 1) / (2 * lane + 2 + y) + 1);
         long long tiles = 0;
         for (int c = 0; c < a.B; c += 32) {
           if (cb != c) {
@@ -419,19 +420,28 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
             load_chunk();
           }
           const int t = tiles_of(my_len);
-          for (int x = 0; x < min(32, a.B - c); ++x)
-          {
+          for (int x = 0; x < min(32, a.B - c); ++x) {
             const int n = __shfl_sync(0xffffffffu, cnt, x), tx = __shfl_sync(0xffffffffu, t, x);
-            pieces += n * ((tx + mine - 1) / mine);
+            if (n == 0) continue;
+            for (int y = 0; y < 2; ++y) {
+              const int np = (tx + mine[y] - 1) / mine[y];
+              pieces[y] += n * np;
+              top[y] = max(top[y], (tx + np - 1) / np);
+            }
             tiles += (long long)n * tx;
           }
         }
         const int sms = (int)gridDim.x;
-        const long long cost8 = (long long)((pieces + pieces / 16 + sms - 1) / sms) * (8 * tiles / max(pieces, 1) + 40) +
-                                10 * (longest / mine);
-        const uint32_t cost = pieces > MASKED_PIECES ? 0x7ffffffu : (uint32_t)min(cost8, 0x3ffffffll);
-        const uint32_t best = __reduce_min_sync(0xffffffffu, cost << 5 | (uint32_t)lane);
-        if ((best >> 5) != 0x7ffffffu) piece_tiles = __shfl_sync(0xffffffffu, mine, (int)(best & 31u));
+        uint32_t cost = 0xffffffffu;
+        for (int y = 0; y < 2; ++y) {
+          const int rounds = pieces[y] <= sms ? 1 : (pieces[y] + pieces[y] / 16 + sms - 1) / sms;
+          const long long c8 = max((long long)8 * top[y] + 40, rounds * (8 * tiles / max(pieces[y], 1) + 40)) +
+                               10 * (longest / mine[y]);
+          if (pieces[y] <= MASKED_PIECES) cost = min(cost, (uint32_t)min(c8, 0x1ffffffll) << 6 | (uint32_t)(2 * lane + y));
+        }
+        const uint32_t best = __reduce_min_sync(0xffffffffu, cost);
+        const int won = __shfl_sync(0xffffffffu, best & 1 ? mine[1] : mine[0], (int)((best & 63u) >> 1));
+        if (best != 0xffffffffu) piece_tiles = won;
         cb = stale ? a.B : 0;
         if (cb < a.B) load_chunk();
         if (stale && lane == 0) record_error(a.err, INK_DEVERR_WAIT_TIMEOUT);   // left unusable by a timeout
