@@ -876,6 +876,10 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
       float4* part_o = reinterpret_cast<float4*>(a.part_o) + (size_t)(it.slot * 2 + h) * (D / 4) * MASKED_ROWS + r;
       float4* part_ml = reinterpret_cast<float4*>(a.part_ml) + (size_t)(it.slot * 2 + h) * MASKED_ROWS + r;
       constexpr size_t PART = (size_t)2 * (D / 4) * MASKED_ROWS;   // from one piece to the next
+      // the row that this thread finishes, and its blocks of 32 channels
+      bool wv = rv;
+      size_t wrow = orow;
+      int wlo = lo, whi = hi, cfirst = 0, cstep = 1;
       if (SPLIT && it.np > 1) {
 #pragma unroll 1
         for (int c2 = 0; c2 < D / 32; ++c2) {
@@ -907,6 +911,17 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
           done_item(k);
           continue;
         }
+        // rows past the last token are idle: the rest of the threads take other blocks of the rows there are
+        const int rows = min(a.tok_per_tile, it.ntok - h * a.tok_per_tile) * a.heads_per_tile;
+        cstep = min(MASKED_ROWS / rows, D / 32);
+        cfirst = r / rows;
+        const int row = r - cfirst * rows, wi = row / a.heads_per_tile, wg = row - wi * a.heads_per_tile;
+        const int wt = h * a.tok_per_tile + wi;
+        wv = cfirst < cstep && wg < it.gh;
+        wrow = (size_t)(it.t0 + wt) * a.Hq + it.h0 + wg;
+        if (wv) token_keys(a, it.t0 + wt, it.pos0 + wt, it.L, wlo, whi);
+        part_o += row - r;
+        part_ml += row - r;
         m = -INFINITY;
 #pragma unroll 4
         for (int x = 0; x < it.np; ++x) m = fmaxf(m, __ldcg(part_ml + (size_t)x * 2 * MASKED_ROWS).x);
@@ -921,15 +936,15 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
       const float inv = l > 0.f ? 1.f / l : 0.f;
       const bool nothing = l == 0.f;
 #pragma unroll 1
-      for (int c2 = 0; c2 < D / 32; ++c2) {
+      for (int c2 = cfirst; c2 < D / 32; c2 += cstep) {
         uint32_t ov[32];
         if (SPLIT && it.np > 1) {
           float acc[32];
 #pragma unroll
           for (int x = 0; x < 32; ++x) acc[x] = 0.f;
-          // (two pieces at a time: 17 loads in flight a thread)
-#pragma unroll 2
-          for (int y = 0; y < (rv ? it.np : 0); ++y) {
+          // (four pieces at a time: 36 loads in flight a thread)
+#pragma unroll 4
+          for (int y = 0; y < (wv ? it.np : 0); ++y) {
             const float my = __ldcg(part_ml + (size_t)y * 2 * MASKED_ROWS).x;
             float4 vv[8];
 #pragma unroll
@@ -952,10 +967,10 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
         }
 #pragma unroll
         for (int x = 0; x < 32; ++x) ov[x] = nothing ? 0u : __float_as_uint(__uint_as_float(ov[x]) * (l == l ? inv : l));
-        if (poisoned && rv) {
+        if (poisoned && wv) {
           // infinities and NaN of the keys this row sees
 #pragma unroll 1
-          for (int kk = lo; kk < hi; ++kk) {
+          for (int kk = wlo; kk < whi; ++kk) {
             const int page = __ldg(a.block_table + (size_t)it.b * a.max_pages + (kk >> a.log2_page));
             if (page < 0 || page >= a.num_pages) continue;
             const size_t vrow = ((((size_t)page * a.Hkv + it.kvh) << a.log2_page) + (kk & (P - 1))) * D + c2 * 32;
@@ -967,8 +982,8 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
             }
           }
         }
-        if (rv) {
-          uint4* o = reinterpret_cast<uint4*>(out + orow * D) + c2 * 4;
+        if (wv) {
+          uint4* o = reinterpret_cast<uint4*>(out + wrow * D) + c2 * 4;
 #pragma unroll
           for (int q8 = 0; q8 < 2; ++q8) {
             uint32_t w[8];
@@ -986,7 +1001,7 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
           }
         }
       }
-      if (rv && a.lse) a.lse[orow] = nothing ? -INFINITY : (m == -INFINITY ? 0.f : m) * LN2 + logf(l);
+      if (wv && cfirst == 0 && a.lse) a.lse[wrow] = nothing ? -INFINITY : (m == -INFINITY ? 0.f : m) * LN2 + logf(l);
       tc_fence_before();
       done_item(k);
     }
@@ -1030,8 +1045,8 @@ cudaError_t launch_prefill_masked(const MaskedMaps& m, const MaskedArgs& a, int 
   const int sms = current_device_sms(&dev);
   if (sms <= 0) return cudaErrorInvalidDevice;
   // Every sequence adds at most one unfilled item per KV head.  Cutting pays when the items cannot fill
-  // the SMs and an item can have two pieces' tiles (a chunk of 50 tokens against 30 K keys: 433 us
-  // whole, 200 us cut; a prompt that fills the SMs loses 3 % to the joining code's registers).
+  // the SMs and an item can have two pieces' tiles (50 + 41 + 65 tokens against 25 to 33 K keys: 433 us
+  // whole, 177 us cut; a prompt that fills the SMs loses 3 % to the joining code's registers).
   const long long tpi = 2ll * a.tok_per_tile, per = (long long)a.Hkv * a.head_chunks;
   const long long items = (a.T / tpi + a.B) * per;
   long long reach = (long long)a.max_pages << a.log2_page;
