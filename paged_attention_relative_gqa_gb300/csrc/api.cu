@@ -620,16 +620,28 @@ ink_status_t masked_impl(const ink_attn_params_t* params, const ink_attn_mask_t*
   a.cap_log2 = mk.softcap * 1.4426950408889634f;
   a.cap_k1 = mk.softcap > 0.f ? (float)(2.0 * 1.4426950408889634 * params->sm_scale / mk.softcap) : 0.f;
   a.cap_inv = mk.softcap > 0.f ? params->sm_scale / mk.softcap : 0.f;
-  // tanh(y) / y for |y| <= 0.45 as a polynomial in y^2 of the least relative error (2^-22), in terms
-  // of the raw product; left out (a negative reach) where its coefficients would leave fp32's range
-  static const double kNear[4] = {0.9999997567401877, -0.3332946719023333, 0.13236369052154567, -0.04602819379882759};
+  // tanh(y) / y as polynomials in y^2 of the least relative error, in terms of the raw product: for
+  // |y| <= 0.45 (2^-22) and for |y| <= 1 (2^-20.7, of the score itself: a 64th of a bf16 weight's
+  // rounding for scores to 20).  Left out where the coefficients would leave fp32's range: a negative
+  // reach, or the near one in the other's place.
+  static const double kNear[ink::NEAR_TERMS] = {0.9999997567401877, -0.3332946719023333, 0.13236369052154567,
+                                                -0.04602819379882759};
+  static const double kMid[ink::MID_TERMS] = {0.9999994136103072, -0.3332904245054663, 0.1328143441522219,
+                                              -0.05160568907876395, 0.01674313284460914, -0.003067067657993291};
   const double inv = mk.softcap > 0.f ? (double)params->sm_scale / mk.softcap : 0.0, ainv = inv < 0 ? -inv : inv;
   a.cap_near = ainv >= 1e-5 && ainv <= 1e3 ? (float)(0.45 / ainv) : -1.f;
+  a.cap_mid = ainv > 0 ? (float)(1.0 / ainv) : -1.f;
   double c = 1.4426950408889634 * params->sm_scale;
-  for (int i = 0; i < 4; ++i, c *= inv * inv) a.near[i] = a.cap_near > 0.f ? (float)(c * kNear[i]) : 0.f;
-  // the same for |y| <= 1, as in score_log2, the cap in log2 units folded in
-  a.cap_mid = (float)(1.0 / ainv);
-  for (int i = 0; i < ink::CAP_TERMS; ++i) a.mid[i] = a.cap_log2 * ink::cap_term(i);
+  for (int i = 0; i < ink::MID_TERMS; ++i, c *= inv * inv) {
+    if (i < ink::NEAR_TERMS) a.near[i] = a.cap_near > 0.f ? (float)(c * kNear[i]) : 0.f;
+    const double m = c * kMid[i], am = m < 0 ? -m : m;
+    a.mid[i] = (float)m;
+    if (!(am >= 1e-36 && am <= 1e36)) a.cap_mid = -1.f;
+  }
+  if (a.cap_mid < 0.f) {
+    a.cap_mid = a.cap_near;
+    for (int i = 0; i < ink::MID_TERMS; ++i) a.mid[i] = i < ink::NEAR_TERMS ? a.near[i] : 0.f;
+  }
   a.stale = reinterpret_cast<uint32_t*>(workspace) + 15;   // these three inside the header
   a.counters = reinterpret_cast<uint32_t*>(workspace) + 16;
   // a row tile: the heads of a KV head (in equal chunks when there are more than 128) times as

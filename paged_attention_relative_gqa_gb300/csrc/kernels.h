@@ -167,6 +167,8 @@ struct NormRopeArgs {
 
 cudaError_t launch_qk_norm_rope(NormRopeArgs& a, int head_dim, bool interleaved, int num_sms, cudaStream_t stream);
 
+constexpr int NEAR_TERMS = 4, MID_TERMS = 6;   // of the capped score's polynomials
+
 // One call of the masked attention (no bias tensor; a visible key range per token).
 struct MaskedArgs {
   const void* q;               // bf16 [total_q, Hq, D]
@@ -187,9 +189,9 @@ struct MaskedArgs {
   float cap_k1;                // 2 * sm_scale * log2(e) / softcap
   float cap_log2;              // softcap * log2(e)
   float cap_inv;               // sm_scale / softcap
-  // prefill: for |<q, K[k]>| <= cap_near the capped score is x (near[0] + near[1] x^2 + ...), up to cap_mid
-  // y (mid[0] + mid[1] y^2 + ...) with y = cap_inv x
-  float cap_near, near[4], cap_mid, mid[7];
+  // prefill: for |x| = |<q, K[k]>| <= cap_near the capped score is x (near[0] + near[1] x^2 + ...), up to
+  // cap_mid x (mid[0] + mid[1] x^2 + ...)
+  float cap_near, near[NEAR_TERMS], cap_mid, mid[MID_TERMS];
   unsigned long long wait_ns;  // limit of one pipeline wait (the drain waits keep 2 s)
   // prefill: a row tile holds tok_per_tile tokens x heads_per_tile query heads of one KV head
   int head_chunks, heads_per_tile, tok_per_tile;
@@ -202,14 +204,6 @@ struct MaskedArgs {
   float* part_ml;              // [2 * CTAs, rows, 2] (running max in log2 units, sum); prefill: [pieces, 2, 128 rows] float4
   int32_t* tickets;            // prefill: [pieces, 2]
 };
-
-// tanh(y) / y for |y| <= 1 as a polynomial in y^2 of the least relative error (an exchange iteration;
-// 2^-24.2)
-constexpr int CAP_TERMS = 7;
-__host__ __device__ constexpr float cap_term(int i) {
-  return i == 0 ? 0.99999994f : i == 1 ? -0.3333284f : i == 2 ? 0.13325204f : i == 3 ? -0.05345703f
-       : i == 4 ? 0.02028998f : i == 5 ? -0.006203379f : 0.0010410226f;
-}
 
 constexpr int MASKED_PIECES = 480;        // most pieces of cut items in one masked prefill
 

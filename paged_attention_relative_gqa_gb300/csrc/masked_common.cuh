@@ -27,9 +27,16 @@ __device__ __forceinline__ float fast_rcp(float x) {
 
 // The score in units of log 2 from the raw product x = <q, K[k]>: x scale, or with a cap C
 // C tanh(y), y = x scale / C:
-//   |y| <= 1   y T(y^2), T the polynomial of CAP_TERMS terms (2^-22.6 when evaluated in fp32)
+//   |y| <= 1   y T(y^2), T the polynomial of degree 6 with the least relative error against
+//              tanh(y) / y (an exchange iteration; 2^-24.2, 2^-22.6 when evaluated in fp32)
 //   beyond     1 - 2 / (1 + 2^(k1 x)), off by about 2^-23
 // (The prefill takes whole tiles by polynomials where it can.)
+constexpr int CAP_TERMS = 7;
+__device__ __forceinline__ constexpr float cap_term(int i) {
+  return i == 0 ? 0.99999994f : i == 1 ? -0.3333284f : i == 2 ? 0.13325204f : i == 3 ? -0.05345703f
+       : i == 4 ? 0.02028998f : i == 5 ? -0.006203379f : 0.0010410226f;
+}
+
 template <bool CAP>
 __device__ __forceinline__ float score_log2(const MaskedArgs& a, float x) {
   if constexpr (!CAP) return x * a.scale_log2;

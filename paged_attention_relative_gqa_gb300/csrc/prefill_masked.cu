@@ -130,8 +130,8 @@ __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
 
 // CAP: capped scores.  Models keep most scores well inside the cap: while no score of a warp's tile
 // passes 0.45 of it, tanh is an odd polynomial of four terms in the raw product (relative error
-// 2^-21.8; five packed operations for two scores and no special function), up to the cap one of seven
-// terms (nine packed operations), else score_log2.
+// 2^-21.8; five packed operations for two scores and no special function), up to the cap one of six
+// terms (2^-20.7, seven operations), else score_log2.
 // SPLIT: items may be cut into pieces (a kernel of its own: the joining code would cost the others
 // registers).
 template <int D, bool CAP, bool SPLIT>
@@ -656,7 +656,7 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
     // and below.  As long as it is small (|s| <= 40 in log2 units) in every row of a warp, no maximum is looked
     // for: the numerators are taken against 0 and lie within [2^-40, 2^40], far inside bf16's range (sums
     // of 2^17 of them times V overflow past |V| = 2^70).  2 sequences of 5,000 tokens, 64 + 2 x 8 heads of
-    // 128, cap 50: 905 us with every tile's maximum, 778 without.  A tile with larger scores goes the general
+    // 128, cap 50: 905 us with every tile's maximum, 770 without.  A tile with larger scores goes the general
     // way, whose maximum leaves 0 only when it has to.  Not with slopes, whose scores have no lower bound,
     // nor for an item of one tile: a row of one key has the numerator 1 against its maximum, which bf16 holds
     // exactly.
@@ -732,14 +732,12 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
               uint64_t co[TERMS];
 #pragma unroll
               for (int i = 0; i < TERMS; ++i) {
-                const float f = TERMS == 4 ? a.near[i] : a.mid[i];
+                const float f = TERMS == NEAR_TERMS ? a.near[i] : a.mid[i];
                 co[i] = f2_pack(f, f);
               }
-              const uint64_t inv2 = f2_pack(a.cap_inv, a.cap_inv);
 #pragma unroll
               for (int c = 0; c < 128; c += 2) {
-                uint64_t x = f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
-                if (TERMS != 4) x = f2_mul(x, inv2);
+                const uint64_t x = f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
                 const uint64_t u = f2_mul(x, x);
                 uint64_t t = co[TERMS - 1];
 #pragma unroll
@@ -757,11 +755,11 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
                 return;
               }
               over = ST == Mild && within(calm);
-              polynomial(std::integral_constant<int, ST == Calm ? 4 : CAP_TERMS>{});
+              polynomial(std::integral_constant<int, ST == Calm ? NEAR_TERMS : MID_TERMS>{});
             } else if (within(a.cap_near)) {
-              polynomial(std::integral_constant<int, 4>{});
+              polynomial(std::integral_constant<int, NEAR_TERMS>{});
             } else if (within(a.cap_mid)) {
-              polynomial(std::integral_constant<int, CAP_TERMS>{});
+              polynomial(std::integral_constant<int, MID_TERMS>{});
             } else {
 #pragma unroll
               for (int c = 0; c < 128; ++c) sr[c] = __float_as_uint(score_log2<true>(a, __uint_as_float(sr[c])));
