@@ -626,7 +626,7 @@ ink_status_t masked_impl(const ink_attn_params_t* params, const ink_attn_mask_t*
   // reach, or the near one in the other's place.
   static const double kNear[ink::NEAR_TERMS] = {0.9999997567401877, -0.3332946719023333, 0.13236369052154567,
                                                 -0.04602819379882759};
-  static const double kMid[ink::MID_TERMS] = {0.9999994136103072, -0.3332904245054663, 0.1328143441522219,
+  static const double kMid[ink::MID_TERMS] = {0.99999941361031, -0.3332904245054663, 0.1328143441522219,
                                               -0.05160568907876395, 0.01674313284460914, -0.003067067657993291};
   const double inv = mk.softcap > 0.f ? (double)params->sm_scale / mk.softcap : 0.0, ainv = inv < 0 ? -inv : inv;
   a.cap_near = ainv >= 1e-5 && ainv <= 1e3 ? (float)(0.45 / ainv) : -1.f;

@@ -1053,7 +1053,7 @@ cudaError_t launch_prefill_masked(const MaskedMaps& m, const MaskedArgs& a, int 
   if (a.W > 0 && !a.key_end) reach = std::min<long long>(reach, a.W + tpi + PM_KEYS);
   const long long pieces = reach / (PM_KEYS * PM_PIECE_TILES);
   const bool split = items < sms && pieces >= 2;
-  const int grid = (int)std::max(1ll, std::min<long long>(split ? items * pieces : items, sms));
+  const int grid = (int)std::max(1ll, std::min<long long>(split ? items * (pieces + 1) : items, sms));
   return head_dim == 128 ? launch_d<128>(m, a, grid, split, stream) : launch_d<64>(m, a, grid, split, stream);
 }
 
