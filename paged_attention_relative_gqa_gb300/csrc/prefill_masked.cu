@@ -97,8 +97,8 @@ struct PMSmem {
   static constexpr size_t ring = 2 * (size_t)S::TILE;
   static constexpr size_t bars = ring + (size_t)S::NS * S::TILE;
   // k_full[TILES], v_full[TILES], v_ok[TILES], k_ok[TILES], empty[NS], s_full[2], p_full[2], o_full[2], q_full[2], q_empty[2],
-  // item_full[ITEMS], item_empty[ITEMS], drain
-  static constexpr int NBAR = S::NS + 4 * PM_TILES + 10 + 2 * PM_ITEMS + 1;
+  // item_full[ITEMS], item_empty[ITEMS], stored[2], ticket[2], drain
+  static constexpr int NBAR = S::NS + 4 * PM_TILES + 14 + 2 * PM_ITEMS + 1;
   static constexpr size_t items = bars + (NBAR * 8 + 15) / 16 * 16;
   static constexpr size_t kbad = items + PM_ITEMS * sizeof(PMItem);
   static constexpr size_t poison = kbad + PM_BAD * 16;
@@ -156,7 +156,9 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
   uint64_t* q_empty = q_full + 2;       // [2] the item's last S_h product done
   uint64_t* item_full = q_empty + 2;    // [ITEMS]
   uint64_t* item_empty = item_full + PM_ITEMS;
-  uint64_t* drain = item_empty + PM_ITEMS;
+  uint64_t* stored = item_empty + PM_ITEMS;   // [2] a piece's part of row tile h is in the workspace
+  uint64_t* ticket = stored + 2;        // [2] and its ticket is drawn
+  uint64_t* drain = ticket + 2;
   PMItem* items = reinterpret_cast<PMItem*>(smem + L_::items);
   uint32_t* kbad = reinterpret_cast<uint32_t*>(smem + L_::kbad);      // [BAD][4] bit per unreadable key
   volatile int* poison = reinterpret_cast<volatile int*>(smem + L_::poison);   // [ITEMS]
@@ -181,6 +183,8 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
       mbar_init(&o_full[x], 1);
       mbar_init(&q_full[x], 1);
       mbar_init(&q_empty[x], 1);
+      mbar_init(&stored[x], 4);
+      mbar_init(&ticket[x], 1);
     }
     for (int x = 0; x < PM_ITEMS; ++x) {
       mbar_init(&item_full[x], 1);
@@ -661,7 +665,7 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
     // nor for an item of one tile: a row of one key has the numerator 1 against its maximum, which bf16 holds
     // exactly.
     const float reach = CAP && a.slopes == nullptr ? fminf(a.cap_mid, CALM_LOG2 / fabsf(a.scale_log2)) : -1.f;
-    uint32_t sn = 0, on = 0;
+    uint32_t sn = 0, on = 0, jn = 0;
     int g = 0;
     bool go = true;
     for (int k = 0; go; ++k) {
@@ -894,19 +898,28 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
         }
         __stcg(part_ml + (size_t)it.one * 2 * MASKED_ROWS, make_float4(l == 0.f ? -INFINITY : m, l, poisoned ? 1.f : 0.f, 0.f));
         tc_fence_before();
-        // every thread's stores come before the barrier, the ticket's add releases them and acquires
-        // the other pieces'
-        named_barrier_sync(1 + h, 128);
-        if (r == 0) {
-          int prev;
-          asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;"
-                       : "=r"(prev)
-                       : "l"(a.tickets + 2 * it.slot + h)
-                       : "memory");
-          joins[h] = prev == it.np - 1;
-          if (prev == it.np - 1) a.tickets[2 * it.slot + h] = 0;   // ready for the next call
+        // Every thread's stores come before its warp's arrival, the ticket's add releases them and acquires
+        // the other pieces'.  (Barriers whose waits are bounded: after a timeout a warp may be gone.)
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&stored[h]);
+        if ((warp & 3) == 0) {
+          go = pm_wait(&stored[h], jn & 1u, abort_flag, a);
+          if (!go) break;
+          if (lane == 0) {
+            int prev;
+            asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;"
+                         : "=r"(prev)
+                         : "l"(a.tickets + 2 * it.slot + h)
+                         : "memory");
+            joins[h] = prev == it.np - 1;
+            if (prev == it.np - 1) a.tickets[2 * it.slot + h] = 0;   // ready for the next call
+            mbar_arrive(&ticket[h]);
+          }
+          __syncwarp();
         }
-        named_barrier_sync(1 + h, 128);
+        go = pm_wait(&ticket[h], jn & 1u, abort_flag, a);
+        if (!go) break;
+        ++jn;
         if (!joins[h]) {
           done_item(k);
           continue;
