@@ -363,7 +363,7 @@ typedef struct {
  * Rows from cu_q_lens[B] on belong to no request and are left as they were.  A request with
  * n_b > L_b (INK_DEVERR_QLEN_EXCEEDS_KV) has its rows skipped; a page id outside [0, num_pages)
  * (INK_DEVERR_PAGE_OUT_OF_RANGE) has the K/V rows of its keys skipped.  Two rows that name the
- * same slot (requests sharing a page they write to) race: either row may be kept.
+ * same slot (requests sharing a page they write to) race: each 16 bytes of the slot hold either row's.
  */
 ink_status_t inkling_attn_qk_norm_rope_write(const ink_attn_params_t* params, const ink_norm_rope_t* rope,
                                              const void* q, int64_t q_stride, const void* k, int64_t k_stride,
