@@ -529,3 +529,26 @@ def test_offsets_that_change_between_replays(cuda_device):
         torch.cuda.synchronize()
         assert binding.inkling_attn_read_device_error(ws) == 0
         check(out, lse, reference(prob, opts), f"replayed with {q_lens}")
+
+
+@pytest.mark.parametrize("softcap", [5.0, 30.0, 50.0, 300.0])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("q_lens,seq_lens", [([200, 33], [1500, 900]), ([3, 18], [4000, 2500])])
+def test_tiles_of_small_and_large_scores_in_turn(cuda_device, softcap, dim, q_lens, seq_lens):
+    """The magnitude of the keys changes from one 128-key tile to the next, so that tiles within the short
+    polynomial's reach, within the cap and beyond it follow one another in every order; the first rows of a
+    sequence begin to see keys at different tiles."""
+    prob = problem((8, 2), dim, 64, q_lens, seq_lens, 32, cuda_device, q_std=1.5)
+    table = prob.block_table.cpu().numpy()
+    factors = [0.1, 3.0, 20.0, 0.3, 0.3, 8.0, 3.0, 3.0, 0.1, 40.0, 20.0]
+    for b, L in enumerate(seq_lens):
+        for j in range((L + 63) // 64):
+            prob.k_cache[int(table[b, j])] *= factors[(j // 2 + 3 * b) % len(factors)]
+    rng = np.random.default_rng(33)
+    first = np.concatenate([rng.integers(0, L - n + 1, n) for n, L in zip(q_lens, seq_lens)])
+    for begin in (None, first):
+        opts = options(prob, softcap=softcap, begin=begin)
+        out, lse, ws = call(prob, opts, False)
+        torch.cuda.synchronize()
+        assert binding.inkling_attn_read_device_error(ws) == 0
+        check(out, lse, reference(prob, opts), f"cap {softcap}")
