@@ -135,12 +135,19 @@ struct Walk {
   }
 };
 
+// Bounded wait of a whole warp, with one answer for all its lanes: each reads the flag, the barrier
+// and the clock for itself, and what follows (matrix products, shuffles, branches around them) takes
+// the warp whole.
 __device__ __forceinline__ bool dm_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, const MaskedArgs& a) {
-  if (*abort_flag) return false;
-  if (mbar_wait_limit(bar, parity, a.wait_ns)) return true;
-  record_error(a.err, INK_DEVERR_WAIT_TIMEOUT);
-  *abort_flag = 1;
-  return false;
+  bool ok = false;
+  if (!*abort_flag) {
+    ok = mbar_wait_limit(bar, parity, a.wait_ns);
+    if (!ok) {
+      record_error(a.err, INK_DEVERR_WAIT_TIMEOUT);
+      *abort_flag = 1;
+    }
+  }
+  return __all_sync(0xffffffffu, ok);
 }
 
 // The piece's partial is in the workspace: take the group's ticket (a CTA's run is the start of one cut
@@ -265,7 +272,7 @@ decode_masked_kernel(const __grid_constant__ DecodeMaps maps, const __grid_const
       int cbase = ((w.tile * TILE_KEYS) >> a.log2_page) & ~7;
       int cur = __ldg(bt + min(cbase + lane, last)), nxt = __ldg(bt + min(cbase + 32 + lane, last));
       if (uc >= 2) {
-        go = __all_sync(0xffffffffu, dm_wait(&qempty[slot], (uint32_t)((uc >> 1) - 1) & 1u, abort_flag, a));
+        go = dm_wait(&qempty[slot], (uint32_t)((uc >> 1) - 1) & 1u, abort_flag, a);
         if (!go) break;
       }
       for (int i = 0; i < w.n; ++i, ++n) {
@@ -286,7 +293,7 @@ decode_masked_kernel(const __grid_constant__ DecodeMaps maps, const __grid_const
         const bool whole = P >= TILE_KEYS && lmask == (1u << nseg) - 1u;
         const int row = load ? page * hkvp + (w.kvh << a.log2_page) + (ks & (P - 1)) : 0;
         if (n >= NSTAGE) {
-          go = __all_sync(0xffffffffu, dm_wait(&empty[st], (uint32_t)((n / NSTAGE) - 1) & 1u, abort_flag, a));
+          go = dm_wait(&empty[st], (uint32_t)((n / NSTAGE) - 1) & 1u, abort_flag, a);
           if (!go) break;
         }
         uint8_t* kdst = smem + (size_t)st * S::STAGE;

@@ -1,0 +1,59 @@
+"""Bounded waits whose answer steers a warp, read from the kernels' sources (no GPU).
+
+A bounded wait can end differently for the lanes of a warp: each reads the abort flag, the barrier and
+the clock for itself.  Code behind it that takes the warp whole (matrix products, shuffles, full-mask
+barriers) needs one answer, so outside the helper functions a per-lane wait stands under __all_sync, or
+in one lane alone whose answer is shuffled to the others."""
+import os
+import re
+
+import pytest
+
+from paged_attention_relative_gqa_gb300 import build
+
+VOTED = ["decode_masked.cu"]
+
+
+def code(name):
+    with open(os.path.join(build.CSRC, name)) as f:
+        return re.sub(r"//[^\n]*", "", f.read())
+
+
+def functions(src):
+    """(name, body) of the inline device functions, and what is left of the source without them."""
+    found, rest, at = [], "", 0
+    for m in re.finditer(r"__device__\s+(?:__forceinline__|__noinline__)\s+[\w:]+\s+(\w+)\([^)]*\)\s*\{", src):
+        if m.start() < at:
+            continue
+        depth, end = 1, m.end()
+        while depth:
+            depth += {"{": 1, "}": -1}.get(src[end], 0)
+            end += 1
+        found.append((m.group(1), src[m.end():end - 1]))
+        rest += src[at:m.start()]
+        at = end
+    return found, rest + src[at:]
+
+
+def lone_waits(src):
+    """Statements outside the helpers that wait by lane: neither voted on nor made by lane 0 alone."""
+    helpers, rest = functions(src)
+    by_lane = {"mbar_wait_limit"}
+    for name, body in helpers:
+        if "__all_sync" not in body and any(w + "(" in body for w in by_lane):
+            by_lane.add(name)
+    call = re.compile(r"\b(?:%s)\(" % "|".join(sorted(by_lane)))
+    return [s.strip() for s in re.split(r"[;{}]", rest) if call.search(s) and "__all_sync" not in s and "lane == 0" not in s]
+
+
+def test_the_reader_of_sources():
+    helper = "__device__ __forceinline__ bool w(int* p) { if (*p) { return mbar_wait_limit(p); } return true; }"
+    voted = helper.replace("return true", "return __all_sync(~0u, *p)")
+    assert lone_waits(helper + "void k() { const bool ok = w(p); }") == ["const bool ok = w(p)"]
+    assert lone_waits(helper + "void k() { ok = __all_sync(~0u, w(p)); if (lane == 0) ok = w(p); }") == []
+    assert lone_waits(voted + "void k() { ok = w(p); if (n) ok = mbar_wait_limit(p); }") == ["if (n) ok = mbar_wait_limit(p)"]
+
+
+@pytest.mark.parametrize("name", VOTED)
+def test_waits_of_a_warp_have_one_answer(name):
+    assert lone_waits(code(name)) == []
