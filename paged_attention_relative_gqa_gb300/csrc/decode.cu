@@ -518,8 +518,10 @@ decode_persistent_kernel(const __grid_constant__ CUtensorMap tmKs, const __grid_
 
     for (int i = 0; i < cur.n_my; ++i, ++n) {
       const int st = n % NSTAGE;
-      const bool ok = wait_or_abort(&full[st], (uint32_t)(n / NSTAGE) & 1u, abort_flag, a.err, a.wait_ns) &&
-                      wait_or_abort(&bfull[n % BIAS_SLOTS], (uint32_t)(n / BIAS_SLOTS) & 1u, abort_flag, a.err, a.wait_ns);
+      // (one answer for the warp: its lanes wait each for itself, the products take it whole)
+      const bool ok = __all_sync(0xffffffffu,
+          wait_or_abort(&full[st], (uint32_t)(n / NSTAGE) & 1u, abort_flag, a.err, a.wait_ns) &&
+          wait_or_abort(&bfull[n % BIAS_SLOTS], (uint32_t)(n / BIAS_SLOTS) & 1u, abort_flag, a.err, a.wait_ns));
       if (i == 0) {
         const uint32_t qbase = smem_u32(smem + L_::q + qslot * S::QSLOT_BYTES);
 #pragma unroll
