@@ -272,7 +272,7 @@ decode_masked_kernel(const __grid_constant__ DecodeMaps maps, const __grid_const
       int cbase = ((w.tile * TILE_KEYS) >> a.log2_page) & ~7;
       int cur = __ldg(bt + min(cbase + lane, last)), nxt = __ldg(bt + min(cbase + 32 + lane, last));
       if (uc >= 2) {
-        go = dm_wait(&qempty[slot], (uint32_t)((uc >> 1) - 1) & 1u, abort_flag, a);
+        go = __all_sync(0xffffffffu, dm_wait(&qempty[slot], (uint32_t)((uc >> 1) - 1) & 1u, abort_flag, a) && !*abort_flag);
         if (!go) break;
       }
       for (int i = 0; i < w.n; ++i, ++n) {
@@ -293,7 +293,7 @@ decode_masked_kernel(const __grid_constant__ DecodeMaps maps, const __grid_const
         const bool whole = P >= TILE_KEYS && lmask == (1u << nseg) - 1u;
         const int row = load ? page * hkvp + (w.kvh << a.log2_page) + (ks & (P - 1)) : 0;
         if (n >= NSTAGE) {
-          go = dm_wait(&empty[st], (uint32_t)((n / NSTAGE) - 1) & 1u, abort_flag, a);
+          go = __all_sync(0xffffffffu, dm_wait(&empty[st], (uint32_t)((n / NSTAGE) - 1) & 1u, abort_flag, a) && !*abort_flag);
           if (!go) break;
         }
         uint8_t* kdst = smem + (size_t)st * S::STAGE;
@@ -389,11 +389,18 @@ decode_masked_kernel(const __grid_constant__ DecodeMaps maps, const __grid_const
     for (int i = 0; i < w.n; ++i, ++n) {
       const int st = n % NSTAGE;
       const bool ok = dm_wait(&full[st], (uint32_t)(n / NSTAGE) & 1u, abort_flag, a);
+      // The copies of a tile whose wait ran out may be in flight: its stage and Q slot are not handed
+      // back (its barrier would be armed a second time, and the loader's last waits would not know which
+      // copies they wait for).  The rest of the run is left out.
+      if (!ok) {
+        n += w.n - i;
+        break;
+      }
       if (i == 0) {
         const uint32_t qbase = smem_u32(smem + L_::q + (uc & 1) * S::QSLOT);
 #pragma unroll
         for (int j = 0; j < NB; ++j) {
-          const bool hv = ok && 8 * j + gq < w.nh;
+          const bool hv = 8 * j + gq < w.nh;
 #pragma unroll
           for (int kk = 0; kk < KSTEPS; kk += 2) {
             const int chunk = 2 * kk + mi;
@@ -409,7 +416,7 @@ decode_masked_kernel(const __grid_constant__ DecodeMaps maps, const __grid_const
         if (lane == 0) mbar_arrive(&qempty[uc & 1]);
       }
       const int kw = (w.tile + i) * TILE_KEYS + 16 * warp;
-      const uint64_t bad = ok ? badmask[st] : ~0ull;
+      const uint64_t bad = badmask[st];
       const int jlo = max(w.lo - kw, 0), jhi = min(w.hi - 1 - kw, 15);
       uint32_t valid = jhi >= jlo ? ((0xFFFFu >> (15 - jhi)) & (0xFFFFu << jlo)) : 0u;
       valid &= ~(uint32_t)(bad >> (16 * warp)) & 0xFFFFu;

@@ -1,0 +1,52 @@
+"""Waits that run out somewhere in a call: limits between none and the default.
+
+A call ends in any case.  Without an error bit it gives what it gives otherwise, bit for bit; with one
+it reports the timeout and no other error, and the next calls are right."""
+import pytest
+import torch
+
+from paged_attention_relative_gqa_gb300 import binding
+from tests.masked_common import call, check, options, problem, reference
+
+pytestmark = pytest.mark.gpu
+LIMITS = [0, 1, 300, 1000, 2000, 4000, 8000, 16000, 40000]
+DEFAULT_LIMIT_NS = 2_000_000_000
+
+
+@pytest.fixture
+def limit():
+    yield binding.inkling_attn_set_wait_limit_ns
+    torch.cuda.synchronize()
+    binding.inkling_attn_set_wait_limit_ns(DEFAULT_LIMIT_NS)
+
+
+def sweep(limit, run, ws):
+    """`run` (its outputs as a tuple) under every limit, three times each."""
+    want = [x.clone() for x in run()]
+    assert binding.inkling_attn_read_device_error(ws) == 0
+    ran_out = 0
+    for ns in LIMITS:
+        for _ in range(3):
+            limit(ns)
+            got = run()
+            err = binding.inkling_attn_read_device_error(ws)
+            assert err in (0, binding.DEVERR_WAIT_TIMEOUT)
+            ran_out += err != 0
+            if not err:
+                assert all(torch.equal(a, b) for a, b in zip(got, want)), f"limit {ns} ns"
+            limit(DEFAULT_LIMIT_NS)
+            got = run()
+            assert binding.inkling_attn_read_device_error(ws) == 0
+            assert all(torch.equal(a, b) for a, b in zip(got, want)), f"after a limit of {ns} ns"
+    assert ran_out
+
+
+@pytest.mark.parametrize("heads,dim,page,softcap", [((8, 2), 128, 64, 0.0), ((16, 1), 128, 16, 20.0), ((8, 8), 64, 8, 0.0)])
+def test_masked_decode(cuda_device, limit, heads, dim, page, softcap):
+    seq_lens = [1500 + 97 * i for i in range(24)]
+    prob = problem(heads, dim, page, [1] * 24, seq_lens, 50, cuda_device)
+    opts = options(prob, softcap=softcap)
+    ws = binding.alloc_masked_workspace(binding.params_of(prob), True, cuda_device)
+    out, lse, _ = call(prob, opts, True, workspace=ws)
+    check(out, lse, reference(prob, opts), "before")
+    sweep(limit, lambda: call(prob, opts, True, workspace=ws)[:2], ws)

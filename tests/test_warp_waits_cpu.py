@@ -11,6 +11,7 @@ import pytest
 
 from paged_attention_relative_gqa_gb300 import build
 
+RINGS = ["decode_masked.cu"]
 VOTED = ["decode_masked.cu", "decode.cu"]
 
 
@@ -57,3 +58,15 @@ def test_the_reader_of_sources():
 @pytest.mark.parametrize("name", VOTED)
 def test_waits_of_a_warp_have_one_answer(name):
     assert lone_waits(code(name)) == []
+
+
+@pytest.mark.parametrize("name", RINGS)
+def test_a_stage_is_handed_back_only_after_a_wait_that_succeeded(name):
+    """The wait for a tile is followed at once by the way out, before any arrival that frees its stage, and the
+    loader looks at the abort flag again after a stage or a Q slot has come back."""
+    src = code(name)
+    waits = [m for m in re.finditer(r"const bool ok = [^;]*&full\[[^;]*;", src)]
+    assert len(waits) == 1
+    assert re.match(r"\s*if \(!ok\) \{[^{}]*break;\s*\}", src[waits[0].end():])
+    frees = [s for s in re.split(r"[;{}]", src) if re.search(r"wait\w*\(&q?empty", s)]
+    assert len(frees) == 2 and all("&& !*abort_flag" in s for s in frees)
