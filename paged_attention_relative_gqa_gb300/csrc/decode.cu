@@ -338,13 +338,15 @@ decode_persistent_kernel(const __grid_constant__ CUtensorMap tmKs, const __grid_
         tma_prefetch_l2_4d(&tmVt, 0, 0, 0, row >> 4);
       };
       if (uc >= 2) {
-        if (lane == 0) go = wait_or_abort(&qempty[slot], (uint32_t)((uc >> 1) - 1) & 1u, abort_flag, a.err, a.wait_ns);
+        if (lane == 0)
+          go = wait_or_abort(&qempty[slot], (uint32_t)((uc >> 1) - 1) & 1u, abort_flag, a.err, a.wait_ns) && !*abort_flag;
         go = __shfl_sync(0xffffffffu, go ? 1 : 0, 0) != 0;
       }
       for (int i = 0; i < cur.n_my && go; ++i, ++n) {
         const int st = n % NSTAGE;
         if (n >= NSTAGE) {
-          if (lane == 0) go = wait_or_abort(&empty[st], (uint32_t)((n / NSTAGE) - 1) & 1u, abort_flag, a.err, a.wait_ns);
+          if (lane == 0)
+            go = wait_or_abort(&empty[st], (uint32_t)((n / NSTAGE) - 1) & 1u, abort_flag, a.err, a.wait_ns) && !*abort_flag;
           go = __shfl_sync(0xffffffffu, go ? 1 : 0, 0) != 0;
           if (!go) break;
         }
@@ -522,11 +524,18 @@ decode_persistent_kernel(const __grid_constant__ CUtensorMap tmKs, const __grid_
       const bool ok = __all_sync(0xffffffffu,
           wait_or_abort(&full[st], (uint32_t)(n / NSTAGE) & 1u, abort_flag, a.err, a.wait_ns) &&
           wait_or_abort(&bfull[n % BIAS_SLOTS], (uint32_t)(n / BIAS_SLOTS) & 1u, abort_flag, a.err, a.wait_ns));
+      // The copies of a tile whose wait ran out may be in flight: its stage and Q slot are not handed
+      // back (its barrier would be armed a second time), nor is its bias slot filled again.  The rest of
+      // the unit is left out.
+      if (!ok) {
+        n += cur.n_my - i;
+        break;
+      }
       if (i == 0) {
         const uint32_t qbase = smem_u32(smem + L_::q + qslot * S::QSLOT_BYTES);
 #pragma unroll
         for (int j = 0; j < NB; ++j) {
-          const bool hv = ok && 8 * j + gq < cur.nh;
+          const bool hv = 8 * j + gq < cur.nh;
 #pragma unroll
           for (int kk = 0; kk < KSTEPS; kk += 2) {
             const int row = 8 * j + (lane & 7);
@@ -543,7 +552,7 @@ decode_persistent_kernel(const __grid_constant__ CUtensorMap tmKs, const __grid_
         if (lane == 0) mbar_arrive(&qempty[qslot]);
       }
       const int kw = (cur.tb + i) * TILE_KEYS + 16 * warp;
-      const uint64_t bad = ok ? badmask[st] : ~0ull;
+      const uint64_t bad = badmask[st];
       // keys kw + j (j < 16) with lo <= key <= p, minus keys of unreadable pages
       const int jlo = max(cur.lo - kw, 0), jhi = min(cur.p - kw, 15);
       uint32_t valid16 = jhi >= jlo ? ((0xFFFFu >> (15 - jhi)) & (0xFFFFu << jlo)) : 0u;

@@ -6,7 +6,9 @@ import pytest
 import torch
 
 from paged_attention_relative_gqa_gb300 import binding
+from paged_attention_relative_gqa_gb300 import workloads as W
 from tests.masked_common import call, check, options, problem, reference
+from tests.parity import compare, oracle_full
 
 pytestmark = pytest.mark.gpu
 LIMITS = [0, 1, 300, 1000, 2000, 4000, 8000, 16000, 40000]
@@ -50,3 +52,15 @@ def test_masked_decode(cuda_device, limit, heads, dim, page, softcap):
     out, lse, _ = call(prob, opts, True, workspace=ws)
     check(out, lse, reference(prob, opts), "before")
     sweep(limit, lambda: call(prob, opts, True, workspace=ws)[:2], ws)
+
+
+@pytest.mark.parametrize("heads,dim,page,window", [((16, 4), 128, 64, 512), ((32, 2), 64, 16, -1), ((16, 4), 128, 8, -1)])
+def test_decode_with_a_bias(cuda_device, limit, heads, dim, page, window):
+    prob = W.make_problem(num_q_heads=heads[0], num_kv_heads=heads[1], head_dim=dim, page_size=page, rel_extent=512,
+                          window=window, q_lens=[1] * 24, seq_lens=[1500 + 97 * i for i in range(24)], seed=51,
+                          device=cuda_device)
+    params = binding.params_of(prob)
+    ws = binding.alloc_workspace(params, True, cuda_device)
+    run = lambda: (binding.run(prob, out=torch.zeros_like(prob.q), workspace=ws),)
+    compare(run()[0].float().cpu().numpy(), oracle_full(prob), "before")
+    sweep(limit, run, ws)

@@ -11,7 +11,7 @@ import pytest
 
 from paged_attention_relative_gqa_gb300 import build
 
-RINGS = ["decode_masked.cu"]
+RINGS = ["decode_masked.cu", "decode.cu"]
 VOTED = ["decode_masked.cu", "decode.cu"]
 
 
