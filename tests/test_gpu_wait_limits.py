@@ -64,3 +64,17 @@ def test_decode_with_a_bias(cuda_device, limit, heads, dim, page, window):
     run = lambda: (binding.run(prob, out=torch.zeros_like(prob.q), workspace=ws),)
     compare(run()[0].float().cpu().numpy(), oracle_full(prob), "before")
     sweep(limit, run, ws)
+
+
+@pytest.mark.parametrize("form,heads,dim,page,extent", [
+    ("lowrank", (8, 2), 128, 64, 1024), ("lowrank", (4, 4), 64, 16, 300), ("fp32", (8, 2), 128, 64, 1024),
+    ("fp32", (4, 2), 64, 8, 301), ("bf16", (8, 8), 128, 64, 1024), ("bf16", (3, 1), 64, 32, 96)])
+def test_prefill_with_a_bias(cuda_device, limit, form, heads, dim, page, extent):
+    kw = {"lowrank": dict(lowrank_d=64), "fp32": {}, "bf16": dict(bias_dtype=torch.bfloat16)}[form]
+    prob = W.make_problem(num_q_heads=heads[0], num_kv_heads=heads[1], head_dim=dim, page_size=page, rel_extent=extent,
+                          window=-1, q_lens=[300, 130], seq_lens=[300, 900], seed=52, device=cuda_device, **kw)
+    params = binding.params_of(prob)
+    ws = binding.alloc_workspace(params, True, cuda_device)
+    run = lambda: (binding.run(prob, out=torch.zeros_like(prob.q), workspace=ws),)
+    compare(run()[0].float().cpu().numpy(), oracle_full(prob), "before")
+    sweep(limit, run, ws)

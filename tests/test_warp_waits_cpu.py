@@ -12,7 +12,7 @@ import pytest
 from paged_attention_relative_gqa_gb300 import build
 
 RINGS = ["decode_masked.cu", "decode.cu"]
-VOTED = ["decode_masked.cu", "decode.cu"]
+VOTED = ["decode_masked.cu", "decode.cu", "prefill_tc.cu"]
 
 
 def code(name):
@@ -70,3 +70,11 @@ def test_a_stage_is_handed_back_only_after_a_wait_that_succeeded(name):
     assert re.match(r"\s*if \(!ok\) \{[^{}]*break;\s*\}", src[waits[0].end():])
     frees = [s for s in re.split(r"[;{}]", src) if re.search(r"wait\w*\(&q?empty", s)]
     assert len(frees) == 2 and all("&& !*abort_flag" in s for s in frees)
+
+
+def test_loaders_of_the_prefill_fill_no_slot_after_an_abort():
+    """There warps whose waits ran out go on handing slots back: whoever fills them looks at the flag again."""
+    src = code("prefill_tc.cu")
+    assert re.search(r"bool wait_slot\([^{]*\{\s*return wait_flag\([^;]*&& !\*abort_flag;", src)
+    for slot in (r"q_empty", r"&empty\[st\]", r"&b_empty\[slot\]", r"bc_empty"):
+        assert re.findall(r"\b(wait_\w+)\(%s," % slot, src) == ["wait_slot"], slot
