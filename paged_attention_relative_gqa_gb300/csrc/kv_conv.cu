@@ -355,7 +355,8 @@ __global__ void __launch_bounds__(KVS_THREADS, 1) kv_conv_staged_kernel(const Kv
     int issued = 0;
     for (int u = blockIdx.x + ps * gridDim.x; u < units; u += NS * gridDim.x, k += NS) {
       const int s = ps;
-      if (k >= NS && !mbar_wait_limit(&empty[s], ((k / NS) - 1) & 1, a.wait_ns)) {
+      // (one answer for the warp, here and below: its lanes wait each for itself)
+      if (k >= NS && !__all_sync(0xffffffffu, mbar_wait_limit(&empty[s], ((k / NS) - 1) & 1, a.wait_ns))) {
         if (lane == 0) record_error(a.err, INK_DEVERR_WAIT_TIMEOUT);
         *reinterpret_cast<volatile int*>(abort_flag) = 1;
         break;
@@ -439,11 +440,9 @@ __global__ void __launch_bounds__(KVS_THREADS, 1) kv_conv_staged_kernel(const Kv
   int k = 0;
   for (int u = blockIdx.x; u < units; u += gridDim.x, ++k) {
     const int s = k % NS;
-    const bool ok = mbar_wait_limit(&full[s], (k / NS) & 1, a.wait_ns);
-    if (!ok || *reinterpret_cast<volatile int*>(abort_flag)) {
-      if (!ok) record_error(a.err, INK_DEVERR_WAIT_TIMEOUT);
-      break;
-    }
+    const bool ok = __all_sync(0xffffffffu, mbar_wait_limit(&full[s], (k / NS) & 1, a.wait_ns));
+    if (!ok && lane == 0) record_error(a.err, INK_DEVERR_WAIT_TIMEOUT);
+    if (__any_sync(0xffffffffu, !ok || *reinterpret_cast<volatile int*>(abort_flag))) break;
     const int z = u & 1, tile = u >> 1;
     const int t0 = tile * TT;
     const int n_tile = min(a.T, t0 + TT) - t0;

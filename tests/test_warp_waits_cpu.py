@@ -12,7 +12,7 @@ import pytest
 from paged_attention_relative_gqa_gb300 import build
 
 RINGS = ["decode_masked.cu", "decode.cu"]
-VOTED = ["decode_masked.cu", "decode.cu", "prefill_tc.cu"]
+VOTED = ["decode_masked.cu", "decode.cu", "prefill_tc.cu", "kv_conv.cu", "prefill_pair.cu", "prefill_masked.cu"]
 
 
 def code(name):
