@@ -311,6 +311,10 @@ decode_persistent_kernel(const __grid_constant__ CUtensorMap tmKs, const __grid_
     int n = 0, uc = 0;
     bool go = true;
     while (ucur < total_units && go) {
+      // The slice staged below goes over the one of the unit before: lane 0 has read that first.
+      // (Without this the other lanes, which meet it only where a stage has to be waited for, ran units
+      // ahead of it: with pages of less than 64 keys tiles came from other sequences' pages.)
+      __syncwarp();
       const int unxt2 = unxt < total_units ? next_active(unxt + gridDim.x, nxt2) : total_units;
       stage_ptab(unxt2 < total_units ? &nxt2 : nullptr, (uc + 2) % 3);
       asm volatile("cp.async.wait_group 1;" ::: "memory");
