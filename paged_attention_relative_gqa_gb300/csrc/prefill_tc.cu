@@ -262,6 +262,8 @@ __device__ __forceinline__ void lr_advance(const PrefillArgs& a, int total_items
 
 // A completed phase returns at once; otherwise give up at once if another warp of the
 // CTA has timed out, else wait (bounded) and on a timeout record it and tell the others.
+// Each lane answers for itself.  Where the answer steers code that takes a warp whole
+// (products, full-mask barriers, loads by one lane for all), the warp votes on it first.
 __device__ __forceinline__ bool wait_flag(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t* err,
                                           unsigned long long limit_ns) {
   if (mbar_probe(bar, parity, limit_ns)) return true;
@@ -270,20 +272,6 @@ __device__ __forceinline__ bool wait_flag(uint64_t* bar, uint32_t parity, volati
   record_error(err, INK_DEVERR_WAIT_TIMEOUT);
   *abort_flag = 1;
   return false;
-}
-
-// The same for a whole warp, with one answer for all its lanes: each reads the barrier, the flag and the
-// clock for itself, and what follows (tensor-memory loads, products, barriers) takes the warp whole.
-__device__ __forceinline__ bool wait_flag_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t* err,
-                                               unsigned long long limit_ns) {
-  return __all_sync(0xffffffffu, wait_flag(bar, parity, abort_flag, err, limit_ns));
-}
-
-// A loader's wait for a slot (all lanes, or one alone).  Warps whose waits ran out go on handing slots
-// back, of copies that may be in flight: after an abort none is filled again.
-__device__ __forceinline__ bool wait_slot(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t* err,
-                                          unsigned long long limit_ns) {
-  return wait_flag(bar, parity, abort_flag, err, limit_ns) && !*abort_flag;
 }
 
 template <int D, int BM>
@@ -404,10 +392,12 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       if (!get_item(a, i, it) || it.ntile == 0) continue;
       if (is_k) {
         bool ok = true;
-        if (lane == 0 && icount > 0) ok = wait_slot(q_empty, (uint32_t)(icount - 1) & 1u, abort_flag, a.err, a.wait_ns);
-        if (lane == 0 && ok) {
-          mbar_arrive_expect_tx(q_full, (uint32_t)S::Q_BYTES);
-          tma_load_3d(smem + L_::q, &tmQ3, 0, it.t0, it.h * S::CB, q_full);   // 128 rows x all column blocks
+        if (lane == 0) {
+          ok = icount == 0 || wait_flag(q_empty, (uint32_t)(icount - 1) & 1u, abort_flag, a.err, a.wait_ns);
+          if (ok) {
+            mbar_arrive_expect_tx(q_full, (uint32_t)S::Q_BYTES);
+            tma_load_3d(smem + L_::q, &tmQ3, 0, it.t0, it.h * S::CB, q_full);   // 128 rows x all column blocks
+          }
         }
         if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) break;
         ++q_issued;
@@ -417,7 +407,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       for (int j = 0; j < it.ntile; ++j, ++g) {
         const int st = g % NR;
         bool ok = true;
-        if (lane == 0 && g >= NR) ok = wait_slot(&empty[st], (uint32_t)((g / NR) - 1) & 1u, abort_flag, a.err, a.wait_ns);
+        if (lane == 0 && g >= NR) ok = wait_flag(&empty[st], (uint32_t)((g / NR) - 1) & 1u, abort_flag, a.err, a.wait_ns);
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
         if (!ok) {
           go = false;
@@ -491,13 +481,14 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
     for (int i = blockIdx.x; i < total_items && go; i += gridDim.x) {
       PItem it;
       if (!get_item(a, i, it) || it.ntile == 0) continue;
-      go = wait_flag_warp(q_full, (uint32_t)icount & 1u, abort_flag, a.err, a.wait_ns);
+      go = __all_sync(0xffffffffu, wait_flag(q_full, (uint32_t)icount & 1u, abort_flag, a.err, a.wait_ns));
 #pragma unroll 1
       for (int j = 0; j < it.ntile && go; ++j, ++g) {
         const int ks_ = g % NK;
-        go = wait_flag_warp(&k_full[ks_], (uint32_t)(g / NK) & 1u, abort_flag, a.err, a.wait_ns);
+        go = __all_sync(0xffffffffu, wait_flag(&k_full[ks_], (uint32_t)(g / NK) & 1u, abort_flag, a.err, a.wait_ns));
         if (go && g >= 2)
-          go = wait_flag_warp(&s_empty[g & 1], (uint32_t)((g >> 1) - 1) & 1u, abort_flag, a.err, a.wait_ns);
+          go = __all_sync(0xffffffffu,
+                          wait_flag(&s_empty[g & 1], (uint32_t)((g >> 1) - 1) & 1u, abort_flag, a.err, a.wait_ns));
         if (!go) break;   // after an abort no MMA is issued
         tc_fence_after();
         const uint32_t qbase = smem_u32(smem + L_::q);
@@ -561,19 +552,19 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
         bool ok = true;
         // the product of chunk n - 1 has been read out of TMEM: its MMA is complete, so
         // TMEM, the r rows and chunk slot (n - 1) % 3 are free
-        if (n >= 1)
-          ok = __all_sync(0xffffffffu, wait_slot(bc_empty, (uint32_t)(n - 1) & 1u, abort_flag, a.err, a.wait_ns));
+        if (n >= 1) ok = wait_flag(bc_empty, (uint32_t)(n - 1) & 1u, abort_flag, a.err, a.wait_ns);
         if (ok && cur.first) {
           if (lane == 0) {
             mbar_arrive_expect_tx(r_full, (uint32_t)(PT_ROWS * LOWRANK_MAX_D * 2));
             tma_load_3d(smem + L_::lr_r, &tmR, 0, cur.it.h, cur.it.t0, r_full);
           }
           r_pending = true;
-          ok = wait_flag_warp(r_full, (uint32_t)ritems & 1u, abort_flag, a.err, a.wait_ns);
+          ok = wait_flag(r_full, (uint32_t)ritems & 1u, abort_flag, a.err, a.wait_ns);
           ++ritems;
           r_pending = !ok;
         }
-        if (ok) ok = wait_flag_warp(&pt_full[n % 3], (uint32_t)(n / 3) & 1u, abort_flag, a.err, a.wait_ns);
+        ok = __all_sync(0xffffffffu,
+                        ok && wait_flag(&pt_full[n % 3], (uint32_t)(n / 3) & 1u, abort_flag, a.err, a.wait_ns));
         if (!ok) break;
         tc_fence_after();
         const uint32_t rb = smem_u32(smem + L_::lr_r);
@@ -623,8 +614,11 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
         const int slot = (g & 1) * BS::PER_WG + u % BS::PER_WG, use = u / BS::PER_WG;
         BT* sb = reinterpret_cast<BT*>(smem + L_::bias + (size_t)slot * BS::SLOT_BYTES);
         const int dmin0 = it.pos0 - (k0 + TILE_KEYS - 1);
+        // (softmax warps go on handing slots back after a wait for a fill has run out: none is filled
+        // again after an abort)
         if (use >= 1 &&
-            !__all_sync(0xffffffffu, wait_slot(&b_empty[slot], (uint32_t)(use - 1) & 1u, abort_flag, a.err, a.wait_ns))) {
+            !__all_sync(0xffffffffu, wait_flag(&b_empty[slot], (uint32_t)(use - 1) & 1u, abort_flag, a.err, a.wait_ns) &&
+                                         !*abort_flag)) {
           go = false;
           break;
         }
@@ -696,7 +690,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
           const int nch = j == jb ? 3 : 1;
 #pragma unroll 1
           for (int m = 0; m < nch; ++m) {
-            const bool ok = wait_flag_warp(bc_full, (uint32_t)n & 1u, abort_flag, a.err, a.wait_ns);
+            (void)wait_flag(bc_full, (uint32_t)n & 1u, abort_flag, a.err, a.wait_ns);   // (after an abort: any values)
             ++n;
             tc_fence_after();
             uint32_t h[32];   // this row's 64 buckets of the chunk, fp16 pairs
@@ -715,7 +709,6 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bc_empty);   // TMEM may take the next product
-            if (!ok) continue;
             const int off0 = j == jb ? LOWRANK_CHUNK * m : 0;   // the chunk's offset in tile t's window
 #pragma unroll 1
             for (int k = 0; k < 3; ++k) {
@@ -723,7 +716,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
               if (off >= 3 * LOWRANK_CHUNK || j + k >= it.ntile) break;
               const int tt = t + k, sl = tt & 3;
               if (tt > waited) {
-                if (tt >= 4) (void)wait_flag_warp(&b_empty[sl], (uint32_t)((tt >> 2) - 1) & 1u, abort_flag, a.err, a.wait_ns);
+                if (tt >= 4) (void)wait_flag(&b_empty[sl], (uint32_t)((tt >> 2) - 1) & 1u, abort_flag, a.err, a.wait_ns);
                 waited = tt;
               }
               __half* dst = reinterpret_cast<__half*>(smem + L_::bias + (size_t)sl * BS::SLOT_BYTES) +
@@ -841,7 +834,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
         const uint32_t bpar = BM == BM_LOWRANK ? (uint32_t)(my_bt >> 2) & 1u : (uint32_t)(buse / BS::PER_WG) & 1u;
         const BT* bslot = reinterpret_cast<const BT*>(smem + L_::bias + (size_t)bslot_i * BS::SLOT_BYTES);
         uint64_t bad = item_bad ? tile_bad(k0) : 0ull;
-        bool ok = wait_flag_warp(&s_full[g & 1], (uint32_t)(g >> 1) & 1u, abort_flag, a.err, a.wait_ns);
+        bool ok = wait_flag(&s_full[g & 1], (uint32_t)(g >> 1) & 1u, abort_flag, a.err, a.wait_ns);
         tc_fence_after();
         uint32_t sr[64];
         {
@@ -868,7 +861,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
         // slot when the tile reads no bucket from it
         const BT* brow = bslot + (TILE_KEYS - 1);
         if (needs) {
-          (void)wait_flag_warp(&b_full[bslot_i], bpar, abort_flag, a.err, a.wait_ns);
+          (void)wait_flag(&b_full[bslot_i], bpar, abort_flag, a.err, a.wait_ns);
           const int gr = r / BIAS_BOX_ROWS;
           brow = bslot + gr * BS::GROUP + (r % BIAS_BOX_ROWS) * BS::COLS + (dmin - bias_group_x<BS::ALIGN>(dmin - r, gr)) +
                  (TILE_KEYS - 1);
@@ -915,7 +908,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
           const bool mine = m_new > m + RESCALE_NAT;
           if (__any_sync(0xffffffffu, mine)) {
             // this warpgroup's O must be stable: its previous P V product (tile g - 2) is done
-            (void)wait_flag_warp(&o_done[g & 1], (uint32_t)((g - 2) >> 1) & 1u, abort_flag, a.err, a.wait_ns);
+            (void)wait_flag(&o_done[g & 1], (uint32_t)((g - 2) >> 1) & 1u, abort_flag, a.err, a.wait_ns);
             tc_fence_after();
             const float f = mine ? fast_exp2((m - m_new) * LOG2E) : 1.f;
 #pragma unroll 1
@@ -945,7 +938,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
         }
         l += (lsv[0] + lsv[1]) + (lsv[2] + lsv[3]);
         // P buffer g & 1 was last read by the P V product of tile g - 2
-        if (g >= 2) (void)wait_flag_warp(&o_done[g & 1], (uint32_t)((g - 2) >> 1) & 1u, abort_flag, a.err, a.wait_ns);
+        if (g >= 2) (void)wait_flag(&o_done[g & 1], (uint32_t)((g - 2) >> 1) & 1u, abort_flag, a.err, a.wait_ns);
         tmem_st32(tlane + TM_P + (g & 1) * 32, pk);
         tmem_wait_st();
         tc_fence_before();
@@ -953,10 +946,10 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
         if (sw == 0) {
           // O[wg] += P(g) V(g), issued by this warpgroup's first warp
           const int vs = g % NV;   // NV is even: this warpgroup's own V slots
-          bool pv_ok = wait_flag_warp(&v_full[vs], (uint32_t)(g / NV) & 1u, abort_flag, a.err, a.wait_ns);
+          bool pv_ok = wait_flag(&v_full[vs], (uint32_t)(g / NV) & 1u, abort_flag, a.err, a.wait_ns);
           // warpgroup 1's first product of an item overwrites O[1], which the previous
           // item's epilogue (warpgroup 0) reads: wait until it has
-          if (fresh && wg == 1 && icount > 0) pv_ok = wait_flag_warp(o_free, (uint32_t)(icount - 1) & 1u, abort_flag, a.err, a.wait_ns) && pv_ok;
+          if (fresh && wg == 1 && icount > 0) pv_ok = wait_flag(o_free, (uint32_t)(icount - 1) & 1u, abort_flag, a.err, a.wait_ns) && pv_ok;
           // zero the V rows of keys that no row of this item may read
           const uint64_t vb = pv_ok ? vbad[vs] : ~0ull;
           uint8_t* vt = smem + L_::vst + (size_t)vs * S::KV_TILE;
@@ -974,8 +967,9 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
               }
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
           }
+          __syncwarp();
+          pv_ok = __all_sync(0xffffffffu, pv_ok);
           tc_fence_after();
           if (pv_ok) {
             const uint32_t vbase = smem_u32(vt);
@@ -985,8 +979,8 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
               umma_ts_warp(tmem + TM_O + (uint32_t)(wg * D), tmem + TM_P + (g & 1) * 32 + ks * 8, bdesc, IDESC_PV,
                            (fresh && ks == 0) ? 0u : 1u);
             }
+            umma_commit_warp(&v_empty[vs]);   // (not after a failed wait: the slot's copy may be in flight)
           }
-          umma_commit_warp(&v_empty[vs]);
           umma_commit_warp(&o_done[g & 1]);
           __syncwarp();
         }
@@ -995,7 +989,7 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
       // ---- item epilogue
       const int g_last = g - 1;
       if (wg == 1) {
-        if (icount > 0) (void)wait_flag_warp(ml_free, (uint32_t)(icount - 1) & 1u, abort_flag, a.err, a.wait_ns);
+        if (icount > 0) (void)wait_flag(ml_free, (uint32_t)(icount - 1) & 1u, abort_flag, a.err, a.wait_ns);
         ml1[r] = make_float2(m, l);
         __syncwarp();
         if (lane == 0) mbar_arrive(ml_full);
@@ -1004,11 +998,11 @@ prefill_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant
         // product two tiles back, so o_done[1] is at most one phase short of the count
         // awaited below.  Waiting on o_done[1] earlier could see a phase two behind,
         // whose parity matches, and read O_1 before its last product lands.
-        (void)wait_flag_warp(ml_full, (uint32_t)icount & 1u, abort_flag, a.err, a.wait_ns);
+        (void)wait_flag(ml_full, (uint32_t)icount & 1u, abort_flag, a.err, a.wait_ns);
         // both warpgroups' last P V products of the item are done
-        (void)wait_flag_warp(&o_done[g_last & 1], (uint32_t)(g_last >> 1) & 1u, abort_flag, a.err, a.wait_ns);
+        (void)wait_flag(&o_done[g_last & 1], (uint32_t)(g_last >> 1) & 1u, abort_flag, a.err, a.wait_ns);
         if (g_last > g0)
-          (void)wait_flag_warp(&o_done[(g_last - 1) & 1], (uint32_t)((g_last - 1) >> 1) & 1u, abort_flag, a.err, a.wait_ns);
+          (void)wait_flag(&o_done[(g_last - 1) & 1], (uint32_t)((g_last - 1) >> 1) & 1u, abort_flag, a.err, a.wait_ns);
         tc_fence_after();
         const float2 o1 = ml1[r];
         __syncwarp();

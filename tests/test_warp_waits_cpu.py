@@ -3,7 +3,7 @@
 A bounded wait can end differently for the lanes of a warp: each reads the abort flag, the barrier and
 the clock for itself.  Code behind it that takes the warp whole (matrix products, shuffles, full-mask
 barriers) needs one answer, so outside the helper functions a per-lane wait stands under __all_sync, or
-in one lane alone whose answer is shuffled to the others."""
+in one lane alone whose answer is shuffled to the others, or nothing goes by its answer ("(void)")."""
 import os
 import re
 
@@ -37,14 +37,30 @@ def functions(src):
 
 
 def lone_waits(src):
-    """Statements outside the helpers that wait by lane: neither voted on nor made by lane 0 alone."""
+    """Statements outside the helpers that wait by lane: neither voted on (at once, or by way of a variable), nor
+    made by lane 0 alone, nor with an answer that is thrown away or only masks the lane's own keys."""
     helpers, rest = functions(src)
     by_lane = {"mbar_wait_limit"}
     for name, body in helpers:
         if "__all_sync" not in body and any(w + "(" in body for w in by_lane):
             by_lane.add(name)
     call = re.compile(r"\b(?:%s)\(" % "|".join(sorted(by_lane)))
-    return [s.strip() for s in re.split(r"[;{}]", rest) if call.search(s) and "__all_sync" not in s and "lane == 0" not in s]
+    found = []
+    for m in re.finditer(r"[^;{}]+", rest):
+        s = m.group().strip()
+        if not call.search(s) or re.search(r"__all_sync|lane == 0|\(void\)", s):
+            continue
+        if re.search(r"if \(lane == 0\) \{\s*$", rest[:m.start()]):
+            continue
+        kept = re.search(r"(\w+) = [^=]*\b%s" % call.pattern, s)
+        after = rest[m.end():m.end() + 2500]
+        if kept and re.search(r"\b%s = __all_sync\(0xffffffffu,\s*%s\b" % (kept.group(1), kept.group(1)), after):
+            continue
+        uses = re.findall(r"[^;{}]*\bok\b[^;{}]*", after.split("for (")[0]) if kept and kept.group(1) == "ok" else []
+        if uses and all(u.strip() == "if (!ok) bad = ~0ull" for u in uses):
+            continue
+        found.append(s)
+    return found
 
 
 def test_the_reader_of_sources():
@@ -52,6 +68,9 @@ def test_the_reader_of_sources():
     voted = helper.replace("return true", "return __all_sync(~0u, *p)")
     assert lone_waits(helper + "void k() { const bool ok = w(p); }") == ["const bool ok = w(p)"]
     assert lone_waits(helper + "void k() { ok = __all_sync(~0u, w(p)); if (lane == 0) ok = w(p); }") == []
+    assert lone_waits(helper + "void k() { ok = w(p); ok = __all_sync(0xffffffffu, ok && w(q)); if (!ok) return; }") == []
+    assert lone_waits(helper + "void k() { ok = w(p); if (!ok) bad = ~0ull; }") == []
+    assert lone_waits(helper + "void k() { ok = w(p); if (!ok) bad = ~0ull; if (ok) f(); }") == ["ok = w(p)"]
     assert lone_waits(voted + "void k() { ok = w(p); if (n) ok = mbar_wait_limit(p); }") == ["if (n) ok = mbar_wait_limit(p)"]
 
 
@@ -72,9 +91,10 @@ def test_a_stage_is_handed_back_only_after_a_wait_that_succeeded(name):
     assert len(frees) == 2 and all("&& !*abort_flag" in s for s in frees)
 
 
-def test_loaders_of_the_prefill_fill_no_slot_after_an_abort():
-    """There warps whose waits ran out go on handing slots back: whoever fills them looks at the flag again."""
+def test_the_prefill_fills_no_slot_again_whose_wait_failed():
+    """Its warps go on after a timeout.  A V slot goes back with the product that read it; the bias loader looks at
+    the flag again."""
     src = code("prefill_tc.cu")
-    assert re.search(r"bool wait_slot\([^{]*\{\s*return wait_flag\([^;]*&& !\*abort_flag;", src)
-    for slot in (r"q_empty", r"&empty\[st\]", r"&b_empty\[slot\]", r"bc_empty"):
-        assert re.findall(r"\b(wait_\w+)\(%s," % slot, src) == ["wait_slot"], slot
+    assert src.count("umma_commit_warp(&v_empty") == 1
+    assert re.search(r"if \(pv_ok\) \{(?:(?!\n          \}).)*umma_commit_warp\(&v_empty\[vs\]\);", src, re.S)
+    assert re.search(r"wait_flag\(&b_empty\[slot\][^;]*&&\s*!\*abort_flag\)", src)
