@@ -48,7 +48,10 @@ constexpr int dec_ctas_per_sm() { return HB == 8 ? 2 : 1; }
 constexpr int DEC_THREADS = (DEC_CONSUMERS + 1) * 32;
 constexpr int QROWS = 16;       // query-head rows per unit (MMA M)
 constexpr int SEG_ROWS = 16;    // fine TMA box rows for partial tiles
-constexpr int PTAB = 576;       // staged block-table entries per unit (>= 64 tiles x 64/8 + 2)
+// Staged block-table entries per unit.  A unit of up to 64 tiles has no more at any page size; tables of
+// more than 4096 tiles make longer units (the splits are counted), whose later entries are read where
+// they are needed.
+constexpr int PTAB = 576;
 constexpr int L2_AHEAD = 1;     // whole tiles prefetched into L2 ahead of their loads
 
 template <int D>
@@ -299,7 +302,7 @@ decode_persistent_kernel(const __grid_constant__ CUtensorMap tmKs, const __grid_
         unit_page_span(a, *w, first, count);
         const int32_t* src = a.block_table + (size_t)w->b * a.max_pages + first;
         const uint32_t dst = smem_u32(ptab + slot * PTAB);
-        for (int j = lane; j < count; j += 32) cp_async_4(dst + 4 * j, src + j);
+        for (int j = lane; j < min(count, PTAB); j += 32) cp_async_4(dst + 4 * j, src + j);
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
@@ -332,10 +335,14 @@ decode_persistent_kernel(const __grid_constant__ CUtensorMap tmKs, const __grid_
       int nfirst = 0, ncount = 0;
       if (unxt < total_units) unit_page_span(a, nxt, nfirst, ncount);
       const int* ntab = ptab + ((uc + 1) % 3) * PTAB;
+      auto entry = [&](const Unit& w, const int* wtab, int wfirst, int idx) {   // table entry idx of unit w
+        const int j = idx - wfirst;
+        return j < PTAB ? wtab[j] : __ldg(a.block_table + (size_t)w.b * a.max_pages + idx);
+      };
       auto prefetch_whole = [&](const Unit& w, const int* wtab, int wfirst, int i) {
         const int k0 = (w.tb + i) * TILE_KEYS;
         if (P < TILE_KEYS || k0 < w.lo || k0 + TILE_KEYS - 1 > w.p) return;
-        const int page = wtab[(k0 >> a.log2_page) - wfirst];
+        const int page = entry(w, wtab, wfirst, k0 >> a.log2_page);
         if (page < 0 || page >= a.num_pages) return;
         const int row = page * hkvp + (w.kvh << a.log2_page) + (k0 & (P - 1));
         tma_prefetch_l2_4d(&tmKt, 0, 0, 0, row >> 4);
@@ -364,7 +371,7 @@ decode_persistent_kernel(const __grid_constant__ CUtensorMap tmKs, const __grid_
           uint8_t* vdst = kdst + S::TILE_BYTES;
           const uint32_t qbytes = i == 0 ? (uint32_t)(S::COL_BLOCKS * QROWS * 128) : 0u;
           if (P >= TILE_KEYS && k0 >= cur.lo && k0 + TILE_KEYS - 1 <= cur.p) {
-            const int page = tab[(k0 >> a.log2_page) - pfirst];
+            const int page = entry(cur, tab, pfirst, k0 >> a.log2_page);
             const bool okp = page >= 0 && page < a.num_pages;
             badmask[st] = okp ? 0ull : ~0ull;
             if (!okp) record_error(a.err, INK_DEVERR_PAGE_OUT_OF_RANGE);
@@ -384,7 +391,7 @@ decode_persistent_kernel(const __grid_constant__ CUtensorMap tmKs, const __grid_
             uint32_t bytes = qbytes;
             for (int ks = k0; ks < k0 + TILE_KEYS; ks += seg) {
               if (ks > klast || ks + seg - 1 < kfirst) continue;
-              const int page = tab[(ks >> a.log2_page) - pfirst];
+              const int page = entry(cur, tab, pfirst, ks >> a.log2_page);
               if (page < 0 || page >= a.num_pages) {
                 bad |= ((1ull << seg) - 1) << (ks - k0);
                 record_error(a.err, INK_DEVERR_PAGE_OUT_OF_RANGE);
@@ -396,7 +403,7 @@ decode_persistent_kernel(const __grid_constant__ CUtensorMap tmKs, const __grid_
             mbar_arrive_expect_tx(&full[st], bytes);
             for (int ks = k0; ks < k0 + TILE_KEYS; ks += seg) {
               if (ks > klast || ks + seg - 1 < kfirst) continue;
-              const int page = tab[(ks >> a.log2_page) - pfirst];
+              const int page = entry(cur, tab, pfirst, ks >> a.log2_page);
               if (page < 0 || page >= a.num_pages) continue;
               const int row = page * hkvp + row_kv + (ks & (P - 1));
               const int off = ((ks - k0) >> 4) * S::GROUP_BYTES;
