@@ -83,7 +83,8 @@ struct PMItem {
   int b, kvh, h0, gh;        // sequence, KV head, first query head, heads of the item
   int t0, ntok, pos0, L;     // first packed row, tokens, position of the first, length
   int lo_min, hi_max;        // keys any row sees lie in [lo_min, hi_max)
-  int lo_max, hi_min;        // keys in [lo_max, hi_min) are seen by every row
+  int lo_max, hi_min;        // keys in [lo_max, hi_min) are seen by every row (ends of tiles are not added up:
+                             // the last tile before 2^31 ends past the integers)
   int kt0, nt, nh, bad_len;  // first key tile, tiles (-1: no more items), row tiles
   int slot, np, one;         // of a cut item: its first place in the partials, its pieces, this one
 };
@@ -588,7 +589,7 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
             if (!go) break;
             const int kb = (it.kt0 + j) * PM_KEYS;
             const uint4 kw = *reinterpret_cast<const uint4*>(kbad + (g % PM_BAD) * 4);
-            if (kb < it.lo_min || kb + PM_KEYS > it.hi_max || (kw.x | kw.y | kw.z | kw.w)) {
+            if (kb < it.lo_min || it.hi_max - kb < PM_KEYS || (kw.x | kw.y | kw.z | kw.w)) {
               const uint32_t kbw[4] = {kw.x, kw.y, kw.z, kw.w};
               uint8_t* kt = smem + L_::ring + (size_t)((2 * g) % NS) * S::TILE;
 #pragma unroll 1
@@ -610,7 +611,7 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
           if (!go) break;
           const int k0 = (it.kt0 + j) * PM_KEYS;
           const uint4 bad = *reinterpret_cast<const uint4*>(kbad + (g % PM_BAD) * 4);
-          if (k0 < it.lo_max || k0 + PM_KEYS > it.hi_min || (bad.x | bad.y | bad.z | bad.w)) {
+          if (k0 < it.lo_max || it.hi_min - k0 < PM_KEYS || (bad.x | bad.y | bad.z | bad.w)) {
             const uint32_t badw[4] = {bad.x, bad.y, bad.z, bad.w};
             uint8_t* vt = smem + L_::ring + (size_t)st * S::TILE;
 #pragma unroll 1
@@ -779,7 +780,7 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
               sr[c] = __float_as_uint(fmaf(-slope2, fabsf(d0 - (float)c), __uint_as_float(sr[c])));
           }
           // ---- keys that this row does not see
-          if (k0 < lo_max || k0 + PM_KEYS > hi_min || (bad.x | bad.y | bad.z | bad.w)) {
+          if (k0 < lo_max || hi_min - k0 < PM_KEYS || (bad.x | bad.y | bad.z | bad.w)) {
             const uint32_t badw[4] = {bad.x, bad.y, bad.z, bad.w};
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
