@@ -663,8 +663,9 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
     // of 2^17 of them times V overflow past |V| = 2^70).  2 sequences of 5,000 tokens, 64 + 2 x 8 heads of
     // 128, cap 50: 905 us with every tile's maximum, 770 without.  A tile with larger scores goes the general
     // way, whose maximum leaves 0 only when it has to.  Not with slopes, whose scores have no lower bound,
-    // nor for an item of one tile: a row of one key has the numerator 1 against its maximum, which bf16 holds
-    // exactly.
+    // nor for an item of one tile, whose rows see few keys: against its maximum a row's largest numerator
+    // is 1, which bf16 holds exactly.  (Against 0 it is rounded; a row of one key divides by what was
+    // rounded.)
     const float reach = CAP && a.slopes == nullptr ? fminf(a.cap_mid, CALM_LOG2 / fabsf(a.scale_log2)) : -1.f;
     uint32_t sn = 0, on = 0, jn = 0;
     int g = 0;
@@ -947,7 +948,8 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
           poisoned = poisoned || ml.z != 0.f;
         }
       }
-      const float inv = l > 0.f ? 1.f / l : 0.f;
+      // (a row of one key: the numerator that V was multiplied by was rounded, so that it drops out)
+      const float inv = l > 0.f ? 1.f / (whi - wlo == 1 ? __bfloat162float(__float2bfloat16(l)) : l) : 0.f;
       const bool nothing = l == 0.f;
 #pragma unroll 1
       for (int c2 = cfirst; c2 < D / 32; c2 += cstep) {
