@@ -292,7 +292,8 @@ size_t inkling_attn_masked_workspace_bytes(const ink_attn_params_t* params, int 
  * range per token (ink_attn_mask_t).  For models that take their positions from a rotation of q
  * and k (inkling_attn_qk_norm_rope_write) or from the distance bias.
  *   q, cu_q_lens, k_cache, v_cache, block_table, seq_lens, out: as for inkling_attn_prefill,
- *              except that there is no max_q_len; out must not overlap q (INK_ERR_BAD_SHAPE)
+ *              except that there is no max_q_len; out, lse and the workspace must overlap neither
+ *              one another nor anything that is read (INK_ERR_BAD_SHAPE)
  *   total_q    rows of q and out; rows from cu_q_lens[B] on belong to no sequence: they are not
  *              written, and what they hold changes nothing
  *   lse        device, fp32 [total_q, Hq], or NULL: log of the sum of exp(s_k) over the visible
@@ -357,8 +358,8 @@ typedef struct {
  *   q_out         device, bf16 [total_q, Hq, D]; may be q itself when q_stride == Hq * D
  *   k_cache, v_cache  device, bf16 [num_pages, Hkv, P, D]; only the slots of the step's
  *                 positions are written
- *                 What is written must overlap neither q, k, v nor what else is written, but for
- *                 q in place (INK_ERR_BAD_SHAPE).
+ *                 What is written (the workspace's first 256 bytes among it) must overlap neither
+ *                 what is read nor what else is written, but for q in place (INK_ERR_BAD_SHAPE).
  *   workspace     device, initialised, of any entry point's size; only its error word is used
  * Rows from cu_q_lens[B] on belong to no request and are left as they were.  A request with
  * n_b > L_b (INK_DEVERR_QLEN_EXCEEDS_KV) has its rows skipped; a page id outside [0, num_pages)

@@ -566,10 +566,24 @@ bool make_token_map(CUtensorMap* map, const void* q, const ink_attn_params_t* p,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool overlap(const void* a, size_t an, const void* b, size_t bn) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + bn && y < x + an;
+struct Span {
+  const void* at;   // (null: absent)
+  size_t bytes;
+};
+
+// Does one of the first `written` of n spans share bytes with another one?
+bool overlap(const Span* s, int written, int n) {
+  for (int w = 0; w < written; ++w)
+    for (int x = w + 1; x < n; ++x) {
+      const uintptr_t a = reinterpret_cast<uintptr_t>(s[w].at), b = reinterpret_cast<uintptr_t>(s[x].at);
+      if (a && b && a < b + s[x].bytes && b < a + s[w].bytes) return true;
+    }
+  return false;
 }
+
+size_t pool_bytes(const ink_attn_params_t* p) { return pool_rows(p) * p->head_dim * 2; }
+
+size_t table_bytes(const ink_attn_params_t* p) { return (size_t)p->num_seqs * p->max_pages_per_seq * 4; }
 
 ink_status_t masked_impl(const ink_attn_params_t* params, const ink_attn_mask_t* mask, const void* q,
                          const int32_t* cu_q_lens, int32_t total_q, const void* k_cache, const void* v_cache,
@@ -587,10 +601,16 @@ ink_status_t masked_impl(const ink_attn_params_t* params, const ink_attn_mask_t*
       !aligned(mk.key_begin, 4) || !aligned(mk.key_end, 4) || !aligned(mk.slopes, 4) || !aligned(workspace, 256))
     return INK_ERR_ALIGNMENT;
   if ((long long)total_q * params->num_q_heads >= (1ll << 31)) return INK_ERR_TOO_LARGE;
-  if (workspace_bytes < inkling_attn_masked_workspace_bytes(params, decode ? 1 : 0)) return INK_ERR_WORKSPACE;
+  const MaskedLayout lay = masked_layout(params, decode);
+  if (workspace_bytes < lay.total) return INK_ERR_WORKSPACE;
   if (params->num_seqs == 0 || total_q == 0) return INK_OK;
-  const size_t row_bytes = (size_t)params->num_q_heads * params->head_dim * 2;
-  if (overlap(q, total_q * row_bytes, out, total_q * row_bytes)) return INK_ERR_BAD_SHAPE;
+  const size_t rows = (size_t)total_q * params->num_q_heads, seqs = (size_t)params->num_seqs * 4;
+  const Span spans[] = {{out, rows * params->head_dim * 2}, {lse, rows * 4}, {workspace, lay.total},
+                        {q, rows * params->head_dim * 2}, {k_cache, pool_bytes(params)}, {v_cache, pool_bytes(params)},
+                        {block_table, table_bytes(params)}, {seq_lens, seqs}, {decode ? nullptr : cu_q_lens, seqs + 4},
+                        {mk.key_begin, (size_t)total_q * 4}, {mk.key_end, (size_t)total_q * 4},
+                        {mk.slopes, (size_t)params->num_q_heads * 4}};
+  if (overlap(spans, 3, sizeof spans / sizeof *spans)) return INK_ERR_BAD_SHAPE;
   ink::MaskedArgs a;
   a.q = q;
   a.cu_q = decode ? nullptr : cu_q_lens;
@@ -649,7 +669,6 @@ ink_status_t masked_impl(const ink_attn_params_t* params, const ink_attn_mask_t*
   a.head_chunks = (a.G + ink::MASKED_ROWS - 1) / ink::MASKED_ROWS;
   a.heads_per_tile = (a.G + a.head_chunks - 1) / a.head_chunks;
   a.tok_per_tile = ink::MASKED_ROWS / a.heads_per_tile;
-  const MaskedLayout lay = masked_layout(params, decode);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.tickets = reinterpret_cast<int32_t*>(ws + (decode ? lay.decode_tickets : lay.prefill_tickets));
   a.part_o = reinterpret_cast<float*>(ws + lay.part_o_off);
@@ -726,12 +745,13 @@ ink_status_t inkling_attn_qk_norm_rope_write(const ink_attn_params_t* params, co
   if (params->num_seqs == 0 || total_q == 0) return INK_OK;
   // what is written overlaps neither what is read (but for q in place) nor what else is written
   auto span = [&](int64_t stride, int n) { return 2 * ((size_t)(total_q - 1) * (size_t)stride + (size_t)n * D); };
-  const void* at[6] = {q, k, v, q_out, k_cache, v_cache};
-  const size_t pool = 2 * (size_t)pool_rows(params) * D;
-  const size_t bytes[6] = {span(q_stride, Hq), span(k_stride, Hkv), span(v_stride, Hkv), span((int64_t)Hq * D, Hq), pool, pool};
-  for (int w = 3; w < 6; ++w)
-    for (int x = 0; x < w; ++x)
-      if (overlap(at[w], bytes[w], at[x], bytes[x]) && !(w == 3 && x == 0 && q_out == q)) return INK_ERR_BAD_SHAPE;
+  const Span spans[] = {{q_out, span((int64_t)Hq * D, Hq)}, {k_cache, pool_bytes(params)}, {v_cache, pool_bytes(params)},
+                        {workspace, kHeaderBytes}, {q_out == q ? nullptr : q, span(q_stride, Hq)},
+                        {k, span(k_stride, Hkv)}, {v, span(v_stride, Hkv)}, {block_table, table_bytes(params)},
+                        {seq_lens, (size_t)params->num_seqs * 4}, {cu_q_lens, (size_t)params->num_seqs * 4 + 4},
+                        {rope->w_q, (size_t)D * 4}, {rope->w_k, (size_t)D * 4},
+                        {rope->rot_dim > 0 ? rope->inv_freq : nullptr, (size_t)rope->rot_dim * 2}};
+  if (overlap(spans, 4, sizeof spans / sizeof *spans)) return INK_ERR_BAD_SHAPE;
   ink::NormRopeArgs a;
   a.x[0] = static_cast<const uint16_t*>(q);
   a.x[1] = static_cast<const uint16_t*>(k);
