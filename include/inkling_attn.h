@@ -361,8 +361,9 @@ typedef struct {
  *                 What is written (the workspace's first 256 bytes among it) must overlap neither
  *                 what is read nor what else is written, but for q in place (INK_ERR_BAD_SHAPE).
  *   workspace     device, initialised, of any entry point's size; only its error word is used
- * Rows from cu_q_lens[B] on belong to no request and are left as they were.  A request with
- * n_b > L_b (INK_DEVERR_QLEN_EXCEEDS_KV) has its rows skipped; a page id outside [0, num_pages)
+ * Rows from cu_q_lens[B] on belong to no request and are left as they were.  A request whose rows
+ * lie outside [0, total_q) (INK_DEVERR_BAD_ROWS) or with n_b > L_b (INK_DEVERR_QLEN_EXCEEDS_KV) has
+ * its rows skipped, as the attention entry points skip them; a page id outside [0, num_pages)
  * (INK_DEVERR_PAGE_OUT_OF_RANGE) has the K/V rows of its keys skipped.  Two rows that name the
  * same slot (requests sharing a page they write to) race: each 16 bytes of the slot hold either row's.
  */

@@ -64,9 +64,9 @@ __device__ __forceinline__ void turn(int p, float f, float scale, float& c, floa
   s = sn * scale;
 }
 
-// The last b with cu_q[b] <= t < cu_q[B] (-1: t lies outside), by a whole warp: 32 offsets a step.
-__device__ __forceinline__ int find_seq_warp(const int32_t* cu_q, int B, int t, int lane) {
-  if (t >= __ldg(cu_q + B) || t < __ldg(cu_q)) return -1;
+// The last b with cu_q[b] <= t < cu_q[B] = end (-1: t lies outside), by a whole warp: 32 offsets a step.
+__device__ __forceinline__ int find_seq_warp(const int32_t* cu_q, int B, int end, int t, int lane) {
+  if (t >= end || t < __ldg(cu_q)) return -1;
   int lo = 0, n = B;   // the answer is among lo .. lo + n - 1
   while (n > 1) {
     const int step = (n + 31) >> 5;
@@ -74,9 +74,9 @@ __device__ __forceinline__ int find_seq_warp(const int32_t* cu_q, int B, int t, 
     const bool le = lane * step < n && __ldg(cu_q + i) <= t;
     const uint32_t m = __ballot_sync(0xffffffffu, le);
     const int k = m ? 31 - __clz(m) : 0;
-    const int end = lo + n;
+    const int last = lo + n;
     lo += k * step;
-    n = min(step, end - lo);
+    n = min(step, last - lo);
   }
   return lo;
 }
@@ -125,10 +125,16 @@ __global__ void __launch_bounds__(NR_THREADS, NR_BLOCKS) qk_norm_rope_kernel(con
     load(first, q0, q1);
   }
 
-  const int b = find_seq_warp(a.cu_q, a.B, t, lane);
+  const int end = __ldg(a.cu_q + a.B);
+  // (by the first row's warp too: requests that lie behind the last row have none)
+  if (end > a.T && t == 0 && lane == 0) record_error(a.err, INK_DEVERR_BAD_ROWS);
+  const int b = find_seq_warp(a.cu_q, a.B, end, t, lane);
   if (b < 0) return;                  // a row of no request
-  const int c0 = __ldg(a.cu_q + b), n = __ldg(a.cu_q + b + 1) - c0, L = __ldg(a.seq_lens + b);
-  if (c0 < 0 || t - c0 >= n) return;  // offsets that do not increase
+  const int c0 = __ldg(a.cu_q + b), c1 = __ldg(a.cu_q + b + 1), n = c1 - c0, L = __ldg(a.seq_lens + b);
+  if (c0 < 0 || c1 > a.T || t >= c1) {   // rows outside [0, T), or offsets that do not increase
+    if (lane == 0) record_error(a.err, INK_DEVERR_BAD_ROWS);
+    return;
+  }
   if (n > L) {
     if (lane == 0) record_error(a.err, INK_DEVERR_QLEN_EXCEEDS_KV);
     return;
