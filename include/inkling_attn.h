@@ -348,8 +348,8 @@ typedef struct {
  *   y = x * (mean(x^2) + eps)^(-1/2) * w          (fp32; without weights y = x)
  *   pair (a, b) of channels with frequency f at position p, in fp32:
  *     a' = rot_scale * (a cos(p f) - b sin(p f)),  b' = rot_scale * (b cos(p f) + a sin(p f))
- * rounded to bf16 once.  The angle is reduced exactly enough that far positions (any int32) keep
- * an error of a few fp32 roundings of one turn.  V is stored as it is.
+ * rounded to bf16 once.  p f is reduced to a turn in integers, so that its error is below 2^-25 of a
+ * turn at any position (f up to 50).  V is stored as it is.
  *   q, k, v       device, bf16; row t of q holds Hq heads of D contiguous channels at
  *                 q + t * q_stride elements (k, v: Hkv heads): parts of a fused projection's
  *                 rows pass without a copy.  Strides are multiples of 8, 16-byte aligned bases.
