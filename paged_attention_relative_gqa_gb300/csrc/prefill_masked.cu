@@ -103,7 +103,7 @@ struct PMSmem {
   static constexpr size_t items = bars + (NBAR * 8 + 15) / 16 * 16;
   static constexpr size_t kbad = items + PM_ITEMS * sizeof(PMItem);
   static constexpr size_t poison = kbad + PM_BAD * 16;
-  static constexpr size_t misc = poison + PM_ITEMS * 4;
+  static constexpr size_t misc = poison + PM_ITEMS * 8;
   static constexpr size_t total = misc + 32;
   static constexpr size_t alloc = total + 1024;
   static_assert(alloc <= 227 * 1024, "shared memory budget");
@@ -162,7 +162,7 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
   uint64_t* drain = ticket + 2;
   PMItem* items = reinterpret_cast<PMItem*>(smem + L_::items);
   uint32_t* kbad = reinterpret_cast<uint32_t*>(smem + L_::kbad);      // [BAD][4] bit per unreadable key
-  volatile int* poison = reinterpret_cast<volatile int*>(smem + L_::poison);   // [ITEMS]
+  int* poison = reinterpret_cast<int*>(smem + L_::poison);   // [ITEMS][2] first and last tile of V with an infinity or NaN
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L_::misc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L_::misc + 4);
   volatile int* joins = reinterpret_cast<volatile int*>(smem + L_::misc + 8);   // [2] this piece joins its item
@@ -538,7 +538,8 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
           if (it.bad_len) record_error(a.err, INK_DEVERR_QLEN_EXCEEDS_KV);
           else if ((long long)it.L > ((long long)a.max_pages << a.log2_page)) record_error(a.err, INK_DEVERR_PAGE_OUT_OF_RANGE);
           items[sl] = it;
-          poison[sl] = 0;
+          reinterpret_cast<volatile int*>(poison)[2 * sl] = INT_MAX;
+          reinterpret_cast<volatile int*>(poison)[2 * sl + 1] = -1;
           mbar_arrive(&item_full[sl]);
         }
         __syncwarp();
@@ -579,7 +580,6 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
       bool go = true;
       PMItem it;
       for (int k = 0; go && next_item(k, it); ++k) {
-        bool found = false;
         for (int j = 0; j < it.nt; ++j, ++g) {
           const int st = (2 * g + 1) % NS;
           if constexpr (CAP) {
@@ -614,6 +614,7 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
           if (k0 < it.lo_max || it.hi_min - k0 < PM_KEYS || (bad.x | bad.y | bad.z | bad.w)) {
             const uint32_t badw[4] = {bad.x, bad.y, bad.z, bad.w};
             uint8_t* vt = smem + L_::ring + (size_t)st * S::TILE;
+            bool found = false;
 #pragma unroll 1
             for (int x = 0; x < 4; ++x) {
               const int kk = k0 + 32 * x + lane;
@@ -638,7 +639,10 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
                   for (int y = 0; y < 8; ++y) row[c * (S::SUB / 16) + (y ^ (lane & 7))] = make_uint4(0u, 0u, 0u, 0u);
               }
             }
-            if (found) poison[k % PM_ITEMS] = 1;
+            if (found) {
+              atomicMin(poison + 2 * (k % PM_ITEMS), it.kt0 + j);
+              atomicMax(poison + 2 * (k % PM_ITEMS) + 1, it.kt0 + j);
+            }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           }
           __syncwarp();
@@ -877,7 +881,8 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
       if (!go) break;
       ++on;
       tc_fence_after();
-      bool poisoned = poison[k % PM_ITEMS] != 0;
+      int pfirst = reinterpret_cast<volatile int*>(poison)[2 * (k % PM_ITEMS)];
+      int plast = reinterpret_cast<volatile int*>(poison)[2 * (k % PM_ITEMS) + 1];
       // a piece of a cut item: its part into the workspace; who is last goes on with the joined row
       float4* part_o = reinterpret_cast<float4*>(a.part_o) + (size_t)(it.slot * 2 + h) * (D / 4) * MASKED_ROWS + r;
       float4* part_ml = reinterpret_cast<float4*>(a.part_ml) + (size_t)(it.slot * 2 + h) * MASKED_ROWS + r;
@@ -898,7 +903,7 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
                    make_float4(__uint_as_float(ov[4 * x]), __uint_as_float(ov[4 * x + 1]), __uint_as_float(ov[4 * x + 2]),
                                __uint_as_float(ov[4 * x + 3])));
         }
-        __stcg(part_ml + (size_t)it.one * 2 * MASKED_ROWS, make_float4(l == 0.f ? -INFINITY : m, l, poisoned ? 1.f : 0.f, 0.f));
+        __stcg(part_ml + (size_t)it.one * 2 * MASKED_ROWS, make_float4(l == 0.f ? -INFINITY : m, l, __int_as_float(pfirst), __int_as_float(plast)));
         tc_fence_before();
         // Every thread's stores come before its warp's arrival, the ticket's add releases them and acquires
         // the other pieces'.  (Barriers whose waits are bounded: after a timeout a warp may be gone.)
@@ -945,7 +950,8 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
         for (int x = 0; x < it.np; ++x) {
           const float4 ml = __ldcg(part_ml + (size_t)x * 2 * MASKED_ROWS);
           l += ml.y * (ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - m));
-          poisoned = poisoned || ml.z != 0.f;
+          pfirst = min(pfirst, __float_as_int(ml.z));
+          plast = max(plast, __float_as_int(ml.w));
         }
       }
       // (a row of one key: the numerator that V was multiplied by was rounded, so that it drops out)
@@ -983,10 +989,12 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
         }
 #pragma unroll
         for (int x = 0; x < 32; ++x) ov[x] = nothing ? 0u : __float_as_uint(__uint_as_float(ov[x]) * (l == l ? inv : l));
-        if (poisoned && wv) {
-          // infinities and NaN of the keys this row sees
+        if (plast >= 0 && wv) {
+          // infinities and NaN of the keys this row sees (key by key, but from the first tile to the last that
+          // holds one: over a whole history of a million keys that took as long as a wait may)
+          const int kend = min(whi - 1, plast * PM_KEYS + PM_KEYS - 1);
 #pragma unroll 1
-          for (int kk = wlo; kk < whi; ++kk) {
+          for (int kk = max(wlo, pfirst * PM_KEYS); kk <= kend; ++kk) {
             const int page = __ldg(a.block_table + (size_t)it.b * a.max_pages + (kk >> a.log2_page));
             if (page < 0 || page >= a.num_pages) continue;
             const size_t vrow = ((((size_t)page * a.Hkv + it.kvh) << a.log2_page) + (kk & (P - 1))) * D + c2 * 32;
