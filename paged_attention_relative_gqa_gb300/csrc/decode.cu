@@ -151,10 +151,11 @@ __device__ __forceinline__ void named_barrier_consumers() {
   asm volatile("bar.sync 1, %0;" ::"n"(DEC_CONSUMERS * 32) : "memory");
 }
 
-// Wait on an mbarrier phase unless the CTA has aborted; on timeout, record the error
-// and abort the CTA (every later wait returns at once).
+// Wait on an mbarrier phase: a completed one returns at once, and so does any when the CTA has
+// aborted; on timeout, record the error and abort the CTA.
 __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
                                               uint32_t* err, unsigned long long limit_ns) {
+  if (mbar_probe(bar, parity, limit_ns)) return true;
   if (*abort_flag) return false;
   if (mbar_wait_limit(bar, parity, limit_ns)) return true;
   record_error(err, INK_DEVERR_WAIT_TIMEOUT);

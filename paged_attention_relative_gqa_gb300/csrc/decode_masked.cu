@@ -139,8 +139,8 @@ struct Walk {
 // and the clock for itself, and what follows (matrix products, shuffles, branches around them) takes
 // the warp whole.
 __device__ __forceinline__ bool dm_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, const MaskedArgs& a) {
-  bool ok = false;
-  if (!*abort_flag) {
+  bool ok = mbar_probe(bar, parity, a.wait_ns);
+  if (!ok && !*abort_flag) {
     ok = mbar_wait_limit(bar, parity, a.wait_ns);
     if (!ok) {
       record_error(a.err, INK_DEVERR_WAIT_TIMEOUT);
