@@ -299,7 +299,12 @@ size_t inkling_attn_masked_workspace_bytes(const ink_attn_params_t* params, int 
  *   lse        device, fp32 [total_q, Hq], or NULL: log of the sum of exp(s_k) over the visible
  *              keys (natural units), with which outputs over parts of a history are joined
  *   workspace  device, >= inkling_attn_masked_workspace_bytes(params, 0), initialised once
- * A token that sees no key gets a zero output row and lse = -infinity.  Sums are held in fp32 and divided
+ * A token that sees no key gets a zero output row and lse = -infinity; one that sees a single key gets
+ * that key's V.  Softmax weights are rounded to bf16 before they multiply V and divided by the sum of
+ * the unrounded ones, so an output may be off by 2^-8 of sum_k w_k |V_k| beside its own rounding.  Capped
+ * scores are off by at most 2^-20 of themselves (beyond the cap, 2^-21 of the cap); which of three forms of
+ * the tanh a row takes goes by the largest score of the 32 rows that are computed together, so within
+ * these bounds its bits may change with how a prompt is cut into calls.  Sums are held in fp32 and divided
  * at the end: |V| up to 2^100 is safe (2^70 when scores are capped).  params.rel_extent is not used
  * (any valid value).  A sequence whose rows lie outside [0, total_q) is skipped
  * (INK_DEVERR_BAD_ROWS); one with more new tokens than history gets zero rows

@@ -17,10 +17,10 @@
 // row is padding when few heads share a KV head (a product this thin is bound by its bytes: the
 // fifth-generation tensor cores' 128-row tiles would hold 8 useful rows).
 //
-// Measured, 64 + 2 x 8 heads of 128: 32 sequences of up to 32 K keys (3.1 GB) 445 us, 7.0 TB/s, as fast as a copy;
-// one sequence of 114 K keys 81 us, 5.8 TB/s; 128 of 2 K keys 126 us, 6.4 TB/s; windows of 512 keys, 16 KV heads, 64
-// sequences 51 us, 5.3 TB/s: below 100 us the start (2.5 us), the first tiles' latency and the joins show.
-// One short sequence 10 us.  Three stages with half the O buffer (445 -> 464 us), and the next piece's table
+// Measured (GPU time alone), 64 + 2 x 8 heads of 128: 32 sequences of up to 32 K keys (3.1 GB) 438 us, 7.1 TB/s, as
+// fast as a copy; one sequence of 114 K keys 80 us, 5.8 TB/s; 128 of 2 K keys 125 us, 6.4 TB/s; windows of 512 keys, 16
+// KV heads, 64 sequences 51 us, 5.3 TB/s: below 100 us the start (2.5 us), the first tiles' latency and the joins show.
+// One short sequence 10 us, a chain of dependent latencies: lengths, table, tiles, products, partials, ticket, join.  Three stages with half the O buffer (445 -> 464 us), and the next piece's table
 // entries and first tile ahead (no change), are not kept.
 #include <algorithm>
 

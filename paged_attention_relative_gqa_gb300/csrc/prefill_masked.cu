@@ -38,9 +38,11 @@
 // but about 2650 pass: a row tile's chain (128 scores from tensor memory, 1200 clocks of softmax, P V and the
 // next S, four hand-overs of about 100 clocks) is longer than half of that, and the exponentials of both
 // tiles alone keep the special function units busy for 1024.  Measured with 64 query and 8 KV heads of
-// 128, prompts of about 5,000 tokens: 1.36 PFLOP/s causal, 1.44 on whole histories, 1.10 capped, 1.02 with
-// slopes (which cost 3 operations a score); 0.86 at D = 64, where a score has half the products.  A window
-// of 512 keys: 0.83, since an item is 5 tiles long and its start, masks and output run in no tile's shadow.
+// 128, prompts of about 5,000 tokens, GPU time alone: 1.36 PFLOP/s causal, 1.43 on whole histories, 1.11
+// capped, 1.01 with slopes (which cost 3 operations a score).  D = 64: 0.86 causal, 0.90 on whole histories;
+// there the products of both tiles take 1024 clocks, no longer than their exponentials take the special
+// function units, and the chain stays as long as at D = 128.  A window of 512 keys: 0.82, since an item is 5
+// tiles long and its start, masks and output run in no tile's shadow.
 // Tried without gain: P V in two halves, numerators against the last tile's maximum, P beside S, 64-key
 // tiles with Q in tensor memory, a third Q tile, S read in halves, output rows staged in shared memory.
 #include <algorithm>
@@ -132,7 +134,8 @@ __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
 // CAP: capped scores.  Models keep most scores well inside the cap: while no score of a warp's tile
 // passes 0.45 of it, tanh is an odd polynomial of four terms in the raw product (relative error
 // 2^-21.8; five packed operations for two scores and no special function), up to the cap one of six
-// terms (2^-20.7, seven operations), else score_log2.
+// terms (2^-20.7, seven operations), else score_log2.  The choice is a warp's: its 32 rows (of one sequence) go
+// one way, so the bits of a token's output can change with the tokens that share its row tile.
 // SPLIT: items may be cut into pieces (a kernel of its own: the joining code would cost the others
 // registers).
 template <int D, bool CAP, bool SPLIT>
@@ -665,7 +668,7 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
     // and below.  As long as it is small (|s| <= 40 in log2 units) in every row of a warp, no maximum is looked
     // for: the numerators are taken against 0 and lie within [2^-40, 2^40], far inside bf16's range (sums
     // of 2^17 of them times V overflow past |V| = 2^70).  2 sequences of 5,000 tokens, 64 + 2 x 8 heads of
-    // 128, cap 50: 905 us with every tile's maximum, 770 without.  A tile with larger scores goes the general
+    // 128, cap 50: 886 us with every tile's maximum, 760 without.  A tile with larger scores goes the general
     // way, whose maximum leaves 0 only when it has to.  Not with slopes, whose scores have no lower bound,
     // nor for an item of one tile, whose rows see few keys: against its maximum a row's largest numerator
     // is 1, which bf16 holds exactly.  (Against 0 it is rounded; a row of one key divides by what was

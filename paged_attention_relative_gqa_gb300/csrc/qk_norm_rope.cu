@@ -16,9 +16,10 @@
 // partner channels sit rot_dim / 16 lanes away and come by shuffle as raw bf16 (4 registers for
 // 8 channels), normed with the partner's weights.
 //
-// Measured: 34,500 tokens of 64 + 2 x 8 heads of 128 (1.4 GB) 210 us, 6.7 TB/s, as fast as a copy; 5,161 tokens of
-// 40 + 2 x 8 heads of 128, half of the channels rotated, 31 us, 4.8 TB/s; 64 tokens of a decode 5 us, one token 3 us (a
-// launch).
+// Measured (GPU time alone): 34,500 tokens of 64 + 2 x 8 heads of 128 (1.4 GB) 211 us, 6.7 TB/s, as fast as a copy;
+// 5,161 tokens of 40 + 2 x 8 heads of 128, half of the channels rotated, 31 us, 4.8 TB/s: there a warp's serial start
+// (offsets, length, angles, page) and the 2 to 4 passes it has on their way show; 64 tokens of a decode 5 us, one token
+// 3 us (a launch).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>

@@ -8,7 +8,9 @@ kernel:
 * ``yarn`` (Peng et al., "YaRN: Efficient Context Window Extension of Large Language Models"):
   with r the turns a pair makes over ``original_len`` positions, pairs with r > beta_fast keep
   their frequency, pairs with r < beta_slow are interpolated, a linear ramp lies between; cos and
-  sin are multiplied by 0.1 ln(factor) + 1.
+  sin are multiplied by 0.1 ln(factor) + 1.  The ramp is linear in r.  Checkpoints are also run with a
+  ramp that is linear in the pair's index between two rounded bounds: for those make the table from
+  their own formula (the kernel takes any table).
 """
 from __future__ import annotations
 
