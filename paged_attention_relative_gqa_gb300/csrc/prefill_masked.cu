@@ -25,7 +25,7 @@
 //   10  scheduler: hands out items (a counter in the workspace, longest first within a sequence),
 //       finds their key ranges, publishes them in shared memory, and loads their Q tiles by TMA.
 //   11  K and V check: in a V tile that not every row of the item sees whole, rows of V that nobody sees
-//       are zeroed, and so are rows with an infinity or NaN (0 * NaN would reach rows that do not
+//       are zeroed, and so is every infinity or NaN (0 * NaN would reach rows that do not
 //       see the key); rows that do see one get it back in the epilogue.
 // When there are fewer items than SMs (a chunk of a prompt or a few drafted tokens against a long
 // history), the key tiles of an item are cut into pieces of one length, chosen on the device so that
@@ -622,7 +622,7 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
             for (int x = 0; x < 4; ++x) {
               const int kk = k0 + 32 * x + lane;
               uint4* row = reinterpret_cast<uint4*>(vt + (32 * x + lane) * 128);
-              bool zero = kk < it.lo_min || kk >= it.hi_max || ((badw[x] >> lane) & 1u);
+              const bool zero = kk < it.lo_min || kk >= it.hi_max || ((badw[x] >> lane) & 1u);
               if (!zero) {   // exponents all ones carry into the sign places
                 uint32_t odd = 0;
 #pragma unroll
@@ -633,9 +633,18 @@ prefill_masked_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
                     odd |= ((w.x & 0x7F807F80u) + 0x00800080u) | ((w.y & 0x7F807F80u) + 0x00800080u) |
                            ((w.z & 0x7F807F80u) + 0x00800080u) | ((w.w & 0x7F807F80u) + 0x00800080u);
                   }
-                if (odd & 0x80008000u) zero = found = true;
-              }
-              if (zero) {
+                if (odd & 0x80008000u) {
+                  found = true;
+                  auto finite = [](uint32_t w) {   // infinities and NaN to zero, the other half as it is
+                    return w & ~(((((w & 0x7F807F80u) + 0x00800080u) >> 15) & 0x00010001u) * 0xFFFFu);
+                  };
+#pragma unroll 1
+                  for (int y = 0; y < 8 * S::CB; ++y) {
+                    uint4& w = row[(y >> 3) * (S::SUB / 16) + ((y & 7) ^ (lane & 7))];
+                    w = make_uint4(finite(w.x), finite(w.y), finite(w.z), finite(w.w));
+                  }
+                }
+              } else {
 #pragma unroll
                 for (int c = 0; c < S::CB; ++c)
 #pragma unroll

@@ -1,9 +1,11 @@
 """One infinity of V in a long history: the rows that see it get it, and finding it takes no time that a wait
 would run out in."""
+import numpy as np
 import pytest
 import torch
 
 from paged_attention_relative_gqa_gb300 import binding
+from tests.masked_common import call, check, options, problem, reference
 
 pytestmark = pytest.mark.gpu
 
@@ -42,3 +44,33 @@ def test_it_is_found_at_once(cuda_device, L, tokens, heads, softcap):
         assert torch.equal(lse, outs[0][1])
         assert torch.equal(out[..., rest], outs[0][0][..., rest]) and torch.equal(out[~seen], outs[0][0][~seen])
     assert torch.isposinf(outs[1][0][seen][..., 3]).all() and torch.isnan(outs[2][0][seen][..., 3]).all()
+
+
+@pytest.mark.parametrize("decode", [False, True])
+@pytest.mark.parametrize("softcap", [0.0, 30.0])
+@pytest.mark.parametrize("heads,dim,page,q_lens,seq_lens", [
+    ((8, 2), 64, 16, [150, 40], [150, 300]), ((8, 8), 128, 64, [300], [500]), ((8, 1), 128, 64, [20, 3], [6000, 4000])])
+def test_the_other_channels_keep_their_values(cuda_device, decode, softcap, heads, dim, page, q_lens, seq_lens):
+    """Infinities and NaN in some channels of some keys, near the rows' own positions: every other channel of every
+    row against the oracle, which sums over those keys too."""
+    if decode:
+        q_lens = [1] * len(q_lens)
+    prob = problem(heads, dim, page, q_lens, seq_lens, 121, cuda_device)
+    rng = np.random.default_rng(122)
+    table = prob.block_table.cpu().numpy()
+    for b, (n, L) in enumerate(zip(q_lens, seq_lens)):
+        for _ in range(4):
+            k = int(rng.integers(max(0, L - n - 3), L))
+            for value in (float("inf"), -float("inf"), float("nan")):
+                prob.v_cache[int(table[b, k // page]), :, k % page, int(rng.integers(dim))] = value
+    opts = options(prob, softcap=softcap)
+    out, lse, ws = call(prob, opts, decode)
+    assert binding.inkling_attn_read_device_error(ws) == 0
+    with np.errstate(invalid="ignore"):
+        want, want_lse, mag, smag = reference(prob, opts)
+    got = out.double().cpu().numpy()
+    odd = ~np.isfinite(want)
+    assert odd.any() and not odd.all(-1).any()
+    assert np.array_equal(np.isnan(want), np.isnan(got)) and np.array_equal(want[np.isinf(want)], got[np.isinf(want)])
+    clean = torch.from_numpy(np.where(odd, 0.0, got)).float()
+    check(clean, lse, (np.where(odd, 0.0, want), want_lse, np.where(odd, 0.0, mag), smag), "other channels")
