@@ -44,7 +44,8 @@ __device__ __forceinline__ void unpack_bf16x8(const uint4 r, float (&f)[8]) {
   }
 }
 
-// cos and sin of p * f, p any non-negative int32.  In turns, in fixed point: g = f / (2 pi) modulo 1 in
+// cos and sin of p * f, p any non-negative int32.  In turns, in fixed point (the idea of Payne and Hanek's
+// "Radian reduction for trigonometric functions": only what is left of whole turns is kept): g = f / (2 pi) modulo 1 in
 // 64 bits, from f's 24 digits and 2^66 / (2 pi) rounded to 64 bits; p g modulo 1 is then the low 64
 // bits of a product of integers.  Cutting g off costs p 2^-64 <= 2^-33 of a turn, the constant's
 // rounding p f 2^-68, cutting the turn to 32 bits 2^-32 and its float 2^-26: the error does not grow with
