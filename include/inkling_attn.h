@@ -72,6 +72,7 @@ typedef enum {
 #define INK_DEVERR_WAIT_TIMEOUT      0x4u  /* a bounded wait on a copy ran out */
 #define INK_DEVERR_QLEN_EXCEEDS_MAX  0x8u  /* a sequence has more new tokens than max_q_len */
 #define INK_DEVERR_BAD_ROWS          0x10u /* cu_q_lens names rows outside [0, total_q) */
+#define INK_DEVERR_BAD_TREE          0x20u /* a parent or an accepted path that no tree of drafted tokens has */
 
 /* Per-call shape and layer scalars.  All sizes are element counts. */
 typedef struct {
@@ -378,6 +379,159 @@ ink_status_t inkling_attn_qk_norm_rope_write(const ink_attn_params_t* params, co
                                              int32_t total_q, const int32_t* seq_lens, const int32_t* block_table,
                                              void* q_out, void* k_cache, void* v_cache, void* workspace,
                                              size_t workspace_bytes, void* stream);
+
+/*
+ * ---- Trees of drafted tokens.
+ *
+ * A step that checks drafted tokens writes the n_b = cu_q_lens[b+1] - cu_q_lens[b] tokens of sequence b
+ * behind its history of H_b = seq_lens[b] - n_b keys, parents before children: token i takes slot
+ * H_b + i of the cache, whatever its position.  Its position is H_b plus its depth in the tree (siblings
+ * share one), and it sees the history and the drafted tokens on its way to the root, itself among them.
+ * The step's calls, in order:
+ *     inkling_attn_tree_plan                once: positions and visible drafted tokens from the parents
+ *     per layer: inkling_attn_qk_norm_rope_write_at or inkling_attn_kv_conv_write_tree, then
+ *                inkling_attn_tree
+ *     inkling_attn_tree_commit              once: the accepted path's K and V rows move to where a
+ *                                           sequence without the other tokens would have them
+ *     inkling_attn_kv_conv_state_tree       per layer with a convolution: its state behind that path
+ *
+ * Plan of a tree, from the parents.
+ *   cu_q_lens, seq_lens   as for inkling_attn_prefill
+ *   total_q    rows of parents, positions and ancestors; rows from cu_q_lens[B] on are left as they were
+ *   parents    device, int32 [total_q]: the parent's place i in its sequence, -1 for a child of the last
+ *              token of the history (a sequence may have several).  One that is not in [-1, own place)
+ *              sets INK_DEVERR_BAD_TREE and counts as -1.
+ *   words      32-bit words of a token's bits, 1..16: a sequence may draft up to 32 * words tokens; one with
+ *              more sets INK_DEVERR_QLEN_EXCEEDS_MAX and is skipped
+ *   positions  device, int32 [total_q]: H_b + depth, the depth of a child of the history being 0
+ *   ancestors  device, uint32 [total_q, words]: bit j % 32 of word j / 32 is set for every drafted token j on
+ *              the way from the token to the root and for the token itself
+ *   workspace  device, initialised, of any entry point's size; only its error word is used
+ * Outputs (the workspace's first 256 bytes among them) must overlap neither inputs nor one another
+ * (INK_ERR_BAD_SHAPE).  Only num_seqs of params is used; the rest must still be valid.  A sequence whose
+ * rows lie outside [0, total_q) (INK_DEVERR_BAD_ROWS) or with n_b > seq_lens[b]
+ * (INK_DEVERR_QLEN_EXCEEDS_KV) is skipped.
+ */
+ink_status_t inkling_attn_tree_plan(const ink_attn_params_t* params, const int32_t* cu_q_lens, int32_t total_q,
+                                    const int32_t* seq_lens, const int32_t* parents, int32_t words,
+                                    int32_t* positions, uint32_t* ancestors, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
+/* The drafted tokens of a call, as inkling_attn_tree_plan lays them out (or the caller: any bits will do). */
+typedef struct {
+  const int32_t* positions;   /* device int32 [total_q]; one below H_b counts as H_b */
+  const uint32_t* ancestors;  /* device uint32 [total_q, words]; bits from n_b on are not looked at */
+  int32_t words;              /* 1..16 */
+} ink_attn_tree_t;
+
+/* Options of inkling_attn_tree (a NULL pointer to this struct: none of them). */
+typedef struct {
+  float softcap;              /* in [1e-6, 1e6]: scores capped by a tanh; 0: not capped */
+  const float* slopes;        /* device fp32 [Hq], or NULL: no bias linear in the distance */
+  const void* rel_logits;     /* device [total_q, Hq, rel_extent], 4-byte (bf16: 2-byte) aligned, or NULL: no
+                                 bias tensor */
+  int32_t rel_is_bf16;        /* rel_logits holds bf16 instead of fp32 */
+} ink_attn_tree_options_t;
+
+/* Bytes of device workspace inkling_attn_tree needs; initialise it once with inkling_attn_workspace_init.
+ * Returns 0 if the parameters are invalid.  It depends on head_dim only (about 43 MB at D = 128), so one
+ * workspace serves calls of any sizes, one after the other; calls that share a workspace must not overlap on the GPU. */
+size_t inkling_attn_tree_workspace_bytes(const ink_attn_params_t* params);
+
+/*
+ * Attention of drafted tokens over the paged cache.  Token t at place i of sequence b has position
+ * p = max(positions[t], H_b); key k < H_b has position k, drafted key H_b + j the position of token j.
+ * Of the keys below seq_lens[b] the token sees
+ *     k < H_b,  and  H_b + j when bit j of its ancestors is set,
+ * both only at p - pos(k) <= window - 1 when window > 0.  The score of a visible key, d = |p - pos(k)|:
+ *     x   = sm_scale * <q[t,h,:], K[k,h/G,:]>
+ *     s_k = (softcap > 0 ? softcap * tanh(x / softcap) : x) - slopes[h] * d + rel_logits[t, h, min(d, E - 1)]
+ *   q, cu_q_lens, total_q, k_cache, v_cache, block_table, seq_lens, out, lse: as for
+ *              inkling_attn_prefill_masked; the step's K and V rows must already be written
+ *   workspace  device, >= inkling_attn_tree_workspace_bytes(params), initialised once
+ * One token per sequence with a bit of its own makes this a decode, so that a batch may mix sequences that
+ * draft with sequences that do not.  What is written must overlap nothing else (INK_ERR_BAD_SHAPE).
+ * Rounding, infinities and NaN, |V|: as for inkling_attn_prefill_masked.  A token that sees no key gets a zero row and
+ * lse = -infinity; so do the tokens of a sequence with n_b > seq_lens[b] (INK_DEVERR_QLEN_EXCEEDS_KV) or
+ * n_b > 32 * words (INK_DEVERR_QLEN_EXCEEDS_MAX).  A sequence whose rows lie outside [0, total_q) is skipped
+ * (INK_DEVERR_BAD_ROWS).
+ */
+ink_status_t inkling_attn_tree(const ink_attn_params_t* params, const ink_attn_tree_t* tree,
+                               const ink_attn_tree_options_t* options, const void* q, const int32_t* cu_q_lens,
+                               int32_t total_q, const void* k_cache, const void* v_cache,
+                               const int32_t* block_table, const int32_t* seq_lens, void* out, float* lse,
+                               void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * inkling_attn_qk_norm_rope_write with a position per row: row t is rotated by positions[t] (device int32
+ * [total_q]; a negative one counts as 0) and still written to slot H_b + i.  Every other argument and result as there.
+ */
+ink_status_t inkling_attn_qk_norm_rope_write_at(const ink_attn_params_t* params, const ink_norm_rope_t* rope,
+                                                const int32_t* positions, const void* q, int64_t q_stride,
+                                                const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                                                const int32_t* cu_q_lens, int32_t total_q, const int32_t* seq_lens,
+                                                const int32_t* block_table, void* q_out, void* k_cache, void* v_cache,
+                                                void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * inkling_attn_kv_conv_write for a tree of drafted tokens: the rows before a token are those of its ancestors,
+ * and past the root those of the state,
+ *     y_i = sum_{d=0}^{ks-1} w[g, d', ks-1-d] * x[ancestor of i at distance d]      (d = 0: the token itself)
+ * with the state's newest row as the parent of a root.  y_i goes to slot H_b + i.  The state is not advanced: that takes the
+ * accepted path (inkling_attn_kv_conv_state_tree).
+ *   parents    device, int32 [total_q], as for inkling_attn_tree_plan (a bad one: INK_DEVERR_BAD_TREE, -1)
+ * Every other argument as for inkling_attn_kv_conv_write.  What is written (the workspace's first 256 bytes
+ * among it) must overlap nothing else (INK_ERR_BAD_SHAPE).  A request whose rows lie outside [0, total_q)
+ * or with n_b > seq_lens[b] has its rows skipped and reported, a page id outside [0, num_pages) its row.
+ */
+ink_status_t inkling_attn_kv_conv_write_tree(const ink_attn_params_t* params, const void* k_new, const void* v_new,
+                                             const int32_t* cu_q_lens, int32_t total_q, const int32_t* seq_lens,
+                                             const int32_t* block_table, const int32_t* parents, const float* w_k,
+                                             const float* w_v, int32_t kernel_size, const void* state_k_in,
+                                             const void* state_v_in, void* k_cache, void* v_cache, void* workspace,
+                                             size_t workspace_bytes, void* stream);
+
+/*
+ * The convolution state behind an accepted path: state_k_out[b] receives the last kernel_size - 1 rows of
+ * (state_k_in[b], k_new of the path's tokens), and likewise V.
+ *   path, path_lens, max_path   as for inkling_attn_tree_commit; a path that is refused there counts as
+ *              empty (INK_DEVERR_BAD_TREE): the state is copied
+ * Other arguments as for inkling_attn_kv_conv_write.  A request whose rows lie outside [0, total_q) has its
+ * state copied (INK_DEVERR_BAD_ROWS).  With kernel_size 1 nothing is done.  What is written (the workspace's first 256
+ * bytes among it) must overlap nothing else (INK_ERR_BAD_SHAPE).
+ */
+ink_status_t inkling_attn_kv_conv_state_tree(const ink_attn_params_t* params, const void* k_new, const void* v_new,
+                                             const int32_t* cu_q_lens, int32_t total_q, const int32_t* path,
+                                             const int32_t* path_lens, int32_t max_path, int32_t kernel_size,
+                                             const void* state_k_in, const void* state_v_in, void* state_k_out,
+                                             void* state_v_out, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Most pairs of pools in one inkling_attn_tree_commit. */
+#define INK_TREE_MAX_POOLS 128
+
+/*
+ * Acceptance of a path: in every pool the K and V rows of token path[b][j] move from slot H_b + path[b][j] to slot
+ * H_b + j, j < path_lens[b].  The rows behind them stay as they are.
+ *   cu_q_lens, seq_lens, block_table   of the step (seq_lens with all drafted tokens)
+ *   path       device, int32 [B, max_path]: places of the accepted tokens in their sequence, from the root on,
+ *              so strictly increasing; entries from path_lens[b] on are not looked at
+ *   path_lens  device, int32 [B], 0..max_path
+ *   k_caches, v_caches   host arrays of num_pools device pointers (1..INK_TREE_MAX_POOLS): pools of the layers that share
+ *              block_table and the geometry of params
+ *   seq_lens_out  device, int32 [B], or NULL: H_b + path_lens[b], the lengths without what was not accepted
+ *   workspace  device, initialised, of any entry point's size; only its error word is used
+ * Pools must not overlap one another, and what is written must overlap nothing that is read
+ * (INK_ERR_BAD_SHAPE).  A path whose entries are not strictly increasing places of drafted tokens, or whose
+ * length is not in [0, max_path], moves nothing and counts as empty (INK_DEVERR_BAD_TREE); a sequence with n_b > seq_lens[b]
+ * (INK_DEVERR_QLEN_EXCEEDS_KV) or n_b < 0 (INK_DEVERR_BAD_ROWS) is skipped and keeps its length; a row
+ * on a page outside [0, num_pages) is skipped (INK_DEVERR_PAGE_OUT_OF_RANGE).
+ * Two sequences that share a page they move rows on race.
+ */
+ink_status_t inkling_attn_tree_commit(const ink_attn_params_t* params, const int32_t* cu_q_lens,
+                                      const int32_t* seq_lens, const int32_t* block_table, const int32_t* path,
+                                      const int32_t* path_lens, int32_t max_path, int32_t num_pools,
+                                      void* const* k_caches, void* const* v_caches, int32_t* seq_lens_out,
+                                      void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * Synchronise `stream`, copy the sticky device error word (INK_DEVERR_* bits) to

@@ -26,6 +26,7 @@ DEVERR_QLEN_EXCEEDS_KV = 0x2
 DEVERR_WAIT_TIMEOUT = 0x4
 DEVERR_QLEN_EXCEEDS_MAX = 0x8
 DEVERR_BAD_ROWS = 0x10
+DEVERR_BAD_TREE = 0x20
 
 EXPORTED_SYMBOLS = ("inkling_attn_workspace_bytes", "inkling_attn_workspace_init",
                     "inkling_attn_prefill", "inkling_attn_prefill_bf16bias",
@@ -33,6 +34,9 @@ EXPORTED_SYMBOLS = ("inkling_attn_workspace_bytes", "inkling_attn_workspace_init
                     "inkling_attn_decode_noalloc", "inkling_attn_kv_conv_write",
                     "inkling_attn_masked_workspace_bytes", "inkling_attn_prefill_masked",
                     "inkling_attn_decode_masked", "inkling_attn_qk_norm_rope_write",
+                    "inkling_attn_qk_norm_rope_write_at", "inkling_attn_tree_plan",
+                    "inkling_attn_tree_workspace_bytes", "inkling_attn_tree", "inkling_attn_tree_commit",
+                    "inkling_attn_kv_conv_write_tree", "inkling_attn_kv_conv_state_tree",
                     "inkling_attn_read_device_error", "inkling_attn_status_string",
                     "inkling_attn_version", "inkling_attn_set_wait_limit_ns")
 
@@ -60,6 +64,15 @@ class ink_norm_rope_t(ctypes.Structure):
     _fields_ = [("w_q", ctypes.c_void_p), ("w_k", ctypes.c_void_p), ("eps", ctypes.c_float),
                 ("inv_freq", ctypes.c_void_p), ("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int32),
                 ("rot_scale", ctypes.c_float)]
+
+
+class ink_attn_tree_t(ctypes.Structure):
+    _fields_ = [("positions", ctypes.c_void_p), ("ancestors", ctypes.c_void_p), ("words", ctypes.c_int32)]
+
+
+class ink_attn_tree_options_t(ctypes.Structure):
+    _fields_ = [("softcap", ctypes.c_float), ("slopes", ctypes.c_void_p), ("rel_logits", ctypes.c_void_p),
+                ("rel_is_bf16", ctypes.c_int32)]
 
 
 ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
@@ -106,6 +119,21 @@ def load_library(path: Optional[str] = None):
     lib.inkling_attn_decode_masked.restype = ctypes.c_int
     lib.inkling_attn_qk_norm_rope_write.argtypes = [PP, RP, V, I64, V, I64, V, I64, V, I32, V, V, V, V, V, V, S, V]
     lib.inkling_attn_qk_norm_rope_write.restype = ctypes.c_int
+    lib.inkling_attn_qk_norm_rope_write_at.argtypes = [PP, RP, V, V, I64, V, I64, V, I64, V, I32, V, V, V, V, V, V, S, V]
+    lib.inkling_attn_qk_norm_rope_write_at.restype = ctypes.c_int
+    lib.inkling_attn_tree_plan.argtypes = [PP, V, I32, V, V, I32, V, V, V, S, V]
+    lib.inkling_attn_tree_plan.restype = ctypes.c_int
+    lib.inkling_attn_tree_workspace_bytes.argtypes = [PP]
+    lib.inkling_attn_tree_workspace_bytes.restype = S
+    TP, OP = ctypes.POINTER(ink_attn_tree_t), ctypes.POINTER(ink_attn_tree_options_t)
+    lib.inkling_attn_tree.argtypes = [PP, TP, OP, V, V, I32, V, V, V, V, V, V, V, S, V]
+    lib.inkling_attn_tree.restype = ctypes.c_int
+    lib.inkling_attn_kv_conv_write_tree.argtypes = [PP, V, V, V, I32, V, V, V, V, V, I32, V, V, V, V, V, S, V]
+    lib.inkling_attn_kv_conv_write_tree.restype = ctypes.c_int
+    lib.inkling_attn_kv_conv_state_tree.argtypes = [PP, V, V, V, I32, V, V, I32, I32, V, V, V, V, V, S, V]
+    lib.inkling_attn_kv_conv_state_tree.restype = ctypes.c_int
+    lib.inkling_attn_tree_commit.argtypes = [PP, V, V, V, V, V, I32, I32, V, V, V, V, S, V]
+    lib.inkling_attn_tree_commit.restype = ctypes.c_int
     lib.inkling_attn_read_device_error.argtypes = [V, S, V, ctypes.POINTER(ctypes.c_uint32), ctypes.c_int]
     lib.inkling_attn_read_device_error.restype = ctypes.c_int
     lib.inkling_attn_status_string.argtypes = [ctypes.c_int]
@@ -431,11 +459,12 @@ def _token_stride(t, name, shape, device) -> int:
 
 def inkling_attn_qk_norm_rope_write(params, q, k, v, cu_q_lens, seq_lens, block_table, q_out, k_cache, v_cache,
                                     workspace, *, w_q=None, w_k=None, eps: float = 1e-6, inv_freq=None,
-                                    layout: str = "half", rot_scale: float = 1.0, stream=None):
+                                    layout: str = "half", rot_scale: float = 1.0, positions=None, stream=None):
     """Per-head RMS norm and rotation of q and k, and the write of k and v into the paged caches.
 
     ``q``, ``k`` and ``v`` may be views of one fused projection; ``inv_freq`` (see ``rotary.inv_freq``)
-    has one frequency per rotated pair, None for no rotation."""
+    has one frequency per rotated pair, None for no rotation.  ``positions`` (int32 [T]; drafted trees) rotates
+    row t by positions[t] instead of its slot's (inkling_attn_qk_norm_rope_write_at)."""
     pairing = ROPE_LAYOUTS.get(layout)
     if pairing is None:
         raise ValueError(f"layout must be one of {sorted(ROPE_LAYOUTS)}, got {layout!r}")
@@ -454,17 +483,212 @@ def inkling_attn_qk_norm_rope_write(params, q, k, v, cu_q_lens, seq_lens, block_
             v.data_ptr(), strides[2], cu, T, seq_lens.data_ptr(), block_table.data_ptr(), q_out.data_ptr(),
             k_cache.data_ptr(), v_cache.data_ptr(), workspace.data_ptr(), workspace.numel(), _raw_stream(device) if stream
             is None else _stream_handle(stream))
+    at = _opt(positions, "positions", _I32, (T,), device)
     if T == 0 or params.num_seqs == 0:   # (empty tensors have no address)
         return q_out
-    fn = (_lib or load_library()).inkling_attn_qk_norm_rope_write
+    lib, where = _lib or load_library(), "inkling_attn_qk_norm_rope_write"
+    fn = lib.inkling_attn_qk_norm_rope_write
+    if positions is not None:
+        fn, where = lib.inkling_attn_qk_norm_rope_write_at, "inkling_attn_qk_norm_rope_write_at"
+        args = (*args[:2], at, *args[2:])
     if _current_device() == device:
         code = fn(*args)
     else:
         with torch.cuda.device(device):
             code = fn(*args)
     if code != INK_OK:
-        raise InkError(code, "inkling_attn_qk_norm_rope_write")
+        raise InkError(code, where)
     return q_out
+
+
+def _run_on(device, fn, args, where):
+    """Call the library with `device` current, raise for a status."""
+    if _current_device() == device:
+        code = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            code = fn(*args)
+    if code != INK_OK:
+        raise InkError(code, where)
+
+
+def _held(t, dtype, shape, device) -> bool:
+    return (isinstance(t, torch.Tensor) and t.dtype is dtype and (shape is None or t.shape == shape)
+            and t.get_device() == device and t.is_contiguous())
+
+
+def _need(device, *args):
+    """Every (tensor, name, dtype, shape or None) is what it has to be, on `device`."""
+    for t, name, dtype, shape in args:
+        if not _held(t, dtype, shape, device):
+            _refuse(device, (t, name, dtype, shape))
+
+
+def _rows_of(t, name) -> tuple:
+    """(device, rows) of the tensor that a call's other tensors are checked against."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    device = t.get_device()
+    if device < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() == 0:
+        raise ValueError(f"{name} must have rows")
+    return device, t.shape[0]
+
+
+def inkling_attn_tree_plan(params, cu_q_lens, seq_lens, parents, positions, ancestors, workspace, stream=None):
+    """Positions (int32 [T]) and ancestor bits (int32 [T, words]) of drafted tokens from their parents (int32 [T])."""
+    device, T = _rows_of(parents, "parents")
+    B = params.num_seqs
+    words = ancestors.shape[1] if isinstance(ancestors, torch.Tensor) and ancestors.dim() == 2 else 1
+    _need(device, (parents, "parents", _I32, (T,)), (cu_q_lens, "cu_q_lens", _I32, (B + 1,)),
+          (seq_lens, "seq_lens", _I32, (B,)), (positions, "positions", _I32, (T,)),
+          (ancestors, "ancestors", _I32, (T, words)), (workspace, "workspace", _U8, None))
+    if T == 0 or B == 0:   # (empty tensors have no address)
+        return positions, ancestors
+    args = (ctypes.byref(params), cu_q_lens.data_ptr(), T, seq_lens.data_ptr(), parents.data_ptr(), words,
+            positions.data_ptr(), ancestors.data_ptr(), workspace.data_ptr(), workspace.numel(),
+            _raw_stream(device) if stream is None else _stream_handle(stream))
+    _run_on(device, (_lib or load_library()).inkling_attn_tree_plan, args, "inkling_attn_tree_plan")
+    return positions, ancestors
+
+
+def inkling_attn_tree_workspace_bytes(params: ink_attn_params_t) -> int:
+    return int(load_library().inkling_attn_tree_workspace_bytes(ctypes.byref(params)))
+
+
+def alloc_tree_workspace(params: ink_attn_params_t, device="cuda") -> torch.Tensor:
+    """Allocate (through PyTorch) and initialise a workspace for the calls on trees of drafted tokens."""
+    n = inkling_attn_tree_workspace_bytes(params)
+    if n == 0:
+        raise InkError(2, "inkling_attn_tree_workspace_bytes")
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    with torch.cuda.device(ws.device):
+        inkling_attn_workspace_init(ws)
+    return ws
+
+
+def inkling_attn_tree(params, q, cu_q_lens, k_cache, v_cache, block_table, seq_lens, positions, ancestors, out, workspace,
+                      *, rel_logits=None, softcap: float = 0.0, slopes=None, lse=None, stream=None):
+    """Attention of drafted tokens over the history and their ancestors, with a bias tensor (fp32 or bf16
+    [T, Hq, rel_extent]), capped scores or a distance bias."""
+    device = _device_of(q)
+    T, Hq = q.shape[0], params.num_q_heads
+    rows = (T, Hq, params.head_dim)
+    if q.dtype is not _BF16 or q.shape != rows or not q.is_contiguous():
+        _refuse(device, (q, "q", _BF16, rows))
+    _pools_hold(params, device, rows, q, out, k_cache, v_cache, block_table, seq_lens, workspace)
+    words = ancestors.shape[1] if isinstance(ancestors, torch.Tensor) and ancestors.dim() == 2 else 1
+    _need(device, (cu_q_lens, "cu_q_lens", _I32, (params.num_seqs + 1,)), (positions, "positions", _I32, (T,)),
+          (ancestors, "ancestors", _I32, (T, words)))
+    bf16 = isinstance(rel_logits, torch.Tensor) and rel_logits.dtype is _BF16
+    rel = _opt(rel_logits, "rel_logits", _BF16 if bf16 else _F32, (T, Hq, params.rel_extent), device)
+    tree = ink_attn_tree_t(positions.data_ptr(), ancestors.data_ptr(), words)
+    opts = ink_attn_tree_options_t(softcap, _opt(slopes, "slopes", _F32, (Hq,), device), rel, bf16)
+    args = (ctypes.byref(params), ctypes.byref(tree), ctypes.byref(opts), q.data_ptr(), cu_q_lens.data_ptr(), T,
+            k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(),
+            _opt(lse, "lse", _F32, (T, Hq), device), workspace.data_ptr(), workspace.numel(),
+            _raw_stream(device) if stream is None else _stream_handle(stream))
+    if T == 0 or params.num_seqs == 0:   # (empty tensors have no address)
+        return out
+    _run_on(device, (_lib or load_library()).inkling_attn_tree, args, "inkling_attn_tree")
+    return out
+
+
+def inkling_attn_kv_conv_write_tree(params, k_new, v_new, cu_q_lens, seq_lens, block_table, parents, w_k, w_v,
+                                    state_k_in, state_v_in, k_cache, v_cache, workspace, stream=None):
+    """The short convolution of drafted K/V rows along their paths to the root, into the paged caches; with
+    kernel size 1 (the last dimension of ``w_k``) the state tensors may be None."""
+    device, T = _rows_of(k_new, "k_new")
+    B, Hkv, D = params.num_seqs, params.num_kv_heads, params.head_dim
+    ks = int(w_k.shape[-1]) if isinstance(w_k, torch.Tensor) and w_k.dim() == 3 else 1
+    rows, taps, state = (T, Hkv, D), (Hkv, D, ks), (B, ks - 1, Hkv, D)
+    pool = (params.num_pages, Hkv, params.page_size, D)
+    _need(device, (k_new, "k_new", _BF16, rows), (v_new, "v_new", _BF16, rows), (cu_q_lens, "cu_q_lens", _I32, (B + 1,)),
+          (seq_lens, "seq_lens", _I32, (B,)), (block_table, "block_table", _I32, (B, params.max_pages_per_seq)),
+          (parents, "parents", _I32, (T,)), (w_k, "w_k", _F32, taps), (w_v, "w_v", _F32, taps),
+          (k_cache, "k_cache", _BF16, pool), (v_cache, "v_cache", _BF16, pool),
+          (workspace, "workspace", _U8, None))
+    if ks > 1:
+        _need(device, (state_k_in, "state_k_in", _BF16, state), (state_v_in, "state_v_in", _BF16, state))
+    if T == 0 or B == 0:   # (empty tensors have no address)
+        return k_cache, v_cache
+    args = (ctypes.byref(params), k_new.data_ptr(), v_new.data_ptr(), cu_q_lens.data_ptr(), T, seq_lens.data_ptr(),
+            block_table.data_ptr(), parents.data_ptr(), w_k.data_ptr(), w_v.data_ptr(), ks,
+            state_k_in.data_ptr() if ks > 1 else None, state_v_in.data_ptr() if ks > 1 else None, k_cache.data_ptr(),
+            v_cache.data_ptr(), workspace.data_ptr(), workspace.numel(),
+            _raw_stream(device) if stream is None else _stream_handle(stream))
+    _run_on(device, (_lib or load_library()).inkling_attn_kv_conv_write_tree, args, "inkling_attn_kv_conv_write_tree")
+    return k_cache, v_cache
+
+
+def inkling_attn_kv_conv_state_tree(params, k_new, v_new, cu_q_lens, path, path_lens, state_k_in, state_v_in, state_k_out,
+                                    state_v_out, workspace, stream=None):
+    """The convolution state behind the accepted path (int32 [B, max_path], lengths int32 [B]) of each sequence."""
+    device, T = _rows_of(k_new, "k_new")
+    B, Hkv, D = params.num_seqs, params.num_kv_heads, params.head_dim
+    keep = state_k_in.shape[1] if isinstance(state_k_in, torch.Tensor) and state_k_in.dim() == 4 else 1
+    width = path.shape[1] if isinstance(path, torch.Tensor) and path.dim() == 2 else 1
+    rows, state = (T, Hkv, D), (B, keep, Hkv, D)
+    _need(device, (k_new, "k_new", _BF16, rows), (v_new, "v_new", _BF16, rows), (cu_q_lens, "cu_q_lens", _I32, (B + 1,)),
+          (path, "path", _I32, (B, width)), (path_lens, "path_lens", _I32, (B,)), (state_k_in, "state_k_in", _BF16, state),
+          (state_v_in, "state_v_in", _BF16, state), (state_k_out, "state_k_out", _BF16, state),
+          (state_v_out, "state_v_out", _BF16, state), (workspace, "workspace", _U8, None))
+    if B == 0 or keep == 0:   # (empty tensors have no address)
+        return state_k_out, state_v_out
+    args = (ctypes.byref(params), k_new.data_ptr() or None, v_new.data_ptr() or None, cu_q_lens.data_ptr(), T,
+            path.data_ptr(), path_lens.data_ptr(), width, keep + 1, state_k_in.data_ptr(), state_v_in.data_ptr(),
+            state_k_out.data_ptr(), state_v_out.data_ptr(), workspace.data_ptr(), workspace.numel(),
+            _raw_stream(device) if stream is None else _stream_handle(stream))
+    _run_on(device, (_lib or load_library()).inkling_attn_kv_conv_state_tree, args, "inkling_attn_kv_conv_state_tree")
+    return state_k_out, state_v_out
+
+
+class TreePools:
+    """The K and V pools of the layers that share a block table, checked once (see :func:`tree_pools`).
+
+    It holds the tensors, so that the addresses it hands to the library stay theirs."""
+
+    def __init__(self, params, k_caches, v_caches):
+        self.k_caches, self.v_caches = tuple(k_caches), tuple(v_caches)
+        if not self.k_caches or len(self.k_caches) != len(self.v_caches):
+            raise ValueError("k_caches and v_caches must be equally many, one at least")
+        self.device, _ = _rows_of(self.k_caches[0], "k_caches")
+        self.shape = (params.num_pages, params.num_kv_heads, params.page_size, params.head_dim)
+        _need(self.device, *((t, name, _BF16, self.shape) for name, ts in (("k_caches", self.k_caches),
+                                                                           ("v_caches", self.v_caches)) for t in ts))
+        pointers = ctypes.c_void_p * len(self.k_caches)
+        self.k_ptrs = pointers(*(t.data_ptr() for t in self.k_caches))
+        self.v_ptrs = pointers(*(t.data_ptr() for t in self.v_caches))
+
+
+def tree_pools(params, k_caches, v_caches) -> TreePools:
+    """The pools that :func:`inkling_attn_tree_commit` moves rows in: a list of K and one of V tensors."""
+    return TreePools(params, k_caches, v_caches)
+
+
+def inkling_attn_tree_commit(params, cu_q_lens, seq_lens, block_table, path, path_lens, pools, seq_lens_out, workspace,
+                             stream=None):
+    """Move the K and V rows of each sequence's accepted path behind its history, in all ``pools``; the
+    lengths without what was not accepted go to ``seq_lens_out`` (or None)."""
+    if not isinstance(pools, TreePools):
+        raise TypeError("pools must come from tree_pools()")
+    device, B = pools.device, params.num_seqs
+    shape = (params.num_pages, params.num_kv_heads, params.page_size, params.head_dim)
+    if pools.shape != shape:
+        raise ValueError(f"pools have shape {pools.shape}, params say {shape}")
+    width = path.shape[1] if isinstance(path, torch.Tensor) and path.dim() == 2 else 1
+    _need(device, (cu_q_lens, "cu_q_lens", _I32, (B + 1,)), (seq_lens, "seq_lens", _I32, (B,)),
+          (block_table, "block_table", _I32, (B, params.max_pages_per_seq)), (path, "path", _I32, (B, width)),
+          (path_lens, "path_lens", _I32, (B,)), (workspace, "workspace", _U8, None))
+    args = (ctypes.byref(params), cu_q_lens.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(), path.data_ptr(),
+            path_lens.data_ptr(), width, len(pools.k_caches), pools.k_ptrs, pools.v_ptrs,
+            _opt(seq_lens_out, "seq_lens_out", _I32, (B,), device), workspace.data_ptr(), workspace.numel(),
+            _raw_stream(device) if stream is None else _stream_handle(stream))
+    if B == 0:   # (empty tensors have no address)
+        return seq_lens_out
+    _run_on(device, (_lib or load_library()).inkling_attn_tree_commit, args, "inkling_attn_tree_commit")
+    return seq_lens_out
 
 
 def inkling_attn_set_wait_limit_ns(limit_ns: int) -> None:

@@ -6,9 +6,11 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <atomic>
-#include <mutex>
 #include <cstring>
+#include <functional>
+#include <mutex>
 
 #include "../../include/inkling_attn.h"
 #include "kernels.h"
@@ -581,6 +583,15 @@ bool overlap(const Span* s, int written, int n) {
   return false;
 }
 
+struct TreeLayout {
+  size_t total;
+};
+
+TreeLayout tree_layout(const ink_attn_params_t* p) {
+  (void)p;
+  return {kHeaderBytes};
+}
+
 size_t pool_bytes(const ink_attn_params_t* p) { return pool_rows(p) * p->head_dim * 2; }
 
 size_t table_bytes(const ink_attn_params_t* p) { return (size_t)p->num_seqs * p->max_pages_per_seq * 4; }
@@ -717,12 +728,16 @@ ink_status_t inkling_attn_decode_masked(const ink_attn_params_t* params, const i
                      seq_lens, out, lse, workspace, workspace_bytes, stream, true);
 }
 
-ink_status_t inkling_attn_qk_norm_rope_write(const ink_attn_params_t* params, const ink_norm_rope_t* rope,
-                                             const void* q, int64_t q_stride, const void* k, int64_t k_stride,
-                                             const void* v, int64_t v_stride, const int32_t* cu_q_lens,
-                                             int32_t total_q, const int32_t* seq_lens, const int32_t* block_table,
-                                             void* q_out, void* k_cache, void* v_cache, void* workspace,
-                                             size_t workspace_bytes, void* stream) {
+}  // extern "C"
+
+namespace {
+
+ink_status_t norm_rope_impl(const ink_attn_params_t* params, const ink_norm_rope_t* rope, const int32_t* positions,
+                            const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                            const void* v, int64_t v_stride, const int32_t* cu_q_lens,
+                            int32_t total_q, const int32_t* seq_lens, const int32_t* block_table,
+                            void* q_out, void* k_cache, void* v_cache, void* workspace,
+                            size_t workspace_bytes, void* stream) {
   ink_status_t st = validate(params);
   if (st != INK_OK) return st;
   if (!rope || !q || !k || !v || !cu_q_lens || !seq_lens || !block_table || !q_out || !k_cache || !v_cache ||
@@ -738,7 +753,7 @@ ink_status_t inkling_attn_qk_norm_rope_write(const ink_attn_params_t* params, co
   if (q_stride % 8 != 0 || k_stride % 8 != 0 || v_stride % 8 != 0 || !aligned(q, 16) || !aligned(k, 16) ||
       !aligned(v, 16) || !aligned(q_out, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
       !aligned(rope->w_q, 16) || !aligned(rope->w_k, 16) || !aligned(rope->inv_freq, 4) || !aligned(cu_q_lens, 4) ||
-      !aligned(seq_lens, 4) || !aligned(block_table, 4) || !aligned(workspace, 256))
+      !aligned(seq_lens, 4) || !aligned(block_table, 4) || !aligned(positions, 4) || !aligned(workspace, 256))
     return INK_ERR_ALIGNMENT;
   if (q_out == q && q_stride != (int64_t)Hq * D) return INK_ERR_BAD_SHAPE;
   if (workspace_bytes < kHeaderBytes) return INK_ERR_WORKSPACE;
@@ -750,7 +765,8 @@ ink_status_t inkling_attn_qk_norm_rope_write(const ink_attn_params_t* params, co
                         {k, span(k_stride, Hkv)}, {v, span(v_stride, Hkv)}, {block_table, table_bytes(params)},
                         {seq_lens, (size_t)params->num_seqs * 4}, {cu_q_lens, (size_t)params->num_seqs * 4 + 4},
                         {rope->w_q, (size_t)D * 4}, {rope->w_k, (size_t)D * 4},
-                        {rope->rot_dim > 0 ? rope->inv_freq : nullptr, (size_t)rope->rot_dim * 2}};
+                        {rope->rot_dim > 0 ? rope->inv_freq : nullptr, (size_t)rope->rot_dim * 2},
+                        {positions, (size_t)total_q * 4}};
   if (overlap(spans, 4, sizeof spans / sizeof *spans)) return INK_ERR_BAD_SHAPE;
   ink::NormRopeArgs a;
   a.x[0] = static_cast<const uint16_t*>(q);
@@ -777,6 +793,7 @@ ink_status_t inkling_attn_qk_norm_rope_write(const ink_attn_params_t* params, co
   a.max_pages = params->max_pages_per_seq;
   a.num_pages = params->num_pages;
   a.rot_dim = rope->rot_dim;
+  a.positions = positions;
   a.eps = rope->eps;
   a.rot_scale = rope->rot_scale;
   int dev = 0;
@@ -785,6 +802,287 @@ ink_status_t inkling_attn_qk_norm_rope_write(const ink_attn_params_t* params, co
   if (ink::launch_qk_norm_rope(a, D, rope->layout == INK_ROPE_INTERLEAVED, sms, (cudaStream_t)stream) != cudaSuccess)
     return INK_ERR_CUDA;
   return INK_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+ink_status_t inkling_attn_qk_norm_rope_write(const ink_attn_params_t* params, const ink_norm_rope_t* rope,
+                                             const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                             const void* v, int64_t v_stride, const int32_t* cu_q_lens,
+                                             int32_t total_q, const int32_t* seq_lens, const int32_t* block_table,
+                                             void* q_out, void* k_cache, void* v_cache, void* workspace,
+                                             size_t workspace_bytes, void* stream) {
+  return norm_rope_impl(params, rope, nullptr, q, q_stride, k, k_stride, v, v_stride, cu_q_lens, total_q, seq_lens,
+                        block_table, q_out, k_cache, v_cache, workspace, workspace_bytes, stream);
+}
+
+ink_status_t inkling_attn_qk_norm_rope_write_at(const ink_attn_params_t* params, const ink_norm_rope_t* rope,
+                                                const int32_t* positions, const void* q, int64_t q_stride,
+                                                const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                                                const int32_t* cu_q_lens, int32_t total_q, const int32_t* seq_lens,
+                                                const int32_t* block_table, void* q_out, void* k_cache, void* v_cache,
+                                                void* workspace, size_t workspace_bytes, void* stream) {
+  if (params && !positions) return INK_ERR_NULL_PTR;
+  return norm_rope_impl(params, rope, positions, q, q_stride, k, k_stride, v, v_stride, cu_q_lens, total_q, seq_lens,
+                        block_table, q_out, k_cache, v_cache, workspace, workspace_bytes, stream);
+}
+
+ink_status_t inkling_attn_tree_plan(const ink_attn_params_t* params, const int32_t* cu_q_lens, int32_t total_q,
+                                    const int32_t* seq_lens, const int32_t* parents, int32_t words,
+                                    int32_t* positions, uint32_t* ancestors, void* workspace,
+                                    size_t workspace_bytes, void* stream) {
+  ink_status_t st = validate(params);
+  if (st != INK_OK) return st;
+  if (!cu_q_lens || !seq_lens || !parents || !positions || !ancestors || !workspace) return INK_ERR_NULL_PTR;
+  if (total_q < 0 || words < 1 || words > ink::TREE_MAX_WORDS) return INK_ERR_BAD_SHAPE;
+  if (!aligned(cu_q_lens, 4) || !aligned(seq_lens, 4) || !aligned(parents, 4) || !aligned(positions, 4) ||
+      !aligned(ancestors, 4) || !aligned(workspace, 256))
+    return INK_ERR_ALIGNMENT;
+  if (workspace_bytes < kHeaderBytes) return INK_ERR_WORKSPACE;
+  if (params->num_seqs == 0 || total_q == 0) return INK_OK;
+  const size_t seqs = (size_t)params->num_seqs * 4, rows = (size_t)total_q * 4;
+  const Span spans[] = {{positions, rows}, {ancestors, rows * words}, {workspace, kHeaderBytes}, {cu_q_lens, seqs + 4},
+                        {seq_lens, seqs}, {parents, rows}};
+  if (overlap(spans, 3, sizeof spans / sizeof *spans)) return INK_ERR_BAD_SHAPE;
+  ink::TreePlanArgs a;
+  a.cu_q = cu_q_lens;
+  a.seq_lens = seq_lens;
+  a.parents = parents;
+  a.positions = positions;
+  a.ancestors = ancestors;
+  a.err = reinterpret_cast<uint32_t*>(workspace);
+  a.B = params->num_seqs;
+  a.T = total_q;
+  a.words = words;
+  return ink::launch_tree_plan(a, (cudaStream_t)stream) == cudaSuccess ? INK_OK : INK_ERR_CUDA;
+}
+
+size_t inkling_attn_tree_workspace_bytes(const ink_attn_params_t* params) {
+  if (validate(params) != INK_OK) return 0;
+  return tree_layout(params).total;
+}
+
+ink_status_t inkling_attn_tree(const ink_attn_params_t* params, const ink_attn_tree_t* tree,
+                               const ink_attn_tree_options_t* options, const void* q, const int32_t* cu_q_lens,
+                               int32_t total_q, const void* k_cache, const void* v_cache,
+                               const int32_t* block_table, const int32_t* seq_lens, void* out, float* lse,
+                               void* workspace, size_t workspace_bytes, void* stream) {
+  ink_status_t st = validate(params);
+  if (st != INK_OK) return st;
+  static const ink_attn_tree_options_t kNone = {0.f, nullptr, nullptr, 0};
+  const ink_attn_tree_options_t& o = options ? *options : kNone;
+  if (!tree || !tree->positions || !tree->ancestors || !q || !cu_q_lens || !k_cache || !v_cache || !block_table ||
+      !seq_lens || !out || !workspace)
+    return INK_ERR_NULL_PTR;
+  if (total_q < 0 || tree->words < 1 || tree->words > ink::TREE_MAX_WORDS) return INK_ERR_BAD_SHAPE;
+  if (!(o.softcap == 0.f || (o.softcap >= 1e-6f && o.softcap <= 1e6f))) return INK_ERR_BAD_SHAPE;
+  if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) ||
+      !aligned(cu_q_lens, 4) || !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(lse, 4) ||
+      !aligned(tree->positions, 4) || !aligned(tree->ancestors, 4) || !aligned(o.slopes, 4) ||
+      !aligned(o.rel_logits, o.rel_is_bf16 ? 2 : 4) || !aligned(workspace, 256))
+    return INK_ERR_ALIGNMENT;
+  if ((long long)total_q * params->num_q_heads >= (1ll << 31)) return INK_ERR_TOO_LARGE;
+  const TreeLayout lay = tree_layout(params);
+  if (workspace_bytes < lay.total) return INK_ERR_WORKSPACE;
+  if (params->num_seqs == 0 || total_q == 0) return INK_OK;
+  const size_t rows = (size_t)total_q * params->num_q_heads, seqs = (size_t)params->num_seqs * 4;
+  const Span spans[] = {{out, rows * params->head_dim * 2}, {lse, rows * 4}, {workspace, lay.total},
+                        {q, rows * params->head_dim * 2}, {k_cache, pool_bytes(params)}, {v_cache, pool_bytes(params)},
+                        {block_table, table_bytes(params)}, {seq_lens, seqs}, {cu_q_lens, seqs + 4},
+                        {tree->positions, (size_t)total_q * 4}, {tree->ancestors, (size_t)total_q * tree->words * 4},
+                        {o.slopes, (size_t)params->num_q_heads * 4},
+                        {o.rel_logits, rows * params->rel_extent * (o.rel_is_bf16 ? 2 : 4)}};
+  if (overlap(spans, 3, sizeof spans / sizeof *spans)) return INK_ERR_BAD_SHAPE;
+  ink::TreeArgs a;
+  a.q = q;
+  a.cu_q = cu_q_lens;
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.positions = tree->positions;
+  a.ancestors = tree->ancestors;
+  a.words = tree->words;
+  a.slopes = o.slopes;
+  a.rel = o.rel_logits;
+  a.rel_bf16 = o.rel_is_bf16 ? 1 : 0;
+  a.k = k_cache;
+  a.v = v_cache;
+  a.out = out;
+  a.lse = lse;
+  a.err = reinterpret_cast<uint32_t*>(workspace);
+  a.B = params->num_seqs;
+  a.T = total_q;
+  a.Hq = params->num_q_heads;
+  a.Hkv = params->num_kv_heads;
+  a.G = params->num_q_heads / params->num_kv_heads;
+  a.log2_page = ilog2(params->page_size);
+  a.max_pages = params->max_pages_per_seq;
+  a.num_pages = params->num_pages;
+  a.W = params->window;
+  a.E = params->rel_extent;
+  a.softcap = o.softcap;
+  a.scale_log2 = params->sm_scale * 1.4426950408889634f;
+  a.cap_log2 = o.softcap * 1.4426950408889634f;
+  a.cap_k1 = o.softcap > 0.f ? (float)(2.0 * 1.4426950408889634 * params->sm_scale / o.softcap) : 0.f;
+  a.cap_inv = o.softcap > 0.f ? params->sm_scale / o.softcap : 0.f;
+  a.wait_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
+  return ink::launch_tree(a, params->head_dim, (cudaStream_t)stream) == cudaSuccess ? INK_OK : INK_ERR_CUDA;
+}
+
+ink_status_t inkling_attn_kv_conv_write_tree(const ink_attn_params_t* params, const void* k_new, const void* v_new,
+                                             const int32_t* cu_q_lens, int32_t total_q, const int32_t* seq_lens,
+                                             const int32_t* block_table, const int32_t* parents, const float* w_k,
+                                             const float* w_v, int32_t kernel_size, const void* state_k_in,
+                                             const void* state_v_in, void* k_cache, void* v_cache, void* workspace,
+                                             size_t workspace_bytes, void* stream) {
+  ink_status_t st = validate(params);
+  if (st != INK_OK) return st;
+  if (kernel_size < 1 || kernel_size > 8 || total_q < 0) return INK_ERR_BAD_SHAPE;
+  if (!k_new || !v_new || !cu_q_lens || !seq_lens || !block_table || !parents || !w_k || !w_v || !k_cache || !v_cache ||
+      !workspace || (kernel_size > 1 && (!state_k_in || !state_v_in)))
+    return INK_ERR_NULL_PTR;
+  if (kernel_size == 1) state_k_in = state_v_in = nullptr;
+  if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(w_k, 16) ||
+      !aligned(w_v, 16) || !aligned(state_k_in, 16) || !aligned(state_v_in, 16) || !aligned(cu_q_lens, 4) ||
+      !aligned(seq_lens, 4) || !aligned(block_table, 4) || !aligned(parents, 4) || !aligned(workspace, 256))
+    return INK_ERR_ALIGNMENT;
+  if (workspace_bytes < kHeaderBytes) return INK_ERR_WORKSPACE;
+  if ((long long)params->num_seqs * (kernel_size - 1) >= (1ll << 31)) return INK_ERR_TOO_LARGE;   // rows of the states
+  if (params->num_seqs == 0 || total_q == 0) return INK_OK;
+  const size_t row = (size_t)params->num_kv_heads * params->head_dim * 2, taps = row * 2 * kernel_size;
+  const size_t state = (size_t)params->num_seqs * (kernel_size - 1) * row, seqs = (size_t)params->num_seqs * 4;
+  const Span spans[] = {{k_cache, pool_bytes(params)}, {v_cache, pool_bytes(params)}, {workspace, kHeaderBytes},
+                        {k_new, total_q * row}, {v_new, total_q * row}, {cu_q_lens, seqs + 4}, {seq_lens, seqs},
+                        {block_table, table_bytes(params)}, {parents, (size_t)total_q * 4}, {w_k, taps}, {w_v, taps},
+                        {state_k_in, state}, {state_v_in, state}};
+  if (overlap(spans, 3, sizeof spans / sizeof *spans)) return INK_ERR_BAD_SHAPE;
+  ink::TreeConvArgs a{};
+  a.x[0] = static_cast<const uint16_t*>(k_new);
+  a.x[1] = static_cast<const uint16_t*>(v_new);
+  a.w[0] = w_k;
+  a.w[1] = w_v;
+  a.st_in[0] = static_cast<const uint16_t*>(state_k_in);
+  a.st_in[1] = static_cast<const uint16_t*>(state_v_in);
+  a.cache[0] = static_cast<uint16_t*>(k_cache);
+  a.cache[1] = static_cast<uint16_t*>(v_cache);
+  a.cu_q = cu_q_lens;
+  a.seq_lens = seq_lens;
+  a.block_table = block_table;
+  a.parents = parents;
+  a.err = reinterpret_cast<uint32_t*>(workspace);
+  a.B = params->num_seqs;
+  a.T = total_q;
+  a.D = params->head_dim;
+  a.log2_page = ilog2(params->page_size);
+  a.max_pages = params->max_pages_per_seq;
+  a.num_pages = params->num_pages;
+  a.nvec = params->num_kv_heads * params->head_dim / 8;
+  int dev = 0;
+  const int sms = ink::current_device_sms(&dev);
+  if (sms <= 0) return INK_ERR_CUDA;
+  return ink::launch_kv_conv_tree(a, kernel_size, sms, (cudaStream_t)stream) == cudaSuccess ? INK_OK : INK_ERR_CUDA;
+}
+
+ink_status_t inkling_attn_kv_conv_state_tree(const ink_attn_params_t* params, const void* k_new, const void* v_new,
+                                             const int32_t* cu_q_lens, int32_t total_q, const int32_t* path,
+                                             const int32_t* path_lens, int32_t max_path, int32_t kernel_size,
+                                             const void* state_k_in, const void* state_v_in, void* state_k_out,
+                                             void* state_v_out, void* workspace, size_t workspace_bytes, void* stream) {
+  ink_status_t st = validate(params);
+  if (st != INK_OK) return st;
+  if (kernel_size < 1 || kernel_size > 8 || total_q < 0 || max_path < 1) return INK_ERR_BAD_SHAPE;
+  if (!cu_q_lens || !path || !path_lens || !workspace || (total_q > 0 && (!k_new || !v_new))) return INK_ERR_NULL_PTR;
+  if (kernel_size > 1 && (!state_k_in || !state_v_in || !state_k_out || !state_v_out)) return INK_ERR_NULL_PTR;
+  if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(cu_q_lens, 4) || !aligned(path, 4) || !aligned(path_lens, 4) ||
+      !aligned(workspace, 256))
+    return INK_ERR_ALIGNMENT;
+  if (kernel_size > 1 && (!aligned(state_k_in, 16) || !aligned(state_v_in, 16) || !aligned(state_k_out, 16) ||
+                          !aligned(state_v_out, 16)))
+    return INK_ERR_ALIGNMENT;
+  if (workspace_bytes < kHeaderBytes) return INK_ERR_WORKSPACE;
+  if ((long long)params->num_seqs * (kernel_size - 1) >= (1ll << 31)) return INK_ERR_TOO_LARGE;
+  if (params->num_seqs == 0 || kernel_size == 1) return INK_OK;
+  const size_t row = (size_t)params->num_kv_heads * params->head_dim * 2, seqs = (size_t)params->num_seqs * 4;
+  const size_t state = (size_t)params->num_seqs * (kernel_size - 1) * row;
+  const Span spans[] = {{state_k_out, state}, {state_v_out, state}, {workspace, kHeaderBytes}, {state_k_in, state},
+                        {state_v_in, state}, {k_new, total_q * row}, {v_new, total_q * row}, {cu_q_lens, seqs + 4},
+                        {path, seqs * max_path}, {path_lens, seqs}};
+  if (overlap(spans, 3, sizeof spans / sizeof *spans)) return INK_ERR_BAD_SHAPE;
+  ink::TreeConvArgs a{};
+  a.x[0] = static_cast<const uint16_t*>(k_new);
+  a.x[1] = static_cast<const uint16_t*>(v_new);
+  a.st_in[0] = static_cast<const uint16_t*>(state_k_in);
+  a.st_in[1] = static_cast<const uint16_t*>(state_v_in);
+  a.st_out[0] = static_cast<uint16_t*>(state_k_out);
+  a.st_out[1] = static_cast<uint16_t*>(state_v_out);
+  a.cu_q = cu_q_lens;
+  a.path = path;
+  a.path_lens = path_lens;
+  a.max_path = max_path;
+  a.err = reinterpret_cast<uint32_t*>(workspace);
+  a.B = params->num_seqs;
+  a.T = total_q;
+  a.D = params->head_dim;
+  a.nvec = params->num_kv_heads * params->head_dim / 8;
+  return ink::launch_kv_conv_state_tree(a, kernel_size, (cudaStream_t)stream) == cudaSuccess ? INK_OK : INK_ERR_CUDA;
+}
+
+ink_status_t inkling_attn_tree_commit(const ink_attn_params_t* params, const int32_t* cu_q_lens,
+                                      const int32_t* seq_lens, const int32_t* block_table, const int32_t* path,
+                                      const int32_t* path_lens, int32_t max_path, int32_t num_pools,
+                                      void* const* k_caches, void* const* v_caches, int32_t* seq_lens_out,
+                                      void* workspace, size_t workspace_bytes, void* stream) {
+  ink_status_t st = validate(params);
+  if (st != INK_OK) return st;
+  if (!cu_q_lens || !seq_lens || !block_table || !path || !path_lens || !k_caches || !v_caches || !workspace)
+    return INK_ERR_NULL_PTR;
+  if (max_path < 1 || num_pools < 1 || num_pools > INK_TREE_MAX_POOLS) return INK_ERR_BAD_SHAPE;
+  if (!aligned(cu_q_lens, 4) || !aligned(seq_lens, 4) || !aligned(block_table, 4) || !aligned(path, 4) ||
+      !aligned(path_lens, 4) || !aligned(seq_lens_out, 4) || !aligned(workspace, 256))
+    return INK_ERR_ALIGNMENT;
+  ink::TreeCommitArgs a;
+  a.npools = 2 * num_pools;
+  for (int i = 0; i < num_pools; ++i) {
+    a.pool[2 * i] = static_cast<uint16_t*>(k_caches[i]);
+    a.pool[2 * i + 1] = static_cast<uint16_t*>(v_caches[i]);
+  }
+  for (int i = 0; i < a.npools; ++i) {
+    if (!a.pool[i]) return INK_ERR_NULL_PTR;
+    if (!aligned(a.pool[i], 16)) return INK_ERR_ALIGNMENT;
+  }
+  if (workspace_bytes < kHeaderBytes) return INK_ERR_WORKSPACE;
+  if (params->num_seqs == 0) return INK_OK;
+  const size_t seqs = (size_t)params->num_seqs * 4, pool = pool_bytes(params);
+  Span spans[] = {{nullptr, pool}, {seq_lens_out, seqs}, {workspace, kHeaderBytes}, {cu_q_lens, seqs + 4}, {seq_lens, seqs},
+                  {block_table, table_bytes(params)}, {path, seqs * max_path}, {path_lens, seqs}};
+  constexpr int kSpans = sizeof spans / sizeof *spans;
+  for (int i = 0; i < a.npools; ++i) {
+    spans[0].at = a.pool[i];
+    if (overlap(spans, i == 0 ? 3 : 1, kSpans)) return INK_ERR_BAD_SHAPE;
+  }
+  const uint16_t* sorted[2 * INK_TREE_MAX_POOLS];   // pools side by side: each ends before the next begins
+  std::copy(a.pool, a.pool + a.npools, sorted);
+  std::sort(sorted, sorted + a.npools, std::less<const uint16_t*>());
+  for (int i = 0; i + 1 < a.npools; ++i)
+    if (reinterpret_cast<uintptr_t>(sorted[i]) + pool > reinterpret_cast<uintptr_t>(sorted[i + 1])) return INK_ERR_BAD_SHAPE;
+  a.cu_q = cu_q_lens;
+  a.seq_lens = seq_lens;
+  a.block_table = block_table;
+  a.path = path;
+  a.path_lens = path_lens;
+  a.max_path = max_path;
+  a.seq_lens_out = seq_lens_out;
+  a.err = reinterpret_cast<uint32_t*>(workspace);
+  a.B = params->num_seqs;
+  a.Hkv = params->num_kv_heads;
+  a.log2_page = ilog2(params->page_size);
+  a.max_pages = params->max_pages_per_seq;
+  a.num_pages = params->num_pages;
+  int dev = 0;
+  const int sms = ink::current_device_sms(&dev);
+  if (sms <= 0) return INK_ERR_CUDA;
+  return ink::launch_tree_commit(a, params->head_dim, sms, (cudaStream_t)stream) == cudaSuccess ? INK_OK : INK_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -7,6 +7,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "../../include/inkling_attn.h"
+
 namespace ink {
 
 // Keys per K/V tile: one TMA box is 64 rows of 128 bytes (64 bf16 of head_dim).
@@ -160,6 +162,7 @@ struct NormRopeArgs {
   uint32_t* err;
   int B, T, H[3], log2_page, max_pages, num_pages;
   int rot_dim;
+  const int32_t* positions;    // [T] positions of the rotation, or null: the slot's
   float eps, rot_scale;
   int passes;                  // passes of a warp over one token's rows: ceil(Hq / rows) + 2 ceil(Hkv / rows)
   int chunk, nchunks;          // passes per warp, warps per token
@@ -219,5 +222,82 @@ struct MaskedMaps {
 
 cudaError_t launch_prefill_masked(const MaskedMaps& m, const MaskedArgs& a, int head_dim, cudaStream_t stream);
 cudaError_t launch_decode_masked(const DecodeMaps& m, const MaskedArgs& a, int head_dim, cudaStream_t stream);
+
+// Rows of a tree of drafted tokens: plan and commit (tree_plan.cu).
+constexpr int TREE_MAX_WORDS = 16;   // words of a token's ancestor bits: 512 drafted tokens a sequence
+
+struct TreePlanArgs {
+  const int32_t* cu_q;         // [B+1]
+  const int32_t* seq_lens;     // [B]
+  const int32_t* parents;      // [T]
+  int32_t* positions;          // [T]
+  uint32_t* ancestors;         // [T, words]
+  uint32_t* err;
+  int B, T, words;
+};
+
+cudaError_t launch_tree_plan(const TreePlanArgs& a, cudaStream_t stream);
+
+struct TreeCommitArgs {
+  uint16_t* pool[2 * INK_TREE_MAX_POOLS];   // K and V of each layer: bf16 [num_pages, Hkv, P, D]
+  const int32_t* cu_q;         // [B+1]
+  const int32_t* seq_lens;     // [B]
+  const int32_t* block_table;  // [B, max_pages]
+  const int32_t* path;         // [B, max_path]
+  const int32_t* path_lens;    // [B]
+  int32_t* seq_lens_out;       // [B] or null
+  uint32_t* err;
+  int npools;                  // K and V counted
+  int B, Hkv, log2_page, max_pages, num_pages, max_path;
+  int heads, slices;           // heads of a warp, warps per sequence and pool
+};
+
+cudaError_t launch_tree_commit(TreeCommitArgs& a, int head_dim, int num_sms, cudaStream_t stream);
+
+// The K/V short convolution along the paths of a tree, and its state behind an accepted path (kv_conv_tree.cu).
+struct TreeConvArgs {
+  const uint16_t* x[2];        // k_new, v_new: bf16 [T, Hkv, D]
+  const float* w[2];           // taps: fp32 [Hkv, D, ks]
+  const uint16_t* st_in[2];    // bf16 [B, ks-1, Hkv, D], oldest row first
+  uint16_t* st_out[2];
+  uint16_t* cache[2];          // bf16 [num_pages, Hkv, P, D]
+  const int32_t* cu_q;         // [B+1]
+  const int32_t* seq_lens;     // [B]
+  const int32_t* block_table;  // [B, max_pages]
+  const int32_t* parents;      // [T]
+  const int32_t* path;         // [B, max_path]
+  const int32_t* path_lens;    // [B]
+  uint32_t* err;
+  int B, T, D, log2_page, max_pages, num_pages, max_path;
+  int nvec;                    // Hkv * D / 8
+};
+
+cudaError_t launch_kv_conv_tree(const TreeConvArgs& a, int kernel_size, int num_sms, cudaStream_t stream);
+cudaError_t launch_kv_conv_state_tree(const TreeConvArgs& a, int kernel_size, cudaStream_t stream);
+
+// One call of the attention over a tree of drafted tokens (tree.cu).
+struct TreeArgs {
+  const void* q;               // bf16 [T, Hq, D]
+  const int32_t* cu_q;         // [B+1]
+  const int32_t* block_table;  // [B, max_pages]
+  const int32_t* seq_lens;     // [B]
+  const int32_t* positions;    // [T]
+  const uint32_t* ancestors;   // [T, words]
+  const float* slopes;         // [Hq] or null
+  const void* rel;             // [T, Hq, E] fp32 or bf16, or null
+  const void* k;               // bf16 [num_pages, Hkv, P, D]
+  const void* v;
+  void* out;                   // bf16 [T, Hq, D]
+  float* lse;                  // fp32 [T, Hq] or null
+  uint32_t* err;
+  int B, T, Hq, Hkv, G, log2_page, max_pages, num_pages, W, E, words;
+  int rel_bf16;
+  float softcap;
+  float scale_log2;            // sm_scale * log2(e)
+  float cap_k1, cap_log2, cap_inv;   // as in MaskedArgs
+  unsigned long long wait_ns;  // limit of one pipeline wait (the drain waits keep 2 s)
+};
+
+cudaError_t launch_tree(const TreeArgs& a, int head_dim, cudaStream_t stream);
 
 }  // namespace ink

@@ -137,6 +137,7 @@ __global__ void __launch_bounds__(NR_THREADS, NR_BLOCKS) qk_norm_rope_kernel(con
     load(first, q0, q1);
   }
 
+  const int at = a.positions ? __ldg(a.positions + t) : 0;
   const int end = __ldg(a.cu_q + a.B);
   // (by the first row's warp too: requests that lie behind the last row have none)
   if (end > a.T && t == 0 && lane == 0) record_error(a.err, INK_DEVERR_BAD_ROWS);
@@ -152,6 +153,7 @@ __global__ void __launch_bounds__(NR_THREADS, NR_BLOCKS) qk_norm_rope_kernel(con
     return;
   }
   const int p = L - n + (t - c0);     // in [0, L)
+  const int rp = a.positions ? max(at, 0) : p;   // of the rotation
 
   const int hl = a.rot_dim >> 4;      // halves: lanes of half the rotated channels
   const bool turned = LAYOUT != 0 && d < a.rot_dim;
@@ -161,7 +163,7 @@ __global__ void __launch_bounds__(NR_THREADS, NR_BLOCKS) qk_norm_rope_kernel(con
   if constexpr (LAYOUT != 0) {
     for (int f = lane; f < a.rot_dim / 2; f += 32) {
       float c, sn;
-      turn(p, __ldg(a.inv_freq + f), a.rot_scale, c, sn);
+      turn(rp, __ldg(a.inv_freq + f), a.rot_scale, c, sn);
       mine[f] = make_float2(c, sn);
     }
     __syncwarp();
