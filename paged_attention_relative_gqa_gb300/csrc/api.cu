@@ -584,17 +584,63 @@ bool overlap(const Span* s, int written, int n) {
 }
 
 struct TreeLayout {
-  size_t total;
+  size_t cuts, part_ml_off, part_o_off, total;
 };
 
+// Header, then what a call writes before it reads it: nothing is kept between calls.
 TreeLayout tree_layout(const ink_attn_params_t* p) {
-  (void)p;
-  return {kHeaderBytes};
+  const size_t rows = 4 * (size_t)ink::TREE_MAX_CTAS * ink::TREE_ROWS;   // two places of two row tiles a CTA
+  TreeLayout l;
+  l.cuts = kHeaderBytes;
+  l.part_ml_off = align_up(l.cuts + ink::TREE_MAX_CTAS * sizeof(ink::TreeCut), 256);
+  l.part_o_off = l.part_ml_off + rows * 2 * sizeof(float);
+  l.total = l.part_o_off + rows * p->head_dim * sizeof(float);
+  return l;
 }
 
 size_t pool_bytes(const ink_attn_params_t* p) { return pool_rows(p) * p->head_dim * 2; }
 
 size_t table_bytes(const ink_attn_params_t* p) { return (size_t)p->num_seqs * p->max_pages_per_seq * 4; }
+
+// Scale and cap of the scores, for the masked and the tree kernels.
+template <class Args>
+void fill_scores(Args& a, float sm_scale, float softcap) {
+  a.softcap = softcap;
+  a.scale_log2 = sm_scale * 1.4426950408889634f;
+  a.cap_log2 = softcap * 1.4426950408889634f;
+  a.cap_k1 = softcap > 0.f ? (float)(2.0 * 1.4426950408889634 * sm_scale / softcap) : 0.f;
+  a.cap_inv = softcap > 0.f ? sm_scale / softcap : 0.f;
+  // tanh(y) / y as polynomials in y^2 of the least relative error, in terms of the raw product: for
+  // |y| <= 0.45 (2^-22) and for |y| <= 1 (2^-20.7, of the score itself: a 64th of a bf16 weight's
+  // rounding for scores to 20).  Left out where the coefficients would leave fp32's range: a negative
+  // reach, or the near one in the other's place.
+  static const double kNear[ink::NEAR_TERMS] = {0.9999997567401877, -0.3332946719023333, 0.13236369052154567,
+                                                -0.04602819379882759};
+  static const double kMid[ink::MID_TERMS] = {0.99999941361031, -0.3332904245054663, 0.1328143441522219,
+                                              -0.05160568907876395, 0.01674313284460914, -0.003067067657993291};
+  const double inv = softcap > 0.f ? (double)sm_scale / softcap : 0.0, ainv = inv < 0 ? -inv : inv;
+  a.cap_near = ainv >= 1e-5 && ainv <= 1e3 ? (float)(0.45 / ainv) : -1.f;
+  a.cap_mid = ainv > 0 ? (float)(1.0 / ainv) : -1.f;
+  double c = 1.4426950408889634 * sm_scale;
+  for (int i = 0; i < ink::MID_TERMS; ++i, c *= inv * inv) {
+    if (i < ink::NEAR_TERMS) a.near[i] = a.cap_near > 0.f ? (float)(c * kNear[i]) : 0.f;
+    const double m = c * kMid[i], am = m < 0 ? -m : m;
+    a.mid[i] = (float)m;
+    if (!(am >= 1e-36 && am <= 1e36)) a.cap_mid = -1.f;
+  }
+  if (a.cap_mid < 0.f) {
+    a.cap_mid = a.cap_near;
+    for (int i = 0; i < ink::MID_TERMS; ++i) a.mid[i] = i < ink::NEAR_TERMS ? a.near[i] : 0.f;
+  }
+}
+
+// A row tile: the heads of a KV head (in equal chunks when there are more than 128) times as many tokens as fit.
+template <class Args>
+void fill_rows(Args& a) {
+  a.head_chunks = (a.G + ink::MASKED_ROWS - 1) / ink::MASKED_ROWS;
+  a.heads_per_tile = (a.G + a.head_chunks - 1) / a.head_chunks;
+  a.tok_per_tile = ink::MASKED_ROWS / a.heads_per_tile;
+}
 
 ink_status_t masked_impl(const ink_attn_params_t* params, const ink_attn_mask_t* mask, const void* q,
                          const int32_t* cu_q_lens, int32_t total_q, const void* k_cache, const void* v_cache,
@@ -645,41 +691,11 @@ ink_status_t masked_impl(const ink_attn_params_t* params, const ink_attn_mask_t*
   a.num_pages = params->num_pages;
   a.W = params->window;
   a.sm_scale = params->sm_scale;
-  a.softcap = mk.softcap;
   a.wait_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
-  a.scale_log2 = params->sm_scale * 1.4426950408889634f;
-  a.cap_log2 = mk.softcap * 1.4426950408889634f;
-  a.cap_k1 = mk.softcap > 0.f ? (float)(2.0 * 1.4426950408889634 * params->sm_scale / mk.softcap) : 0.f;
-  a.cap_inv = mk.softcap > 0.f ? params->sm_scale / mk.softcap : 0.f;
-  // tanh(y) / y as polynomials in y^2 of the least relative error, in terms of the raw product: for
-  // |y| <= 0.45 (2^-22) and for |y| <= 1 (2^-20.7, of the score itself: a 64th of a bf16 weight's
-  // rounding for scores to 20).  Left out where the coefficients would leave fp32's range: a negative
-  // reach, or the near one in the other's place.
-  static const double kNear[ink::NEAR_TERMS] = {0.9999997567401877, -0.3332946719023333, 0.13236369052154567,
-                                                -0.04602819379882759};
-  static const double kMid[ink::MID_TERMS] = {0.99999941361031, -0.3332904245054663, 0.1328143441522219,
-                                              -0.05160568907876395, 0.01674313284460914, -0.003067067657993291};
-  const double inv = mk.softcap > 0.f ? (double)params->sm_scale / mk.softcap : 0.0, ainv = inv < 0 ? -inv : inv;
-  a.cap_near = ainv >= 1e-5 && ainv <= 1e3 ? (float)(0.45 / ainv) : -1.f;
-  a.cap_mid = ainv > 0 ? (float)(1.0 / ainv) : -1.f;
-  double c = 1.4426950408889634 * params->sm_scale;
-  for (int i = 0; i < ink::MID_TERMS; ++i, c *= inv * inv) {
-    if (i < ink::NEAR_TERMS) a.near[i] = a.cap_near > 0.f ? (float)(c * kNear[i]) : 0.f;
-    const double m = c * kMid[i], am = m < 0 ? -m : m;
-    a.mid[i] = (float)m;
-    if (!(am >= 1e-36 && am <= 1e36)) a.cap_mid = -1.f;
-  }
-  if (a.cap_mid < 0.f) {
-    a.cap_mid = a.cap_near;
-    for (int i = 0; i < ink::MID_TERMS; ++i) a.mid[i] = i < ink::NEAR_TERMS ? a.near[i] : 0.f;
-  }
+  fill_scores(a, params->sm_scale, mk.softcap);
+  fill_rows(a);
   a.stale = reinterpret_cast<uint32_t*>(workspace) + 15;   // these three inside the header
   a.counters = reinterpret_cast<uint32_t*>(workspace) + 16;
-  // a row tile: the heads of a KV head (in equal chunks when there are more than 128) times as
-  // many tokens as fit
-  a.head_chunks = (a.G + ink::MASKED_ROWS - 1) / ink::MASKED_ROWS;
-  a.heads_per_tile = (a.G + a.head_chunks - 1) / a.head_chunks;
-  a.tok_per_tile = ink::MASKED_ROWS / a.heads_per_tile;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.tickets = reinterpret_cast<int32_t*>(ws + (decode ? lay.decode_tickets : lay.prefill_tickets));
   a.part_o = reinterpret_cast<float*>(ws + lay.part_o_off);
@@ -921,13 +937,19 @@ ink_status_t inkling_attn_tree(const ink_attn_params_t* params, const ink_attn_t
   a.num_pages = params->num_pages;
   a.W = params->window;
   a.E = params->rel_extent;
-  a.softcap = o.softcap;
-  a.scale_log2 = params->sm_scale * 1.4426950408889634f;
-  a.cap_log2 = o.softcap * 1.4426950408889634f;
-  a.cap_k1 = o.softcap > 0.f ? (float)(2.0 * 1.4426950408889634 * params->sm_scale / o.softcap) : 0.f;
-  a.cap_inv = o.softcap > 0.f ? params->sm_scale / o.softcap : 0.f;
+  fill_scores(a, params->sm_scale, o.softcap);
+  fill_rows(a);
   a.wait_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
-  return ink::launch_tree(a, params->head_dim, (cudaStream_t)stream) == cudaSuccess ? INK_OK : INK_ERR_CUDA;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.cuts = reinterpret_cast<ink::TreeCut*>(ws + lay.cuts);
+  a.part_ml = reinterpret_cast<float*>(ws + lay.part_ml_off);
+  a.part_o = reinterpret_cast<float*>(ws + lay.part_o_off);
+  const int box = ink::tree_tile_keys(a.rel || a.slopes);
+  ink::MaskedMaps maps;
+  if (!make_pool_map(&maps.k, k_cache, params, box) || !make_pool_map(&maps.v, v_cache, params, box) ||
+      !make_token_map(&maps.q, q, params, total_q, a.heads_per_tile, a.tok_per_tile))
+    return INK_ERR_CUDA;
+  return ink::launch_tree(maps, a, params->head_dim, (cudaStream_t)stream) == cudaSuccess ? INK_OK : INK_ERR_CUDA;
 }
 
 ink_status_t inkling_attn_kv_conv_write_tree(const ink_attn_params_t* params, const void* k_new, const void* v_new,

@@ -294,10 +294,24 @@ struct TreeArgs {
   int rel_bf16;
   float softcap;
   float scale_log2;            // sm_scale * log2(e)
-  float cap_k1, cap_log2, cap_inv;   // as in MaskedArgs
+  float cap_k1, cap_log2, cap_inv, cap_near, near[NEAR_TERMS], cap_mid, mid[MID_TERMS];   // as in MaskedArgs
   unsigned long long wait_ns;  // limit of one pipeline wait (the drain waits keep 2 s)
+  int head_chunks, heads_per_tile, tok_per_tile;   // as in MaskedArgs
+  // partials of cut items, two places of two row tiles per CTA, and the item that each CTA begins and does not end
+  float* part_o;               // [2 CTAs, 2, D / 4, 128 rows] float4
+  float* part_ml;              // [2 CTAs, 2, 128 rows] (maximum in log2 units, sum)
+  struct TreeCut* cuts;        // [CTAs]
 };
 
-cudaError_t launch_tree(const TreeArgs& a, int head_dim, cudaStream_t stream);
+struct TreeCut {
+  int parts;                   // pieces (at most one: no such item)
+  int t0, ntok, h0, gh;        // first row, tokens; first query head, heads
+};
+
+constexpr int TREE_ROWS = 128;       // rows of a row tile
+constexpr int TREE_MAX_CTAS = 160;   // most CTAs (bounds the partials)
+
+int tree_tile_keys(bool bias);   // keys of a tile
+cudaError_t launch_tree(const MaskedMaps& m, const TreeArgs& a, int head_dim, cudaStream_t stream);
 
 }  // namespace ink

@@ -37,8 +37,8 @@ __device__ __forceinline__ constexpr float cap_term(int i) {
        : i == 4 ? 0.02028998f : i == 5 ? -0.006203379f : 0.0010410226f;
 }
 
-template <bool CAP>
-__device__ __forceinline__ float score_log2(const MaskedArgs& a, float x) {
+template <bool CAP, class Args>
+__device__ __forceinline__ float score_log2(const Args& a, float x) {
   if constexpr (!CAP) return x * a.scale_log2;
   const float y = x * a.cap_inv, u = y * y;
   float t = cap_term(CAP_TERMS - 1);
