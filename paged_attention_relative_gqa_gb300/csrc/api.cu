@@ -922,6 +922,7 @@ ink_status_t inkling_attn_tree(const ink_attn_params_t* params, const ink_attn_t
   a.slopes = o.slopes;
   a.rel = o.rel_logits;
   a.rel_bf16 = o.rel_is_bf16 ? 1 : 0;
+  a.rel_rows = aligned(o.rel_logits, 16) && rows * params->rel_extent * (a.rel_bf16 ? 2 : 4) % 16 == 0;
   a.k = k_cache;
   a.v = v_cache;
   a.out = out;

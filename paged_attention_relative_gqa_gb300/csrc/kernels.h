@@ -292,6 +292,7 @@ struct TreeArgs {
   uint32_t* err;
   int B, T, Hq, Hkv, G, log2_page, max_pages, num_pages, W, E, words;
   int rel_bf16;
+  int rel_rows;                // rel begins and ends on 16-byte boundaries: its rows can be copied in bulk
   float softcap;
   float scale_log2;            // sm_scale * log2(e)
   float cap_k1, cap_log2, cap_inv, cap_near, near[NEAR_TERMS], cap_mid, mid[MID_TERMS];   // as in MaskedArgs

@@ -25,11 +25,12 @@
 //   10  scheduler: cuts the run into pieces, publishes them in shared memory, loads their Q tiles by TMA
 //   11  V check: in tiles that not every row sees whole, rows of V that nobody sees are zeroed and so is
 //       every infinity or NaN (0 * NaN would reach rows that do not see the key); rows that do see one get it back at the end
-//   12-15 (with a bias) bias: the KT values of a row, by cp.async where they are fp32 and all there is to add, a lane
-//       a key, into rows of shared memory whose pitch of KT + 1 words has neither their nor the softmax's accesses collide
-// The bias of a row has no alignment (it starts at the row's distance from the tile) and behind the history no order
-// either, so it comes element by element; a lane a key makes that 128 contiguous bytes.  With a bias tiles
-// have 64 keys: two buffers of 128 rows of values take 66 KB of shared memory.
+//   12-15 (with a bias) bias, see below
+// The bias of a row has no alignment: it starts at the row's distance from the tile.  Within the history it is KT values side
+// by side, which one bulk copy a row brings from the 16-byte boundary before them; the softmax reads its row 16 bytes at a time (a
+// pitch of KT + 4 words keeps 8 rows in different banks) and shifts the values into place with two selects each.  Tiles whose
+// distances are all E - 1 or more take one value a row.  Behind the history distances have no order, and a bias warp brings them element
+// by element, a lane a key.  With a bias tiles have 64 keys: two buffers of 128 rows take 70 KB of shared memory.
 // Every wait is bounded; after a timeout the CTA records it, stops issuing, waits for what is in flight and exits.
 #include <algorithm>
 #include <climits>
@@ -59,7 +60,8 @@ struct TRShape {
   static constexpr int QSUB = TREE_ROWS * 128;
   static constexpr int QTILE = CB * QSUB;
   static constexpr int NS = D == 128 ? 5 : 8;      // ring slots, K and V tiles in turn
-  static constexpr int PITCH = KT + 1;             // words of a bias row
+  static constexpr int PITCH = KT + 4;             // words of a bias row: KT values from a 16-byte boundary on
+  static constexpr int ELEMENTS = KT + 1;          // the same of one filled element by element
   static constexpr uint32_t TO = 256;              // S_h at 128 h, O_h at TO + D h
 };
 
@@ -247,6 +249,16 @@ __device__ __forceinline__ TRRow tr_row(const TreeArgs& a, const TRItem& it, int
   r.lo = a.W > 0 ? max(0, r.p - a.W + 1) : 0;
   r.cut = a.W > 0 && r.p - it.H >= a.W;
   return r;
+}
+
+// How the bias of a tile comes to the softmax.  Behind the history distances have no order.  Before it a row's are KT values
+// side by side, one copy a row where 16-byte boundaries can be kept inside the tensor; all of them at E - 1 or more are one value.
+enum TRBias { NoLoad, RowCopies, Elements };
+
+__device__ __forceinline__ TRBias tr_bias(const TreeArgs& a, const TRItem& it, int k0, int kt) {
+  if (min(it.H, it.hi) - k0 < kt) return Elements;
+  if (!a.rel || it.H - (k0 + kt - 1) >= a.E - 1) return NoLoad;
+  return a.rel_rows ? RowCopies : Elements;
 }
 
 __device__ __forceinline__ uint64_t tr_mul(uint64_t a, uint64_t b) {
@@ -636,8 +648,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
       // ---------------------------------------------------------------- bias loads: two warps a chain, 64 rows each
       const int h = (warp - 12) >> 1, r0 = ((warp - 12) & 1) * 64;
       float* buf = bias + (size_t)h * TREE_ROWS * S::PITCH;
-      const int last = a.E - 1;
-      const bool async = a.rel && !a.rel_bf16 && !a.slopes;   // (what is loaded is what is added)
+      const int last = a.E - 1, size = a.rel_bf16 ? 2 : 4;
       uint32_t fills = 0;
       bool go = true;
       TRItem it;
@@ -645,59 +656,96 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
         done_item(k);
         const int first = it.pair ? 0 : h, step = it.pair ? 1 : 2, tok0 = it.pair ? h * a.tok_per_tile : 0;
         const int rows = min(a.tok_per_tile, it.ntok - tok0) * a.heads_per_tile;
+        const int i0 = r0 / a.heads_per_tile;
+        // this lane's rows r0 + lane and 32 more: position and elements before the row; tokens of the warp's rows
+        int pr[2], pt[2];
+        size_t at[2];
+        bool live[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int r = r0 + 32 * x + lane, i = r / a.heads_per_tile, hd = r - i * a.heads_per_tile;
+          live[x] = r < rows && hd < it.gh;
+          const int t = it.t0 + tok0 + (live[x] ? i : 0);
+          pr[x] = max(__ldg(a.positions + t), it.H);
+          at[x] = ((size_t)t * a.Hq + it.h0 + hd) * a.E;
+          const int ti = min(i0 + 32 * x + lane, it.ntok - tok0 - 1);
+          pt[x] = max(__ldg(a.positions + it.t0 + tok0 + ti), it.H);
+        }
         for (int j = first; j < it.nt && go; j += step) {
+          const int k0 = (it.kt0 + j) * KT;
+          const TRBias how = tr_bias(a, it, k0, KT);
+          if (how == NoLoad) continue;
           if (fills > 0) go = tr_wait(&bias_empty[h], (fills - 1) & 1u, abort_flag, a);
           if (!go) break;
           ++fills;
-          // positions of this lane's two keys
+          if (how == RowCopies) {
+            // distances [s, e) of a row, from the 16 bytes that hold the first to those that hold the last
+            uint32_t bytes[2];
+            uintptr_t from[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const int s = pr[x] - (k0 + KT - 1), e = min(pr[x] - k0, last) + 1;
+              const uintptr_t base = reinterpret_cast<uintptr_t>(a.rel) + at[x] * size;
+              from[x] = (base + (size_t)s * size) & ~(uintptr_t)15;
+              bytes[x] = live[x] && s < e ? (uint32_t)(((base + (size_t)e * size + 15) & ~(uintptr_t)15) - from[x]) : 0u;
+            }
+            mbar_arrive_expect_tx(&bias_full[h], bytes[0] + bytes[1]);
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+              if (bytes[x])
+                bulk_copy_g2s(smem_u32(buf + (r0 + 32 * x + lane) * S::PITCH), reinterpret_cast<const void*>(from[x]), bytes[x],
+                              &bias_full[h]);
+            __syncwarp();
+            continue;
+          }
+          // element by element: a lane has two keys and goes over the rows
           int pk[2];
           bool on[2];
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            const int kk = (it.kt0 + j) * KT + 32 * x + lane;
+            const int kk = k0 + 32 * x + lane;
             on[x] = kk >= it.lo && kk < it.hi;
             pk[x] = on[x] && kk >= it.H ? max(__ldg(a.positions + it.c0 + kk - it.H), it.H) : kk;
           }
-          const int end = min(r0 + 64, rows);
-          int r = r0, i = r0 / a.heads_per_tile, hd = r0 - i * a.heads_per_tile;
+          auto fill = [&](auto load) {
+            int i = i0, hd = r0 - i0 * a.heads_per_tile;
 #pragma unroll 1
-          while (r < end) {   // a token's rows
-            const int t = it.t0 + tok0 + i, p = max(__ldg(a.positions + t), it.H);
-            const int d0 = abs(p - pk[0]), d1 = abs(p - pk[1]);
-            const int e0 = min(d0, last), e1 = min(d1, last);
-            const int stop = min(end, (i + 1) * a.heads_per_tile);
-            size_t src = ((size_t)t * a.Hq + it.h0 + hd) * a.E;
-            const int live = min(stop, i * a.heads_per_tile + it.gh);
-            if (async) {
-              const float* rel = static_cast<const float*>(a.rel);
-#pragma unroll 4
-              for (; r < live; ++r, src += a.E) {
-                if (on[0]) cp_async_4(smem_u32(buf + r * S::PITCH + lane), rel + src + e0);
-                if (on[1]) cp_async_4(smem_u32(buf + r * S::PITCH + 32 + lane), rel + src + e1);
+            for (int r = r0; r < min(r0 + 64, rows); r += 8) {
+              float v[8][2];
+#pragma unroll
+              for (int y = 0; y < 8; ++y) {
+                const int off = min(i - i0, 63);
+                const int p0 = __shfl_sync(0xffffffffu, pt[0], off & 31), p1 = __shfl_sync(0xffffffffu, pt[1], off & 31);
+                const int p = off < 32 ? p0 : p1;
+                const bool ok = r + y < rows && hd < it.gh;
+                const size_t row = ((size_t)(it.t0 + tok0 + i) * a.Hq + it.h0 + hd) * a.E;
+                const float slope = ok && a.slopes ? __ldg(a.slopes + it.h0 + hd) : 0.f;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                  const int d = abs(p - pk[x]);
+                  v[y][x] = ok && on[x] ? fmaf(-slope, (float)d, load(row + min(d, last))) : 0.f;
+                }
+                if (++hd == a.heads_per_tile) {
+                  hd = 0;
+                  ++i;
+                }
               }
-            } else {
-              auto rel = [&](size_t at) {
-                if (!a.rel) return 0.f;
-                return a.rel_bf16 ? __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t*>(a.rel) + at) << 16)
-                                  : __ldg(static_cast<const float*>(a.rel) + at);
-              };
-#pragma unroll 8
-              for (; r < live; ++r, src += a.E, ++hd) {
-                const float slope = a.slopes ? __ldg(a.slopes + it.h0 + hd) : 0.f;
-                buf[r * S::PITCH + lane] = on[0] ? fmaf(-slope, (float)d0, rel(src + e0)) : 0.f;
-                buf[r * S::PITCH + 32 + lane] = on[1] ? fmaf(-slope, (float)d1, rel(src + e1)) : 0.f;
+#pragma unroll
+              for (int y = 0; y < 8; ++y) {
+                buf[(r + y) * S::ELEMENTS + lane] = v[y][0];
+                buf[(r + y) * S::ELEMENTS + 32 + lane] = v[y][1];
               }
             }
-            r = stop;
-            ++i;
-            hd = 0;
-          }
-          if (async) cp_async_mbar_arrive_noinc(&bias_full[h]);
-          else mbar_arrive(&bias_full[h]);
+          };
+          if (!a.rel) fill([](size_t) { return 0.f; });
+          else if (a.rel_bf16) fill([&](size_t x) { return __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t*>(a.rel) + x) << 16); });
+          else fill([&](size_t x) { return __ldg(static_cast<const float*>(a.rel) + x); });
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // (copies may write here next)
+          mbar_arrive(&bias_full[h]);
           __syncwarp();
         }
       }
-      asm volatile("cp.async.wait_all;" ::: "memory");
+      if (lane == 0 && fills > 0 && !mbar_wait_bounded(&bias_full[h], (fills - 1) & 1u)) record_error(a.err, INK_DEVERR_WAIT_TIMEOUT);
     }
   } else {
     // ------------------------------------------------------------------ softmax
@@ -735,6 +783,16 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
       const bool rv = my_i < a.tok_per_tile && ti < it.ntok && my_g < it.gh;
       const int t = it.t0 + (rv ? ti : 0), head = it.h0 + (rv ? my_g : 0);
       auto my_row = [&]() { return tr_row(a, it, t, rv); };
+      int p = 0;
+      float rc = 0.f;   // the row's last value
+      if constexpr (BIAS) {
+        p = max(__ldg(a.positions + t), it.H);
+        if (a.rel) {
+          const size_t x = ((size_t)t * a.Hq + head + 1) * a.E - 1;
+          rc = a.rel_bf16 ? __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t*>(a.rel) + x) << 16)
+                          : __ldg(static_cast<const float*>(a.rel) + x);
+        }
+      }
       const int hist = min(it.H, it.hi);
       float m = -INFINITY, l = 0.f;
       bool begun = false;   // O_h holds something
@@ -805,14 +863,83 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
           for (int c = 0; c < KT; ++c) sr[c] = __float_as_uint(__uint_as_float(sr[c]) * a.scale_log2);
         }
         if constexpr (BIAS) {
-          go = tr_wait(&bias_full[h], bn & 1u, abort_flag, a);
-          if (!go) break;
-          ++bn;
-          const float* br = bias + ((size_t)h * TREE_ROWS + r) * S::PITCH;
+          const TRBias how = tr_bias(a, it, k0, KT);
+          const float* br = bias + (size_t)h * TREE_ROWS * S::PITCH;
+          if (how != NoLoad) {
+            go = tr_wait(&bias_full[h], bn & 1u, abort_flag, a);
+            if (!go) break;
+            ++bn;
+          }
+          if (how == Elements) {
+            br += r * S::ELEMENTS;
 #pragma unroll
-          for (int c = 0; c < KT; ++c) sr[c] = __float_as_uint(fmaf(br[c], LOG2E, __uint_as_float(sr[c])));
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bias_empty[h]);
+            for (int c = 0; c < KT; ++c) sr[c] = __float_as_uint(fmaf(br[c], LOG2E, __uint_as_float(sr[c])));
+          } else {
+            if (how == RowCopies) {
+              // element e of the tile's distances, s = p - (k0 + KT - 1) up: key KT - 1 - e
+              const int d0 = p - k0;   // of key 0
+              const uintptr_t src = reinterpret_cast<uintptr_t>(a.rel) + (((size_t)t * a.Hq + head) * a.E + (size_t)(d0 - KT + 1)) * (a.rel_bf16 ? 2 : 4);
+              const bool beyond = __any_sync(0xffffffffu, d0 >= a.E - 1);
+              const int c_last = d0 - (a.E - 1);   // keys up to this one are at a distance of E - 1 or more
+              const uint4* row = reinterpret_cast<const uint4*>(br + r * S::PITCH);
+              uint4 cur = row[0];
+              if (a.rel_bf16) {
+                const bool o1 = src & 2, o2 = src & 4, o4 = src & 8;
+#pragma unroll
+                for (int q = 0; q < KT / 8; ++q) {
+                  const uint4 nxt = row[q + 1];
+                  const uint32_t w[8] = {cur.x, cur.y, cur.z, cur.w, nxt.x, nxt.y, nxt.z, nxt.w};
+                  cur = nxt;
+                  uint32_t u[6], v[4];
+                  uint32_t o[7];
+#pragma unroll
+                  for (int i = 0; i < 7; ++i) o[i] = o1 ? __funnelshift_r(w[i], w[i + 1], 16) : w[i];
+#pragma unroll
+                  for (int i = 0; i < 6; ++i) u[i] = o2 ? o[i + 1] : o[i];
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) v[i] = o4 ? u[i + 2] : u[i];
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) {
+                    const int c = KT - 1 - (8 * q + i);
+                    float x = __uint_as_float(i & 1 ? v[i >> 1] & 0xFFFF0000u : v[i >> 1] << 16);
+                    if (beyond) x = c <= c_last ? rc : x;
+                    sr[c] = __float_as_uint(fmaf(x, LOG2E, __uint_as_float(sr[c])));
+                  }
+                }
+              } else {
+                const bool o1 = src & 4, o2 = src & 8;
+#pragma unroll
+                for (int q = 0; q < KT / 4; ++q) {
+                  const uint4 nxt = row[q + 1];
+                  const uint32_t w[7] = {cur.x, cur.y, cur.z, cur.w, nxt.x, nxt.y, nxt.z};
+                  cur = nxt;
+                  uint32_t u[6];
+#pragma unroll
+                  for (int i = 0; i < 6; ++i) u[i] = o1 ? w[i + 1] : w[i];
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) {
+                    const int c = KT - 1 - (4 * q + i);
+                    float x = __uint_as_float(o2 ? u[i + 2] : u[i]);
+                    if (beyond) x = c <= c_last ? rc : x;
+                    sr[c] = __float_as_uint(fmaf(x, LOG2E, __uint_as_float(sr[c])));
+                  }
+                }
+              }
+            } else if (a.rel) {   // all at E - 1 or beyond
+              const float x = rc * LOG2E;
+#pragma unroll
+              for (int c = 0; c < KT; ++c) sr[c] = __float_as_uint(__uint_as_float(sr[c]) + x);
+            }
+            if (a.slopes) {
+              const float slope2 = __ldg(a.slopes + head) * LOG2E, d0 = (float)(p - k0);
+#pragma unroll
+              for (int c = 0; c < KT; ++c) sr[c] = __float_as_uint(fmaf(-slope2, d0 - (float)c, __uint_as_float(sr[c])));
+            }
+          }
+          if (how != NoLoad) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bias_empty[h]);
+          }
         }
         // ---- keys that this row does not see
         if (part) {
