@@ -43,10 +43,11 @@ namespace {
 
 using namespace pf;
 
-constexpr int TR_ITEMS = 4;       // published pieces in flight
+constexpr int TR_ITEMS = 3;       // published items in flight
 constexpr int TR_BAD = 8;         // tiles whose unreadable keys are remembered
 constexpr int TR_TILES = 4;       // barriers of K and V tiles go by tile (at most 4 of a kind are in the ring)
 constexpr int TR_MIN_TILES = 2;   // least run of a CTA
+constexpr int TR_DUAL_SLACK = 4;  // most tiles that two pieces may differ in to run side by side
 constexpr int TR_REGS_SOFTMAX = 208, TR_REGS_REST = 88;   // registers a thread after the split (without a bias)
 constexpr float TR_RESCALE_LOG2 = 8.f;
 
@@ -65,14 +66,29 @@ struct TRShape {
   static constexpr uint32_t TO = 256;              // S_h at 128 h, O_h at TO + D h
 };
 
-// A run of key tiles of one item.
-struct TRItem {
+// A run of key tiles of one or two row tiles.
+struct TRPart {
   int b, kvh, h0, gh;        // sequence, KV head, first query head, heads
   int t0, ntok, c0, n;       // first packed row, tokens; the sequence's first row and tokens
   int H, lo, hi, lo_max;     // history; keys any row sees lie in [lo, hi), every row sees [lo_max, min(H, hi))
-  int kt0, nt;               // first key tile, tiles (-1: no more pieces)
-  int pair, qs;              // two row tiles; else the slot of the only Q tile
+  int kt0, nt;               // first key tile, tiles
   int place, parts;          // of a cut item (parts > 1): where this piece leaves its partials
+};
+
+// What the two chains do: two row tiles over the same key tiles; the even and the odd tiles of one piece (part 1 is part 0 with
+// other tiles); a piece each.
+enum TRMode { End = -1, Pair, Split, Dual };
+
+struct TRItem {
+  TRPart part[2];
+  int mode, qs;              // (qs: the Q slot of Split; part or row tile h has slot h otherwise)
+
+  __device__ __forceinline__ const TRPart& of(int h) const { return part[mode == Pair ? 0 : h]; }
+  __device__ __forceinline__ int step() const { return mode == Split ? 2 : 1; }
+  // Place of chain h's tile j among the item's tiles, which take turns: j + min(j + h, beside(h)).
+  __device__ __forceinline__ int beside(int h) const { return mode == Pair ? 0 : part[h ^ 1].nt; }
+  __device__ __forceinline__ int tiles() const { return part[0].nt + (mode == Pair ? 0 : part[1].nt); }
+  __device__ __forceinline__ int longest() const { return mode == Pair ? part[0].nt : max(part[0].nt, part[1].nt); }
 };
 
 template <int D, bool BIAS>
@@ -88,7 +104,7 @@ struct TRSmem {
   static constexpr size_t items = bars + (NBAR * 8 + 15) / 16 * 16;
   static constexpr size_t kbad = items + TR_ITEMS * sizeof(TRItem);
   static constexpr size_t poison = kbad + TR_BAD * 16;
-  static constexpr size_t ml = poison + TR_ITEMS * 8;            // [2 chains][128 rows] float2
+  static constexpr size_t ml = poison + TR_ITEMS * 16;           // [2 chains][128 rows] float2
   static constexpr size_t misc = ml + 2 * TREE_ROWS * 8;
   static constexpr size_t alloc = misc + 16;   // (no room to align within: the array itself has to be)
   static_assert(alloc <= 227 * 1024, "shared memory budget");
@@ -139,10 +155,14 @@ struct TRSeq {
   }
 };
 
-// The row of tiles, walked by a whole warp: 32 sequences at a time in the lanes.
+// The row of tiles, walked by a whole warp: 32 sequences at a time in the lanes.  Divisions, which take as long as a load, are
+// made once per run: later pieces begin with their item.
 struct TRWalk {
   long long base, incl, chunk, total;   // tiles before sequence cb; up to and with this lane's; of a run; of the 32
-  int cb, per, items, kt;
+  long long pos, end;                   // of this CTA's run
+  int cb, per, items, kt, cta;
+  int src, groups, left;                // the sequence's lane; its items; of these not begun
+  int kvh, hc, item;                    // the next one
   TRSeq s;
 
   __device__ __forceinline__ void load(const TreeArgs& a, int lane) {
@@ -159,10 +179,10 @@ struct TRWalk {
     total = __shfl_sync(0xffffffffu, incl, 31);
   }
 
-  // All tiles of the call; leaves the walk at its start.
-  __device__ __forceinline__ long long begin(const TreeArgs& a, int lane, int tile_keys) {
+  __device__ __forceinline__ void begin(const TreeArgs& a, int lane, int tile_keys) {
     kt = tile_keys;
     per = a.Hkv * a.head_chunks;
+    cta = (int)blockIdx.x;
     long long all = 0;
     for (cb = ((a.B - 1) >> 5) << 5; cb >= 0; cb -= 32) {
       load(a, lane);
@@ -170,43 +190,65 @@ struct TRWalk {
     }
     cb = 0;
     base = 0;
-    return all;
+    left = 0;
+    chunk = max((all + gridDim.x - 1) / (long long)gridDim.x, (long long)TR_MIN_TILES);
+    pos = min(cta * chunk, all);
+    end = min(pos + chunk, all);
   }
 
-  // The piece that starts at tile `pos` of a run that ends at `end`; places go by CTA.
-  __device__ __forceinline__ TRItem at(const TreeArgs& a, int lane, long long pos, long long end, int cta, int& first) {
-    while (pos >= base + total) {
-      base += total;
-      cb += 32;
-      load(a, lane);
+  // The next piece of the run; first: the CTA where its item begins.
+  __device__ __forceinline__ TRPart next(const TreeArgs& a, int lane, int& first) {
+    int x0 = 0;
+    first = cta;
+    if (left == 0) {   // of another sequence than the one before
+      while (pos >= base + total) {
+        base += total;
+        cb += 32;
+        load(a, lane);
+      }
+      src = __ffs(__ballot_sync(0xffffffffu, pos < base + incl)) - 1;
+      const int ni = __shfl_sync(0xffffffffu, items, src), tiles = __shfl_sync(0xffffffffu, s.tiles, src);
+      groups = ni * per;
+      const long long off = pos - (base + __shfl_sync(0xffffffffu, incl - (long long)s.tiles * items * per, src));
+      int gi = 0;
+      if (off > 0) {   // the run begins within a sequence
+        gi = (int)(off / tiles);
+        x0 = (int)(off - (long long)gi * tiles);
+        first = (int)((pos - x0) / chunk);
+      }
+      left = groups - gi;
+      const int hk = gi / ni;
+      item = gi - hk * ni;
+      kvh = hk / a.head_chunks;
+      hc = hk - kvh * a.head_chunks;
     }
-    const int src = __ffs(__ballot_sync(0xffffffffu, pos < base + incl)) - 1;
-    const int tiles = __shfl_sync(0xffffffffu, s.tiles, src), ni = __shfl_sync(0xffffffffu, items, src);
-    const int L = __shfl_sync(0xffffffffu, s.L, src);
-    TRItem w;
+    const int ni = __shfl_sync(0xffffffffu, items, src), tiles = __shfl_sync(0xffffffffu, s.tiles, src);
+    TRPart w;
     w.b = cb + src;
     w.c0 = __shfl_sync(0xffffffffu, s.c0, src);
     w.n = __shfl_sync(0xffffffffu, s.n, src);
     w.lo = __shfl_sync(0xffffffffu, s.lo, src);
     w.hi = __shfl_sync(0xffffffffu, s.hi, src);
-    w.H = L - w.n;
-    const long long off = pos - (base + __shfl_sync(0xffffffffu, incl - (long long)s.tiles * items * per, src));
-    const long long gi = off / tiles;
-    const int x0 = (int)(off - gi * tiles);
-    const int hk = (int)(gi / ni), item = (int)(gi - (long long)hk * ni);
-    w.kvh = hk / a.head_chunks;
-    const int hc = hk - w.kvh * a.head_chunks;
-    w.h0 = w.kvh * a.G + hc * a.heads_per_tile;
+    w.H = __shfl_sync(0xffffffffu, s.L, src) - w.n;
+    w.kvh = kvh;
+    w.h0 = kvh * a.G + hc * a.heads_per_tile;
     w.gh = min(a.heads_per_tile, a.G - hc * a.heads_per_tile);
     w.t0 = w.c0 + item * 2 * a.tok_per_tile;
     w.ntok = min(2 * a.tok_per_tile, w.n - item * 2 * a.tok_per_tile);
-    w.pair = w.ntok > a.tok_per_tile;
     w.kt0 = w.lo / kt + x0;
     w.nt = (int)min((long long)(tiles - x0), end - pos);
-    const long long g0 = pos - x0;
-    first = (int)(g0 / chunk);
-    w.parts = (int)((g0 + tiles - 1) / chunk) - first + 1;
+    const long long g1 = pos - x0 + tiles;
+    w.parts = (g1 <= end ? cta : (int)((g1 - 1) / chunk)) - first + 1;
     w.place = 2 * cta + (cta == first ? 1 : 0);
+    pos += w.nt;
+    --left;
+    if (++item == ni) {
+      item = 0;
+      if (++hc == a.head_chunks) {
+        hc = 0;
+        ++kvh;
+      }
+    }
     return w;
   }
 };
@@ -214,11 +256,12 @@ struct TRWalk {
 // Bit c: does the row see key base + c?  History [lo, hist) and, behind H, the row's bits.
 struct TRRow {
   const uint32_t* bits;
+  uint32_t w0;                    // bits[0]
   int p, lo, hist, H, nlim, c0;   // hist: readable end of the history; nlim: drafted keys that can be read
   bool cut;                       // the window may hide an ancestor
 
   __device__ __forceinline__ uint32_t word(const TreeArgs& a, int i) const {
-    return i >= 0 && i < a.words ? __ldg(bits + i) : 0u;
+    return i == 0 ? w0 : i > 0 && i < a.words ? __ldg(bits + i) : 0u;
   }
   __device__ __forceinline__ uint32_t sees(const TreeArgs& a, int base) const {
     const int x0 = max(lo - base, 0), x1 = min(hist - base, 32);
@@ -238,16 +281,18 @@ struct TRRow {
   }
 };
 
-__device__ __forceinline__ TRRow tr_row(const TreeArgs& a, const TRItem& it, int t, bool valid) {
+// Row t at position p, w0 its first bits.
+__device__ __forceinline__ TRRow tr_row(const TreeArgs& a, const TRPart& it, int t, int p, uint32_t w0, bool valid) {
   TRRow r;
   r.bits = a.ancestors + (size_t)t * a.words;
-  r.p = max(__ldg(a.positions + t), it.H);
+  r.w0 = w0;
+  r.p = p;
   r.H = it.H;
   r.c0 = it.c0;
   r.hist = valid ? min(it.H, it.hi) : 0;
   r.nlim = valid ? min(it.n, it.hi - it.H) : 0;
-  r.lo = a.W > 0 ? max(0, r.p - a.W + 1) : 0;
-  r.cut = a.W > 0 && r.p - it.H >= a.W;
+  r.lo = a.W > 0 ? max(0, p - a.W + 1) : 0;
+  r.cut = a.W > 0 && p - it.H >= a.W;
   return r;
 }
 
@@ -255,7 +300,7 @@ __device__ __forceinline__ TRRow tr_row(const TreeArgs& a, const TRItem& it, int
 // side by side, one copy a row where 16-byte boundaries can be kept inside the tensor; all of them at E - 1 or more are one value.
 enum TRBias { NoLoad, RowCopies, Elements };
 
-__device__ __forceinline__ TRBias tr_bias(const TreeArgs& a, const TRItem& it, int k0, int kt) {
+__device__ __forceinline__ TRBias tr_bias(const TreeArgs& a, const TRPart& it, int k0, int kt) {
   if (min(it.H, it.hi) - k0 < kt) return Elements;
   if (!a.rel || it.H - (k0 + kt - 1) >= a.E - 1) return NoLoad;
   return a.rel_rows ? RowCopies : Elements;
@@ -293,12 +338,12 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
   uint64_t* bias_empty = bias_full + 2; // [2]
   uint64_t* item_full = bias_empty + 2; // [ITEMS]
   uint64_t* item_empty = item_full + TR_ITEMS;
-  uint64_t* o_free = item_empty + TR_ITEMS;   // both O of the piece read
+  uint64_t* o_free = item_empty + TR_ITEMS;   // both O of a Split item read
   uint64_t* ml_bar = o_free + 1;        // maxima and sums of both chains written
   uint64_t* drain = ml_bar + 1;
   TRItem* items = reinterpret_cast<TRItem*>(smem + L_::items);
   uint32_t* kbad = reinterpret_cast<uint32_t*>(smem + L_::kbad);   // [BAD][4] bit per unreadable key
-  int* poison = reinterpret_cast<int*>(smem + L_::poison);   // [ITEMS][2] first and last tile of V with an infinity or NaN
+  int* poison = reinterpret_cast<int*>(smem + L_::poison);   // [ITEMS][2 chains][2] first and last tile of V with an infinity or NaN
   float2* ml = reinterpret_cast<float2*>(smem + L_::ml);
   float* bias = reinterpret_cast<float*>(smem + L_::bias);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L_::misc);
@@ -340,6 +385,8 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
     fence_mbar_init();
     *abort_flag = 0;
   }
+  TRWalk walk;
+  if (warp == 10) walk.begin(a, lane, KT);   // (its loads are on their way while the rest is set up)
   // rows of a Q tile past the last (token, head) pair stay zero
   for (int x = tid; x < 2 * S::QTILE / 16; x += S::THREADS)
     *reinterpret_cast<uint4*>(smem + L_::q + (size_t)x * 16) = make_uint4(0u, 0u, 0u, 0u);
@@ -354,11 +401,9 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  // The k-th piece of this CTA into `it`; false when there is none (or after a timeout).
-  auto next_item = [&](int k, TRItem& it) -> bool {
-    if (!tr_wait(&item_full[k % TR_ITEMS], (uint32_t)(k / TR_ITEMS) & 1u, abort_flag, a)) return false;
-    it = items[k % TR_ITEMS];
-    return it.nt >= 0;
+  // The k-th item of this CTA is in its slot; false when there is none (or after a timeout).
+  auto next_item = [&](int k) -> bool {
+    return tr_wait(&item_full[k % TR_ITEMS], (uint32_t)(k / TR_ITEMS) & 1u, abort_flag, a) && items[k % TR_ITEMS].mode != End;
   };
   auto done_item = [&](int k) {
     __syncwarp();
@@ -374,23 +419,26 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
         prefetch_tensormap(&tmV);
       }
       const int seg = min(P, KT), nseg = KT / seg;
-      int chunk_base = 0, chunk_val = -1;   // table entries chunk_base + lane
       int f = 0;                            // fills issued
       bool go = true;
-      TRItem it;
-      for (int k = 0; go && next_item(k, it); ++k) {
-        done_item(k);
-        for (int j = 0; j < it.nt && go; ++j) {
-          const int k0 = (it.kt0 + j) * KT;
+      for (int k = 0; go && next_item(k); ++k) {
+        const TRItem& item = items[k % TR_ITEMS];
+        int chunk_base[2] = {0, 0}, chunk_val[2] = {-1, -1};   // table entries chunk_base + lane, of each chain's part
+        for (int j = 0; j < item.longest() && go; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const TRPart& it = item.part[h];
+          if (!go || (h == 1 && item.mode == Pair) || j >= it.nt) continue;
+          const int k0 = (it.kt0 + j * item.step()) * KT;
           const int last_idx = (it.hi - 1) >> a.log2_page;
           const int pfirst = k0 >> a.log2_page, plast = (k0 + KT - 1) >> a.log2_page;
-          if (j == 0 || plast >= chunk_base + 32) {
-            chunk_base = pfirst;   // entries past the sequence's last key are not read
-            chunk_val = __ldg(a.block_table + (size_t)it.b * a.max_pages + min(chunk_base + lane, last_idx));
+          if (j == 0 || plast >= chunk_base[h] + 32) {
+            chunk_base[h] = pfirst;   // entries past the sequence's last key are not read
+            chunk_val[h] = __ldg(a.block_table + (size_t)it.b * a.max_pages + min(chunk_base[h] + lane, last_idx));
           }
           const int ks = k0 + lane * seg;                 // lane < nseg takes one segment
           const bool want = lane < nseg && ks < it.hi && ks + seg > it.lo;
-          const int page = __shfl_sync(0xffffffffu, chunk_val, min(max((ks >> a.log2_page) - chunk_base, 0), 31));
+          const int page = __shfl_sync(0xffffffffu, chunk_val[h], min(max((ks >> a.log2_page) - chunk_base[h], 0), 31));
           const bool bad_seg = want && (page < 0 || page >= a.num_pages);
           const bool load = want && !bad_seg;
           const uint32_t nload = __popc(__ballot_sync(0xffffffffu, load));
@@ -425,6 +473,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
             }
           }
         }
+        done_item(k);
       }
       if (lane == 0) {
         pp_drain_ring(k_full, TR_TILES, (f + 1) >> 1, a.err);
@@ -435,84 +484,90 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
       constexpr uint32_t IDESC_S = umma_idesc_bf16(128, KT, false, false);
       constexpr uint32_t IDESC_PV = umma_idesc_bf16(128, D, false, true);
       const uint32_t qaddr = smem_u32(smem + L_::q), raddr = smem_u32(smem + L_::ring);
-      int g = 0;                       // tiles walked: K of tile g is fill 2 g, V fill 2 g + 1
+      // S and P V products each walk the tiles in their order: K of tile g is fill 2 g, V fill 2 g + 1
+      int gk = 0, gv = 0, k_slot = 0, v_slot = 1;
       uint32_t qn = 0, pn = 0;         // a parity bit per Q tile and per chain
       bool go = true;
-      auto slot = [&](int f) { return f % NS; };
       auto wait_tile = [&](uint64_t* bars, int tile) {
         return tr_wait(&bars[tile % TR_TILES], (uint32_t)(tile / TR_TILES) & 1u, abort_flag, a);
-      };
-      auto issue_s = [&](int h, int f, int qs) {
-        const uint64_t ad = umma_desc_sw128(qaddr + qs * S::QTILE, 16, 1024);
-        const uint64_t bd = umma_desc_sw128(raddr + slot(f) * S::TILE, 16, 1024);
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          umma_ss_warp(tmem + 128u * h, ad + (uint64_t)(((kk >> 2) * S::QSUB + (kk & 3) * 32) >> 4),
-                       bd + (uint64_t)(((kk >> 2) * S::SUB + (kk & 3) * 32) >> 4), IDESC_S, kk > 0 ? 1u : 0u);
-        umma_commit_warp(&s_full[h]);
-      };
-      auto issue_pv = [&](int h, int f, bool acc) {
-        const uint64_t bd = umma_desc_sw128(raddr + slot(f) * S::TILE, S::SUB, 1024);
-#pragma unroll
-        for (int ks = 0; ks < KT / 16; ++ks)
-          umma_ts_warp(tmem + S::TO + (uint32_t)(D * h), tmem + 128u * h + ks * 8, bd + (uint64_t)((ks * 16 * 128) >> 4),
-                       IDESC_PV, (acc || ks > 0) ? 1u : 0u);
       };
       auto wait_q = [&](int s) {
         const bool ok = tr_wait(&q_full[s], (qn >> s) & 1u, abort_flag, a);
         qn ^= 1u << s;
         return ok;
       };
-      auto wait_p = [&](int h) {
-        const bool ok = tr_wait(&p_full[h], (pn >> h) & 1u, abort_flag, a);
-        pn ^= 1u << h;
-        tc_fence_after();
-        return ok;
+      // S_h of tile gk with Q tile qs; the tile's last product frees its slot, a Q tile's last one that
+      auto issue_s = [&](int h, int qs, bool frees_k, bool frees_q) {
+        const uint64_t ad = umma_desc_sw128(qaddr + qs * S::QTILE, 16, 1024);
+        const uint64_t bd = umma_desc_sw128(raddr + k_slot * S::TILE, 16, 1024);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          umma_ss_warp(tmem + 128u * h, ad + (uint64_t)(((kk >> 2) * S::QSUB + (kk & 3) * 32) >> 4),
+                       bd + (uint64_t)(((kk >> 2) * S::SUB + (kk & 3) * 32) >> 4), IDESC_S, kk > 0 ? 1u : 0u);
+        umma_commit_warp(&s_full[h]);
+        if (frees_k) {
+          umma_commit_warp(&empty[k_slot]);
+          ++gk;
+          k_slot = k_slot + 2 < NS ? k_slot + 2 : k_slot + 2 - NS;
+        }
+        if (frees_q) umma_commit_warp(&q_empty[qs]);
+        __syncwarp();
       };
-      TRItem it;
-      for (int k = 0; go && next_item(k, it); ++k) {
-        done_item(k);
-        const int nt = it.nt, ahead = it.pair ? 1 : min(2, nt);   // key tiles whose S is in flight
-        go = it.pair ? wait_q(0) && wait_q(1) : wait_q(it.qs);
-        for (int j = 0; j < ahead && go; ++j) {
-          go = wait_tile(k_full, g + j);
+      auto issue_pv = [&](int h, bool acc, bool frees_v) {
+        const uint64_t bd = umma_desc_sw128(raddr + v_slot * S::TILE, S::SUB, 1024);
+#pragma unroll
+        for (int ks = 0; ks < KT / 16; ++ks)
+          umma_ts_warp(tmem + S::TO + (uint32_t)(D * h), tmem + 128u * h + ks * 8, bd + (uint64_t)((ks * 16 * 128) >> 4),
+                       IDESC_PV, (acc || ks > 0) ? 1u : 0u);
+        if (frees_v) {
+          umma_commit_warp(&empty[v_slot]);
+          ++gv;
+          v_slot = v_slot + 2 < NS ? v_slot + 2 : v_slot + 2 - NS;
+        }
+      };
+      uint32_t merges = 0;             // Split items so far
+      bool merged = false;             // the item before was one
+      for (int k = 0; go && next_item(k); ++k) {
+        const TRItem& it = items[k % TR_ITEMS];
+        const int mode = it.mode, qs1 = mode == Split ? it.qs : 1, qs0 = mode == Split ? it.qs : 0;
+        const int n0 = it.part[0].nt, n1 = mode == Pair ? n0 : it.part[1].nt, last = gk + n0 + n1 - 1;
+        const bool pair = mode == Pair;
+        // the last S with a Q tile: of the chain, of the piece in Split
+        auto last_s = [&](int j, int h) { return mode == Split ? gk == last : j == (h ? n1 : n0) - 1; };
+        for (int h = 0; h < 2 && go; ++h) {
+          if (h == 1 && n1 == 0) continue;
+          if (mode != Split || h == 0) go = wait_q(h ? qs1 : qs0);
+          if (go && (!pair || h == 0)) go = wait_tile(k_full, gk);
           if (!go) break;
           tc_fence_after();
-          issue_s(j, 2 * (g + j), it.pair ? 0 : it.qs);
-          if (it.pair) issue_s(1, 2 * g, 1);
-          umma_commit_warp(&empty[slot(2 * (g + j))]);
-          if (j == nt - 1) {
-            umma_commit_warp(&q_empty[it.pair ? 0 : it.qs]);
-            if (it.pair) umma_commit_warp(&q_empty[1]);
-          }
-          __syncwarp();
+          issue_s(h, h ? qs1 : qs0, !pair || h == 1, last_s(0, h));
         }
-        // the O of the piece before have been read
-        if (go && k > 0) go = tr_wait(o_free, (uint32_t)(k - 1) & 1u, abort_flag, a);
-        for (int j = 0; j < nt && go; ++j) {
-          const int tile = g + j, nk = j + ahead;
-          const bool more = nk < nt;
-          go = wait_tile(v_full, tile) && wait_tile(v_ok, tile);
-          for (int x = 0; x < (it.pair ? 2 : 1) && go; ++x) {
-            const int h = it.pair ? x : j & 1;
-            go = wait_p(h);
-            if (!go) break;
-            issue_pv(h, 2 * tile + 1, j >= (it.pair ? 1 : 2));
-            if (x == (it.pair ? 1 : 0)) umma_commit_warp(&empty[slot(2 * tile + 1)]);
-            if (more) {
-              if (x == 0) go = wait_tile(k_full, g + nk);
-              if (!go) break;
-              issue_s(h, 2 * (g + nk), it.pair ? x : it.qs);
-              if (nk == nt - 1) umma_commit_warp(&q_empty[it.pair ? x : it.qs]);
+        // both O of a Split item have been read
+        if (go && merged) go = tr_wait(o_free, (merges - 1) & 1u, abort_flag, a);
+        merged = mode == Split;
+        merges += merged;
+        for (int j = 0; j < max(n0, n1) && go; ++j)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int nh = h ? n1 : n0;
+            if (!go || j >= nh) continue;
+            // (v_ok comes after v_full)
+            if (!pair || h == 0) go = wait_tile(v_ok, gv);
+            if (go) go = tr_wait(&p_full[h], (pn >> h) & 1u, abort_flag, a);
+            if (!go) continue;
+            pn ^= 1u << h;
+            tc_fence_after();
+            issue_pv(h, j > 0, !pair || h == 1);
+            if (j + 1 < nh) {
+              if (!pair || h == 0) go = wait_tile(k_full, gk);
+              if (!go) continue;
+              issue_s(h, h ? qs1 : qs0, !pair || h == 1, last_s(j + 1, h));
             } else {
               umma_commit_warp(&o_full[h]);
+              __syncwarp();
             }
-            __syncwarp();
           }
-          if (go && more) umma_commit_warp(&empty[slot(2 * (g + nk))]);
-          __syncwarp();
-        }
-        g += nt;
+        done_item(k);
       }
       umma_commit_warp(drain);
       __syncwarp();
@@ -520,57 +575,85 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
     } else if (warp == 10) {
       // ---------------------------------------------------------------- scheduler and Q loads
       if (lane == 0) prefetch_tensormap(&tmQ);
-      TRWalk walk;
-      const long long all = walk.begin(a, lane, KT);
-      walk.chunk = max((all + gridDim.x - 1) / (long long)gridDim.x, (long long)TR_MIN_TILES);
-      long long pos = min((long long)blockIdx.x * walk.chunk, all);
-      const long long end = min(pos + walk.chunk, all);
       TreeCut cut;                       // the item that this run begins and does not end
       cut.parts = 0;
       uint32_t qn = 0, loaded = 0;       // bits per Q tile: loads so far, odd or even; any
       int qs = 1;
+      auto piece = [&]() {               // the next one of the run
+        int first;
+        TRPart w = walk.next(a, lane, first);
+        if (w.parts > 1 && first == (int)blockIdx.x) cut = {w.parts, w.t0, w.ntok, w.h0, w.gh};
+        // all rows see the keys from the largest first one on
+        w.lo_max = 0;
+        if (a.W > 0) {
+          for (int i = lane; i < w.ntok; i += 32) w.lo_max = max(w.lo_max, max(__ldg(a.positions + w.t0 + i), w.H) - a.W + 1);
+          w.lo_max = __reduce_max_sync(0xffffffffu, w.lo_max);
+        }
+        return w;
+      };
+      TRPart next;
+      bool have = false;                 // next was looked at, and is an item of its own
       for (int k = 0;; ++k) {
         const int sl = k % TR_ITEMS;
+        TRItem it;
+        it.mode = End;
+        it.qs = 0;
+        if (have || walk.pos < walk.end) {
+          it.part[0] = have ? next : piece();
+          have = false;
+          if (it.part[0].ntok > a.tok_per_tile) {
+            it.mode = Pair;
+          } else {
+            it.mode = Split;
+            if (walk.pos < walk.end) {
+              next = piece();
+              have = next.ntok > a.tok_per_tile || abs(it.part[0].nt - next.nt) > TR_DUAL_SLACK;
+              if (!have) it.mode = Dual;
+            }
+          }
+        }
         if (k >= TR_ITEMS && !tr_wait(&item_empty[sl], (uint32_t)((k / TR_ITEMS) - 1) & 1u, abort_flag, a)) break;
-        if (pos >= end) {
+        if (it.mode == End) {
           if (lane == 0) {
-            items[sl].nt = -1;
+            items[sl].mode = End;
             mbar_arrive(&item_full[sl]);
           }
           break;
         }
-        int first;
-        TRItem it = walk.at(a, lane, pos, end, (int)blockIdx.x, first);
-        pos += it.nt;
-        if (it.pair) qs = 1; else qs ^= 1;
+        qs = it.mode == Split ? qs ^ 1 : 1;
         it.qs = qs;
-        // all rows see the keys from the largest first one on
-        it.lo_max = 0;
-        if (a.W > 0) {
-          for (int i = lane; i < it.ntok; i += 32) it.lo_max = max(it.lo_max, max(__ldg(a.positions + it.t0 + i), it.H) - a.W + 1);
-          it.lo_max = __reduce_max_sync(0xffffffffu, it.lo_max);
+        if (it.mode == Dual) {
+          it.part[1] = next;
+        } else {
+          it.part[1] = it.part[0];
+          if (it.mode == Split) {
+            it.part[0].nt = (it.part[0].nt + 1) >> 1;
+            it.part[1].nt >>= 1;
+            ++it.part[1].kt0;
+          }
         }
-        if (it.parts > 1 && first == (int)blockIdx.x) cut = {it.parts, it.t0, it.ntok, it.h0, it.gh};
         if (lane == 0) {
           items[sl] = it;
-          reinterpret_cast<volatile int*>(poison)[2 * sl] = INT_MAX;
-          reinterpret_cast<volatile int*>(poison)[2 * sl + 1] = -1;
+          volatile int* p = poison + 4 * sl;
+          p[0] = p[2] = INT_MAX;
+          p[1] = p[3] = -1;
           mbar_arrive(&item_full[sl]);
         }
         __syncwarp();
         bool go = true;
-        for (int x = 0; x < 1 + it.pair && go; ++x) {
-          const int s = it.pair ? x : qs;
+        for (int x = 0; x < (it.mode == Split ? 1 : 2) && go; ++x) {
+          const int s = it.mode == Split ? qs : x;
           if ((loaded >> s) & 1u) go = tr_wait(&q_empty[s], ((qn >> s) & 1u) ^ 1u, abort_flag, a);
           if (!go) break;
           qn ^= 1u << s;
           loaded |= 1u << s;
           if (lane == 0) {
+            const TRPart& w = it.part[x];
+            const int t0 = w.t0 + (it.mode == Pair ? x * a.tok_per_tile : 0);
             mbar_arrive_expect_tx(&q_full[s], (uint32_t)(S::CB * a.heads_per_tile * a.tok_per_tile * 128));
 #pragma unroll
             for (int c = 0; c < S::CB; ++c)
-              tma_load_3d(smem + L_::q + s * S::QTILE + c * S::QSUB, &tmQ, c * 64, it.h0, it.t0 + x * a.tok_per_tile,
-                          &q_full[s]);
+              tma_load_3d(smem + L_::q + s * S::QTILE + c * S::QSUB, &tmQ, c * 64, w.h0, t0, &q_full[s]);
           }
           __syncwarp();
         }
@@ -585,14 +668,17 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
       // ---------------------------------------------------------------- V check
       int g = 0;
       bool go = true;
-      TRItem it;
-      for (int k = 0; go && next_item(k, it); ++k) {
-        const int hist = min(it.H, it.hi);
-        for (int j = 0; j < it.nt; ++j, ++g) {
+      for (int k = 0; go && next_item(k); ++k) {
+        const TRItem& item = items[k % TR_ITEMS];
+        for (int j = 0; j < item.longest() && go; ++j)
+        for (int h = 0; h < (item.mode == Pair ? 1 : 2); ++h) {
+          const TRPart& it = item.part[h];
+          if (j >= it.nt) continue;
+          const int hist = min(it.H, it.hi), kt = it.kt0 + j * item.step();
           const int st = (2 * g + 1) % NS;
           go = tr_wait(&v_full[g % TR_TILES], (uint32_t)(g / TR_TILES) & 1u, abort_flag, a);
           if (!go) break;
-          const int k0 = (it.kt0 + j) * KT;
+          const int k0 = kt * KT;
           const uint32_t* badw = kbad + (g % TR_BAD) * 4;
           uint32_t any = 0;
 #pragma unroll
@@ -605,6 +691,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
               const int kk = k0 + 32 * x + lane;
               uint4* row = reinterpret_cast<uint4*>(vt + (32 * x + lane) * 128);
               const bool zero = kk < it.lo || kk >= it.hi || ((badw[x] >> lane) & 1u);
+              if (!zero && kk >= it.lo_max && kk < hist) continue;   // every row sees it
               if (!zero) {   // exponents all ones carry into the sign places
                 uint32_t odd = 0;
 #pragma unroll
@@ -634,13 +721,14 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
               }
             }
             if (found) {
-              atomicMin(poison + 2 * (k % TR_ITEMS), it.kt0 + j);
-              atomicMax(poison + 2 * (k % TR_ITEMS) + 1, it.kt0 + j);
+              atomicMin(poison + 4 * (k % TR_ITEMS) + 2 * h, kt);
+              atomicMax(poison + 4 * (k % TR_ITEMS) + 2 * h + 1, kt);
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&v_ok[g % TR_TILES]);
+          ++g;
         }
         done_item(k);
       }
@@ -651,10 +739,10 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
       const int last = a.E - 1, size = a.rel_bf16 ? 2 : 4;
       uint32_t fills = 0;
       bool go = true;
-      TRItem it;
-      for (int k = 0; go && next_item(k, it); ++k) {
-        done_item(k);
-        const int first = it.pair ? 0 : h, step = it.pair ? 1 : 2, tok0 = it.pair ? h * a.tok_per_tile : 0;
+      for (int k = 0; go && next_item(k); ++k) {
+        const TRItem& item = items[k % TR_ITEMS];
+        const TRPart& it = item.of(h);
+        const int tok0 = item.mode == Pair ? h * a.tok_per_tile : 0;
         const int rows = min(a.tok_per_tile, it.ntok - tok0) * a.heads_per_tile;
         const int i0 = r0 / a.heads_per_tile;
         // this lane's rows r0 + lane and 32 more: position and elements before the row; tokens of the warp's rows
@@ -671,8 +759,8 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
           const int ti = min(i0 + 32 * x + lane, it.ntok - tok0 - 1);
           pt[x] = max(__ldg(a.positions + it.t0 + tok0 + ti), it.H);
         }
-        for (int j = first; j < it.nt && go; j += step) {
-          const int k0 = (it.kt0 + j) * KT;
+        for (int j = 0; j < it.nt && go; ++j) {
+          const int k0 = (it.kt0 + j * item.step()) * KT;
           const TRBias how = tr_bias(a, it, k0, KT);
           if (how == NoLoad) continue;
           if (fills > 0) go = tr_wait(&bias_empty[h], (fills - 1) & 1u, abort_flag, a);
@@ -700,30 +788,30 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
           }
           // element by element: a lane has two keys and goes over the rows
           int pk[2];
-          bool on[2];
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             const int kk = k0 + 32 * x + lane;
-            on[x] = kk >= it.lo && kk < it.hi;
-            pk[x] = on[x] && kk >= it.H ? max(__ldg(a.positions + it.c0 + kk - it.H), it.H) : kk;
+            pk[x] = kk >= it.H && kk < it.hi ? max(__ldg(a.positions + it.c0 + kk - it.H), it.H) : kk;
           }
+          // (all loads of a batch first, from rows that are there: what is not seen is masked)
           auto fill = [&](auto load) {
             int i = i0, hd = r0 - i0 * a.heads_per_tile;
 #pragma unroll 1
-            for (int r = r0; r < min(r0 + 64, rows); r += 8) {
-              float v[8][2];
+            for (int r = r0; r < min(r0 + 64, rows); r += 16) {
+              float v[16][2], far[16][2], slope[16];
 #pragma unroll
-              for (int y = 0; y < 8; ++y) {
+              for (int y = 0; y < 16; ++y) {
                 const int off = min(i - i0, 63);
                 const int p0 = __shfl_sync(0xffffffffu, pt[0], off & 31), p1 = __shfl_sync(0xffffffffu, pt[1], off & 31);
                 const int p = off < 32 ? p0 : p1;
-                const bool ok = r + y < rows && hd < it.gh;
-                const size_t row = ((size_t)(it.t0 + tok0 + i) * a.Hq + it.h0 + hd) * a.E;
-                const float slope = ok && a.slopes ? __ldg(a.slopes + it.h0 + hd) : 0.f;
+                const int head = it.h0 + min(hd, it.gh - 1);
+                const size_t row = ((size_t)(it.t0 + min(tok0 + i, it.ntok - 1)) * a.Hq + head) * a.E;
+                slope[y] = a.slopes ? __ldg(a.slopes + head) : 0.f;
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                   const int d = abs(p - pk[x]);
-                  v[y][x] = ok && on[x] ? fmaf(-slope, (float)d, load(row + min(d, last))) : 0.f;
+                  far[y][x] = (float)d;
+                  v[y][x] = load(row + min(d, last));
                 }
                 if (++hd == a.heads_per_tile) {
                   hd = 0;
@@ -731,9 +819,9 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
                 }
               }
 #pragma unroll
-              for (int y = 0; y < 8; ++y) {
-                buf[(r + y) * S::ELEMENTS + lane] = v[y][0];
-                buf[(r + y) * S::ELEMENTS + 32 + lane] = v[y][1];
+              for (int y = 0; y < 16; ++y) {
+                buf[(r + y) * S::ELEMENTS + lane] = fmaf(-slope[y], far[y][0], v[y][0]);
+                buf[(r + y) * S::ELEMENTS + 32 + lane] = fmaf(-slope[y], far[y][1], v[y][1]);
               }
             }
           };
@@ -744,6 +832,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
           mbar_arrive(&bias_full[h]);
           __syncwarp();
         }
+        done_item(k);
       }
       if (lane == 0 && fills > 0 && !mbar_wait_bounded(&bias_full[h], (fills - 1) & 1u)) record_error(a.err, INK_DEVERR_WAIT_TIMEOUT);
     }
@@ -773,31 +862,36 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
     uint32_t sn = 0, on = 0, bn = 0, mn = 0;   // (on: a parity bit per chain)
     int g = 0;
     bool go = true;
-    for (int k = 0; go; ++k) {
+    for (int k = 0; go && next_item(k); ++k) {
       // (read where it is needed, from shared memory: the tile loop has no registers to spare)
-      const TRItem& it = items[k % TR_ITEMS];
-      if (!tr_wait(&item_full[k % TR_ITEMS], (uint32_t)(k / TR_ITEMS) & 1u, abort_flag, a) || it.nt < 0) break;
+      const TRItem& item = items[k % TR_ITEMS];
+      const TRPart& it = item.of(h);
       const int nt = it.nt;
-      const bool pair = it.pair;
+      const bool pair = item.mode == Pair, merge = item.mode == Split;
       const int ti = (pair ? h * a.tok_per_tile : 0) + my_i;
       const bool rv = my_i < a.tok_per_tile && ti < it.ntok && my_g < it.gh;
       const int t = it.t0 + (rv ? ti : 0), head = it.h0 + (rv ? my_g : 0);
-      auto my_row = [&]() { return tr_row(a, it, t, rv); };
+      // (position and bits come from L1 where they are needed; without a bias there are no registers for them)
+      prefetch_l1(a.positions + t);
+      prefetch_l1(a.ancestors + (size_t)t * a.words);
       int p = 0;
+      if constexpr (BIAS) p = max(__ldg(a.positions + t), it.H);
+      auto my_row = [&]() {
+        return tr_row(a, it, t, BIAS ? p : max(__ldg(a.positions + t), it.H), __ldg(a.ancestors + (size_t)t * a.words), rv);
+      };
       float rc = 0.f;   // the row's last value
       if constexpr (BIAS) {
-        p = max(__ldg(a.positions + t), it.H);
         if (a.rel) {
           const size_t x = ((size_t)t * a.Hq + head + 1) * a.E - 1;
           rc = a.rel_bf16 ? __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t*>(a.rel) + x) << 16)
                           : __ldg(static_cast<const float*>(a.rel) + x);
         }
       }
-      const int hist = min(it.H, it.hi);
+      const int beside = item.beside(h), kstep = item.step() * KT, lo_max = it.lo_max, hist = min(it.H, it.hi);
+      int k0 = it.kt0 * KT;
       float m = -INFINITY, l = 0.f;
-      bool begun = false;   // O_h holds something
-      for (int j = pair ? 0 : h; j < nt; j += pair ? 1 : 2) {
-        const int k0 = (it.kt0 + j) * KT, tile = g + j;
+      for (int j = 0; j < nt; ++j, k0 += kstep) {
+        const int tile = g + j + min(j + h, beside);
         go = tr_wait(&s_full[h], sn & 1u, abort_flag, a);
         if (!go) break;
         ++sn;
@@ -809,7 +903,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
         uint32_t badw[KW], any = 0;
 #pragma unroll
         for (int x = 0; x < KW; ++x) any |= badw[x] = kbad[(tile % TR_BAD) * 4 + x];
-        const bool part = k0 < it.lo_max || hist - k0 < KT || any;   // not every row sees all of it
+        const bool part = k0 < lo_max || hist - k0 < KT || any;   // not every row sees all of it
         if (CAP && part) {   // (what nobody may see has no say in how scores are capped)
           const TRRow row = my_row();
 #pragma unroll
@@ -960,7 +1054,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
         const float mx = fmaxf(fmaxf(mxv[0], mxv[1]), fmaxf(mxv[2], mxv[3])) * mul;
         const bool mine = mx > m + TR_RESCALE_LOG2;
         if (__any_sync(0xffffffffu, mine)) {
-          if (begun) {   // every earlier product into O_h is done: s_full came after it
+          if (j > 0) {   // every earlier product into O_h is done: s_full came after it
             const float fr = mine ? fast_exp2(m - mx) : 1.f;
 #pragma unroll 1
             for (int c2 = 0; c2 < D / 16; ++c2) {
@@ -975,7 +1069,6 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
           }
           if (mine) m = mx;
         }
-        begun = true;
         // ---- numerators
         const float nm = m == -INFINITY ? 0.f : -m;
         const uint64_t mul2 = f2_pack(mul, mul), nm2 = f2_pack(nm, nm);
@@ -1006,57 +1099,70 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
         if (lane == 0) mbar_arrive(&p_full[h]);
       }
       if (!go) break;
-      g += nt;
+      g += item.tiles();
       // ---- epilogue
-      const bool other = !pair && nt > 1;   // both chains hold a part of this row
-      if (begun) {
+      if (nt > 0) {
         go = tr_wait(&o_full[h], (on >> h) & 1u, abort_flag, a);
         if (!go) break;
       }
-      float M = l == 0.f ? -INFINITY : m, f0 = 1.f, f1 = 0.f;   // weights of O_0 (the own one in a pair) and O_1
-      if (!pair) {
-        // (The next piece's are written once its own O is there, which waits for o_free.  A chain without a tile has nothing to say.)
-        if (begun) ml[h * TREE_ROWS + r] = make_float2(M, l);
+      const bool both = merge && item.part[1].nt > 0;   // both chains hold a part of this row
+      float M = l == 0.f ? -INFINITY : m, f0 = 1.f, f1 = 0.f;   // weights of O_h, or of O_0 and O_1
+      if (merge) {
+        // (The next item's are written once its own O is there, which waits for o_free.  A chain without a tile has nothing to say.)
+        if (nt > 0) ml[h * TREE_ROWS + r] = make_float2(M, l);
         __syncwarp();
         if (lane == 0) mbar_arrive(ml_bar);
         go = tr_wait(ml_bar, mn & 1u, abort_flag, a);
         if (!go) break;
         ++mn;
-        if (h == 1 || other) go = tr_wait(&o_full[h ^ 1], (on >> (h ^ 1)) & 1u, abort_flag, a);   // (its warps have waited for it)
+        if (h == 1 || both) go = tr_wait(&o_full[h ^ 1], (on >> (h ^ 1)) & 1u, abort_flag, a);   // (its warps have waited for it)
         if (!go) break;
-        const float2 x0 = ml[r], x1 = other ? ml[TREE_ROWS + r] : make_float2(-INFINITY, 0.f);
+        const float2 x0 = ml[r], x1 = both ? ml[TREE_ROWS + r] : make_float2(-INFINITY, 0.f);
         M = fmaxf(x0.x, x1.x);
         f0 = x0.x == -INFINITY ? 0.f : fast_exp2(x0.x - M);
         f1 = x1.x == -INFINITY ? 0.f : fast_exp2(x1.x - M);
         l = (x0.y == 0.f ? 0.f : x0.y * f0) + (x1.y == 0.f ? 0.f : x1.y * f1);
       }
-      on ^= pair || nt > 1 ? 3u : 1u;
+      on ^= merge && !both ? 1u : 3u;
       tc_fence_after();
-      const int pfirst = reinterpret_cast<volatile int*>(poison)[2 * (k % TR_ITEMS)];
-      const int plast = reinterpret_cast<volatile int*>(poison)[2 * (k % TR_ITEMS) + 1];
+      const volatile int* ps = poison + 4 * (k % TR_ITEMS) + (merge || pair ? 0 : 2 * h);
+      const int pfirst = both ? min(ps[0], ps[2]) : ps[0], plast = both ? max(ps[1], ps[3]) : ps[1];
       const bool whole = it.parts <= 1, nothing = l == 0.f;
-      const float inv = whole ? (nothing ? 0.f : 1.f / l) : 1.f;
-      const uint32_t o0 = tm_o + (pair ? D * h : 0);
+      const float inv = whole ? (nothing ? 0.f : 1.f / l) : 1.f;   // (a NaN stays one)
+      const float g0 = nothing ? 0.f : f0 * inv, g1 = nothing ? 0.f : f1 * inv;
+      const uint32_t o0 = tm_o + (merge ? 0 : D * h);
       const size_t orow = (size_t)t * a.Hq + head;
       const int rt = pair ? h : 0;   // row tile
       float4* part_o = reinterpret_cast<float4*>(a.part_o) + ((size_t)it.place * 2 + rt) * (D / 4) * TREE_ROWS + r;
-      const int c_first = pair ? 0 : h * (D / 64), c_end = pair ? D / 32 : c_first + D / 64;
+      // after a merge each of the two threads of a row has half of its channels
+      const int c_first = merge ? h * (D / 64) : 0, c_end = merge ? c_first + D / 64 : D / 32;
 #pragma unroll 1
       for (int c2 = c_first; c2 < c_end; ++c2) {
         uint32_t ov[32];
         tmem_ld32(o0 + c2 * 32, ov);
-        if (other) {
+        float odd = 0.f;   // NaN if there is an infinity or NaN
+        if (both) {
           uint32_t ow[32];
           tmem_ld32(tm_o + D + c2 * 32, ow);
           tmem_wait_ld();
 #pragma unroll
-          for (int x = 0; x < 32; ++x)
-            ov[x] = __float_as_uint(tr_weigh(f0, __uint_as_float(ov[x])) + tr_weigh(f1, __uint_as_float(ow[x])));
+          for (int x = 0; x < 32; ++x) {
+            const float y = fmaf(g1, __uint_as_float(ow[x]), g0 * __uint_as_float(ov[x]));
+            odd = fmaf(y, 0.f, odd);
+            ov[x] = __float_as_uint(y);
+          }
+          if (__any_sync(0xffffffffu, odd != odd)) {   // (an infinity must not meet a weight of 0)
+            tmem_ld32(o0 + c2 * 32, ov);
+            tmem_wait_ld();
+#pragma unroll
+            for (int x = 0; x < 32; ++x)
+              ov[x] = nothing ? 0u : __float_as_uint(tr_weigh(g0, __uint_as_float(ov[x])) + tr_weigh(g1, __uint_as_float(ow[x])));
+          }
         } else {
           tmem_wait_ld();
-        }
 #pragma unroll
-        for (int x = 0; x < 32; ++x) ov[x] = nothing ? 0u : __float_as_uint(__uint_as_float(ov[x]) * (l == l ? inv : l));
+          for (int x = 0; x < 32; ++x) ov[x] = nothing ? 0u : __float_as_uint(__uint_as_float(ov[x]) * g0);
+        }
         if (plast >= 0 && rv) {
           const TRRow row = my_row();
           // infinities and NaN of the keys this row sees, from the first tile to the last that holds one
@@ -1094,13 +1200,13 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
                               pack_bf16(__uint_as_float(ov[8 * x + 6]), __uint_as_float(ov[8 * x + 7])));
         }
       }
-      if (pair || h == 0) {
+      if (!merge || h == 0) {
         if (!whole) __stcg(reinterpret_cast<float2*>(a.part_ml) + ((size_t)it.place * 2 + rt) * TREE_ROWS + r, make_float2(M, l));
         else if (rv && a.lse) a.lse[orow] = nothing ? -INFINITY : M * LN2 + logf(l);
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(o_free);
+      if (merge && lane == 0) mbar_arrive(o_free);
       done_item(k);
     }
   }
