@@ -945,9 +945,14 @@ ink_status_t inkling_attn_tree(const ink_attn_params_t* params, const ink_attn_t
   a.cuts = reinterpret_cast<ink::TreeCut*>(ws + lay.cuts);
   a.part_ml = reinterpret_cast<float*>(ws + lay.part_ml_off);
   a.part_o = reinterpret_cast<float*>(ws + lay.part_o_off);
-  const int box = ink::tree_tile_keys(a.rel || a.slopes);
   ink::MaskedMaps maps;
-  if (!make_pool_map(&maps.k, k_cache, params, box) || !make_pool_map(&maps.v, v_cache, params, box) ||
+  // whole tiles by one box where they lie in one page, else boxes of a page and 64 channels
+  auto pool_map = [&](CUtensorMap* m, const void* base) {
+    return params->page_size >= ink::TILE_KEYS ? make_rows_map3(m, base, pool_rows(params), params->head_dim, params->head_dim / 64,
+                                                                ink::TILE_KEYS)
+                                               : make_pool_map(m, base, params, ink::TILE_KEYS);
+  };
+  if (!pool_map(&maps.k, k_cache) || !pool_map(&maps.v, v_cache) ||
       !make_token_map(&maps.q, q, params, total_q, a.heads_per_tile, a.tok_per_tile))
     return INK_ERR_CUDA;
   return ink::launch_tree(maps, a, params->head_dim, (cudaStream_t)stream) == cudaSuccess ? INK_OK : INK_ERR_CUDA;

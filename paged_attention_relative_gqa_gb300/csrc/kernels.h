@@ -312,7 +312,6 @@ struct TreeCut {
 constexpr int TREE_ROWS = 128;       // rows of a row tile
 constexpr int TREE_MAX_CTAS = 160;   // most CTAs (bounds the partials)
 
-int tree_tile_keys(bool bias);   // keys of a tile
 cudaError_t launch_tree(const MaskedMaps& m, const TreeArgs& a, int head_dim, cudaStream_t stream);
 
 }  // namespace ink

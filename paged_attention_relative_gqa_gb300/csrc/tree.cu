@@ -43,27 +43,32 @@ namespace {
 
 using namespace pf;
 
-constexpr int TR_ITEMS = 3;       // published items in flight
-constexpr int TR_BAD = 8;         // tiles whose unreadable keys are remembered
-constexpr int TR_TILES = 4;       // barriers of K and V tiles go by tile (at most 4 of a kind are in the ring)
-constexpr int TR_MIN_TILES = 2;   // least run of a CTA
+constexpr int TR_ITEMS = 2;       // published items in flight
+constexpr int TR_BAD = 16;        // tiles whose unreadable keys are remembered (K is up to 8 ahead of a softmax)
+// Barriers of K and V tiles go by tile.  A chain waits for its own tiles only, so a barrier must not be two of its phases behind
+// one who waits: next to a chain's last tile its next is at most TR_DUAL_SLACK + 1 behind it (the other chain's longer
+// piece, or two items of one tile, whose Q tiles a chain without tiles waits for).
+constexpr int TR_TILES = 8;
+constexpr int TR_MIN_TILES = 4;   // least run of a CTA
 constexpr int TR_DUAL_SLACK = 4;  // most tiles that two pieces may differ in to run side by side
-constexpr int TR_REGS_SOFTMAX = 208, TR_REGS_REST = 88;   // registers a thread after the split (without a bias)
 constexpr float TR_RESCALE_LOG2 = 8.f;
+
+constexpr int KT = TILE_KEYS, KW = KT / 32;   // keys of a tile, words of 32
 
 template <int D, bool BIAS>
 struct TRShape {
-  static constexpr int KT = BIAS ? 64 : 128;       // keys of a tile
-  static constexpr int THREADS = BIAS ? 512 : 384;
   static constexpr int CB = D / 64;
   static constexpr int SUB = KT * 128;             // one 64-channel block of a K or V tile
   static constexpr int TILE = CB * SUB;
   static constexpr int QSUB = TREE_ROWS * 128;
   static constexpr int QTILE = CB * QSUB;
-  static constexpr int NS = D == 128 ? 5 : 8;      // ring slots, K and V tiles in turn
+  static constexpr int NS = D == 128 && BIAS ? 5 : 10;   // ring slots, K and V tiles in turn
+  static constexpr bool TWO = NS % 2 == 0;         // K and V have slots, and a producer, of their own
+  static constexpr int V_WARP = BIAS ? 15 : 13;    // the one of V
+  static constexpr int THREADS = (V_WARP + TWO) * 32;
   static constexpr int PITCH = KT + 4;             // words of a bias row: KT values from a 16-byte boundary on
   static constexpr int ELEMENTS = KT + 1;          // the same of one filled element by element
-  static constexpr uint32_t TO = 256;              // S_h at 128 h, O_h at TO + D h
+  static constexpr uint32_t TO = 256;              // S_h at 128 h, two of them; O_h at TO + D h
 };
 
 // A run of key tiles of one or two row tiles.
@@ -98,12 +103,12 @@ struct TRSmem {
   static constexpr size_t ring = 2 * (size_t)S::QTILE;
   static constexpr size_t bias = ring + (size_t)S::NS * S::TILE;
   static constexpr size_t bars = bias + (BIAS ? 2 * (size_t)TREE_ROWS * S::PITCH * 4 : 0);
-  // k_full[TILES], v_full[TILES], v_ok[TILES], empty[NS], s_full[2], p_full[2], o_full[2], q_full[2], q_empty[2],
-  // bias_full[2], bias_empty[2], item_full[ITEMS], item_empty[ITEMS], o_free, ml, drain
-  static constexpr int NBAR = S::NS + 3 * TR_TILES + 14 + 2 * TR_ITEMS + 3;
+  // k_full[TILES], v_full[TILES], v_ok[TILES], empty[NS], s_full[2][2], p_full[2][2], o_done[2][2], q_full[2], q_empty[2],
+  // item_full[ITEMS], item_empty[ITEMS], o_free, ml, drain[2], bias_full[2], bias_empty[2]
+  static constexpr int NBAR = S::NS + 3 * TR_TILES + 16 + 2 * TR_ITEMS + 4 + (BIAS ? 4 : 0);
   static constexpr size_t items = bars + (NBAR * 8 + 15) / 16 * 16;
   static constexpr size_t kbad = items + TR_ITEMS * sizeof(TRItem);
-  static constexpr size_t poison = kbad + TR_BAD * 16;
+  static constexpr size_t poison = kbad + TR_BAD * KW * 4;
   static constexpr size_t ml = poison + TR_ITEMS * 16;           // [2 chains][128 rows] float2
   static constexpr size_t misc = ml + 2 * TREE_ROWS * 8;
   static constexpr size_t alloc = misc + 16;   // (no room to align within: the array itself has to be)
@@ -129,7 +134,7 @@ struct TRSeq {
   int c0, n, L, lo, hi, tiles;
   uint32_t bad;   // error bits; BAD_ROWS: its rows are not touched
 
-  __device__ __forceinline__ void load(const TreeArgs& a, int b, int kt) {
+  __device__ __forceinline__ void load(const TreeArgs& a, int b) {
     c0 = __ldg(a.cu_q + b);
     const int c1 = __ldg(a.cu_q + b + 1);
     L = __ldg(a.seq_lens + b);
@@ -150,7 +155,7 @@ struct TRSeq {
       if (L > cap) bad = INK_DEVERR_PAGE_OUT_OF_RANGE;
       hi = (int)min((long long)L, cap);
       lo = a.W > 0 ? max(0, L - n - a.W + 1) : 0;
-      if (lo < hi) tiles = (hi - 1) / kt - lo / kt + 1;
+      if (lo < hi) tiles = (hi - 1) / KT - lo / KT + 1;
     }
   }
 };
@@ -160,7 +165,7 @@ struct TRSeq {
 struct TRWalk {
   long long base, incl, chunk, total;   // tiles before sequence cb; up to and with this lane's; of a run; of the 32
   long long pos, end;                   // of this CTA's run
-  int cb, per, items, kt, cta;
+  int cb, per, items, cta;
   int src, groups, left;                // the sequence's lane; its items; of these not begun
   int kvh, hc, item;                    // the next one
   TRSeq s;
@@ -168,7 +173,7 @@ struct TRWalk {
   __device__ __forceinline__ void load(const TreeArgs& a, int lane) {
     const int b = cb + lane;
     s.tiles = s.n = 0;
-    if (b < a.B) s.load(a, b, kt);
+    if (b < a.B) s.load(a, b);
     items = (s.n + 2 * a.tok_per_tile - 1) / (2 * a.tok_per_tile);
     incl = (long long)s.tiles * items * per;
 #pragma unroll
@@ -179,8 +184,7 @@ struct TRWalk {
     total = __shfl_sync(0xffffffffu, incl, 31);
   }
 
-  __device__ __forceinline__ void begin(const TreeArgs& a, int lane, int tile_keys) {
-    kt = tile_keys;
+  __device__ __forceinline__ void begin(const TreeArgs& a, int lane) {
     per = a.Hkv * a.head_chunks;
     cta = (int)blockIdx.x;
     long long all = 0;
@@ -235,7 +239,7 @@ struct TRWalk {
     w.gh = min(a.heads_per_tile, a.G - hc * a.heads_per_tile);
     w.t0 = w.c0 + item * 2 * a.tok_per_tile;
     w.ntok = min(2 * a.tok_per_tile, w.n - item * 2 * a.tok_per_tile);
-    w.kt0 = w.lo / kt + x0;
+    w.kt0 = w.lo / KT + x0;
     w.nt = (int)min((long long)(tiles - x0), end - pos);
     const long long g1 = pos - x0 + tiles;
     w.parts = (g1 <= end ? cta : (int)((g1 - 1) / chunk)) - first + 1;
@@ -300,9 +304,9 @@ __device__ __forceinline__ TRRow tr_row(const TreeArgs& a, const TRPart& it, int
 // side by side, one copy a row where 16-byte boundaries can be kept inside the tensor; all of them at E - 1 or more are one value.
 enum TRBias { NoLoad, RowCopies, Elements };
 
-__device__ __forceinline__ TRBias tr_bias(const TreeArgs& a, const TRPart& it, int k0, int kt) {
-  if (min(it.H, it.hi) - k0 < kt) return Elements;
-  if (!a.rel || it.H - (k0 + kt - 1) >= a.E - 1) return NoLoad;
+__device__ __forceinline__ TRBias tr_bias(const TreeArgs& a, const TRPart& it, int k0) {
+  if (min(it.H, it.hi) - k0 < KT) return Elements;
+  if (!a.rel || it.H - (k0 + KT - 1) >= a.E - 1) return NoLoad;
   return a.rel_rows ? RowCopies : Elements;
 }
 
@@ -322,27 +326,27 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
             const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ TreeArgs a) {
   using S = TRShape<D, BIAS>;
   using L_ = TRSmem<D, BIAS>;
-  constexpr int NS = S::NS, KT = S::KT, KW = KT / 32;
+  constexpr int NS = S::NS;
 
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + L_::bars);
   uint64_t* v_full = k_full + TR_TILES;
   uint64_t* v_ok = v_full + TR_TILES;   // V tile checked
   uint64_t* empty = v_ok + TR_TILES;
-  uint64_t* s_full = empty + NS;        // [2] S_h in TMEM, every earlier product of h done
-  uint64_t* p_full = s_full + 2;        // [2] P_h written
-  uint64_t* o_full = p_full + 2;        // [2] the piece's last O_h product done
-  uint64_t* q_full = o_full + 2;        // [2]
+  uint64_t* s_full = empty + NS;        // [2 chains][2] S in TMEM, every product before it done
+  uint64_t* p_full = s_full + 4;        // [2 chains][2] P written
+  uint64_t* o_done = p_full + 4;        // [2 chains][2] product of that P done
+  uint64_t* q_full = o_done + 4;        // [2]
   uint64_t* q_empty = q_full + 2;       // [2] the piece's last product with a Q tile done
-  uint64_t* bias_full = q_empty + 2;    // [2]
-  uint64_t* bias_empty = bias_full + 2; // [2]
-  uint64_t* item_full = bias_empty + 2; // [ITEMS]
+  uint64_t* item_full = q_empty + 2;    // [ITEMS]
   uint64_t* item_empty = item_full + TR_ITEMS;
   uint64_t* o_free = item_empty + TR_ITEMS;   // both O of a Split item read
   uint64_t* ml_bar = o_free + 1;        // maxima and sums of both chains written
-  uint64_t* drain = ml_bar + 1;
+  uint64_t* drain = ml_bar + 1;         // [2]
+  uint64_t* bias_full = drain + 2;      // [2]
+  uint64_t* bias_empty = bias_full + 2; // [2]
   TRItem* items = reinterpret_cast<TRItem*>(smem + L_::items);
-  uint32_t* kbad = reinterpret_cast<uint32_t*>(smem + L_::kbad);   // [BAD][4] bit per unreadable key
+  uint32_t* kbad = reinterpret_cast<uint32_t*>(smem + L_::kbad);   // [BAD][KW] bit per unreadable key
   int* poison = reinterpret_cast<int*>(smem + L_::poison);   // [ITEMS][2 chains][2] first and last tile of V with an infinity or NaN
   float2* ml = reinterpret_cast<float2*>(smem + L_::ml);
   float* bias = reinterpret_cast<float*>(smem + L_::bias);
@@ -360,33 +364,38 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
     return;
   }
   if (tid == 0) {
-    for (int x = 0; x < NS; ++x) mbar_init(&empty[x], 1);
+    for (int x = 0; x < NS; ++x) mbar_init(&empty[x], 2);
     for (int x = 0; x < TR_TILES; ++x) {
       mbar_init(&k_full[x], 1);
       mbar_init(&v_full[x], 1);
       mbar_init(&v_ok[x], 1);
     }
     for (int x = 0; x < 2; ++x) {
-      mbar_init(&s_full[x], 1);
-      mbar_init(&p_full[x], 4);
-      mbar_init(&o_full[x], 1);
+      mbar_init(&s_full[2 * x], 1);
+      mbar_init(&s_full[2 * x + 1], 1);
+      mbar_init(&p_full[2 * x], 4);
+      mbar_init(&p_full[2 * x + 1], 4);
+      mbar_init(&o_done[2 * x], 1);
+      mbar_init(&o_done[2 * x + 1], 1);
       mbar_init(&q_full[x], 1);
-      mbar_init(&q_empty[x], 1);
-      mbar_init(&bias_full[x], 64);   // every lane of two warps
-      mbar_init(&bias_empty[x], 4);
+      mbar_init(&q_empty[x], 2);
+      mbar_init(&drain[x], 1);
+      if constexpr (BIAS) {
+        mbar_init(&bias_full[x], 32);   // every lane of a warp
+        mbar_init(&bias_empty[x], 4);
+      }
     }
     for (int x = 0; x < TR_ITEMS; ++x) {
       mbar_init(&item_full[x], 1);
-      mbar_init(&item_empty[x], 11 + (BIAS ? 4 : 0));   // producer, MMA, V check, 8 softmax warps, bias warps
+      mbar_init(&item_empty[x], 12 + S::TWO + (BIAS ? 2 : 0));   // producers, 2 MMA, V check, 8 softmax warps, bias warps
     }
     mbar_init(o_free, 8);
     mbar_init(ml_bar, 8);
-    mbar_init(drain, 1);
     fence_mbar_init();
     *abort_flag = 0;
   }
   TRWalk walk;
-  if (warp == 10) walk.begin(a, lane, KT);   // (its loads are on their way while the rest is set up)
+  if (warp == 10) walk.begin(a, lane);   // (its loads are on their way while the rest is set up)
   // rows of a Q tile past the last (token, head) pair stay zero
   for (int x = tid; x < 2 * S::QTILE / 16; x += S::THREADS)
     *reinterpret_cast<uint4*>(smem + L_::q + (size_t)x * 16) = make_uint4(0u, 0u, 0u, 0u);
@@ -411,167 +420,172 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
   };
 
   if (warp >= 8) {
-    if constexpr (!BIAS) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(TR_REGS_REST));
-    if (warp == 8) {
+    if (warp == 8 || (S::TWO && warp == S::V_WARP)) {
       // ---------------------------------------------------------------- K and V producer
       if (lane == 0) {
         prefetch_tensormap(&tmK);
         prefetch_tensormap(&tmV);
       }
       const int seg = min(P, KT), nseg = KT / seg;
-      int f = 0;                            // fills issued
-      bool go = true;
+      const bool wide = P >= KT;            // a tile lies in one page: one box a tensor
+      const int kv0 = warp != 8, kv1 = S::TWO ? kv0 : 1;   // K, V or both
+      int x = 0, st = kv0;                  // tiles issued, slot of the next fill
+      uint32_t round = 0;                   // times the slots have been gone through
+      bool go = true, k_only = false;       // the last fill was a K without its V
       for (int k = 0; go && next_item(k); ++k) {
         const TRItem& item = items[k % TR_ITEMS];
-        int chunk_base[2] = {0, 0}, chunk_val[2] = {-1, -1};   // table entries chunk_base + lane, of each chain's part
-        for (int j = 0; j < item.longest() && go; ++j)
+        const int parts = item.mode == Pair ? 1 : 2, longest = item.longest(), kstep = item.step() * KT;
+        const int32_t* bt[2];
+        int kvh[2], lo[2], hi[2], nt[2], k0[2], chunk_base[2], chunk_val[2];   // table entries chunk_base + lane, of each chain's part
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const TRPart& it = item.part[h];
-          if (!go || (h == 1 && item.mode == Pair) || j >= it.nt) continue;
-          const int k0 = (it.kt0 + j * item.step()) * KT;
-          const int last_idx = (it.hi - 1) >> a.log2_page;
-          const int pfirst = k0 >> a.log2_page, plast = (k0 + KT - 1) >> a.log2_page;
-          if (j == 0 || plast >= chunk_base[h] + 32) {
-            chunk_base[h] = pfirst;   // entries past the sequence's last key are not read
-            chunk_val[h] = __ldg(a.block_table + (size_t)it.b * a.max_pages + min(chunk_base[h] + lane, last_idx));
+          bt[h] = a.block_table + (size_t)it.b * a.max_pages;
+          kvh[h] = it.kvh;
+          lo[h] = it.lo;
+          hi[h] = it.hi;
+          nt[h] = h < parts ? it.nt : 0;
+          k0[h] = it.kt0 * KT;
+          chunk_base[h] = k0[h] >> a.log2_page;   // entries past the sequence's last key are not read
+          chunk_val[h] = __ldg(bt[h] + min(chunk_base[h] + lane, (hi[h] - 1) >> a.log2_page));
+        }
+        done_item(k);
+        for (int j = 0; j < longest && go; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (!go || j >= nt[h]) continue;
+          if (((k0[h] + KT - 1) >> a.log2_page) >= chunk_base[h] + 32) {
+            chunk_base[h] = k0[h] >> a.log2_page;
+            chunk_val[h] = __ldg(bt[h] + min(chunk_base[h] + lane, (hi[h] - 1) >> a.log2_page));
           }
-          const int ks = k0 + lane * seg;                 // lane < nseg takes one segment
-          const bool want = lane < nseg && ks < it.hi && ks + seg > it.lo;
+          const int ks = k0[h] + (wide ? 0 : lane * seg);   // lane < nseg takes one segment
+          const bool want = lane < nseg && ks < hi[h] && ks + seg > lo[h];
           const int page = __shfl_sync(0xffffffffu, chunk_val[h], min(max((ks >> a.log2_page) - chunk_base[h], 0), 31));
           const bool bad_seg = want && (page < 0 || page >= a.num_pages);
           const bool load = want && !bad_seg;
-          const uint32_t nload = __popc(__ballot_sync(0xffffffffu, load));
           const uint32_t bmask = __ballot_sync(0xffffffffu, bad_seg);
-          const int row = load ? ((page * a.Hkv + it.kvh) << a.log2_page) + (ks & (P - 1)) : 0;
-#pragma unroll 1
-          for (int kv = 0; kv < 2; ++kv, ++f) {
-            const int st = f % NS;
-            if (f >= NS && !tr_wait(&empty[st], (uint32_t)((f / NS) - 1) & 1u, abort_flag, a)) {
-              go = false;
-              break;
-            }
-            if (kv == 0 && lane < KW) {   // keys of this tile whose page is outside the pool
-              uint32_t bad = 0;
-              for (uint32_t mm = bmask; mm; mm &= mm - 1) {
-                const int x0 = (__ffs(mm) - 1) * seg - 32 * lane, x1 = x0 + seg;   // bits [x0, x1) of this word
-                const int y0 = max(x0, 0), y1 = min(x1, 32);
-                if (y1 > y0) bad |= (0xffffffffu >> (32 - (y1 - y0))) << y0;
+          const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, load)) * (uint32_t)(seg * D * 2);
+          const int row = load ? ((page * a.Hkv + kvh[h]) << a.log2_page) + (ks & (P - 1)) : 0;
+#pragma unroll
+          for (int y = 0; y < (S::TWO ? 1 : 2); ++y) {
+            const int kv = S::TWO ? kv0 : y;
+            if (go && round > 0) go = tr_wait(&empty[st], (round - 1) & 1u, abort_flag, a);
+            if (!go) break;
+            uint64_t* full = (kv ? v_full : k_full) + x % TR_TILES;
+            uint8_t* dst = smem + L_::ring + (size_t)st * S::TILE + (wide ? 0 : lane * seg * 128);
+            if (lane == 0) {
+              if (kv == 0) {   // keys of this tile whose page is outside the pool
+                uint64_t bad = 0;
+                for (uint32_t mm = bmask; mm; mm &= mm - 1) bad |= (~0ull >> (64 - seg)) << ((__ffs(mm) - 1) * seg);
+                *reinterpret_cast<uint64_t*>(kbad + x % TR_BAD * KW) = bad;
+                if (bmask) record_error(a.err, INK_DEVERR_PAGE_OUT_OF_RANGE);
               }
-              kbad[((f >> 1) % TR_BAD) * 4 + lane] = bad;
-              if (bmask && lane == 0) record_error(a.err, INK_DEVERR_PAGE_OUT_OF_RANGE);
+              mbar_arrive_expect_tx(full, bytes);
+              if (wide && load) tma_load_3d(dst, kv ? &tmV : &tmK, 0, row, 0, full);
             }
-            uint64_t* full = (kv ? v_full : k_full) + (f >> 1) % TR_TILES;
-            __syncwarp();
-            if (lane == 0) mbar_arrive_expect_tx(full, nload * (uint32_t)(seg * D * 2));
-            __syncwarp();
-            if (load) {
-              uint8_t* dst = smem + L_::ring + (size_t)st * S::TILE + lane * seg * 128;
+            if (!wide && load) {
 #pragma unroll
               for (int cb = 0; cb < S::CB; ++cb)
                 tma_load_2d(dst + cb * S::SUB, kv ? &tmV : &tmK, cb * 64, row, full);
             }
+            st += S::TWO ? 2 : 1;
+            if (st >= NS) {
+              st -= NS;
+              ++round;
+            }
+            k_only = kv != kv1;
+            if (kv == kv1) ++x;
           }
+          k0[h] += kstep;
         }
-        done_item(k);
       }
       if (lane == 0) {
-        pp_drain_ring(k_full, TR_TILES, (f + 1) >> 1, a.err);
-        pp_drain_ring(v_full, TR_TILES, f >> 1, a.err);
+        if (kv0 == 0) pp_drain_ring(k_full, TR_TILES, x + (!S::TWO && k_only), a.err);
+        if (kv1 == 1) pp_drain_ring(v_full, TR_TILES, x, a.err);
       }
-    } else if (warp == 9) {
-      // ---------------------------------------------------------------- MMA issue
+    } else if (warp == 9 || warp == 12) {
+      // ---------------------------------------------------------------- MMA issue of one chain
       constexpr uint32_t IDESC_S = umma_idesc_bf16(128, KT, false, false);
       constexpr uint32_t IDESC_PV = umma_idesc_bf16(128, D, false, true);
+      const int h = warp == 12;
       const uint32_t qaddr = smem_u32(smem + L_::q), raddr = smem_u32(smem + L_::ring);
-      // S and P V products each walk the tiles in their order: K of tile g is fill 2 g, V fill 2 g + 1
-      int gk = 0, gv = 0, k_slot = 0, v_slot = 1;
-      uint32_t qn = 0, pn = 0;         // a parity bit per Q tile and per chain
+      const uint32_t tm_s = tmem + 128u * h, tm_o = tmem + S::TO + (uint32_t)(D * h);
+      int g = 0;                       // tiles of earlier items: K of tile x is fill 2 x, V fill 2 x + 1
+      uint32_t qn = 0;                 // a parity bit per Q tile
+      uint32_t sc = 0, pc = 0;         // S and P V products so far: the two S take turns
       bool go = true;
-      auto wait_tile = [&](uint64_t* bars, int tile) {
-        return tr_wait(&bars[tile % TR_TILES], (uint32_t)(tile / TR_TILES) & 1u, abort_flag, a);
+      auto wait_tile = [&](uint64_t* bars, int x) {
+        return tr_wait(&bars[x % TR_TILES], (uint32_t)(x / TR_TILES) & 1u, abort_flag, a);
       };
-      auto wait_q = [&](int s) {
-        const bool ok = tr_wait(&q_full[s], (qn >> s) & 1u, abort_flag, a);
-        qn ^= 1u << s;
-        return ok;
-      };
-      // S_h of tile gk with Q tile qs; the tile's last product frees its slot, a Q tile's last one that
-      auto issue_s = [&](int h, int qs, bool frees_k, bool frees_q) {
-        const uint64_t ad = umma_desc_sw128(qaddr + qs * S::QTILE, 16, 1024);
-        const uint64_t bd = umma_desc_sw128(raddr + k_slot * S::TILE, 16, 1024);
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          umma_ss_warp(tmem + 128u * h, ad + (uint64_t)(((kk >> 2) * S::QSUB + (kk & 3) * 32) >> 4),
-                       bd + (uint64_t)(((kk >> 2) * S::SUB + (kk & 3) * 32) >> 4), IDESC_S, kk > 0 ? 1u : 0u);
-        umma_commit_warp(&s_full[h]);
-        if (frees_k) {
-          umma_commit_warp(&empty[k_slot]);
-          ++gk;
-          k_slot = k_slot + 2 < NS ? k_slot + 2 : k_slot + 2 - NS;
-        }
-        if (frees_q) umma_commit_warp(&q_empty[qs]);
-        __syncwarp();
-      };
-      auto issue_pv = [&](int h, bool acc, bool frees_v) {
-        const uint64_t bd = umma_desc_sw128(raddr + v_slot * S::TILE, S::SUB, 1024);
-#pragma unroll
-        for (int ks = 0; ks < KT / 16; ++ks)
-          umma_ts_warp(tmem + S::TO + (uint32_t)(D * h), tmem + 128u * h + ks * 8, bd + (uint64_t)((ks * 16 * 128) >> 4),
-                       IDESC_PV, (acc || ks > 0) ? 1u : 0u);
-        if (frees_v) {
-          umma_commit_warp(&empty[v_slot]);
-          ++gv;
-          v_slot = v_slot + 2 < NS ? v_slot + 2 : v_slot + 2 - NS;
-        }
+      // What both chains may read is free after two arrivals: one of each, or both of the only one.
+      auto free_slot = [&](uint64_t* bar, bool shared) {
+        if (!shared && lane == 0) mbar_arrive(bar);
+        umma_commit_warp(bar);
       };
       uint32_t merges = 0;             // Split items so far
       bool merged = false;             // the item before was one
       for (int k = 0; go && next_item(k); ++k) {
         const TRItem& it = items[k % TR_ITEMS];
-        const int mode = it.mode, qs1 = mode == Split ? it.qs : 1, qs0 = mode == Split ? it.qs : 0;
-        const int n0 = it.part[0].nt, n1 = mode == Pair ? n0 : it.part[1].nt, last = gk + n0 + n1 - 1;
-        const bool pair = mode == Pair;
-        // the last S with a Q tile: of the chain, of the piece in Split
-        auto last_s = [&](int j, int h) { return mode == Split ? gk == last : j == (h ? n1 : n0) - 1; };
-        for (int h = 0; h < 2 && go; ++h) {
-          if (h == 1 && n1 == 0) continue;
-          if (mode != Split || h == 0) go = wait_q(h ? qs1 : qs0);
-          if (go && (!pair || h == 0)) go = wait_tile(k_full, gk);
-          if (!go) break;
+        const bool pair = it.mode == Pair, split = it.mode == Split;
+        const int qs = split ? it.qs : h, beside = it.beside(h), nt = it.of(h).nt, all = it.tiles();
+        const uint64_t qd = umma_desc_sw128(qaddr + qs * S::QTILE, 16, 1024);
+        auto issue_s = [&](int j) {
+          const int x = g + j + min(j + h, beside);
+          go = wait_tile(k_full, x);
+          if (!go) return;
           tc_fence_after();
-          issue_s(h, h ? qs1 : qs0, !pair || h == 1, last_s(0, h));
+          const int st = 2 * x % NS, last = j + 1 == nt;
+          const uint64_t kd = umma_desc_sw128(raddr + st * S::TILE, 16, 1024);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            umma_ss_warp(tm_s + KT * (sc & 1u), qd + (uint64_t)(((kk >> 2) * S::QSUB + (kk & 3) * 32) >> 4),
+                         kd + (uint64_t)(((kk >> 2) * S::SUB + (kk & 3) * 32) >> 4), IDESC_S, kk > 0 ? 1u : 0u);
+          umma_commit_warp(&s_full[2 * h + (sc & 1u)]);
+          ++sc;
+          free_slot(&empty[st], pair);
+          if (last) free_slot(&q_empty[qs], split);
+          __syncwarp();
+        };
+        // (Every phase is waited for, of the other chain's Q tile and by a chain without a tile too: a parity tells a phase from
+        // its neighbours only.)
+        go = tr_wait(&q_full[qs], (qn >> qs) & 1u, abort_flag, a);
+        if (go && !split) go = tr_wait(&q_full[h ^ 1], (qn >> (h ^ 1)) & 1u, abort_flag, a);
+        if (!go) break;
+        if (nt == 0) {                 // (the only tile of a Split item is the other chain's)
+          if (lane == 0) mbar_arrive(&q_empty[qs]);
+          __syncwarp();
+        } else {
+          issue_s(0);
+          if (go && nt > 1) issue_s(1);
         }
         // both O of a Split item have been read
         if (go && merged) go = tr_wait(o_free, (merges - 1) & 1u, abort_flag, a);
-        merged = mode == Split;
-        merges += merged;
-        for (int j = 0; j < max(n0, n1) && go; ++j)
+        for (int j = 0; j < nt && go; ++j) {
+          const int x = g + j + min(j + h, beside);
+          // (v_ok comes after v_full)
+          go = wait_tile(v_ok, x) && tr_wait(&p_full[2 * h + (pc & 1u)], (pc >> 1) & 1u, abort_flag, a);
+          if (!go) break;
+          tc_fence_after();
+          const int st = (2 * x + 1) % NS;
+          const uint64_t vd = umma_desc_sw128(raddr + st * S::TILE, S::SUB, 1024);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int nh = h ? n1 : n0;
-            if (!go || j >= nh) continue;
-            // (v_ok comes after v_full)
-            if (!pair || h == 0) go = wait_tile(v_ok, gv);
-            if (go) go = tr_wait(&p_full[h], (pn >> h) & 1u, abort_flag, a);
-            if (!go) continue;
-            pn ^= 1u << h;
-            tc_fence_after();
-            issue_pv(h, j > 0, !pair || h == 1);
-            if (j + 1 < nh) {
-              if (!pair || h == 0) go = wait_tile(k_full, gk);
-              if (!go) continue;
-              issue_s(h, h ? qs1 : qs0, !pair || h == 1, last_s(j + 1, h));
-            } else {
-              umma_commit_warp(&o_full[h]);
-              __syncwarp();
-            }
-          }
+          for (int ks = 0; ks < KT / 16; ++ks)
+            umma_ts_warp(tm_o, tm_s + KT * (pc & 1u) + ks * 8, vd + (uint64_t)((ks * 16 * 128) >> 4), IDESC_PV, (j > 0 || ks > 0) ? 1u : 0u);
+          umma_commit_warp(&o_done[2 * h + (pc & 1u)]);
+          ++pc;
+          free_slot(&empty[st], pair);
+          __syncwarp();
+          if (j + 2 < nt) issue_s(j + 2);   // over the P just read
+        }
+        qn ^= split ? 1u << qs : 3u;
+        merged = split;
+        merges += split;
+        g += all;
         done_item(k);
       }
-      umma_commit_warp(drain);
+      umma_commit_warp(&drain[h]);
       __syncwarp();
-      if (!mbar_wait_bounded(drain, 0)) record_error(a.err, INK_DEVERR_WAIT_TIMEOUT);
+      if (!mbar_wait_bounded(&drain[h], 0)) record_error(a.err, INK_DEVERR_WAIT_TIMEOUT);
     } else if (warp == 10) {
       // ---------------------------------------------------------------- scheduler and Q loads
       if (lane == 0) prefetch_tensormap(&tmQ);
@@ -670,16 +684,17 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
       bool go = true;
       for (int k = 0; go && next_item(k); ++k) {
         const TRItem& item = items[k % TR_ITEMS];
-        for (int j = 0; j < item.longest() && go; ++j)
+        const int longest = item.longest(), step = item.step();
+        for (int j = 0; j < longest && go; ++j)
         for (int h = 0; h < (item.mode == Pair ? 1 : 2); ++h) {
           const TRPart& it = item.part[h];
           if (j >= it.nt) continue;
-          const int hist = min(it.H, it.hi), kt = it.kt0 + j * item.step();
+          const int hist = min(it.H, it.hi), kt = it.kt0 + j * step;
           const int st = (2 * g + 1) % NS;
           go = tr_wait(&v_full[g % TR_TILES], (uint32_t)(g / TR_TILES) & 1u, abort_flag, a);
           if (!go) break;
           const int k0 = kt * KT;
-          const uint32_t* badw = kbad + (g % TR_BAD) * 4;
+          const uint32_t* badw = kbad + (g % TR_BAD) * KW;
           uint32_t any = 0;
 #pragma unroll
           for (int x = 0; x < KW; ++x) any |= badw[x];
@@ -733,8 +748,8 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
         done_item(k);
       }
     } else if constexpr (BIAS) {
-      // ---------------------------------------------------------------- bias loads: two warps a chain, 64 rows each
-      const int h = (warp - 12) >> 1, r0 = ((warp - 12) & 1) * 64;
+      // ---------------------------------------------------------------- bias loads of one chain
+      const int h = warp - 13;
       float* buf = bias + (size_t)h * TREE_ROWS * S::PITCH;
       const int last = a.E - 1, size = a.rel_bf16 ? 2 : 4;
       uint32_t fills = 0;
@@ -744,44 +759,43 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
         const TRPart& it = item.of(h);
         const int tok0 = item.mode == Pair ? h * a.tok_per_tile : 0;
         const int rows = min(a.tok_per_tile, it.ntok - tok0) * a.heads_per_tile;
-        const int i0 = r0 / a.heads_per_tile;
-        // this lane's rows r0 + lane and 32 more: position and elements before the row; tokens of the warp's rows
-        int pr[2], pt[2];
-        size_t at[2];
-        bool live[2];
+        // this lane's rows lane, lane + 32, ...: position and elements before the row; and tokens lane, lane + 32, ...
+        int pr[4], pt[4];
+        size_t at[4];
+        bool live[4];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int r = r0 + 32 * x + lane, i = r / a.heads_per_tile, hd = r - i * a.heads_per_tile;
+        for (int x = 0; x < 4; ++x) {
+          const int r = 32 * x + lane, i = r / a.heads_per_tile, hd = r - i * a.heads_per_tile;
           live[x] = r < rows && hd < it.gh;
           const int t = it.t0 + tok0 + (live[x] ? i : 0);
           pr[x] = max(__ldg(a.positions + t), it.H);
           at[x] = ((size_t)t * a.Hq + it.h0 + hd) * a.E;
-          const int ti = min(i0 + 32 * x + lane, it.ntok - tok0 - 1);
-          pt[x] = max(__ldg(a.positions + it.t0 + tok0 + ti), it.H);
+          pt[x] = max(__ldg(a.positions + it.t0 + tok0 + min(32 * x + lane, it.ntok - tok0 - 1)), it.H);
         }
         for (int j = 0; j < it.nt && go; ++j) {
           const int k0 = (it.kt0 + j * item.step()) * KT;
-          const TRBias how = tr_bias(a, it, k0, KT);
+          const TRBias how = tr_bias(a, it, k0);
           if (how == NoLoad) continue;
           if (fills > 0) go = tr_wait(&bias_empty[h], (fills - 1) & 1u, abort_flag, a);
           if (!go) break;
           ++fills;
           if (how == RowCopies) {
             // distances [s, e) of a row, from the 16 bytes that hold the first to those that hold the last
-            uint32_t bytes[2];
-            uintptr_t from[2];
+            uint32_t bytes[4], sum = 0;
+            uintptr_t from[4];
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
+            for (int x = 0; x < 4; ++x) {
               const int s = pr[x] - (k0 + KT - 1), e = min(pr[x] - k0, last) + 1;
               const uintptr_t base = reinterpret_cast<uintptr_t>(a.rel) + at[x] * size;
               from[x] = (base + (size_t)s * size) & ~(uintptr_t)15;
               bytes[x] = live[x] && s < e ? (uint32_t)(((base + (size_t)e * size + 15) & ~(uintptr_t)15) - from[x]) : 0u;
+              sum += bytes[x];
             }
-            mbar_arrive_expect_tx(&bias_full[h], bytes[0] + bytes[1]);
+            mbar_arrive_expect_tx(&bias_full[h], sum);
 #pragma unroll
-            for (int x = 0; x < 2; ++x)
+            for (int x = 0; x < 4; ++x)
               if (bytes[x])
-                bulk_copy_g2s(smem_u32(buf + (r0 + 32 * x + lane) * S::PITCH), reinterpret_cast<const void*>(from[x]), bytes[x],
+                bulk_copy_g2s(smem_u32(buf + (32 * x + lane) * S::PITCH), reinterpret_cast<const void*>(from[x]), bytes[x],
                               &bias_full[h]);
             __syncwarp();
             continue;
@@ -795,15 +809,14 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
           }
           // (all loads of a batch first, from rows that are there: what is not seen is masked)
           auto fill = [&](auto load) {
-            int i = i0, hd = r0 - i0 * a.heads_per_tile;
+            int i = 0, hd = 0;
 #pragma unroll 1
-            for (int r = r0; r < min(r0 + 64, rows); r += 16) {
+            for (int r = 0; r < rows; r += 16) {
               float v[16][2], far[16][2], slope[16];
 #pragma unroll
               for (int y = 0; y < 16; ++y) {
-                const int off = min(i - i0, 63);
-                const int p0 = __shfl_sync(0xffffffffu, pt[0], off & 31), p1 = __shfl_sync(0xffffffffu, pt[1], off & 31);
-                const int p = off < 32 ? p0 : p1;
+                const int ic = min(i, 127), p0 = __shfl_sync(0xffffffffu, ic & 32 ? pt[1] : pt[0], ic & 31);
+                const int p1 = __shfl_sync(0xffffffffu, ic & 32 ? pt[3] : pt[2], ic & 31), p = ic & 64 ? p1 : p0;
                 const int head = it.h0 + min(hd, it.gh - 1);
                 const size_t row = ((size_t)(it.t0 + min(tok0 + i, it.ntok - 1)) * a.Hq + head) * a.E;
                 slope[y] = a.slopes ? __ldg(a.slopes + head) : 0.f;
@@ -838,17 +851,16 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
     }
   } else {
     // ------------------------------------------------------------------ softmax
-    if constexpr (!BIAS) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(TR_REGS_SOFTMAX));
     const int h = warp >> 2, r = tid & 127;
     const uint32_t tlane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t tm_s = tlane + 128u * h, tm_o = tlane + S::TO;
+    const uint32_t tm_chain = tlane + 128u * h, tm_o = tlane + S::TO;
     const int my_i = r / a.heads_per_tile, my_g = r - my_i * a.heads_per_tile;
     __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out);
 
     // sequences that see no key: zero rows, shared out over the CTAs; what is wrong with a sequence is told here
     for (int b = (int)blockIdx.x; b < a.B; b += (int)gridDim.x) {
       TRSeq s;
-      s.load(a, b, KT);
+      s.load(a, b);
       if (tid == 0 && s.bad) record_error(a.err, s.bad);
       if (s.tiles > 0 || s.n <= 0) continue;
       for (long long x = tid; x < (long long)s.n * a.Hq * (D / 8); x += 256)
@@ -859,11 +871,10 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
 
     const bool scaled = CAP || BIAS || !(a.scale_log2 > 0.f);
     const float mul = scaled ? 1.f : a.scale_log2;
-    uint32_t sn = 0, on = 0, bn = 0, mn = 0;   // (on: a parity bit per chain)
+    uint32_t c = 0, c_other = 0, bn = 0, mn = 0;   // tiles of this chain and of the other one so far
     int g = 0;
     bool go = true;
     for (int k = 0; go && next_item(k); ++k) {
-      // (read where it is needed, from shared memory: the tile loop has no registers to spare)
       const TRItem& item = items[k % TR_ITEMS];
       const TRPart& it = item.of(h);
       const int nt = it.nt;
@@ -871,14 +882,9 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
       const int ti = (pair ? h * a.tok_per_tile : 0) + my_i;
       const bool rv = my_i < a.tok_per_tile && ti < it.ntok && my_g < it.gh;
       const int t = it.t0 + (rv ? ti : 0), head = it.h0 + (rv ? my_g : 0);
-      // (position and bits come from L1 where they are needed; without a bias there are no registers for them)
-      prefetch_l1(a.positions + t);
-      prefetch_l1(a.ancestors + (size_t)t * a.words);
-      int p = 0;
-      if constexpr (BIAS) p = max(__ldg(a.positions + t), it.H);
-      auto my_row = [&]() {
-        return tr_row(a, it, t, BIAS ? p : max(__ldg(a.positions + t), it.H), __ldg(a.ancestors + (size_t)t * a.words), rv);
-      };
+      const int p = max(__ldg(a.positions + t), it.H);
+      const uint32_t w0 = __ldg(a.ancestors + (size_t)t * a.words);
+      auto my_row = [&]() { return tr_row(a, it, t, p, w0, rv); };
       float rc = 0.f;   // the row's last value
       if constexpr (BIAS) {
         if (a.rel) {
@@ -892,169 +898,165 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < nt; ++j, k0 += kstep) {
         const int tile = g + j + min(j + h, beside);
-        go = tr_wait(&s_full[h], sn & 1u, abort_flag, a);
+        const uint32_t buf = c & 1u, tm_s = tm_chain + KT * buf;
+        go = tr_wait(&s_full[2 * h + buf], (c >> 1) & 1u, abort_flag, a);
         if (!go) break;
-        ++sn;
+        ++c;
         tc_fence_after();
-        uint32_t sr[KT];
+        uint32_t any = 0;
 #pragma unroll
-        for (int c = 0; c < KW; ++c) tmem_ld32(tm_s + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&sr[32 * c]));
-        tmem_wait_ld();
-        uint32_t badw[KW], any = 0;
-#pragma unroll
-        for (int x = 0; x < KW; ++x) any |= badw[x] = kbad[(tile % TR_BAD) * 4 + x];
+        for (int x = 0; x < KW; ++x) any |= kbad[(tile % TR_BAD) * KW + x];
         const bool part = k0 < lo_max || hist - k0 < KT || any;   // not every row sees all of it
-        if (CAP && part) {   // (what nobody may see has no say in how scores are capped)
-          const TRRow row = my_row();
-#pragma unroll
-          for (int w = 0; w < KW; ++w) {
-            const uint32_t vis = row.sees(a, k0 + 32 * w) & ~badw[w];
-#pragma unroll
-            for (int c = 0; c < 32; ++c)
-              if (!((vis >> c) & 1u)) sr[32 * w + c] = 0u;
-          }
-        }
-        // ---- scores
-        if constexpr (CAP) {
-          float fv[4] = {0.f, 0.f, 0.f, 0.f};   // largest |<q, K[k]>| of the tile
-#pragma unroll
-          for (int c = 0; c < KT; c += 2)
-            fv[(c >> 1) & 3] = fmax3(fv[(c >> 1) & 3], fabsf(__uint_as_float(sr[c])), fabsf(__uint_as_float(sr[c + 1])));
-          // (rows of other sequences have no say)
-          const float far = rv ? fmaxf(fmax3(fv[0], fv[1], fv[2]), fv[3]) : 0.f;
-          auto polynomial = [&](auto terms) {
-            constexpr int TERMS = decltype(terms)::value;
-            uint64_t co[TERMS];
-#pragma unroll
-            for (int i = 0; i < TERMS; ++i) {
-              const float f = TERMS == NEAR_TERMS ? a.near[i] : a.mid[i];
-              co[i] = f2_pack(f, f);
-            }
-#pragma unroll
-            for (int c = 0; c < KT; c += 2) {
-              const uint64_t x = f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
-              const uint64_t u = tr_mul(x, x);
-              uint64_t y = co[TERMS - 1];
-#pragma unroll
-              for (int i = TERMS - 2; i >= 0; --i) y = f2_fma(y, u, co[i]);
-              float s0, s1;
-              f2_unpack(tr_mul(y, x), s0, s1);
-              sr[c] = __float_as_uint(s0);
-              sr[c + 1] = __float_as_uint(s1);
-            }
-          };
-          auto within = [&](float reach) { return __all_sync(0xffffffffu, far <= reach); };
-          if (within(a.cap_near)) {
-            polynomial(std::integral_constant<int, NEAR_TERMS>{});
-          } else if (within(a.cap_mid)) {
-            polynomial(std::integral_constant<int, MID_TERMS>{});
-          } else {
-#pragma unroll
-            for (int c = 0; c < KT; ++c) sr[c] = __float_as_uint(score_log2<true>(a, __uint_as_float(sr[c])));
-          }
-        } else if (scaled) {
-#pragma unroll
-          for (int c = 0; c < KT; ++c) sr[c] = __float_as_uint(__uint_as_float(sr[c]) * a.scale_log2);
-        }
+        TRBias how = NoLoad;
         if constexpr (BIAS) {
-          const TRBias how = tr_bias(a, it, k0, KT);
-          const float* br = bias + (size_t)h * TREE_ROWS * S::PITCH;
+          how = tr_bias(a, it, k0);
           if (how != NoLoad) {
             go = tr_wait(&bias_full[h], bn & 1u, abort_flag, a);
             if (!go) break;
             ++bn;
           }
-          if (how == Elements) {
-            br += r * S::ELEMENTS;
+        }
+        // ---- scores and their maximum
+        float mx = -INFINITY;
+        uint32_t all[KT];
 #pragma unroll
-            for (int c = 0; c < KT; ++c) sr[c] = __float_as_uint(fmaf(br[c], LOG2E, __uint_as_float(sr[c])));
-          } else {
-            if (how == RowCopies) {
-              // element e of the tile's distances, s = p - (k0 + KT - 1) up: key KT - 1 - e
-              const int d0 = p - k0;   // of key 0
-              const uintptr_t src = reinterpret_cast<uintptr_t>(a.rel) + (((size_t)t * a.Hq + head) * a.E + (size_t)(d0 - KT + 1)) * (a.rel_bf16 ? 2 : 4);
-              const bool beyond = __any_sync(0xffffffffu, d0 >= a.E - 1);
-              const int c_last = d0 - (a.E - 1);   // keys up to this one are at a distance of E - 1 or more
-              const uint4* row = reinterpret_cast<const uint4*>(br + r * S::PITCH);
-              uint4 cur = row[0];
-              if (a.rel_bf16) {
-                const bool o1 = src & 2, o2 = src & 4, o4 = src & 8;
+        for (int w = 0; w < KW; ++w) tmem_ld32(tm_s + 32 * w, *reinterpret_cast<uint32_t(*)[32]>(&all[32 * w]));
+        tmem_wait_ld();
 #pragma unroll
-                for (int q = 0; q < KT / 8; ++q) {
-                  const uint4 nxt = row[q + 1];
-                  const uint32_t w[8] = {cur.x, cur.y, cur.z, cur.w, nxt.x, nxt.y, nxt.z, nxt.w};
-                  cur = nxt;
-                  uint32_t u[6], v[4];
-                  uint32_t o[7];
+        for (int w = 0; w < KW; ++w) {
+          uint32_t (&sr)[32] = *reinterpret_cast<uint32_t(*)[32]>(&all[32 * w]);
+          uint32_t vis = 0xffffffffu;
+          if (part) vis = my_row().sees(a, k0 + 32 * w) & ~kbad[(tile % TR_BAD) * KW + w];
+          if constexpr (CAP) {
+            if (part) {   // (what nobody may see has no say in how scores are capped)
 #pragma unroll
-                  for (int i = 0; i < 7; ++i) o[i] = o1 ? __funnelshift_r(w[i], w[i + 1], 16) : w[i];
-#pragma unroll
-                  for (int i = 0; i < 6; ++i) u[i] = o2 ? o[i + 1] : o[i];
-#pragma unroll
-                  for (int i = 0; i < 4; ++i) v[i] = o4 ? u[i + 2] : u[i];
-#pragma unroll
-                  for (int i = 0; i < 8; ++i) {
-                    const int c = KT - 1 - (8 * q + i);
-                    float x = __uint_as_float(i & 1 ? v[i >> 1] & 0xFFFF0000u : v[i >> 1] << 16);
-                    if (beyond) x = c <= c_last ? rc : x;
-                    sr[c] = __float_as_uint(fmaf(x, LOG2E, __uint_as_float(sr[c])));
-                  }
-                }
-              } else {
-                const bool o1 = src & 4, o2 = src & 8;
-#pragma unroll
-                for (int q = 0; q < KT / 4; ++q) {
-                  const uint4 nxt = row[q + 1];
-                  const uint32_t w[7] = {cur.x, cur.y, cur.z, cur.w, nxt.x, nxt.y, nxt.z};
-                  cur = nxt;
-                  uint32_t u[6];
-#pragma unroll
-                  for (int i = 0; i < 6; ++i) u[i] = o1 ? w[i + 1] : w[i];
-#pragma unroll
-                  for (int i = 0; i < 4; ++i) {
-                    const int c = KT - 1 - (4 * q + i);
-                    float x = __uint_as_float(o2 ? u[i + 2] : u[i]);
-                    if (beyond) x = c <= c_last ? rc : x;
-                    sr[c] = __float_as_uint(fmaf(x, LOG2E, __uint_as_float(sr[c])));
-                  }
-                }
-              }
-            } else if (a.rel) {   // all at E - 1 or beyond
-              const float x = rc * LOG2E;
-#pragma unroll
-              for (int c = 0; c < KT; ++c) sr[c] = __float_as_uint(__uint_as_float(sr[c]) + x);
+              for (int c = 0; c < 32; ++c)
+                if (!((vis >> c) & 1u)) sr[c] = 0u;
             }
-            if (a.slopes) {
-              const float slope2 = __ldg(a.slopes + head) * LOG2E, d0 = (float)(p - k0);
+            float fv[4] = {0.f, 0.f, 0.f, 0.f};   // largest |<q, K[k]>|
 #pragma unroll
-              for (int c = 0; c < KT; ++c) sr[c] = __float_as_uint(fmaf(-slope2, d0 - (float)c, __uint_as_float(sr[c])));
+            for (int c = 0; c < 32; c += 2)
+              fv[(c >> 1) & 3] = fmax3(fv[(c >> 1) & 3], fabsf(__uint_as_float(sr[c])), fabsf(__uint_as_float(sr[c + 1])));
+            // (rows of other sequences have no say)
+            const float far = rv ? fmaxf(fmax3(fv[0], fv[1], fv[2]), fv[3]) : 0.f;
+            if (__all_sync(0xffffffffu, far <= a.cap_near)) {
+              uint64_t co[NEAR_TERMS];
+#pragma unroll
+              for (int i = 0; i < NEAR_TERMS; ++i) co[i] = f2_pack(a.near[i], a.near[i]);
+#pragma unroll
+              for (int c = 0; c < 32; c += 2) {
+                const uint64_t x = f2_pack(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
+                const uint64_t u = tr_mul(x, x);
+                uint64_t y = co[NEAR_TERMS - 1];
+#pragma unroll
+                for (int i = NEAR_TERMS - 2; i >= 0; --i) y = f2_fma(y, u, co[i]);
+                float s0, s1;
+                f2_unpack(tr_mul(y, x), s0, s1);
+                sr[c] = __float_as_uint(s0);
+                sr[c + 1] = __float_as_uint(s1);
+              }
+            } else {
+#pragma unroll
+              for (int c = 0; c < 32; ++c) sr[c] = __float_as_uint(score_log2<true>(a, __uint_as_float(sr[c])));
+            }
+          } else if (scaled) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) sr[c] = __float_as_uint(__uint_as_float(sr[c]) * a.scale_log2);
+          }
+          if constexpr (BIAS) {
+            const float* br = bias + (size_t)h * TREE_ROWS * S::PITCH;
+            if (how == Elements) {
+              br += r * S::ELEMENTS + 32 * w;
+#pragma unroll
+              for (int c = 0; c < 32; ++c) sr[c] = __float_as_uint(fmaf(br[c], LOG2E, __uint_as_float(sr[c])));
+            } else {
+              if (how == RowCopies) {
+                // element e of the tile's distances, s = p - (k0 + KT - 1) up: key KT - 1 - e
+                const int d0 = p - k0;   // of key 0
+                const uintptr_t src = reinterpret_cast<uintptr_t>(a.rel) +
+                                      (((size_t)t * a.Hq + head) * a.E + (size_t)(d0 - KT + 1)) * (a.rel_bf16 ? 2 : 4);
+                const bool beyond = __any_sync(0xffffffffu, d0 >= a.E - 1);
+                const int c_last = d0 - (a.E - 1) - 32 * w;   // keys up to this one are at a distance of E - 1 or more
+                const uint4* row = reinterpret_cast<const uint4*>(br + r * S::PITCH) + (KW - 1 - w) * (a.rel_bf16 ? 4 : 8);
+                uint4 cur = row[0];
+                if (a.rel_bf16) {
+                  const bool o1 = src & 2, o2 = src & 4, o4 = src & 8;
+#pragma unroll
+                  for (int q = 0; q < 4; ++q) {
+                    const uint4 nxt = row[q + 1];
+                    const uint32_t e[8] = {cur.x, cur.y, cur.z, cur.w, nxt.x, nxt.y, nxt.z, nxt.w};
+                    cur = nxt;
+                    uint32_t o[7], u[6], v[4];
+#pragma unroll
+                    for (int i = 0; i < 7; ++i) o[i] = o1 ? __funnelshift_r(e[i], e[i + 1], 16) : e[i];
+#pragma unroll
+                    for (int i = 0; i < 6; ++i) u[i] = o2 ? o[i + 1] : o[i];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v[i] = o4 ? u[i + 2] : u[i];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                      const int c = 31 - (8 * q + i);
+                      float x = __uint_as_float(i & 1 ? v[i >> 1] & 0xFFFF0000u : v[i >> 1] << 16);
+                      if (beyond) x = c <= c_last ? rc : x;
+                      sr[c] = __float_as_uint(fmaf(x, LOG2E, __uint_as_float(sr[c])));
+                    }
+                  }
+                } else {
+                  const bool o1 = src & 4, o2 = src & 8;
+#pragma unroll
+                  for (int q = 0; q < 8; ++q) {
+                    const uint4 nxt = row[q + 1];
+                    const uint32_t e[7] = {cur.x, cur.y, cur.z, cur.w, nxt.x, nxt.y, nxt.z};
+                    cur = nxt;
+                    uint32_t u[6];
+#pragma unroll
+                    for (int i = 0; i < 6; ++i) u[i] = o1 ? e[i + 1] : e[i];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                      const int c = 31 - (4 * q + i);
+                      float x = __uint_as_float(o2 ? u[i + 2] : u[i]);
+                      if (beyond) x = c <= c_last ? rc : x;
+                      sr[c] = __float_as_uint(fmaf(x, LOG2E, __uint_as_float(sr[c])));
+                    }
+                  }
+                }
+              } else if (a.rel) {   // all at E - 1 or beyond
+                const float x = rc * LOG2E;
+#pragma unroll
+                for (int c = 0; c < 32; ++c) sr[c] = __float_as_uint(__uint_as_float(sr[c]) + x);
+              }
+              if (a.slopes) {
+                const float slope2 = __ldg(a.slopes + head) * LOG2E, d0 = (float)(p - k0 - 32 * w);
+#pragma unroll
+                for (int c = 0; c < 32; ++c) sr[c] = __float_as_uint(fmaf(-slope2, d0 - (float)c, __uint_as_float(sr[c])));
+              }
             }
           }
+          if (part) {   // keys that this row does not see
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (!((vis >> c) & 1u)) sr[c] = 0xff800000u;   // -infinity
+          }
+          float mv[2] = {mx, -INFINITY};
+#pragma unroll
+          for (int c = 0; c < 32; c += 2)
+            mv[(c >> 1) & 1] = fmax3(mv[(c >> 1) & 1], __uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
+          mx = fmaxf(mv[0], mv[1]);
+        }
+        if constexpr (BIAS) {
           if (how != NoLoad) {
             __syncwarp();
             if (lane == 0) mbar_arrive(&bias_empty[h]);
           }
         }
-        // ---- keys that this row does not see
-        if (part) {
-          const TRRow row = my_row();
-#pragma unroll
-          for (int w = 0; w < KW; ++w) {
-            const uint32_t vis = row.sees(a, k0 + 32 * w) & ~badw[w];
-#pragma unroll
-            for (int c = 0; c < 32; ++c)
-              if (!((vis >> c) & 1u)) sr[32 * w + c] = 0xff800000u;   // -infinity
-          }
-        }
         // ---- running maximum, moved only when it grows by more than 2^8
-        float mxv[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int c = 0; c < KT; c += 2)
-          mxv[(c >> 1) & 3] = fmax3(mxv[(c >> 1) & 3], __uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
-        const float mx = fmaxf(fmaxf(mxv[0], mxv[1]), fmaxf(mxv[2], mxv[3])) * mul;
+        mx *= mul;
         const bool mine = mx > m + TR_RESCALE_LOG2;
         if (__any_sync(0xffffffffu, mine)) {
-          if (j > 0) {   // every earlier product into O_h is done: s_full came after it
+          if (j > 0) {   // (s_full came after all products into O_h but the last one)
+            go = tr_wait(&o_done[2 * h + (buf ^ 1u)], ((c - 2) >> 1) & 1u, abort_flag, a);
+            if (!go) break;
+            tc_fence_after();
             const float fr = mine ? fast_exp2(m - mx) : 1.f;
 #pragma unroll 1
             for (int c2 = 0; c2 < D / 16; ++c2) {
@@ -1074,18 +1076,18 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
         const uint64_t mul2 = f2_pack(mul, mul), nm2 = f2_pack(nm, nm);
         uint64_t ls2[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
-        for (int quarter = 0; quarter < KW; ++quarter) {
+        for (int w = 0; w < KW; ++w) {
+          uint32_t (&sr)[32] = *reinterpret_cast<uint32_t(*)[32]>(&all[32 * w]);
           uint32_t pk[16];
 #pragma unroll
           for (int c = 0; c < 16; ++c) {
-            const int e = 32 * quarter + 2 * c;
             float t0, t1;
-            f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[e]), __uint_as_float(sr[e + 1])), mul2, nm2), t0, t1);
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[2 * c]), __uint_as_float(sr[2 * c + 1])), mul2, nm2), t0, t1);
             const float p0 = fast_exp2(t0), p1 = fast_exp2(t1);
             ls2[c & 3] = f2_add(ls2[c & 3], f2_pack(p0, p1));
             pk[c] = pack_bf16(p0, p1);
           }
-          tmem_st16(tm_s + 16 * quarter, pk);
+          tmem_st16(tm_s + 16 * w, pk);
         }
         {
           float x0, x1, y0, y1;
@@ -1096,13 +1098,14 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[h]);
+        if (lane == 0) mbar_arrive(&p_full[2 * h + buf]);
       }
       if (!go) break;
       g += item.tiles();
+      c_other += pair ? nt : item.part[h ^ 1].nt;
       // ---- epilogue
       if (nt > 0) {
-        go = tr_wait(&o_full[h], (on >> h) & 1u, abort_flag, a);
+        go = tr_wait(&o_done[2 * h + ((c - 1) & 1u)], ((c - 1) >> 1) & 1u, abort_flag, a);
         if (!go) break;
       }
       const bool both = merge && item.part[1].nt > 0;   // both chains hold a part of this row
@@ -1115,7 +1118,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
         go = tr_wait(ml_bar, mn & 1u, abort_flag, a);
         if (!go) break;
         ++mn;
-        if (h == 1 || both) go = tr_wait(&o_full[h ^ 1], (on >> (h ^ 1)) & 1u, abort_flag, a);   // (its warps have waited for it)
+        if (h == 1 || both) go = tr_wait(&o_done[2 * (h ^ 1) + ((c_other - 1) & 1u)], ((c_other - 1) >> 1) & 1u, abort_flag, a);   // (its warps have waited for it)
         if (!go) break;
         const float2 x0 = ml[r], x1 = both ? ml[TREE_ROWS + r] : make_float2(-INFINITY, 0.f);
         M = fmaxf(x0.x, x1.x);
@@ -1123,7 +1126,6 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
         f1 = x1.x == -INFINITY ? 0.f : fast_exp2(x1.x - M);
         l = (x0.y == 0.f ? 0.f : x0.y * f0) + (x1.y == 0.f ? 0.f : x1.y * f1);
       }
-      on ^= merge && !both ? 1u : 3u;
       tc_fence_after();
       const volatile int* ps = poison + 4 * (k % TR_ITEMS) + (merge || pair ? 0 : 2 * h);
       const int pfirst = both ? min(ps[0], ps[2]) : ps[0], plast = both ? max(ps[1], ps[3]) : ps[1];
@@ -1272,14 +1274,6 @@ cudaError_t launch_t(const MaskedMaps& m, const TreeArgs& a, int grid, cudaStrea
   static std::atomic<unsigned long long> opted{0};
   cudaError_t e = smem_opt_in_once(tree_kernel<D, CAP, BIAS>, (int)TRSmem<D, BIAS>::alloc, opted);
   if (e != cudaSuccess) return e;
-  // The softmax warps' extra registers come out of what the block is launched with: a build with
-  // fewer would wait for them without end.
-  static const bool enough = [] {
-    cudaFuncAttributes at;
-    return BIAS || (cudaFuncGetAttributes(&at, tree_kernel<D, CAP, BIAS>) == cudaSuccess &&
-                    at.numRegs * S::THREADS >= 128 * (2 * TR_REGS_SOFTMAX + TR_REGS_REST));
-  }();
-  if (!enough) return cudaErrorInvalidConfiguration;
   tree_kernel<D, CAP, BIAS><<<grid, S::THREADS, TRSmem<D, BIAS>::alloc, stream>>>(m.k, m.v, m.q, a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
@@ -1296,14 +1290,12 @@ cudaError_t launch_d(const MaskedMaps& m, const TreeArgs& a, int grid, cudaStrea
 
 }  // namespace
 
-int tree_tile_keys(bool bias) { return bias ? TRShape<128, true>::KT : TRShape<128, false>::KT; }
-
 cudaError_t launch_tree(const MaskedMaps& m, const TreeArgs& a, int head_dim, cudaStream_t stream) {
   int dev = 0;
   const int sms = current_device_sms(&dev);
   if (sms <= 0) return cudaErrorInvalidDevice;
   const long long items = (a.T / (2ll * a.tok_per_tile) + a.B) * a.Hkv * a.head_chunks;
-  const long long tiles = ((long long)a.max_pages << a.log2_page) / tree_tile_keys(a.rel || a.slopes) + 1;
+  const long long tiles = ((long long)a.max_pages << a.log2_page) / KT + 1;
   const int grid = (int)std::min<long long>(std::min(sms, TREE_MAX_CTAS), items * tiles);
   return head_dim == 128 ? launch_d<128>(m, a, grid, stream) : launch_d<64>(m, a, grid, stream);
 }

@@ -251,3 +251,18 @@ def test_a_bias_at_any_address(cuda_device, odd):
         step.rel = held[odd:].view_as(step.rel)
         got = step.call()
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("heads,n,history,window", [
+    ((8, 8), [5] * 40, list(range(100, 900, 20)), -1), ((16, 16), [7] * 64, [600] * 64, 512), ((64, 8), [9, 30, 4] * 10, [700, 90, 3000] * 10, 300),
+    ((8, 2), [3] * 100, list(range(100)), -1), ((64, 8), [16] * 32, [2000 + 97 * i for i in range(32)], -1)])
+@pytest.mark.parametrize("bias", [None, F32])
+def test_many_short_pieces(cuda_device, heads, n, history, window, bias):
+    """Runs of several items of many lengths on every SM: pieces side by side, cut ones, pieces of one tile."""
+    step = Step(heads, 128, 64, n, history, 24, cuda_device, window=window, extent=200, bias=bias)
+    ws = binding.alloc_tree_workspace(step.params, cuda_device)
+    ref = step.reference()
+    for _ in range(3):
+        out, lse, _ = step.call(workspace=ws)
+        assert binding.inkling_attn_read_device_error(ws) == 0
+        check(out, lse, ref, "many pieces")
