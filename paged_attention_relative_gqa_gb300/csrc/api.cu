@@ -605,6 +605,7 @@ size_t table_bytes(const ink_attn_params_t* p) { return (size_t)p->num_seqs * p-
 // Scale and cap of the scores, for the masked and the tree kernels.
 template <class Args>
 void fill_scores(Args& a, float sm_scale, float softcap) {
+  a.sm_scale = sm_scale;
   a.softcap = softcap;
   a.scale_log2 = sm_scale * 1.4426950408889634f;
   a.cap_log2 = softcap * 1.4426950408889634f;
@@ -690,7 +691,6 @@ ink_status_t masked_impl(const ink_attn_params_t* params, const ink_attn_mask_t*
   a.max_pages = params->max_pages_per_seq;
   a.num_pages = params->num_pages;
   a.W = params->window;
-  a.sm_scale = params->sm_scale;
   a.wait_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
   fill_scores(a, params->sm_scale, mk.softcap);
   fill_rows(a);

@@ -293,7 +293,7 @@ struct TreeArgs {
   int B, T, Hq, Hkv, G, log2_page, max_pages, num_pages, W, E, words;
   int rel_bf16;
   int rel_rows;                // rel begins and ends on 16-byte boundaries: its rows can be copied in bulk
-  float softcap;
+  float sm_scale, softcap;
   float scale_log2;            // sm_scale * log2(e)
   float cap_k1, cap_log2, cap_inv, cap_near, near[NEAR_TERMS], cap_mid, mid[MID_TERMS];   // as in MaskedArgs
   unsigned long long wait_ns;  // limit of one pipeline wait (the drain waits keep 2 s)

@@ -55,20 +55,29 @@ constexpr float TR_RESCALE_LOG2 = 8.f;
 
 constexpr int KT = TILE_KEYS, KW = KT / 32;   // keys of a tile, words of 32
 
-template <int D, bool BIAS>
+template <int D, bool CAP, bool BIAS>
 struct TRShape {
   static constexpr int CB = D / 64;
   static constexpr int SUB = KT * 128;             // one 64-channel block of a K or V tile
   static constexpr int TILE = CB * SUB;
   static constexpr int QSUB = TREE_ROWS * 128;
   static constexpr int QTILE = CB * QSUB;
-  static constexpr int NS = D == 128 && BIAS ? 5 : 10;   // ring slots, K and V tiles in turn
-  static constexpr bool TWO = NS % 2 == 0;         // K and V have slots, and a producer, of their own
-  static constexpr int V_WARP = BIAS ? 15 : 13;    // the one of V
-  static constexpr int THREADS = (V_WARP + TWO) * 32;
+  // Ring slots, K and V tiles in turn: each kind has slots, and a producer, of its own.
+  static constexpr int NS = D == 64 ? 16 : BIAS ? 8 : 10;
+  static constexpr int V_WARP = BIAS ? 15 : 13;    // the producer of V
+  static constexpr int THREADS = (V_WARP + 1) * 32;
+  // S that a chain has at a time: the second one waits for no softmax.  A bias takes the room of Q in shared memory, and Q that of
+  // the second S in tensor memory.
+  static constexpr int AHEAD = BIAS ? 1 : 2;
+  // Scores 32 at a time, through tensor memory between their maximum and their exponentials, where there is more to do for a
+  // score: straight-line code for all 64 is then longer than what the warps' instructions come from at once (two in three issue
+  // slots went by without one).
+  static constexpr bool ROLL = CAP || BIAS;
+  static constexpr uint32_t TQ = 128;              // with a bias: S_h at 64 h, Q_h at TQ + 64 h
   static constexpr int PITCH = KT + 4;             // words of a bias row: KT values from a 16-byte boundary on
   static constexpr int ELEMENTS = KT + 1;          // the same of one filled element by element
-  static constexpr uint32_t TO = 256;              // S_h at 128 h, two of them; O_h at TO + D h
+  static constexpr uint32_t TO = 256;              // without: S_h at 128 h, two of them; O_h at TO + D h
+  static constexpr uint32_t TS = BIAS ? 64 : 128;
 };
 
 // A run of key tiles of one or two row tiles.
@@ -96,11 +105,11 @@ struct TRItem {
   __device__ __forceinline__ int longest() const { return mode == Pair ? part[0].nt : max(part[0].nt, part[1].nt); }
 };
 
-template <int D, bool BIAS>
+template <int D, bool CAP, bool BIAS>
 struct TRSmem {
-  using S = TRShape<D, BIAS>;
+  using S = TRShape<D, CAP, BIAS>;
   static constexpr size_t q = 0;
-  static constexpr size_t ring = 2 * (size_t)S::QTILE;
+  static constexpr size_t ring = BIAS ? 0 : 2 * (size_t)S::QTILE;
   static constexpr size_t bias = ring + (size_t)S::NS * S::TILE;
   static constexpr size_t bars = bias + (BIAS ? 2 * (size_t)TREE_ROWS * S::PITCH * 4 : 0);
   // k_full[TILES], v_full[TILES], v_ok[TILES], empty[NS], s_full[2][2], p_full[2][2], o_done[2][2], q_full[2], q_empty[2],
@@ -321,11 +330,11 @@ __device__ __forceinline__ float tr_weigh(float w, float x) { return fabsf(x) <=
 
 // CAP: capped scores, by a polynomial where all scores of a warp's tile allow it (as in the masked prefill).
 template <int D, bool CAP, bool BIAS>
-__global__ void __launch_bounds__(TRShape<D, BIAS>::THREADS, 1)
+__global__ void __launch_bounds__(TRShape<D, CAP, BIAS>::THREADS, 1)
 tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
             const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ TreeArgs a) {
-  using S = TRShape<D, BIAS>;
-  using L_ = TRSmem<D, BIAS>;
+  using S = TRShape<D, CAP, BIAS>;
+  using L_ = TRSmem<D, CAP, BIAS>;
   constexpr int NS = S::NS;
 
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -377,7 +386,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
       mbar_init(&p_full[2 * x + 1], 4);
       mbar_init(&o_done[2 * x], 1);
       mbar_init(&o_done[2 * x + 1], 1);
-      mbar_init(&q_full[x], 1);
+      mbar_init(&q_full[x], BIAS ? 4 : 1);
       mbar_init(&q_empty[x], 2);
       mbar_init(&drain[x], 1);
       if constexpr (BIAS) {
@@ -387,7 +396,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
     }
     for (int x = 0; x < TR_ITEMS; ++x) {
       mbar_init(&item_full[x], 1);
-      mbar_init(&item_empty[x], 12 + S::TWO + (BIAS ? 2 : 0));   // producers, 2 MMA, V check, 8 softmax warps, bias warps
+      mbar_init(&item_empty[x], 13 + (BIAS ? 2 : 0));   // producers, 2 MMA, V check, 8 softmax warps, bias warps
     }
     mbar_init(o_free, 8);
     mbar_init(ml_bar, 8);
@@ -397,9 +406,11 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
   TRWalk walk;
   if (warp == 10) walk.begin(a, lane);   // (its loads are on their way while the rest is set up)
   // rows of a Q tile past the last (token, head) pair stay zero
-  for (int x = tid; x < 2 * S::QTILE / 16; x += S::THREADS)
-    *reinterpret_cast<uint4*>(smem + L_::q + (size_t)x * 16) = make_uint4(0u, 0u, 0u, 0u);
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  if constexpr (!BIAS) {
+    for (int x = tid; x < 2 * S::QTILE / 16; x += S::THREADS)
+      *reinterpret_cast<uint4*>(smem + L_::q + (size_t)x * 16) = make_uint4(0u, 0u, 0u, 0u);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
   if (warp == 9) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
                  "n"(512));
@@ -420,7 +431,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
   };
 
   if (warp >= 8) {
-    if (warp == 8 || (S::TWO && warp == S::V_WARP)) {
+    if (warp == 8 || warp == S::V_WARP) {
       // ---------------------------------------------------------------- K and V producer
       if (lane == 0) {
         prefetch_tensormap(&tmK);
@@ -428,10 +439,10 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
       }
       const int seg = min(P, KT), nseg = KT / seg;
       const bool wide = P >= KT;            // a tile lies in one page: one box a tensor
-      const int kv0 = warp != 8, kv1 = S::TWO ? kv0 : 1;   // K, V or both
-      int x = 0, st = kv0;                  // tiles issued, slot of the next fill
+      const int kv = warp != 8;             // K or V
+      int x = 0, st = kv;                   // tiles issued, slot of the next one
       uint32_t round = 0;                   // times the slots have been gone through
-      bool go = true, k_only = false;       // the last fill was a K without its V
+      bool go = true;
       for (int k = 0; go && next_item(k); ++k) {
         const TRItem& item = items[k % TR_ITEMS];
         const int parts = item.mode == Pair ? 1 : 2, longest = item.longest(), kstep = item.step() * KT;
@@ -466,52 +477,44 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
           const uint32_t bmask = __ballot_sync(0xffffffffu, bad_seg);
           const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, load)) * (uint32_t)(seg * D * 2);
           const int row = load ? ((page * a.Hkv + kvh[h]) << a.log2_page) + (ks & (P - 1)) : 0;
-#pragma unroll
-          for (int y = 0; y < (S::TWO ? 1 : 2); ++y) {
-            const int kv = S::TWO ? kv0 : y;
-            if (go && round > 0) go = tr_wait(&empty[st], (round - 1) & 1u, abort_flag, a);
-            if (!go) break;
-            uint64_t* full = (kv ? v_full : k_full) + x % TR_TILES;
-            uint8_t* dst = smem + L_::ring + (size_t)st * S::TILE + (wide ? 0 : lane * seg * 128);
-            if (lane == 0) {
-              if (kv == 0) {   // keys of this tile whose page is outside the pool
-                uint64_t bad = 0;
-                for (uint32_t mm = bmask; mm; mm &= mm - 1) bad |= (~0ull >> (64 - seg)) << ((__ffs(mm) - 1) * seg);
-                *reinterpret_cast<uint64_t*>(kbad + x % TR_BAD * KW) = bad;
-                if (bmask) record_error(a.err, INK_DEVERR_PAGE_OUT_OF_RANGE);
-              }
-              mbar_arrive_expect_tx(full, bytes);
-              if (wide && load) tma_load_3d(dst, kv ? &tmV : &tmK, 0, row, 0, full);
+          if (round > 0) go = tr_wait(&empty[st], (round - 1) & 1u, abort_flag, a);
+          if (!go) continue;
+          uint64_t* full = (kv ? v_full : k_full) + x % TR_TILES;
+          uint8_t* dst = smem + L_::ring + (size_t)st * S::TILE + (wide ? 0 : lane * seg * 128);
+          if (lane == 0) {
+            if (kv == 0) {   // keys of this tile whose page is outside the pool
+              uint64_t bad = 0;
+              for (uint32_t mm = bmask; mm; mm &= mm - 1) bad |= (~0ull >> (64 - seg)) << ((__ffs(mm) - 1) * seg);
+              *reinterpret_cast<uint64_t*>(kbad + x % TR_BAD * KW) = bad;
+              if (bmask) record_error(a.err, INK_DEVERR_PAGE_OUT_OF_RANGE);
             }
-            if (!wide && load) {
-#pragma unroll
-              for (int cb = 0; cb < S::CB; ++cb)
-                tma_load_2d(dst + cb * S::SUB, kv ? &tmV : &tmK, cb * 64, row, full);
-            }
-            st += S::TWO ? 2 : 1;
-            if (st >= NS) {
-              st -= NS;
-              ++round;
-            }
-            k_only = kv != kv1;
-            if (kv == kv1) ++x;
+            mbar_arrive_expect_tx(full, bytes);
+            if (wide && load) tma_load_3d(dst, kv ? &tmV : &tmK, 0, row, 0, full);
           }
+          if (!wide && load) {
+#pragma unroll
+            for (int cb = 0; cb < S::CB; ++cb)
+              tma_load_2d(dst + cb * S::SUB, kv ? &tmV : &tmK, cb * 64, row, full);
+          }
+          st += 2;
+          if (st >= NS) {
+            st = kv;
+            ++round;
+          }
+          ++x;
           k0[h] += kstep;
         }
       }
-      if (lane == 0) {
-        if (kv0 == 0) pp_drain_ring(k_full, TR_TILES, x + (!S::TWO && k_only), a.err);
-        if (kv1 == 1) pp_drain_ring(v_full, TR_TILES, x, a.err);
-      }
+      if (lane == 0) pp_drain_ring(kv ? v_full : k_full, TR_TILES, x, a.err);
     } else if (warp == 9 || warp == 12) {
       // ---------------------------------------------------------------- MMA issue of one chain
       constexpr uint32_t IDESC_S = umma_idesc_bf16(128, KT, false, false);
       constexpr uint32_t IDESC_PV = umma_idesc_bf16(128, D, false, true);
       const int h = warp == 12;
       const uint32_t qaddr = smem_u32(smem + L_::q), raddr = smem_u32(smem + L_::ring);
-      const uint32_t tm_s = tmem + 128u * h, tm_o = tmem + S::TO + (uint32_t)(D * h);
+      const uint32_t tm_s = tmem + S::TS * h, tm_o = tmem + S::TO + (uint32_t)(D * h), tm_q = tmem + S::TQ + 64u * h;
       int g = 0;                       // tiles of earlier items: K of tile x is fill 2 x, V fill 2 x + 1
-      uint32_t qn = 0;                 // a parity bit per Q tile
+      uint32_t qn = 0;                 // a parity bit per Q tile (with a bias, of the only one)
       uint32_t sc = 0, pc = 0;         // S and P V products so far: the two S take turns
       bool go = true;
       auto wait_tile = [&](uint64_t* bars, int x) {
@@ -538,25 +541,38 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
           const uint64_t kd = umma_desc_sw128(raddr + st * S::TILE, 16, 1024);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
-            umma_ss_warp(tm_s + KT * (sc & 1u), qd + (uint64_t)(((kk >> 2) * S::QSUB + (kk & 3) * 32) >> 4),
-                         kd + (uint64_t)(((kk >> 2) * S::SUB + (kk & 3) * 32) >> 4), IDESC_S, kk > 0 ? 1u : 0u);
+            if constexpr (BIAS)
+              umma_ts_warp(tm_s, tm_q + kk * 8, kd + (uint64_t)(((kk >> 2) * S::SUB + (kk & 3) * 32) >> 4), IDESC_S,
+                           kk > 0 ? 1u : 0u);
+            else
+              umma_ss_warp(tm_s + KT * (sc & 1u), qd + (uint64_t)(((kk >> 2) * S::QSUB + (kk & 3) * 32) >> 4),
+                           kd + (uint64_t)(((kk >> 2) * S::SUB + (kk & 3) * 32) >> 4), IDESC_S, kk > 0 ? 1u : 0u);
           umma_commit_warp(&s_full[2 * h + (sc & 1u)]);
           ++sc;
           free_slot(&empty[st], pair);
-          if (last) free_slot(&q_empty[qs], split);
+          if (!BIAS && last) free_slot(&q_empty[qs], split);
           __syncwarp();
         };
-        // (Every phase is waited for, of the other chain's Q tile and by a chain without a tile too: a parity tells a phase from
-        // its neighbours only.)
-        go = tr_wait(&q_full[qs], (qn >> qs) & 1u, abort_flag, a);
-        if (go && !split) go = tr_wait(&q_full[h ^ 1], (qn >> (h ^ 1)) & 1u, abort_flag, a);
+        if constexpr (BIAS) {
+          if (nt > 0) {                // (its warps have brought the rows)
+            go = tr_wait(&q_full[h], qn, abort_flag, a);
+            qn ^= 1u;
+          }
+        } else {
+          // (Every phase is waited for, of the other chain's Q tile and by a chain without a tile too: a parity tells a phase from
+          // its neighbours only.)
+          go = tr_wait(&q_full[qs], (qn >> qs) & 1u, abort_flag, a);
+          if (go && !split) go = tr_wait(&q_full[h ^ 1], (qn >> (h ^ 1)) & 1u, abort_flag, a);
+          qn ^= split ? 1u << qs : 3u;
+        }
         if (!go) break;
-        if (nt == 0) {                 // (the only tile of a Split item is the other chain's)
+        if (nt > 0) {
+          tc_fence_after();
+          issue_s(0);
+          if (S::AHEAD == 2 && go && nt > 1) issue_s(1);
+        } else if (!BIAS) {            // (the only tile of a Split item is the other chain's)
           if (lane == 0) mbar_arrive(&q_empty[qs]);
           __syncwarp();
-        } else {
-          issue_s(0);
-          if (go && nt > 1) issue_s(1);
         }
         // both O of a Split item have been read
         if (go && merged) go = tr_wait(o_free, (merges - 1) & 1u, abort_flag, a);
@@ -570,14 +586,13 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
           const uint64_t vd = umma_desc_sw128(raddr + st * S::TILE, S::SUB, 1024);
 #pragma unroll
           for (int ks = 0; ks < KT / 16; ++ks)
-            umma_ts_warp(tm_o, tm_s + KT * (pc & 1u) + ks * 8, vd + (uint64_t)((ks * 16 * 128) >> 4), IDESC_PV, (j > 0 || ks > 0) ? 1u : 0u);
+            umma_ts_warp(tm_o, tm_s + (BIAS ? 0 : KT * (pc & 1u)) + ks * 8, vd + (uint64_t)((ks * 16 * 128) >> 4), IDESC_PV, (j > 0 || ks > 0) ? 1u : 0u);
           umma_commit_warp(&o_done[2 * h + (pc & 1u)]);
           ++pc;
           free_slot(&empty[st], pair);
           __syncwarp();
-          if (j + 2 < nt) issue_s(j + 2);   // over the P just read
+          if (j + S::AHEAD < nt) issue_s(j + S::AHEAD);   // (with two: over the P just read)
         }
-        qn ^= split ? 1u << qs : 3u;
         merged = split;
         merges += split;
         g += all;
@@ -655,7 +670,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
         }
         __syncwarp();
         bool go = true;
-        for (int x = 0; x < (it.mode == Split ? 1 : 2) && go; ++x) {
+        for (int x = 0; !BIAS && x < (it.mode == Split ? 1 : 2) && go; ++x) {
           const int s = it.mode == Split ? qs : x;
           if ((loaded >> s) & 1u) go = tr_wait(&q_empty[s], ((qn >> s) & 1u) ^ 1u, abort_flag, a);
           if (!go) break;
@@ -691,7 +706,9 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
           if (j >= it.nt) continue;
           const int hist = min(it.H, it.hi), kt = it.kt0 + j * step;
           const int st = (2 * g + 1) % NS;
-          go = tr_wait(&v_full[g % TR_TILES], (uint32_t)(g / TR_TILES) & 1u, abort_flag, a);
+          // (what cannot be read comes with K)
+          go = tr_wait(&k_full[g % TR_TILES], (uint32_t)(g / TR_TILES) & 1u, abort_flag, a) &&
+               tr_wait(&v_full[g % TR_TILES], (uint32_t)(g / TR_TILES) & 1u, abort_flag, a);
           if (!go) break;
           const int k0 = kt * KT;
           const uint32_t* badw = kbad + (g % TR_BAD) * KW;
@@ -811,10 +828,10 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
           auto fill = [&](auto load) {
             int i = 0, hd = 0;
 #pragma unroll 1
-            for (int r = 0; r < rows; r += 16) {
-              float v[16][2], far[16][2], slope[16];
+            for (int r = 0; r < rows; r += 8) {
+              float v[8][2], far[8][2], slope[8];
 #pragma unroll
-              for (int y = 0; y < 16; ++y) {
+              for (int y = 0; y < 8; ++y) {
                 const int ic = min(i, 127), p0 = __shfl_sync(0xffffffffu, ic & 32 ? pt[1] : pt[0], ic & 31);
                 const int p1 = __shfl_sync(0xffffffffu, ic & 32 ? pt[3] : pt[2], ic & 31), p = ic & 64 ? p1 : p0;
                 const int head = it.h0 + min(hd, it.gh - 1);
@@ -832,7 +849,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
                 }
               }
 #pragma unroll
-              for (int y = 0; y < 16; ++y) {
+              for (int y = 0; y < 8; ++y) {
                 buf[(r + y) * S::ELEMENTS + lane] = fmaf(-slope[y], far[y][0], v[y][0]);
                 buf[(r + y) * S::ELEMENTS + 32 + lane] = fmaf(-slope[y], far[y][1], v[y][1]);
               }
@@ -853,7 +870,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
     // ------------------------------------------------------------------ softmax
     const int h = warp >> 2, r = tid & 127;
     const uint32_t tlane = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t tm_chain = tlane + 128u * h, tm_o = tlane + S::TO;
+    const uint32_t tm_chain = tlane + S::TS * h, tm_o = tlane + S::TO;
     const int my_i = r / a.heads_per_tile, my_g = r - my_i * a.heads_per_tile;
     __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out);
 
@@ -870,7 +887,9 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
     }
 
     const bool scaled = CAP || BIAS || !(a.scale_log2 > 0.f);
-    const float mul = scaled ? 1.f : a.scale_log2;
+    // With a bias scores are kept in natural units until the exponent: what is added needs no factor.
+    const float mul = BIAS ? LOG2E : scaled ? 1.f : a.scale_log2;
+    const float pre = CAP ? LN2 : a.sm_scale;   // of the score to which a bias is added
     uint32_t c = 0, c_other = 0, bn = 0, mn = 0;   // tiles of this chain and of the other one so far
     int g = 0;
     bool go = true;
@@ -885,20 +904,39 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
       const int p = max(__ldg(a.positions + t), it.H);
       const uint32_t w0 = __ldg(a.ancestors + (size_t)t * a.words);
       auto my_row = [&]() { return tr_row(a, it, t, p, w0, rv); };
-      float rc = 0.f;   // the row's last value
+      float rc = 0.f, slope = 0.f;   // the row's last value and its slope
       if constexpr (BIAS) {
+        if (a.slopes) slope = __ldg(a.slopes + head);
         if (a.rel) {
           const size_t x = ((size_t)t * a.Hq + head + 1) * a.E - 1;
           rc = a.rel_bf16 ? __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t*>(a.rel) + x) << 16)
                           : __ldg(static_cast<const float*>(a.rel) + x);
         }
       }
+      const size_t orow = (size_t)t * a.Hq + head;
+      if (BIAS && nt > 0) {   // Q straight into tensor memory, a row a thread (every product with the one before is done)
+#pragma unroll 1
+        for (int c2 = 0; c2 < D / 64; ++c2) {
+          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + orow * D) + 8 * c2;
+          uint32_t qv[32];
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            const uint4 v = rv ? __ldg(src + x) : make_uint4(0u, 0u, 0u, 0u);
+            qv[4 * x] = v.x; qv[4 * x + 1] = v.y; qv[4 * x + 2] = v.z; qv[4 * x + 3] = v.w;
+          }
+          tmem_st32(tlane + S::TQ + 64u * h + 32 * c2, qv);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_full[h]);
+      }
       const int beside = item.beside(h), kstep = item.step() * KT, lo_max = it.lo_max, hist = min(it.H, it.hi);
       int k0 = it.kt0 * KT;
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < nt; ++j, k0 += kstep) {
         const int tile = g + j + min(j + h, beside);
-        const uint32_t buf = c & 1u, tm_s = tm_chain + KT * buf;
+        const uint32_t buf = c & 1u, tm_s = tm_chain + (BIAS ? 0 : KT * buf);
         go = tr_wait(&s_full[2 * h + buf], (c >> 1) & 1u, abort_flag, a);
         if (!go) break;
         ++c;
@@ -918,13 +956,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
         }
         // ---- scores and their maximum
         float mx = -INFINITY;
-        uint32_t all[KT];
-#pragma unroll
-        for (int w = 0; w < KW; ++w) tmem_ld32(tm_s + 32 * w, *reinterpret_cast<uint32_t(*)[32]>(&all[32 * w]));
-        tmem_wait_ld();
-#pragma unroll
-        for (int w = 0; w < KW; ++w) {
-          uint32_t (&sr)[32] = *reinterpret_cast<uint32_t(*)[32]>(&all[32 * w]);
+        auto score = [&](int w, uint32_t (&sr)[32]) {   // of keys 32 w and on
           uint32_t vis = 0xffffffffu;
           if (part) vis = my_row().sees(a, k0 + 32 * w) & ~kbad[(tile % TR_BAD) * KW + w];
           if constexpr (CAP) {
@@ -959,7 +991,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
 #pragma unroll
               for (int c = 0; c < 32; ++c) sr[c] = __float_as_uint(score_log2<true>(a, __uint_as_float(sr[c])));
             }
-          } else if (scaled) {
+          } else if (!BIAS && scaled) {
 #pragma unroll
             for (int c = 0; c < 32; ++c) sr[c] = __float_as_uint(__uint_as_float(sr[c]) * a.scale_log2);
           }
@@ -968,7 +1000,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
             if (how == Elements) {
               br += r * S::ELEMENTS + 32 * w;
 #pragma unroll
-              for (int c = 0; c < 32; ++c) sr[c] = __float_as_uint(fmaf(br[c], LOG2E, __uint_as_float(sr[c])));
+              for (int c = 0; c < 32; ++c) sr[c] = __float_as_uint(fmaf(__uint_as_float(sr[c]), pre, br[c]));
             } else {
               if (how == RowCopies) {
                 // element e of the tile's distances, s = p - (k0 + KT - 1) up: key KT - 1 - e
@@ -998,7 +1030,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
                       const int c = 31 - (8 * q + i);
                       float x = __uint_as_float(i & 1 ? v[i >> 1] & 0xFFFF0000u : v[i >> 1] << 16);
                       if (beyond) x = c <= c_last ? rc : x;
-                      sr[c] = __float_as_uint(fmaf(x, LOG2E, __uint_as_float(sr[c])));
+                      sr[c] = __float_as_uint(fmaf(__uint_as_float(sr[c]), pre, x));
                     }
                   }
                 } else {
@@ -1016,19 +1048,21 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
                       const int c = 31 - (4 * q + i);
                       float x = __uint_as_float(o2 ? u[i + 2] : u[i]);
                       if (beyond) x = c <= c_last ? rc : x;
-                      sr[c] = __float_as_uint(fmaf(x, LOG2E, __uint_as_float(sr[c])));
+                      sr[c] = __float_as_uint(fmaf(__uint_as_float(sr[c]), pre, x));
                     }
                   }
                 }
               } else if (a.rel) {   // all at E - 1 or beyond
-                const float x = rc * LOG2E;
 #pragma unroll
-                for (int c = 0; c < 32; ++c) sr[c] = __float_as_uint(__uint_as_float(sr[c]) + x);
+                for (int c = 0; c < 32; ++c) sr[c] = __float_as_uint(fmaf(__uint_as_float(sr[c]), pre, rc));
+              } else {
+#pragma unroll
+                for (int c = 0; c < 32; ++c) sr[c] = __float_as_uint(__uint_as_float(sr[c]) * pre);
               }
               if (a.slopes) {
-                const float slope2 = __ldg(a.slopes + head) * LOG2E, d0 = (float)(p - k0 - 32 * w);
+                const float d0 = (float)(p - k0 - 32 * w);
 #pragma unroll
-                for (int c = 0; c < 32; ++c) sr[c] = __float_as_uint(fmaf(-slope2, d0 - (float)c, __uint_as_float(sr[c])));
+                for (int c = 0; c < 32; ++c) sr[c] = __float_as_uint(fmaf(-slope, d0 - (float)c, __uint_as_float(sr[c])));
               }
             }
           }
@@ -1042,6 +1076,23 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
           for (int c = 0; c < 32; c += 2)
             mv[(c >> 1) & 1] = fmax3(mv[(c >> 1) & 1], __uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
           mx = fmaxf(mv[0], mv[1]);
+        };
+        uint32_t all[S::ROLL ? 32 : KT];
+        if constexpr (S::ROLL) {
+#pragma unroll 1
+          for (int w = 0; w < KW; ++w) {
+            tmem_ld32(tm_s + 32 * w, all);
+            tmem_wait_ld();
+            score(w, all);
+            tmem_st32(tm_s + 32 * w, all);
+          }
+          tmem_wait_st();
+        } else {
+#pragma unroll
+          for (int w = 0; w < KW; ++w) tmem_ld32(tm_s + 32 * w, *reinterpret_cast<uint32_t(*)[32]>(&all[32 * w]));
+          tmem_wait_ld();
+#pragma unroll
+          for (int w = 0; w < KW; ++w) score(w, *reinterpret_cast<uint32_t(*)[32]>(&all[32 * w]));
         }
         if constexpr (BIAS) {
           if (how != NoLoad) {
@@ -1075,9 +1126,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
         const float nm = m == -INFINITY ? 0.f : -m;
         const uint64_t mul2 = f2_pack(mul, mul), nm2 = f2_pack(nm, nm);
         uint64_t ls2[4] = {0ull, 0ull, 0ull, 0ull};
-#pragma unroll
-        for (int w = 0; w < KW; ++w) {
-          uint32_t (&sr)[32] = *reinterpret_cast<uint32_t(*)[32]>(&all[32 * w]);
+        auto numerators = [&](int w, uint32_t (&sr)[32]) {
           uint32_t pk[16];
 #pragma unroll
           for (int c = 0; c < 16; ++c) {
@@ -1088,6 +1137,17 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
             pk[c] = pack_bf16(p0, p1);
           }
           tmem_st16(tm_s + 16 * w, pk);
+        };
+        if constexpr (S::ROLL) {
+#pragma unroll 1
+          for (int w = 0; w < KW; ++w) {
+            tmem_ld32(tm_s + 32 * w, all);
+            tmem_wait_ld();
+            numerators(w, all);
+          }
+        } else {
+#pragma unroll
+          for (int w = 0; w < KW; ++w) numerators(w, *reinterpret_cast<uint32_t(*)[32]>(&all[32 * w]));
         }
         {
           float x0, x1, y0, y1;
@@ -1133,7 +1193,6 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
       const float inv = whole ? (nothing ? 0.f : 1.f / l) : 1.f;   // (a NaN stays one)
       const float g0 = nothing ? 0.f : f0 * inv, g1 = nothing ? 0.f : f1 * inv;
       const uint32_t o0 = tm_o + (merge ? 0 : D * h);
-      const size_t orow = (size_t)t * a.Hq + head;
       const int rt = pair ? h : 0;   // row tile
       float4* part_o = reinterpret_cast<float4*>(a.part_o) + ((size_t)it.place * 2 + rt) * (D / 4) * TREE_ROWS + r;
       // after a merge each of the two threads of a row has half of its channels
@@ -1270,11 +1329,11 @@ __global__ void __launch_bounds__(TREE_ROWS) tree_join_kernel(const TreeArgs a) 
 
 template <int D, bool CAP, bool BIAS>
 cudaError_t launch_t(const MaskedMaps& m, const TreeArgs& a, int grid, cudaStream_t stream) {
-  using S = TRShape<D, BIAS>;
+  using S = TRShape<D, CAP, BIAS>;
   static std::atomic<unsigned long long> opted{0};
-  cudaError_t e = smem_opt_in_once(tree_kernel<D, CAP, BIAS>, (int)TRSmem<D, BIAS>::alloc, opted);
+  cudaError_t e = smem_opt_in_once(tree_kernel<D, CAP, BIAS>, (int)TRSmem<D, CAP, BIAS>::alloc, opted);
   if (e != cudaSuccess) return e;
-  tree_kernel<D, CAP, BIAS><<<grid, S::THREADS, TRSmem<D, BIAS>::alloc, stream>>>(m.k, m.v, m.q, a);
+  tree_kernel<D, CAP, BIAS><<<grid, S::THREADS, TRSmem<D, CAP, BIAS>::alloc, stream>>>(m.k, m.v, m.q, a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   tree_join_kernel<D><<<dim3(grid, 2 * (D / 16)), TREE_ROWS, 0, stream>>>(a);

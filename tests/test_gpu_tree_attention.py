@@ -266,3 +266,25 @@ def test_many_short_pieces(cuda_device, heads, n, history, window, bias):
         out, lse, _ = step.call(workspace=ws)
         assert binding.inkling_attn_read_device_error(ws) == 0
         check(out, lse, ref, "many pieces")
+
+
+REPEATED = [
+    # heads, dim, page, tokens, history, window, extent, bias
+    ((64, 8), 128, 64, [61, 30, 45], [9000, 500, 4000], -1, 1, None), ((64, 8), 128, 16, [61, 5], [9000, 3000], -1, 1, None),
+    ((64, 8), 64, 8, [61, 20], [9000, 3000], -1, 1, None), ((64, 16), 128, 64, [7] * 40, [600] * 40, 512, 1, None),
+    ((64, 8), 128, 64, [16, 40], [5000, 3000], -1, 1000, F32), ((64, 16), 128, 16, [7] * 40, [600] * 40, 512, 512, BF16),
+    ((64, 8), 64, 64, [16, 40], [5000, 3000], -1, 1000, F32)]
+
+
+@pytest.mark.parametrize("case", range(len(REPEATED)))
+def test_two_hundred_calls_give_the_same_bits(cuda_device, case):
+    """What a warp does not wait for shows at one call in a hundred."""
+    heads, dim, page, n, history, window, extent, bias = REPEATED[case]
+    step = Step(heads, dim, page, n, history, 25, cuda_device, window=window, extent=extent, bias=bias)
+    ws = binding.alloc_tree_workspace(step.params, cuda_device)
+    out, lse, _ = step.call(workspace=ws)
+    check(out, lse, step.reference(), f"case {case}")
+    for i in range(200):
+        a, b, _ = step.call(workspace=ws)
+        assert torch.equal(a.view(torch.int16), out.view(torch.int16)) and torch.equal(b, lse), f"call {i}"
+    assert binding.inkling_attn_read_device_error(ws) == 0
