@@ -850,8 +850,8 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
               }
 #pragma unroll
               for (int y = 0; y < 8; ++y) {
-                buf[(r + y) * S::ELEMENTS + lane] = fmaf(-slope[y], far[y][0], v[y][0]);
-                buf[(r + y) * S::ELEMENTS + 32 + lane] = fmaf(-slope[y], far[y][1], v[y][1]);
+                buf[(r + y) * S::ELEMENTS + KT - 1 - lane] = fmaf(-slope[y], far[y][0], v[y][0]);
+                buf[(r + y) * S::ELEMENTS + KT - 33 - lane] = fmaf(-slope[y], far[y][1], v[y][1]);
               }
             }
           };
@@ -888,7 +888,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
 
     const bool scaled = CAP || BIAS || !(a.scale_log2 > 0.f);
     // With a bias scores are kept in natural units until the exponent: what is added needs no factor.
-    const float mul = BIAS ? LOG2E : scaled ? 1.f : a.scale_log2;
+    const float mul_ = BIAS ? LOG2E : scaled ? 1.f : a.scale_log2;
     const float pre = CAP ? LN2 : a.sm_scale;   // of the score to which a bias is added
     uint32_t c = 0, c_other = 0, bn = 0, mn = 0;   // tiles of this chain and of the other one so far
     int g = 0;
@@ -954,6 +954,27 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
             ++bn;
           }
         }
+        // this row's values, and how many of the tile's keys lie at E - 1 or beyond (the copy of a row ends there; within a window that
+        // is no longer than the row they are not seen)
+        const uint8_t* b_row = nullptr;
+        if constexpr (BIAS) {
+          if (how == RowCopies) {
+            uint8_t* row = reinterpret_cast<uint8_t*>(bias + ((size_t)h * TREE_ROWS + r) * S::PITCH);
+            const int size = a.rel_bf16 ? 2 : 4, d0 = p - k0;   // of key 0
+            row += (reinterpret_cast<uintptr_t>(a.rel) + (orow * a.E + (size_t)(d0 - KT + 1)) * size) & 15;
+            b_row = row;
+            const int n = min(d0 - (a.E - 1), KT);
+            if (!(a.W > 0 && a.W <= a.E) && rv && n > 0) {
+              for (int c = 0; c < n; ++c) {
+                if (a.rel_bf16) reinterpret_cast<uint16_t*>(row)[KT - 1 - c] = (uint16_t)(__float_as_uint(rc) >> 16);
+                else reinterpret_cast<float*>(row)[KT - 1 - c] = rc;
+              }
+              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // (a copy may write here next)
+            }
+          } else {
+            b_row = reinterpret_cast<const uint8_t*>(bias + (size_t)h * TREE_ROWS * S::PITCH + r * S::ELEMENTS);
+          }
+        }
         // ---- scores and their maximum
         float mx = -INFINITY;
         auto score = [&](int w, uint32_t (&sr)[32]) {   // of keys 32 w and on
@@ -996,74 +1017,27 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
             for (int c = 0; c < 32; ++c) sr[c] = __float_as_uint(__uint_as_float(sr[c]) * a.scale_log2);
           }
           if constexpr (BIAS) {
-            const float* br = bias + (size_t)h * TREE_ROWS * S::PITCH;
-            if (how == Elements) {
-              br += r * S::ELEMENTS + 32 * w;
+            if (how != NoLoad) {
+              // value of key c at place KT - 1 - c, distances rising
+              if (how == RowCopies && a.rel_bf16) {
+                const uint16_t* br = reinterpret_cast<const uint16_t*>(b_row) + KT - 1 - 32 * w;
 #pragma unroll
-              for (int c = 0; c < 32; ++c) sr[c] = __float_as_uint(fmaf(__uint_as_float(sr[c]), pre, br[c]));
-            } else {
-              if (how == RowCopies) {
-                // element e of the tile's distances, s = p - (k0 + KT - 1) up: key KT - 1 - e
-                const int d0 = p - k0;   // of key 0
-                const uintptr_t src = reinterpret_cast<uintptr_t>(a.rel) +
-                                      (((size_t)t * a.Hq + head) * a.E + (size_t)(d0 - KT + 1)) * (a.rel_bf16 ? 2 : 4);
-                const bool beyond = __any_sync(0xffffffffu, d0 >= a.E - 1);
-                const int c_last = d0 - (a.E - 1) - 32 * w;   // keys up to this one are at a distance of E - 1 or more
-                const uint4* row = reinterpret_cast<const uint4*>(br + r * S::PITCH) + (KW - 1 - w) * (a.rel_bf16 ? 4 : 8);
-                uint4 cur = row[0];
-                if (a.rel_bf16) {
-                  const bool o1 = src & 2, o2 = src & 4, o4 = src & 8;
-#pragma unroll
-                  for (int q = 0; q < 4; ++q) {
-                    const uint4 nxt = row[q + 1];
-                    const uint32_t e[8] = {cur.x, cur.y, cur.z, cur.w, nxt.x, nxt.y, nxt.z, nxt.w};
-                    cur = nxt;
-                    uint32_t o[7], u[6], v[4];
-#pragma unroll
-                    for (int i = 0; i < 7; ++i) o[i] = o1 ? __funnelshift_r(e[i], e[i + 1], 16) : e[i];
-#pragma unroll
-                    for (int i = 0; i < 6; ++i) u[i] = o2 ? o[i + 1] : o[i];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) v[i] = o4 ? u[i + 2] : u[i];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                      const int c = 31 - (8 * q + i);
-                      float x = __uint_as_float(i & 1 ? v[i >> 1] & 0xFFFF0000u : v[i >> 1] << 16);
-                      if (beyond) x = c <= c_last ? rc : x;
-                      sr[c] = __float_as_uint(fmaf(__uint_as_float(sr[c]), pre, x));
-                    }
-                  }
-                } else {
-                  const bool o1 = src & 4, o2 = src & 8;
-#pragma unroll
-                  for (int q = 0; q < 8; ++q) {
-                    const uint4 nxt = row[q + 1];
-                    const uint32_t e[7] = {cur.x, cur.y, cur.z, cur.w, nxt.x, nxt.y, nxt.z};
-                    cur = nxt;
-                    uint32_t u[6];
-#pragma unroll
-                    for (int i = 0; i < 6; ++i) u[i] = o1 ? e[i + 1] : e[i];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                      const int c = 31 - (4 * q + i);
-                      float x = __uint_as_float(o2 ? u[i + 2] : u[i]);
-                      if (beyond) x = c <= c_last ? rc : x;
-                      sr[c] = __float_as_uint(fmaf(__uint_as_float(sr[c]), pre, x));
-                    }
-                  }
-                }
-              } else if (a.rel) {   // all at E - 1 or beyond
-#pragma unroll
-                for (int c = 0; c < 32; ++c) sr[c] = __float_as_uint(fmaf(__uint_as_float(sr[c]), pre, rc));
+                for (int c = 0; c < 32; ++c)
+                  sr[c] = __float_as_uint(fmaf(__uint_as_float(sr[c]), pre, __uint_as_float((uint32_t)br[-c] << 16)));
               } else {
+                const float* br = reinterpret_cast<const float*>(b_row) + KT - 1 - 32 * w;
 #pragma unroll
-                for (int c = 0; c < 32; ++c) sr[c] = __float_as_uint(__uint_as_float(sr[c]) * pre);
+                for (int c = 0; c < 32; ++c) sr[c] = __float_as_uint(fmaf(__uint_as_float(sr[c]), pre, br[-c]));
               }
-              if (a.slopes) {
-                const float d0 = (float)(p - k0 - 32 * w);
+            } else {
+              const float x = rc;   // (0 without a tensor)
 #pragma unroll
-                for (int c = 0; c < 32; ++c) sr[c] = __float_as_uint(fmaf(-slope, d0 - (float)c, __uint_as_float(sr[c])));
-              }
+              for (int c = 0; c < 32; ++c) sr[c] = __float_as_uint(fmaf(__uint_as_float(sr[c]), pre, x));
+            }
+            if (a.slopes && how != Elements) {
+              const float d0 = (float)(p - k0 - 32 * w);
+#pragma unroll
+              for (int c = 0; c < 32; ++c) sr[c] = __float_as_uint(fmaf(-slope, d0 - (float)c, __uint_as_float(sr[c])));
             }
           }
           if (part) {   // keys that this row does not see
@@ -1078,15 +1052,30 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
           mx = fmaxf(mv[0], mv[1]);
         };
         uint32_t all[S::ROLL ? 32 : KT];
+        float mul = mul_, off = 0.f;      // a score's factor in the exponent, and what is added to it
         if constexpr (S::ROLL) {
+          // One value for a whole row changes no order: such scores stay as they are.
+          const bool lean = BIAS && !CAP && how == NoLoad && !part && !a.slopes && pre > 0.f;
+          if (lean) {
+            mul = a.scale_log2;
+            off = rc * LOG2E;
+          }
 #pragma unroll 1
           for (int w = 0; w < KW; ++w) {
             tmem_ld32(tm_s + 32 * w, all);
             tmem_wait_ld();
-            score(w, all);
-            tmem_st32(tm_s + 32 * w, all);
+            if (lean) {
+              float mv[2] = {mx, -INFINITY};
+#pragma unroll
+              for (int c = 0; c < 32; c += 2)
+                mv[(c >> 1) & 1] = fmax3(mv[(c >> 1) & 1], __uint_as_float(all[c]), __uint_as_float(all[c + 1]));
+              mx = fmaxf(mv[0], mv[1]);
+            } else {
+              score(w, all);
+              tmem_st32(tm_s + 32 * w, all);
+            }
           }
-          tmem_wait_st();
+          if (!lean) tmem_wait_st();
         } else {
 #pragma unroll
           for (int w = 0; w < KW; ++w) tmem_ld32(tm_s + 32 * w, *reinterpret_cast<uint32_t(*)[32]>(&all[32 * w]));
@@ -1101,7 +1090,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
           }
         }
         // ---- running maximum, moved only when it grows by more than 2^8
-        mx *= mul;
+        mx = fmaf(mx, mul, off);
         const bool mine = mx > m + TR_RESCALE_LOG2;
         if (__any_sync(0xffffffffu, mine)) {
           if (j > 0) {   // (s_full came after all products into O_h but the last one)
@@ -1123,7 +1112,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
           if (mine) m = mx;
         }
         // ---- numerators
-        const float nm = m == -INFINITY ? 0.f : -m;
+        const float nm = off - (m == -INFINITY ? 0.f : m);
         const uint64_t mul2 = f2_pack(mul, mul), nm2 = f2_pack(nm, nm);
         uint64_t ls2[4] = {0ull, 0ull, 0ull, 0ull};
         auto numerators = [&](int w, uint32_t (&sr)[32]) {
