@@ -181,15 +181,15 @@ bool make_pool_map(CUtensorMap* map, const void* base, const ink_attn_params_t* 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // rel_logits [total_q, Hq, E] (fp32 or bf16) as a 3-D tensor {E, Hq, total_q}; boxes of
-// box_cols buckets x 1 head x box_rows tokens, out-of-range elements read as 0.
+// box_cols buckets x box_heads heads x box_rows tokens, out-of-range elements read as 0.
 bool make_bias_map(CUtensorMap* map, const void* rel, bool bf16, const ink_attn_params_t* p, int total_q,
-                   int box_cols, int box_rows) {
+                   int box_cols, int box_rows, int box_heads = 1) {
   auto fn = encode_fn();
   if (!fn) return false;
   const cuuint64_t es = bf16 ? 2 : 4;
   cuuint64_t dims[3] = {(cuuint64_t)p->rel_extent, (cuuint64_t)p->num_q_heads, (cuuint64_t)total_q};
   cuuint64_t strides[2] = {(cuuint64_t)p->rel_extent * es, (cuuint64_t)p->rel_extent * es * p->num_q_heads};
-  cuuint32_t box[3] = {(cuuint32_t)box_cols, 1, (cuuint32_t)box_rows};
+  cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
   cuuint32_t estr[3] = {1, 1, 1};
   CUresult r = fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3,
                   const_cast<void*>(rel), dims, strides, box, estr,
@@ -922,7 +922,6 @@ ink_status_t inkling_attn_tree(const ink_attn_params_t* params, const ink_attn_t
   a.slopes = o.slopes;
   a.rel = o.rel_logits;
   a.rel_bf16 = o.rel_is_bf16 ? 1 : 0;
-  a.rel_rows = aligned(o.rel_logits, 16) && rows * params->rel_extent * (a.rel_bf16 ? 2 : 4) % 16 == 0;
   a.k = k_cache;
   a.v = v_cache;
   a.out = out;
@@ -945,6 +944,15 @@ ink_status_t inkling_attn_tree(const ink_attn_params_t* params, const ink_attn_t
   a.cuts = reinterpret_cast<ink::TreeCut*>(ws + lay.cuts);
   a.part_ml = reinterpret_cast<float*>(ws + lay.part_ml_off);
   a.part_o = reinterpret_cast<float*>(ws + lay.part_o_off);
+  // A token's bias box stands on 128 bytes; with few heads a tile holds as many tokens as there is room for.
+  const size_t size = a.rel_bf16 ? 2 : 4, box = (size_t)a.heads_per_tile * ink::tree_bias_cols(a.rel_bf16) * size;
+  a.rel_rows = a.rel && aligned(a.rel, 16) && params->rel_extent * size % 16 == 0;
+  a.bias_stride = (int)align_up(box, 128);
+  if (a.rel_rows && a.tok_per_tile > ink::TREE_BIAS_BYTES / a.bias_stride) a.tok_per_tile = ink::TREE_BIAS_BYTES / a.bias_stride;
+  CUtensorMap bias;
+  std::memset(&bias, 0, sizeof bias);
+  if (a.rel_rows && !make_bias_map(&bias, a.rel, a.rel_bf16 != 0, params, total_q, ink::tree_bias_cols(a.rel_bf16), 1, a.heads_per_tile))
+    return INK_ERR_CUDA;
   ink::MaskedMaps maps;
   // whole tiles by one box where they lie in one page, else boxes of a page and 64 channels
   auto pool_map = [&](CUtensorMap* m, const void* base) {
@@ -955,7 +963,7 @@ ink_status_t inkling_attn_tree(const ink_attn_params_t* params, const ink_attn_t
   if (!pool_map(&maps.k, k_cache) || !pool_map(&maps.v, v_cache) ||
       !make_token_map(&maps.q, q, params, total_q, a.heads_per_tile, a.tok_per_tile))
     return INK_ERR_CUDA;
-  return ink::launch_tree(maps, a, params->head_dim, (cudaStream_t)stream) == cudaSuccess ? INK_OK : INK_ERR_CUDA;
+  return ink::launch_tree(maps, bias, a, params->head_dim, (cudaStream_t)stream) == cudaSuccess ? INK_OK : INK_ERR_CUDA;
 }
 
 ink_status_t inkling_attn_kv_conv_write_tree(const ink_attn_params_t* params, const void* k_new, const void* v_new,

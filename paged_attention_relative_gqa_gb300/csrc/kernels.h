@@ -292,7 +292,8 @@ struct TreeArgs {
   uint32_t* err;
   int B, T, Hq, Hkv, G, log2_page, max_pages, num_pages, W, E, words;
   int rel_bf16;
-  int rel_rows;                // rel begins and ends on 16-byte boundaries: its rows can be copied in bulk
+  int rel_rows;                // rows of rel begin on 16-byte boundaries: boxes of a token's heads can be copied
+  int bias_stride;             // bytes from one token's box to the next in shared memory
   float sm_scale, softcap;
   float scale_log2;            // sm_scale * log2(e)
   float cap_k1, cap_log2, cap_inv, cap_near, near[NEAR_TERMS], cap_mid, mid[MID_TERMS];   // as in MaskedArgs
@@ -311,7 +312,11 @@ struct TreeCut {
 
 constexpr int TREE_ROWS = 128;       // rows of a row tile
 constexpr int TREE_MAX_CTAS = 160;   // most CTAs (bounds the partials)
+constexpr int TREE_BIAS_BYTES = 40960;   // a chain's bias in shared memory
 
-cudaError_t launch_tree(const MaskedMaps& m, const TreeArgs& a, int head_dim, cudaStream_t stream);
+// Columns of a bias box: a tile's values from a 16-byte boundary on.
+__host__ __device__ constexpr int tree_bias_cols(bool bf16) { return TILE_KEYS + (bf16 ? 8 : 4); }
+
+cudaError_t launch_tree(const MaskedMaps& m, const CUtensorMap& bias, const TreeArgs& a, int head_dim, cudaStream_t stream);
 
 }  // namespace ink

@@ -26,11 +26,10 @@
 //   11  V check: in tiles that not every row sees whole, rows of V that nobody sees are zeroed and so is
 //       every infinity or NaN (0 * NaN would reach rows that do not see the key); rows that do see one get it back at the end
 //   12-15 (with a bias) bias, see below
-// The bias of a row has no alignment: it starts at the row's distance from the tile.  Within the history it is KT values side
-// by side, which one bulk copy a row brings from the 16-byte boundary before them; the softmax reads its row 16 bytes at a time (a
-// pitch of KT + 4 words keeps 8 rows in different banks) and shifts the values into place with two selects each.  Tiles whose
-// distances are all E - 1 or more take one value a row.  Behind the history distances have no order, and a bias warp brings them element
-// by element, a lane a key.  With a bias tiles have 64 keys: two buffers of 128 rows take 70 KB of shared memory.
+// The bias of a row has no alignment: it starts at the row's distance from the tile.  Within the history it is KT values side by
+// side, and all heads of a token start at the same distance: one TMA box a token brings them from the 16-byte boundary before
+// them (96 rows by a bulk copy each: 5,000 clocks).  Tiles whose distances are all E - 1 or more take one value a row.  Behind
+// the history distances have no order, and a bias warp brings them element by element, a lane a key.
 // Every wait is bounded; after a timeout the CTA records it, stops issuing, waits for what is in flight and exits.
 #include <algorithm>
 #include <climits>
@@ -74,8 +73,7 @@ struct TRShape {
   // slots went by without one).
   static constexpr bool ROLL = CAP || BIAS;
   static constexpr uint32_t TQ = 128;              // with a bias: S_h at 64 h, Q_h at TQ + 64 h
-  static constexpr int PITCH = KT + 4;             // words of a bias row: KT values from a 16-byte boundary on
-  static constexpr int ELEMENTS = KT + 1;          // the same of one filled element by element
+  static constexpr int ELEMENTS = KT + 1;          // words of a bias row that is filled element by element
   static constexpr uint32_t TO = 256;              // without: S_h at 128 h, two of them; O_h at TO + D h
   static constexpr uint32_t TS = BIAS ? 64 : 128;
 };
@@ -111,7 +109,7 @@ struct TRSmem {
   static constexpr size_t q = 0;
   static constexpr size_t ring = BIAS ? 0 : 2 * (size_t)S::QTILE;
   static constexpr size_t bias = ring + (size_t)S::NS * S::TILE;
-  static constexpr size_t bars = bias + (BIAS ? 2 * (size_t)TREE_ROWS * S::PITCH * 4 : 0);
+  static constexpr size_t bars = bias + (BIAS ? 2 * (size_t)TREE_BIAS_BYTES : 0);
   // k_full[TILES], v_full[TILES], v_ok[TILES], empty[NS], s_full[2][2], p_full[2][2], o_done[2][2], q_full[2], q_empty[2],
   // item_full[ITEMS], item_empty[ITEMS], o_free, ml, drain[2], bias_full[2], bias_empty[2]
   static constexpr int NBAR = S::NS + 3 * TR_TILES + 16 + 2 * TR_ITEMS + 4 + (BIAS ? 4 : 0);
@@ -141,6 +139,7 @@ __device__ __forceinline__ bool tr_wait(uint64_t* bar, uint32_t parity, volatile
 // A sequence's rows and keys; tiles == 0: none of its rows sees a key (or it has none).
 struct TRSeq {
   int c0, n, L, lo, hi, tiles;
+  int far;        // tiles at the start whose distances are all E - 1 or more: no bias is loaded for them
   uint32_t bad;   // error bits; BAD_ROWS: its rows are not touched
 
   __device__ __forceinline__ void load(const TreeArgs& a, int b) {
@@ -148,7 +147,7 @@ struct TRSeq {
     const int c1 = __ldg(a.cu_q + b + 1);
     L = __ldg(a.seq_lens + b);
     n = c1 - c0;
-    lo = hi = tiles = 0;
+    lo = hi = tiles = far = 0;
     bad = 0;
     if (c0 < 0 || c1 > a.T || c1 < c0) {
       bad = INK_DEVERR_BAD_ROWS;
@@ -165,26 +164,31 @@ struct TRSeq {
       hi = (int)min((long long)L, cap);
       lo = a.W > 0 ? max(0, L - n - a.W + 1) : 0;
       if (lo < hi) tiles = (hi - 1) / KT - lo / KT + 1;
+      const long long flat = (long long)(L - n) - (KT - 1) - (a.E - 1);   // last first key of such a tile
+      far = !a.rel ? tiles : flat < 0 ? 0 : min(tiles, max(0, (int)(flat / KT) - lo / KT + 1));
     }
   }
 };
 
 // The row of tiles, walked by a whole warp: 32 sequences at a time in the lanes.  Divisions, which take as long as a load, are
-// made once per run: later pieces begin with their item.
+// made once per run: later pieces begin with their item.  It is measured in units, a tile each; where bias rows are loaded, two for
+// a tile with them (they are as many bytes as its K and V) and for the first one of an odd number of those without: runs and
+// items then begin and end at even units, between tiles.
 struct TRWalk {
-  long long base, incl, chunk, total;   // tiles before sequence cb; up to and with this lane's; of a run; of the 32
-  long long pos, end;                   // of this CTA's run
-  int cb, per, items, cta;
+  long long base, incl, chunk, total;   // units before sequence cb; up to and with this lane's; of a run; of the 32
+  long long pos, end;                   // of this CTA's run, in units
+  int cb, per, items, units, cta;       // (units: of an item of this lane's sequence)
   int src, groups, left;                // the sequence's lane; its items; of these not begun
   int kvh, hc, item;                    // the next one
   TRSeq s;
 
   __device__ __forceinline__ void load(const TreeArgs& a, int lane) {
     const int b = cb + lane;
-    s.tiles = s.n = 0;
+    s.tiles = s.n = s.far = 0;
     if (b < a.B) s.load(a, b);
     items = (s.n + 2 * a.tok_per_tile - 1) / (2 * a.tok_per_tile);
-    incl = (long long)s.tiles * items * per;
+    units = a.rel ? 2 * s.tiles - s.far + (s.far & 1) : s.tiles;
+    incl = (long long)units * items * per;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long v = __shfl_up_sync(0xffffffffu, incl, o);
@@ -205,6 +209,7 @@ struct TRWalk {
     base = 0;
     left = 0;
     chunk = max((all + gridDim.x - 1) / (long long)gridDim.x, (long long)TR_MIN_TILES);
+    if (a.rel) chunk += chunk & 1;
     pos = min(cta * chunk, all);
     end = min(pos + chunk, all);
   }
@@ -220,13 +225,13 @@ struct TRWalk {
         load(a, lane);
       }
       src = __ffs(__ballot_sync(0xffffffffu, pos < base + incl)) - 1;
-      const int ni = __shfl_sync(0xffffffffu, items, src), tiles = __shfl_sync(0xffffffffu, s.tiles, src);
+      const int ni = __shfl_sync(0xffffffffu, items, src), u = __shfl_sync(0xffffffffu, units, src);
       groups = ni * per;
-      const long long off = pos - (base + __shfl_sync(0xffffffffu, incl - (long long)s.tiles * items * per, src));
+      const long long off = pos - (base + __shfl_sync(0xffffffffu, incl - (long long)units * items * per, src));
       int gi = 0;
       if (off > 0) {   // the run begins within a sequence
-        gi = (int)(off / tiles);
-        x0 = (int)(off - (long long)gi * tiles);
+        gi = (int)(off / u);
+        x0 = (int)(off - (long long)gi * u);
         first = (int)((pos - x0) / chunk);
       }
       left = groups - gi;
@@ -235,7 +240,10 @@ struct TRWalk {
       kvh = hk / a.head_chunks;
       hc = hk - kvh * a.head_chunks;
     }
-    const int ni = __shfl_sync(0xffffffffu, items, src), tiles = __shfl_sync(0xffffffffu, s.tiles, src);
+    const int ni = __shfl_sync(0xffffffffu, items, src), u = __shfl_sync(0xffffffffu, units, src);
+    const int far = __shfl_sync(0xffffffffu, s.far, src), odd = a.rel ? far & 1 : 0;
+    // tiles before unit y of an item
+    auto tiles = [&](int y) { return y <= far + odd ? max(0, y - odd) : far + ((y - far - odd) >> 1); };
     TRPart w;
     w.b = cb + src;
     w.c0 = __shfl_sync(0xffffffffu, s.c0, src);
@@ -248,12 +256,13 @@ struct TRWalk {
     w.gh = min(a.heads_per_tile, a.G - hc * a.heads_per_tile);
     w.t0 = w.c0 + item * 2 * a.tok_per_tile;
     w.ntok = min(2 * a.tok_per_tile, w.n - item * 2 * a.tok_per_tile);
-    w.kt0 = w.lo / KT + x0;
-    w.nt = (int)min((long long)(tiles - x0), end - pos);
-    const long long g1 = pos - x0 + tiles;
+    const int x1 = (int)min((long long)u, x0 + (end - pos));
+    w.kt0 = w.lo / KT + tiles(x0);
+    w.nt = tiles(x1) - tiles(x0);
+    const long long g1 = pos - x0 + u;
     w.parts = (g1 <= end ? cta : (int)((g1 - 1) / chunk)) - first + 1;
     w.place = 2 * cta + (cta == first ? 1 : 0);
-    pos += w.nt;
+    pos += x1 - x0;
     --left;
     if (++item == ni) {
       item = 0;
@@ -311,12 +320,12 @@ __device__ __forceinline__ TRRow tr_row(const TreeArgs& a, const TRPart& it, int
 
 // How the bias of a tile comes to the softmax.  Behind the history distances have no order.  Before it a row's are KT values
 // side by side, one copy a row where 16-byte boundaries can be kept inside the tensor; all of them at E - 1 or more are one value.
-enum TRBias { NoLoad, RowCopies, Elements };
+enum TRBias { NoLoad, Boxes, Elements };
 
 __device__ __forceinline__ TRBias tr_bias(const TreeArgs& a, const TRPart& it, int k0) {
   if (min(it.H, it.hi) - k0 < KT) return Elements;
   if (!a.rel || it.H - (k0 + KT - 1) >= a.E - 1) return NoLoad;
-  return a.rel_rows ? RowCopies : Elements;
+  return a.rel_rows ? Boxes : Elements;
 }
 
 __device__ __forceinline__ uint64_t tr_mul(uint64_t a, uint64_t b) {
@@ -332,7 +341,8 @@ __device__ __forceinline__ float tr_weigh(float w, float x) { return fabsf(x) <=
 template <int D, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(TRShape<D, CAP, BIAS>::THREADS, 1)
 tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-            const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ TreeArgs a) {
+            const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmB,
+            const __grid_constant__ TreeArgs a) {
   using S = TRShape<D, CAP, BIAS>;
   using L_ = TRSmem<D, CAP, BIAS>;
   constexpr int NS = S::NS;
@@ -358,7 +368,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
   uint32_t* kbad = reinterpret_cast<uint32_t*>(smem + L_::kbad);   // [BAD][KW] bit per unreadable key
   int* poison = reinterpret_cast<int*>(smem + L_::poison);   // [ITEMS][2 chains][2] first and last tile of V with an infinity or NaN
   float2* ml = reinterpret_cast<float2*>(smem + L_::ml);
-  float* bias = reinterpret_cast<float*>(smem + L_::bias);
+  uint8_t* bias = smem + L_::bias;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L_::misc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L_::misc + 4);
 
@@ -767,8 +777,10 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
     } else if constexpr (BIAS) {
       // ---------------------------------------------------------------- bias loads of one chain
       const int h = warp - 13;
-      float* buf = bias + (size_t)h * TREE_ROWS * S::PITCH;
+      uint8_t* boxes = bias + h * TREE_BIAS_BYTES;
+      float* buf = reinterpret_cast<float*>(boxes);
       const int last = a.E - 1, size = a.rel_bf16 ? 2 : 4;
+      if (lane == 0 && a.rel_rows) prefetch_tensormap(&tmB);
       uint32_t fills = 0;
       bool go = true;
       for (int k = 0; go && next_item(k); ++k) {
@@ -776,19 +788,10 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
         const TRPart& it = item.of(h);
         const int tok0 = item.mode == Pair ? h * a.tok_per_tile : 0;
         const int rows = min(a.tok_per_tile, it.ntok - tok0) * a.heads_per_tile;
-        // this lane's rows lane, lane + 32, ...: position and elements before the row; and tokens lane, lane + 32, ...
-        int pr[4], pt[4];
-        size_t at[4];
-        bool live[4];
+        const int tokens = min(a.tok_per_tile, it.ntok - tok0);
+        int pt[4];                         // positions of this lane's tokens lane, lane + 32, ...
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int r = 32 * x + lane, i = r / a.heads_per_tile, hd = r - i * a.heads_per_tile;
-          live[x] = r < rows && hd < it.gh;
-          const int t = it.t0 + tok0 + (live[x] ? i : 0);
-          pr[x] = max(__ldg(a.positions + t), it.H);
-          at[x] = ((size_t)t * a.Hq + it.h0 + hd) * a.E;
-          pt[x] = max(__ldg(a.positions + it.t0 + tok0 + min(32 * x + lane, it.ntok - tok0 - 1)), it.H);
-        }
+        for (int x = 0; x < 4; ++x) pt[x] = max(__ldg(a.positions + it.t0 + tok0 + min(32 * x + lane, tokens - 1)), it.H);
         for (int j = 0; j < it.nt && go; ++j) {
           const int k0 = (it.kt0 + j * item.step()) * KT;
           const TRBias how = tr_bias(a, it, k0);
@@ -796,24 +799,20 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
           if (fills > 0) go = tr_wait(&bias_empty[h], (fills - 1) & 1u, abort_flag, a);
           if (!go) break;
           ++fills;
-          if (how == RowCopies) {
-            // distances [s, e) of a row, from the 16 bytes that hold the first to those that hold the last
-            uint32_t bytes[4], sum = 0;
-            uintptr_t from[4];
+          if (how == Boxes) {
+            // a token's rows from the 16 bytes that hold their first distance in the tile (those at E - 1 or beyond alone: none)
+            int at[4], n = 0;
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-              const int s = pr[x] - (k0 + KT - 1), e = min(pr[x] - k0, last) + 1;
-              const uintptr_t base = reinterpret_cast<uintptr_t>(a.rel) + at[x] * size;
-              from[x] = (base + (size_t)s * size) & ~(uintptr_t)15;
-              bytes[x] = live[x] && s < e ? (uint32_t)(((base + (size_t)e * size + 15) & ~(uintptr_t)15) - from[x]) : 0u;
-              sum += bytes[x];
+              const int s = pt[x] - (k0 + KT - 1);
+              at[x] = 32 * x + lane < tokens && s < a.E ? s & ~(16 / size - 1) : -1;
+              n += at[x] >= 0;
             }
-            mbar_arrive_expect_tx(&bias_full[h], sum);
+            mbar_arrive_expect_tx(&bias_full[h], (uint32_t)(n * a.heads_per_tile * tree_bias_cols(a.rel_bf16) * size));
 #pragma unroll
             for (int x = 0; x < 4; ++x)
-              if (bytes[x])
-                bulk_copy_g2s(smem_u32(buf + (32 * x + lane) * S::PITCH), reinterpret_cast<const void*>(from[x]), bytes[x],
-                              &bias_full[h]);
+              if (at[x] >= 0)
+                tma_load_3d(boxes + (32 * x + lane) * a.bias_stride, &tmB, at[x], it.h0, it.t0 + tok0 + 32 * x + lane, &bias_full[h]);
             __syncwarp();
             continue;
           }
@@ -958,10 +957,11 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
         // is no longer than the row they are not seen)
         const uint8_t* b_row = nullptr;
         if constexpr (BIAS) {
-          if (how == RowCopies) {
-            uint8_t* row = reinterpret_cast<uint8_t*>(bias + ((size_t)h * TREE_ROWS + r) * S::PITCH);
+          if (how == Boxes) {
             const int size = a.rel_bf16 ? 2 : 4, d0 = p - k0;   // of key 0
-            row += (reinterpret_cast<uintptr_t>(a.rel) + (orow * a.E + (size_t)(d0 - KT + 1)) * size) & 15;
+            uint8_t* row = bias + h * TREE_BIAS_BYTES;   // (a row without a token reads the first one's: its own would lie outside)
+            if (rv) row += my_i * a.bias_stride + my_g * (tree_bias_cols(a.rel_bf16) * size);
+            row += ((d0 - KT + 1) & (16 / size - 1)) * size;
             b_row = row;
             const int n = min(d0 - (a.E - 1), KT);
             if (!(a.W > 0 && a.W <= a.E) && rv && n > 0) {
@@ -972,7 +972,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
               asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // (a copy may write here next)
             }
           } else {
-            b_row = reinterpret_cast<const uint8_t*>(bias + (size_t)h * TREE_ROWS * S::PITCH + r * S::ELEMENTS);
+            b_row = bias + h * TREE_BIAS_BYTES + r * S::ELEMENTS * 4;
           }
         }
         // ---- scores and their maximum
@@ -1019,7 +1019,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
           if constexpr (BIAS) {
             if (how != NoLoad) {
               // value of key c at place KT - 1 - c, distances rising
-              if (how == RowCopies && a.rel_bf16) {
+              if (how == Boxes && a.rel_bf16) {
                 const uint16_t* br = reinterpret_cast<const uint16_t*>(b_row) + KT - 1 - 32 * w;
 #pragma unroll
                 for (int c = 0; c < 32; ++c)
@@ -1045,33 +1045,32 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
             for (int c = 0; c < 32; ++c)
               if (!((vis >> c) & 1u)) sr[c] = 0xff800000u;   // -infinity
           }
+        };
+        uint32_t all[S::ROLL ? 32 : KT];
+        float mul = mul_, off = 0.f;      // a score's factor in the exponent, and what is added to it
+        // One value for a whole row changes no order: such scores stay as they are.
+        const bool lean = BIAS && !CAP && how == NoLoad && !part && !a.slopes && pre > 0.f;
+        if (lean) {
+          mul = a.scale_log2;
+          off = rc * LOG2E;
+        }
+        auto largest = [&](uint32_t (&sr)[32]) {
           float mv[2] = {mx, -INFINITY};
 #pragma unroll
           for (int c = 0; c < 32; c += 2)
             mv[(c >> 1) & 1] = fmax3(mv[(c >> 1) & 1], __uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
           mx = fmaxf(mv[0], mv[1]);
         };
-        uint32_t all[S::ROLL ? 32 : KT];
-        float mul = mul_, off = 0.f;      // a score's factor in the exponent, and what is added to it
         if constexpr (S::ROLL) {
-          // One value for a whole row changes no order: such scores stay as they are.
-          const bool lean = BIAS && !CAP && how == NoLoad && !part && !a.slopes && pre > 0.f;
-          if (lean) {
-            mul = a.scale_log2;
-            off = rc * LOG2E;
-          }
 #pragma unroll 1
           for (int w = 0; w < KW; ++w) {
             tmem_ld32(tm_s + 32 * w, all);
             tmem_wait_ld();
             if (lean) {
-              float mv[2] = {mx, -INFINITY};
-#pragma unroll
-              for (int c = 0; c < 32; c += 2)
-                mv[(c >> 1) & 1] = fmax3(mv[(c >> 1) & 1], __uint_as_float(all[c]), __uint_as_float(all[c + 1]));
-              mx = fmaxf(mv[0], mv[1]);
+              largest(all);
             } else {
               score(w, all);
+              largest(all);
               tmem_st32(tm_s + 32 * w, all);
             }
           }
@@ -1081,7 +1080,11 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
           for (int w = 0; w < KW; ++w) tmem_ld32(tm_s + 32 * w, *reinterpret_cast<uint32_t(*)[32]>(&all[32 * w]));
           tmem_wait_ld();
 #pragma unroll
-          for (int w = 0; w < KW; ++w) score(w, *reinterpret_cast<uint32_t(*)[32]>(&all[32 * w]));
+          for (int w = 0; w < KW; ++w) {
+            uint32_t (&sr)[32] = *reinterpret_cast<uint32_t(*)[32]>(&all[32 * w]);
+            if (!lean) score(w, sr);
+            largest(sr);
+          }
         }
         if constexpr (BIAS) {
           if (how != NoLoad) {
@@ -1317,12 +1320,12 @@ __global__ void __launch_bounds__(TREE_ROWS) tree_join_kernel(const TreeArgs a) 
 }
 
 template <int D, bool CAP, bool BIAS>
-cudaError_t launch_t(const MaskedMaps& m, const TreeArgs& a, int grid, cudaStream_t stream) {
+cudaError_t launch_t(const MaskedMaps& m, const CUtensorMap& bias, const TreeArgs& a, int grid, cudaStream_t stream) {
   using S = TRShape<D, CAP, BIAS>;
   static std::atomic<unsigned long long> opted{0};
   cudaError_t e = smem_opt_in_once(tree_kernel<D, CAP, BIAS>, (int)TRSmem<D, CAP, BIAS>::alloc, opted);
   if (e != cudaSuccess) return e;
-  tree_kernel<D, CAP, BIAS><<<grid, S::THREADS, TRSmem<D, CAP, BIAS>::alloc, stream>>>(m.k, m.v, m.q, a);
+  tree_kernel<D, CAP, BIAS><<<grid, S::THREADS, TRSmem<D, CAP, BIAS>::alloc, stream>>>(m.k, m.v, m.q, bias, a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   tree_join_kernel<D><<<dim3(grid, 2 * (D / 16)), TREE_ROWS, 0, stream>>>(a);
@@ -1330,22 +1333,22 @@ cudaError_t launch_t(const MaskedMaps& m, const TreeArgs& a, int grid, cudaStrea
 }
 
 template <int D>
-cudaError_t launch_d(const MaskedMaps& m, const TreeArgs& a, int grid, cudaStream_t stream) {
+cudaError_t launch_d(const MaskedMaps& m, const CUtensorMap& bias, const TreeArgs& a, int grid, cudaStream_t stream) {
   const bool cap = a.softcap != 0.f;
-  if (a.rel || a.slopes) return cap ? launch_t<D, true, true>(m, a, grid, stream) : launch_t<D, false, true>(m, a, grid, stream);
-  return cap ? launch_t<D, true, false>(m, a, grid, stream) : launch_t<D, false, false>(m, a, grid, stream);
+  if (a.rel || a.slopes) return cap ? launch_t<D, true, true>(m, bias, a, grid, stream) : launch_t<D, false, true>(m, bias, a, grid, stream);
+  return cap ? launch_t<D, true, false>(m, bias, a, grid, stream) : launch_t<D, false, false>(m, bias, a, grid, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_tree(const MaskedMaps& m, const TreeArgs& a, int head_dim, cudaStream_t stream) {
+cudaError_t launch_tree(const MaskedMaps& m, const CUtensorMap& bias, const TreeArgs& a, int head_dim, cudaStream_t stream) {
   int dev = 0;
   const int sms = current_device_sms(&dev);
   if (sms <= 0) return cudaErrorInvalidDevice;
   const long long items = (a.T / (2ll * a.tok_per_tile) + a.B) * a.Hkv * a.head_chunks;
   const long long tiles = ((long long)a.max_pages << a.log2_page) / KT + 1;
   const int grid = (int)std::min<long long>(std::min(sms, TREE_MAX_CTAS), items * tiles);
-  return head_dim == 128 ? launch_d<128>(m, a, grid, stream) : launch_d<64>(m, a, grid, stream);
+  return head_dim == 128 ? launch_d<128>(m, bias, a, grid, stream) : launch_d<64>(m, bias, a, grid, stream);
 }
 
 }  // namespace ink
