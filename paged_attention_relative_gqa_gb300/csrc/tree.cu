@@ -117,29 +117,31 @@ struct TRSmem {
   static constexpr size_t kbad = items + TR_ITEMS * sizeof(TRItem);
   static constexpr size_t poison = kbad + TR_BAD * KW * 4;
   static constexpr size_t ml = poison + TR_ITEMS * 16;           // [2 chains][128 rows] float2
-  static constexpr size_t misc = ml + 2 * TREE_ROWS * 8;
+  static constexpr size_t tokens = ml + 2 * TREE_ROWS * 8;       // [2 chains][128] positions (with a bias)
+  static constexpr size_t misc = tokens + (BIAS ? 2 * TREE_ROWS * 4 : 0);
   static constexpr size_t alloc = misc + 16;   // (no room to align within: the array itself has to be)
   static_assert(alloc <= 227 * 1024, "shared memory budget");
 };
 
-// Bounded wait of a whole warp, with one answer for all its lanes (inline: a call would keep the registers
-// from being split).
+// What runs once in a while is kept out of line: the kernel's code is longer than the caches its instructions come from.
+
+__device__ __noinline__ bool tr_wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint32_t* err,
+                                          unsigned long long wait_ns) {
+  if (*abort_flag) return false;
+  if (mbar_wait_limit(bar, parity, wait_ns)) return true;
+  record_error(err, INK_DEVERR_WAIT_TIMEOUT);
+  *abort_flag = 1;
+  return false;
+}
+
+// Bounded wait of a whole warp, with one answer for all its lanes.
 __device__ __forceinline__ bool tr_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, const TreeArgs& a) {
-  bool ok = mbar_probe(bar, parity, a.wait_ns);
-  if (!ok && !*abort_flag) {
-    ok = mbar_wait_limit(bar, parity, a.wait_ns);
-    if (!ok) {
-      record_error(a.err, INK_DEVERR_WAIT_TIMEOUT);
-      *abort_flag = 1;
-    }
-  }
-  return __all_sync(0xffffffffu, ok);
+  return __all_sync(0xffffffffu, mbar_test_wait(bar, parity) || tr_wait_slow(bar, parity, abort_flag, a.err, a.wait_ns));
 }
 
 // A sequence's rows and keys; tiles == 0: none of its rows sees a key (or it has none).
 struct TRSeq {
   int c0, n, L, lo, hi, tiles;
-  int far;        // tiles at the start whose distances are all E - 1 or more: no bias is loaded for them
   uint32_t bad;   // error bits; BAD_ROWS: its rows are not touched
 
   __device__ __forceinline__ void load(const TreeArgs& a, int b) {
@@ -147,7 +149,7 @@ struct TRSeq {
     const int c1 = __ldg(a.cu_q + b + 1);
     L = __ldg(a.seq_lens + b);
     n = c1 - c0;
-    lo = hi = tiles = far = 0;
+    lo = hi = tiles = 0;
     bad = 0;
     if (c0 < 0 || c1 > a.T || c1 < c0) {
       bad = INK_DEVERR_BAD_ROWS;
@@ -164,31 +166,26 @@ struct TRSeq {
       hi = (int)min((long long)L, cap);
       lo = a.W > 0 ? max(0, L - n - a.W + 1) : 0;
       if (lo < hi) tiles = (hi - 1) / KT - lo / KT + 1;
-      const long long flat = (long long)(L - n) - (KT - 1) - (a.E - 1);   // last first key of such a tile
-      far = !a.rel ? tiles : flat < 0 ? 0 : min(tiles, max(0, (int)(flat / KT) - lo / KT + 1));
     }
   }
 };
 
 // The row of tiles, walked by a whole warp: 32 sequences at a time in the lanes.  Divisions, which take as long as a load, are
-// made once per run: later pieces begin with their item.  It is measured in units, a tile each; where bias rows are loaded, two for
-// a tile with them (they are as many bytes as its K and V) and for the first one of an odd number of those without: runs and
-// items then begin and end at even units, between tiles.
+// made once per run: later pieces begin with their item.
 struct TRWalk {
-  long long base, incl, chunk, total;   // units before sequence cb; up to and with this lane's; of a run; of the 32
-  long long pos, end;                   // of this CTA's run, in units
-  int cb, per, items, units, cta;       // (units: of an item of this lane's sequence)
+  long long base, incl, chunk, total;   // tiles before sequence cb; up to and with this lane's; of a run; of the 32
+  long long pos, end;                   // of this CTA's run
+  int cb, per, items, cta;
   int src, groups, left;                // the sequence's lane; its items; of these not begun
   int kvh, hc, item;                    // the next one
   TRSeq s;
 
-  __device__ __forceinline__ void load(const TreeArgs& a, int lane) {
+  __device__ __noinline__ void load(const TreeArgs& a, int lane) {
     const int b = cb + lane;
-    s.tiles = s.n = s.far = 0;
+    s.tiles = s.n = 0;
     if (b < a.B) s.load(a, b);
     items = (s.n + 2 * a.tok_per_tile - 1) / (2 * a.tok_per_tile);
-    units = a.rel ? 2 * s.tiles - s.far + (s.far & 1) : s.tiles;
-    incl = (long long)units * items * per;
+    incl = (long long)s.tiles * items * per;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long v = __shfl_up_sync(0xffffffffu, incl, o);
@@ -209,13 +206,12 @@ struct TRWalk {
     base = 0;
     left = 0;
     chunk = max((all + gridDim.x - 1) / (long long)gridDim.x, (long long)TR_MIN_TILES);
-    if (a.rel) chunk += chunk & 1;
     pos = min(cta * chunk, all);
     end = min(pos + chunk, all);
   }
 
   // The next piece of the run; first: the CTA where its item begins.
-  __device__ __forceinline__ TRPart next(const TreeArgs& a, int lane, int& first) {
+  __device__ __noinline__ TRPart next(const TreeArgs& a, int lane, int& first) {
     int x0 = 0;
     first = cta;
     if (left == 0) {   // of another sequence than the one before
@@ -225,13 +221,13 @@ struct TRWalk {
         load(a, lane);
       }
       src = __ffs(__ballot_sync(0xffffffffu, pos < base + incl)) - 1;
-      const int ni = __shfl_sync(0xffffffffu, items, src), u = __shfl_sync(0xffffffffu, units, src);
+      const int ni = __shfl_sync(0xffffffffu, items, src), tiles = __shfl_sync(0xffffffffu, s.tiles, src);
       groups = ni * per;
-      const long long off = pos - (base + __shfl_sync(0xffffffffu, incl - (long long)units * items * per, src));
+      const long long off = pos - (base + __shfl_sync(0xffffffffu, incl - (long long)s.tiles * items * per, src));
       int gi = 0;
       if (off > 0) {   // the run begins within a sequence
-        gi = (int)(off / u);
-        x0 = (int)(off - (long long)gi * u);
+        gi = (int)(off / tiles);
+        x0 = (int)(off - (long long)gi * tiles);
         first = (int)((pos - x0) / chunk);
       }
       left = groups - gi;
@@ -240,10 +236,7 @@ struct TRWalk {
       kvh = hk / a.head_chunks;
       hc = hk - kvh * a.head_chunks;
     }
-    const int ni = __shfl_sync(0xffffffffu, items, src), u = __shfl_sync(0xffffffffu, units, src);
-    const int far = __shfl_sync(0xffffffffu, s.far, src), odd = a.rel ? far & 1 : 0;
-    // tiles before unit y of an item
-    auto tiles = [&](int y) { return y <= far + odd ? max(0, y - odd) : far + ((y - far - odd) >> 1); };
+    const int ni = __shfl_sync(0xffffffffu, items, src), tiles = __shfl_sync(0xffffffffu, s.tiles, src);
     TRPart w;
     w.b = cb + src;
     w.c0 = __shfl_sync(0xffffffffu, s.c0, src);
@@ -256,13 +249,12 @@ struct TRWalk {
     w.gh = min(a.heads_per_tile, a.G - hc * a.heads_per_tile);
     w.t0 = w.c0 + item * 2 * a.tok_per_tile;
     w.ntok = min(2 * a.tok_per_tile, w.n - item * 2 * a.tok_per_tile);
-    const int x1 = (int)min((long long)u, x0 + (end - pos));
-    w.kt0 = w.lo / KT + tiles(x0);
-    w.nt = tiles(x1) - tiles(x0);
-    const long long g1 = pos - x0 + u;
+    w.kt0 = w.lo / KT + x0;
+    w.nt = (int)min((long long)(tiles - x0), end - pos);
+    const long long g1 = pos - x0 + tiles;
     w.parts = (g1 <= end ? cta : (int)((g1 - 1) / chunk)) - first + 1;
     w.place = 2 * cta + (cta == first ? 1 : 0);
-    pos += x1 - x0;
+    pos += w.nt;
     --left;
     if (++item == ni) {
       item = 0;
@@ -285,7 +277,7 @@ struct TRRow {
   __device__ __forceinline__ uint32_t word(const TreeArgs& a, int i) const {
     return i == 0 ? w0 : i > 0 && i < a.words ? __ldg(bits + i) : 0u;
   }
-  __device__ __forceinline__ uint32_t sees(const TreeArgs& a, int base) const {
+  __device__ __noinline__ uint32_t sees(const TreeArgs& a, int base) const {
     const int x0 = max(lo - base, 0), x1 = min(hist - base, 32);
     uint32_t vis = x1 > x0 ? (0xffffffffu >> (32 - (x1 - x0))) << x0 : 0u;
     const int j0 = base - H;
@@ -326,6 +318,30 @@ __device__ __forceinline__ TRBias tr_bias(const TreeArgs& a, const TRPart& it, i
   if (min(it.H, it.hi) - k0 < KT) return Elements;
   if (!a.rel || it.H - (k0 + KT - 1) >= a.E - 1) return NoLoad;
   return a.rel_rows ? Boxes : Elements;
+}
+
+// Infinities and NaN of the keys that this row sees, in tiles first to last, into channels [c0, c1) of what it has stored: its
+// output, or its partial (channel c at float 4 (c / 4) rows + c % 4).
+__device__ __noinline__ void tr_infinite(const TreeArgs& a, const TRPart& it, const TRRow& row, int first, int last, int c0, int c1,
+                                         __nv_bfloat16* out, float* part, int D) {
+  for (int base = first * KT; base < (last + 1) * KT; base += 32)
+    for (uint32_t vis = row.sees(a, base); vis; vis &= vis - 1) {
+      const int kk = base + __ffs(vis) - 1;
+      const int page = __ldg(a.block_table + (size_t)it.b * a.max_pages + (kk >> a.log2_page));
+      if (page < 0 || page >= a.num_pages) continue;
+      const uint16_t* v = static_cast<const uint16_t*>(a.v) +
+                          ((((size_t)page * a.Hkv + it.kvh) << a.log2_page) + (kk & ((1 << a.log2_page) - 1))) * D;
+      for (int c = c0; c < c1; ++c) {
+        const uint32_t x = (uint32_t)__ldg(v + c) << 16;
+        if ((x & 0x7F800000u) != 0x7F800000u) continue;
+        if (out) {
+          out[c] = __float2bfloat16(__bfloat162float(out[c]) + __uint_as_float(x));
+        } else {
+          float* y = part + (size_t)(c >> 2) * 4 * TREE_ROWS + (c & 3);
+          __stcg(y, __ldcg(y) + __uint_as_float(x));
+        }
+      }
+    }
 }
 
 __device__ __forceinline__ uint64_t tr_mul(uint64_t a, uint64_t b) {
@@ -578,8 +594,8 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
         if (!go) break;
         if (nt > 0) {
           tc_fence_after();
-          issue_s(0);
-          if (S::AHEAD == 2 && go && nt > 1) issue_s(1);
+#pragma unroll 1
+          for (int j = 0; j < S::AHEAD && j < nt && go; ++j) issue_s(j);
         } else if (!BIAS) {            // (the only tile of a Split item is the other chain's)
           if (lane == 0) mbar_arrive(&q_empty[qs]);
           __syncwarp();
@@ -779,7 +795,12 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
       const int h = warp - 13;
       uint8_t* boxes = bias + h * TREE_BIAS_BYTES;
       float* buf = reinterpret_cast<float*>(boxes);
-      const int last = a.E - 1, size = a.rel_bf16 ? 2 : 4;
+      const int size = a.rel_bf16 ? 2 : 4;
+      // without a tensor the first position is loaded instead, and not used
+      const void* rel = a.rel ? a.rel : a.positions;
+      const int pitch = a.rel ? a.E : 0, last = a.rel ? a.E - 1 : 0;
+      const float per_head = 1.f / a.heads_per_tile;   // (rows are few: no rounding shows)
+      int* at_s = reinterpret_cast<int*>(smem + L_::tokens) + h * TREE_ROWS;   // positions of the part's tokens
       if (lane == 0 && a.rel_rows) prefetch_tensormap(&tmB);
       uint32_t fills = 0;
       bool go = true;
@@ -788,10 +809,14 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
         const TRPart& it = item.of(h);
         const int tok0 = item.mode == Pair ? h * a.tok_per_tile : 0;
         const int rows = min(a.tok_per_tile, it.ntok - tok0) * a.heads_per_tile;
-        const int tokens = min(a.tok_per_tile, it.ntok - tok0);
+        const int tokens = min(a.tok_per_tile, it.ntok - tok0), first_t = it.t0 + tok0;
         int pt[4];                         // positions of this lane's tokens lane, lane + 32, ...
 #pragma unroll
-        for (int x = 0; x < 4; ++x) pt[x] = max(__ldg(a.positions + it.t0 + tok0 + min(32 * x + lane, tokens - 1)), it.H);
+        for (int x = 0; x < 4; ++x) {
+          pt[x] = max(__ldg(a.positions + it.t0 + tok0 + min(32 * x + lane, tokens - 1)), it.H);
+          at_s[32 * x + lane] = pt[x];
+        }
+        __syncwarp();
         for (int j = 0; j < it.nt && go; ++j) {
           const int k0 = (it.kt0 + j * item.step()) * KT;
           const TRBias how = tr_bias(a, it, k0);
@@ -825,38 +850,33 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
           }
           // (all loads of a batch first, from rows that are there: what is not seen is masked)
           auto fill = [&](auto load) {
-            int i = 0, hd = 0;
 #pragma unroll 1
             for (int r = 0; r < rows; r += 8) {
-              float v[8][2], far[8][2], slope[8];
+              float v[8][2];
 #pragma unroll
               for (int y = 0; y < 8; ++y) {
-                const int ic = min(i, 127), p0 = __shfl_sync(0xffffffffu, ic & 32 ? pt[1] : pt[0], ic & 31);
-                const int p1 = __shfl_sync(0xffffffffu, ic & 32 ? pt[3] : pt[2], ic & 31), p = ic & 64 ? p1 : p0;
-                const int head = it.h0 + min(hd, it.gh - 1);
-                const size_t row = ((size_t)(it.t0 + min(tok0 + i, it.ntok - 1)) * a.Hq + head) * a.E;
-                slope[y] = a.slopes ? __ldg(a.slopes + head) : 0.f;
+                const int rr = min(r + y, rows - 1), i = (int)(((float)rr + 0.5f) * per_head), hd = min(rr - i * a.heads_per_tile, it.gh - 1);
+                const int t = first_t + i, p = at_s[i];
+                const float slope = a.slopes ? __ldg(a.slopes + it.h0 + hd) : 0.f;
+                const size_t row = ((size_t)t * a.Hq + it.h0 + hd) * pitch;
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                   const int d = abs(p - pk[x]);
-                  far[y][x] = (float)d;
-                  v[y][x] = load(row + min(d, last));
-                }
-                if (++hd == a.heads_per_tile) {
-                  hd = 0;
-                  ++i;
+                  v[y][x] = fmaf(-slope, (float)d, load(row + min(d, last)));
                 }
               }
 #pragma unroll
               for (int y = 0; y < 8; ++y) {
-                buf[(r + y) * S::ELEMENTS + KT - 1 - lane] = fmaf(-slope[y], far[y][0], v[y][0]);
-                buf[(r + y) * S::ELEMENTS + KT - 33 - lane] = fmaf(-slope[y], far[y][1], v[y][1]);
+                buf[(r + y) * S::ELEMENTS + KT - 1 - lane] = v[y][0];
+                buf[(r + y) * S::ELEMENTS + KT - 33 - lane] = v[y][1];
               }
             }
           };
-          if (!a.rel) fill([](size_t) { return 0.f; });
-          else if (a.rel_bf16) fill([&](size_t x) { return __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t*>(a.rel) + x) << 16); });
-          else fill([&](size_t x) { return __ldg(static_cast<const float*>(a.rel) + x); });
+          if (a.rel_bf16) fill([&](size_t x) { return __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t*>(a.rel) + x) << 16); });
+          else fill([&](size_t x) {
+            const float v = __ldg(static_cast<const float*>(rel) + x);
+            return a.rel ? v : 0.f;
+          });
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // (copies may write here next)
           mbar_arrive(&bias_full[h]);
           __syncwarp();
@@ -1216,27 +1236,6 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
 #pragma unroll
           for (int x = 0; x < 32; ++x) ov[x] = nothing ? 0u : __float_as_uint(__uint_as_float(ov[x]) * g0);
         }
-        if (plast >= 0 && rv) {
-          const TRRow row = my_row();
-          // infinities and NaN of the keys this row sees, from the first tile to the last that holds one
-#pragma unroll 1
-          for (int tile = pfirst; tile <= plast; ++tile)
-#pragma unroll 1
-            for (int w = 0; w < KW; ++w)
-#pragma unroll 1
-              for (uint32_t vis = row.sees(a, tile * KT + 32 * w); vis; vis &= vis - 1) {
-                const int kk = tile * KT + 32 * w + __ffs(vis) - 1;
-                const int page = __ldg(a.block_table + (size_t)it.b * a.max_pages + (kk >> a.log2_page));
-                if (page < 0 || page >= a.num_pages) continue;
-                const uint16_t* vp = static_cast<const uint16_t*>(a.v) +
-                                     ((((size_t)page * a.Hkv + it.kvh) << a.log2_page) + (kk & (P - 1))) * D + c2 * 32;
-#pragma unroll
-                for (int x = 0; x < 32; ++x) {
-                  const uint32_t v = (uint32_t)__ldg(vp + x) << 16;
-                  if ((v & 0x7F800000u) == 0x7F800000u) ov[x] = __float_as_uint(__uint_as_float(ov[x]) + __uint_as_float(v));
-                }
-              }
-        }
         if (!whole) {
 #pragma unroll
           for (int x = 0; x < 8 && rv; ++x)
@@ -1253,6 +1252,9 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
                               pack_bf16(__uint_as_float(ov[8 * x + 6]), __uint_as_float(ov[8 * x + 7])));
         }
       }
+      if (plast >= 0 && rv)
+        tr_infinite(a, it, my_row(), pfirst, plast, 32 * c_first, 32 * c_end, whole ? out + orow * D : nullptr,
+                    reinterpret_cast<float*>(part_o), D);
       if (!merge || h == 0) {
         if (!whole) __stcg(reinterpret_cast<float2*>(a.part_ml) + ((size_t)it.place * 2 + rt) * TREE_ROWS + r, make_float2(M, l));
         else if (rv && a.lse) a.lse[orow] = nothing ? -INFINITY : M * LN2 + logf(l);
