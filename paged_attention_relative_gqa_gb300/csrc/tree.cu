@@ -139,6 +139,13 @@ __device__ __forceinline__ bool tr_wait(uint64_t* bar, uint32_t parity, volatile
   return __all_sync(0xffffffffu, mbar_test_wait(bar, parity) || tr_wait_slow(bar, parity, abort_flag, a.err, a.wait_ns));
 }
 
+// a / b of numbers that are not negative: tiles are fewer than 2^32 in all but the longest calls, and a 64-bit division takes ten
+// times as long as one of 32 bits.
+__device__ __forceinline__ long long tr_div(long long a, long long b) {
+  if (((unsigned long long)(a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
+}
+
 // A sequence's rows and keys; tiles == 0: none of its rows sees a key (or it has none).
 struct TRSeq {
   int c0, n, L, lo, hi, tiles;
@@ -170,8 +177,8 @@ struct TRSeq {
   }
 };
 
-// The row of tiles, walked by a whole warp: 32 sequences at a time in the lanes.  Divisions, which take as long as a load, are
-// made once per run: later pieces begin with their item.
+// The row of tiles, walked by a whole warp: 32 sequences at a time in the lanes.  Divisions are made
+// once per run: later pieces begin with their item.
 struct TRWalk {
   long long base, incl, chunk, total;   // tiles before sequence cb; up to and with this lane's; of a run; of the 32
   long long pos, end;                   // of this CTA's run
@@ -180,7 +187,7 @@ struct TRWalk {
   int kvh, hc, item;                    // the next one
   TRSeq s;
 
-  __device__ __noinline__ void load(const TreeArgs& a, int lane) {
+  __device__ __forceinline__ void load(const TreeArgs& a, int lane) {
     const int b = cb + lane;
     s.tiles = s.n = 0;
     if (b < a.B) s.load(a, b);
@@ -205,13 +212,13 @@ struct TRWalk {
     cb = 0;
     base = 0;
     left = 0;
-    chunk = max((all + gridDim.x - 1) / (long long)gridDim.x, (long long)TR_MIN_TILES);
+    chunk = max(tr_div(all + gridDim.x - 1, gridDim.x), (long long)TR_MIN_TILES);
     pos = min(cta * chunk, all);
     end = min(pos + chunk, all);
   }
 
   // The next piece of the run; first: the CTA where its item begins.
-  __device__ __noinline__ TRPart next(const TreeArgs& a, int lane, int& first) {
+  __device__ __forceinline__ TRPart next(const TreeArgs& a, int lane, int& first) {
     int x0 = 0;
     first = cta;
     if (left == 0) {   // of another sequence than the one before
@@ -226,9 +233,9 @@ struct TRWalk {
       const long long off = pos - (base + __shfl_sync(0xffffffffu, incl - (long long)s.tiles * items * per, src));
       int gi = 0;
       if (off > 0) {   // the run begins within a sequence
-        gi = (int)(off / tiles);
+        gi = (int)tr_div(off, tiles);
         x0 = (int)(off - (long long)gi * tiles);
-        first = (int)((pos - x0) / chunk);
+        first = (int)tr_div(pos - x0, chunk);
       }
       left = groups - gi;
       const int hk = gi / ni;
@@ -252,7 +259,7 @@ struct TRWalk {
     w.kt0 = w.lo / KT + x0;
     w.nt = (int)min((long long)(tiles - x0), end - pos);
     const long long g1 = pos - x0 + tiles;
-    w.parts = (g1 <= end ? cta : (int)((g1 - 1) / chunk)) - first + 1;
+    w.parts = (g1 <= end ? cta : (int)tr_div(g1 - 1, chunk)) - first + 1;
     w.place = 2 * cta + (cta == first ? 1 : 0);
     pos += w.nt;
     --left;
@@ -277,7 +284,7 @@ struct TRRow {
   __device__ __forceinline__ uint32_t word(const TreeArgs& a, int i) const {
     return i == 0 ? w0 : i > 0 && i < a.words ? __ldg(bits + i) : 0u;
   }
-  __device__ __noinline__ uint32_t sees(const TreeArgs& a, int base) const {
+  __device__ __forceinline__ uint32_t sees(const TreeArgs& a, int base) const {
     const int x0 = max(lo - base, 0), x1 = min(hist - base, 32);
     uint32_t vis = x1 > x0 ? (0xffffffffu >> (32 - (x1 - x0))) << x0 : 0u;
     const int j0 = base - H;
