@@ -512,16 +512,23 @@ def _run_on(device, fn, args, where):
         raise InkError(code, where)
 
 
-def _held(t, dtype, shape, device) -> bool:
-    return (isinstance(t, torch.Tensor) and t.dtype is dtype and (shape is None or t.shape == shape)
-            and t.get_device() == device and t.is_contiguous())
-
-
-def _need(device, *args):
-    """Every (tensor, name, dtype, shape or None) is what it has to be, on `device`."""
-    for t, name, dtype, shape in args:
-        if not _held(t, dtype, shape, device):
-            _refuse(device, (t, name, dtype, shape))
+def _need(device, ints, *args):
+    """Every tensor is contiguous and on `device`: `ints` ((tensor, name, shape) each) int32, `args` ((tensor, name, dtype,
+    shape or None) each) what they say.  (Plain loops over cheap checks: a step makes these calls for every layer.)"""
+    try:
+        for t, _, shape in ints:
+            if t.dtype is not _I32 or t.shape != shape or t.get_device() != device or not t.is_contiguous():
+                break
+        else:
+            for t, _, dtype, shape in args:
+                if (t.dtype is not dtype or (shape is not None and t.shape != shape) or t.get_device() != device
+                        or not t.is_contiguous()):
+                    break
+            else:
+                return
+    except AttributeError:
+        pass
+    _refuse(device, *((t, name, _I32, shape) for t, name, shape in ints), *args)
 
 
 def _rows_of(t, name) -> tuple:
@@ -541,9 +548,9 @@ def inkling_attn_tree_plan(params, cu_q_lens, seq_lens, parents, positions, ance
     device, T = _rows_of(parents, "parents")
     B = params.num_seqs
     words = ancestors.shape[1] if isinstance(ancestors, torch.Tensor) and ancestors.dim() == 2 else 1
-    _need(device, (parents, "parents", _I32, (T,)), (cu_q_lens, "cu_q_lens", _I32, (B + 1,)),
-          (seq_lens, "seq_lens", _I32, (B,)), (positions, "positions", _I32, (T,)),
-          (ancestors, "ancestors", _I32, (T, words)), (workspace, "workspace", _U8, None))
+    _need(device, ((parents, "parents", (T,)), (cu_q_lens, "cu_q_lens", (B + 1,)), (seq_lens, "seq_lens", (B,)),
+                   (positions, "positions", (T,)), (ancestors, "ancestors", (T, words))),
+          (workspace, "workspace", _U8, None))
     if T == 0 or B == 0:   # (empty tensors have no address)
         return positions, ancestors
     args = (ctypes.byref(params), cu_q_lens.data_ptr(), T, seq_lens.data_ptr(), parents.data_ptr(), words,
@@ -579,8 +586,8 @@ def inkling_attn_tree(params, q, cu_q_lens, k_cache, v_cache, block_table, seq_l
         _refuse(device, (q, "q", _BF16, rows))
     _pools_hold(params, device, rows, q, out, k_cache, v_cache, block_table, seq_lens, workspace)
     words = ancestors.shape[1] if isinstance(ancestors, torch.Tensor) and ancestors.dim() == 2 else 1
-    _need(device, (cu_q_lens, "cu_q_lens", _I32, (params.num_seqs + 1,)), (positions, "positions", _I32, (T,)),
-          (ancestors, "ancestors", _I32, (T, words)))
+    _need(device, ((cu_q_lens, "cu_q_lens", (params.num_seqs + 1,)), (positions, "positions", (T,)),
+                   (ancestors, "ancestors", (T, words))))
     bf16 = isinstance(rel_logits, torch.Tensor) and rel_logits.dtype is _BF16
     rel = _opt(rel_logits, "rel_logits", _BF16 if bf16 else _F32, (T, Hq, params.rel_extent), device)
     tree = ink_attn_tree_t(positions.data_ptr(), ancestors.data_ptr(), words)
@@ -604,13 +611,11 @@ def inkling_attn_kv_conv_write_tree(params, k_new, v_new, cu_q_lens, seq_lens, b
     ks = int(w_k.shape[-1]) if isinstance(w_k, torch.Tensor) and w_k.dim() == 3 else 1
     rows, taps, state = (T, Hkv, D), (Hkv, D, ks), (B, ks - 1, Hkv, D)
     pool = (params.num_pages, Hkv, params.page_size, D)
-    _need(device, (k_new, "k_new", _BF16, rows), (v_new, "v_new", _BF16, rows), (cu_q_lens, "cu_q_lens", _I32, (B + 1,)),
-          (seq_lens, "seq_lens", _I32, (B,)), (block_table, "block_table", _I32, (B, params.max_pages_per_seq)),
-          (parents, "parents", _I32, (T,)), (w_k, "w_k", _F32, taps), (w_v, "w_v", _F32, taps),
-          (k_cache, "k_cache", _BF16, pool), (v_cache, "v_cache", _BF16, pool),
-          (workspace, "workspace", _U8, None))
-    if ks > 1:
-        _need(device, (state_k_in, "state_k_in", _BF16, state), (state_v_in, "state_v_in", _BF16, state))
+    states = ((state_k_in, "state_k_in", _BF16, state), (state_v_in, "state_v_in", _BF16, state)) if ks > 1 else ()
+    _need(device, ((cu_q_lens, "cu_q_lens", (B + 1,)), (seq_lens, "seq_lens", (B,)), (parents, "parents", (T,)),
+                   (block_table, "block_table", (B, params.max_pages_per_seq))),
+          (k_new, "k_new", _BF16, rows), (v_new, "v_new", _BF16, rows), (w_k, "w_k", _F32, taps), (w_v, "w_v", _F32, taps),
+          (k_cache, "k_cache", _BF16, pool), (v_cache, "v_cache", _BF16, pool), (workspace, "workspace", _U8, None), *states)
     if T == 0 or B == 0:   # (empty tensors have no address)
         return k_cache, v_cache
     args = (ctypes.byref(params), k_new.data_ptr(), v_new.data_ptr(), cu_q_lens.data_ptr(), T, seq_lens.data_ptr(),
@@ -630,8 +635,8 @@ def inkling_attn_kv_conv_state_tree(params, k_new, v_new, cu_q_lens, path, path_
     keep = state_k_in.shape[1] if isinstance(state_k_in, torch.Tensor) and state_k_in.dim() == 4 else 1
     width = path.shape[1] if isinstance(path, torch.Tensor) and path.dim() == 2 else 1
     rows, state = (T, Hkv, D), (B, keep, Hkv, D)
-    _need(device, (k_new, "k_new", _BF16, rows), (v_new, "v_new", _BF16, rows), (cu_q_lens, "cu_q_lens", _I32, (B + 1,)),
-          (path, "path", _I32, (B, width)), (path_lens, "path_lens", _I32, (B,)), (state_k_in, "state_k_in", _BF16, state),
+    _need(device, ((cu_q_lens, "cu_q_lens", (B + 1,)), (path, "path", (B, width)), (path_lens, "path_lens", (B,))),
+          (k_new, "k_new", _BF16, rows), (v_new, "v_new", _BF16, rows), (state_k_in, "state_k_in", _BF16, state),
           (state_v_in, "state_v_in", _BF16, state), (state_k_out, "state_k_out", _BF16, state),
           (state_v_out, "state_v_out", _BF16, state), (workspace, "workspace", _U8, None))
     if B == 0 or keep == 0:   # (empty tensors have no address)
@@ -655,7 +660,7 @@ class TreePools:
             raise ValueError("k_caches and v_caches must be equally many, one at least")
         self.device, _ = _rows_of(self.k_caches[0], "k_caches")
         self.shape = (params.num_pages, params.num_kv_heads, params.page_size, params.head_dim)
-        _need(self.device, *((t, name, _BF16, self.shape) for name, ts in (("k_caches", self.k_caches),
+        _need(self.device, (), *((t, name, _BF16, self.shape) for name, ts in (("k_caches", self.k_caches),
                                                                            ("v_caches", self.v_caches)) for t in ts))
         pointers = ctypes.c_void_p * len(self.k_caches)
         self.k_ptrs = pointers(*(t.data_ptr() for t in self.k_caches))
@@ -678,9 +683,9 @@ def inkling_attn_tree_commit(params, cu_q_lens, seq_lens, block_table, path, pat
     if pools.shape != shape:
         raise ValueError(f"pools have shape {pools.shape}, params say {shape}")
     width = path.shape[1] if isinstance(path, torch.Tensor) and path.dim() == 2 else 1
-    _need(device, (cu_q_lens, "cu_q_lens", _I32, (B + 1,)), (seq_lens, "seq_lens", _I32, (B,)),
-          (block_table, "block_table", _I32, (B, params.max_pages_per_seq)), (path, "path", _I32, (B, width)),
-          (path_lens, "path_lens", _I32, (B,)), (workspace, "workspace", _U8, None))
+    _need(device, ((cu_q_lens, "cu_q_lens", (B + 1,)), (seq_lens, "seq_lens", (B,)), (path, "path", (B, width)),
+                   (path_lens, "path_lens", (B,)), (block_table, "block_table", (B, params.max_pages_per_seq))),
+          (workspace, "workspace", _U8, None))
     args = (ctypes.byref(params), cu_q_lens.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(), path.data_ptr(),
             path_lens.data_ptr(), width, len(pools.k_caches), pools.k_ptrs, pools.v_ptrs,
             _opt(seq_lens_out, "seq_lens_out", _I32, (B,), device), workspace.data_ptr(), workspace.numel(),
