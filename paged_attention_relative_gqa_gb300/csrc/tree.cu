@@ -331,7 +331,8 @@ __device__ __forceinline__ TRBias tr_bias(const TreeArgs& a, const TRPart& it, i
 // output, or its partial (channel c at float 4 (c / 4) rows + c % 4).
 __device__ __noinline__ void tr_infinite(const TreeArgs& a, const TRPart& it, const TRRow& row, int first, int last, int c0, int c1,
                                          __nv_bfloat16* out, float* part, int D) {
-  for (int base = first * KT; base < (last + 1) * KT; base += 32)
+  for (int w = 0; w < (last + 1 - first) * KW; ++w) {
+    const int base = first * KT + 32 * w;
     for (uint32_t vis = row.sees(a, base); vis; vis &= vis - 1) {
       const int kk = base + __ffs(vis) - 1;
       const int page = __ldg(a.block_table + (size_t)it.b * a.max_pages + (kk >> a.log2_page));
@@ -349,6 +350,7 @@ __device__ __noinline__ void tr_infinite(const TreeArgs& a, const TRPart& it, co
         }
       }
     }
+  }
 }
 
 __device__ __forceinline__ uint64_t tr_mul(uint64_t a, uint64_t b) {
