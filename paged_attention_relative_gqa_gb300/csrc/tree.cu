@@ -6,31 +6,43 @@
 //
 // A few tokens against a long history: the bytes of K and V, and of the bias rows where there is a bias tensor, bound
 // it, so they have to flow evenly over the SMs whatever the lengths are.  The rows of a tile of 128 (the M of an MMA) are (token,
-// query head) pairs of one sequence and KV head, tokens outermost; an item is up to two row tiles.  All key tiles of all items
-// stand in one row, tiles of an item side by side, and every CTA takes an equal run of them, found on
+// query head) pairs of one sequence and KV head, tokens outermost; an item is up to two row tiles.  All tiles of 64 keys of all
+// items stand in one row, tiles of an item side by side, and every CTA takes an equal run of them, found on
 // the device from the lengths (a graph replays with other ones).  A run cuts two items at most; pieces of
 // a cut item leave O, maximum and sum in fp32, two places a CTA, and a second kernel joins them in order, spread over
 // all SMs (one CTA that joined the 20 pieces of an item of a single long sequence would take as long as six key tiles).
 //
-// Tensor memory: two chains, each S (KT fp32 columns, with P, the bf16 numerators, over its first half once S is in
-// registers) and O (D columns).  An item of two row tiles gives a chain to each; an item of one (up to 16 tokens of 8 heads)
-// gives the even key tiles to one chain and the odd ones to the other, with maxima and sums of
-// their own that are joined at the end: one row tile's serial chain (scores to registers, softmax, P V, the next S,
-// four hand-overs: about 2650 clocks for 128 keys) is as long as the bytes of its tiles take to arrive.
+// Two chains a CTA, each S (64 fp32 columns of tensor memory, with P, the bf16 numerators, over its first half once S is in
+// registers) and O (D columns).  An item of two row tiles gives a chain to each; two pieces of one row tile (up to 16 tokens of 8
+// heads) run side by side; a piece alone gives its even key tiles to one chain and the odd ones to the other, with maxima and sums
+// of their own that are joined at the end.  One row tile's serial chain (scores to registers, softmax, P V, the next S and the
+// hand-overs between) takes as long as the bytes of its tiles take to arrive, so one chain alone would starve the memory.
+// Without a bias a chain has two S, so that the tensor cores never wait for a softmax to hand the next tile out; 128 keys a tile
+// with one S took 5 % longer, and 35 % with the scores read twice.  With a bias the second S is Q's place, and shared memory holds
+// the bias instead of Q.
 //
 // Warps:
 //   0-3, 4-7  softmax of chain 0 and 1, a thread per row
-//   8   K and V producer: TMA boxes of whole pages or tiles, table entries 32 at a time in lanes
-//   9   MMA issue
-//   10  scheduler: cuts the run into pieces, publishes them in shared memory, loads their Q tiles by TMA
-//   11  V check: in tiles that not every row sees whole, rows of V that nobody sees are zeroed and so is
-//       every infinity or NaN (0 * NaN would reach rows that do not see the key); rows that do see one get it back at the end
-//   12-15 (with a bias) bias, see below
-// The bias of a row has no alignment: it starts at the row's distance from the tile.  Within the history it is KT values side by
+//   8         K producer: TMA boxes of whole pages or tiles, table entries 32 at a time in lanes
+//   9, 12     MMA issue of chain 0 and 1 (one warp for both had each chain wait for the other's barriers)
+//   10        scheduler: cuts the run into pieces, publishes them in shared memory, loads their Q tiles by TMA
+//   11        V check: in tiles that not every row sees whole, rows of V that nobody sees are zeroed and so is
+//             every infinity or NaN (0 * NaN would reach rows that do not see the key); rows that do see one get it back at the end
+//   13        V producer; with a bias 13 and 14 bring the bias of chain 0 and 1, and 15 V
+// The bias of a row has no alignment: it starts at the row's distance from the tile.  Within the history it is 64 values side by
 // side, and all heads of a token start at the same distance: one TMA box a token brings them from the 16-byte boundary before
-// them (96 rows by a bulk copy each: 5,000 clocks).  Tiles whose distances are all E - 1 or more take one value a row.  Behind
-// the history distances have no order, and a bias warp brings them element by element, a lane a key.
+// them (128 rows by a bulk copy each: 5,000 clocks of issue).  Tiles whose distances are all E - 1 or more take one value a row,
+// which changes no order among a row's scores: they stay as the tensor cores left them, and the value joins the exponent.
+// Behind the history distances have no order, and a bias warp brings them element by element, a lane a key.
 // Every wait is bounded; after a timeout the CTA records it, stops issuing, waits for what is in flight and exits.
+//
+// Measured (GPU time alone; 64 query heads, D = 128): 32 trees of up to 16 tokens against up to 16 K keys, 8 KV heads, 252 us
+// (6.5 TB/s), capped 273, with slopes 440, D = 64 187; 4 of up to 16 against 64 K 140 us (5.8 TB/s); 4 of up to 61 (two items that
+// read K and V each for themselves) 282 us, 0.89 PFLOP/s: 64 keys of both chains take 2,000 clocks, of which their softmax warps
+// are busy 1,850 and the tensor cores 1,300;
+// 16 of up to 16 against 16 K with 4,096 fp32 distances 221 us (147 at the rate of a copy); 64 of up to 8 in a window of 512 with
+// 512 distances 138 us (49), without 76 (42): items of nine tiles, whose start, masks, last tile and output run code that the
+// instruction cache does not hold from one item to the next (a quarter of its requests miss, against 6 % on long histories).
 #include <algorithm>
 #include <climits>
 
@@ -205,6 +217,7 @@ struct TRWalk {
     per = a.Hkv * a.head_chunks;
     cta = (int)blockIdx.x;
     long long all = 0;
+#pragma unroll 1
     for (cb = ((a.B - 1) >> 5) << 5; cb >= 0; cb -= 32) {
       load(a, lane);
       all += total;
@@ -222,6 +235,7 @@ struct TRWalk {
     int x0 = 0;
     first = cta;
     if (left == 0) {   // of another sequence than the one before
+#pragma unroll 1
       while (pos >= base + total) {
         base += total;
         cb += 32;
@@ -292,6 +306,7 @@ struct TRRow {
       uint32_t t = __funnelshift_r(word(a, j0 >> 5), word(a, (j0 >> 5) + 1), j0 & 31);
       if (nlim - j0 < 32) t &= (1u << (nlim - j0)) - 1u;
       if (cut)
+#pragma unroll 1
         for (uint32_t x = t; x; x &= x - 1) {
           const int c = __ffs(x) - 1;
           if (p - max(__ldg(a.positions + c0 + j0 + c), H) >= a.W) t &= ~(1u << c);
@@ -331,14 +346,17 @@ __device__ __forceinline__ TRBias tr_bias(const TreeArgs& a, const TRPart& it, i
 // output, or its partial (channel c at float 4 (c / 4) rows + c % 4).
 __device__ __noinline__ void tr_infinite(const TreeArgs& a, const TRPart& it, const TRRow& row, int first, int last, int c0, int c1,
                                          __nv_bfloat16* out, float* part, int D) {
+#pragma unroll 1
   for (int w = 0; w < (last + 1 - first) * KW; ++w) {
     const int base = first * KT + 32 * w;
+#pragma unroll 1
     for (uint32_t vis = row.sees(a, base); vis; vis &= vis - 1) {
       const int kk = base + __ffs(vis) - 1;
       const int page = __ldg(a.block_table + (size_t)it.b * a.max_pages + (kk >> a.log2_page));
       if (page < 0 || page >= a.num_pages) continue;
       const uint16_t* v = static_cast<const uint16_t*>(a.v) +
                           ((((size_t)page * a.Hkv + it.kvh) << a.log2_page) + (kk & ((1 << a.log2_page) - 1))) * D;
+#pragma unroll 1
       for (int c = c0; c < c1; ++c) {
         const uint32_t x = (uint32_t)__ldg(v + c) << 16;
         if ((x & 0x7F800000u) != 0x7F800000u) continue;
@@ -496,7 +514,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
           chunk_val[h] = __ldg(bt[h] + min(chunk_base[h] + lane, (hi[h] - 1) >> a.log2_page));
         }
         done_item(k);
-        for (int j = 0; j < longest && go; ++j)
+        for (int j = 0; j < longest && go; ++j)   // (the chains' tiles take turns)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           if (!go || j >= nt[h]) continue;
@@ -519,6 +537,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
           if (lane == 0) {
             if (kv == 0) {   // keys of this tile whose page is outside the pool
               uint64_t bad = 0;
+#pragma unroll 1
               for (uint32_t mm = bmask; mm; mm &= mm - 1) bad |= (~0ull >> (64 - seg)) << ((__ffs(mm) - 1) * seg);
               *reinterpret_cast<uint64_t*>(kbad + x % TR_BAD * KW) = bad;
               if (bmask) record_error(a.err, INK_DEVERR_PAGE_OUT_OF_RANGE);
@@ -650,30 +669,35 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
         // all rows see the keys from the largest first one on
         w.lo_max = 0;
         if (a.W > 0) {
+#pragma unroll 1
           for (int i = lane; i < w.ntok; i += 32) w.lo_max = max(w.lo_max, max(__ldg(a.positions + w.t0 + i), w.H) - a.W + 1);
           w.lo_max = __reduce_max_sync(0xffffffffu, w.lo_max);
         }
         return w;
       };
       TRPart next;
-      bool have = false;                 // next was looked at, and is an item of its own
+      bool have = false;                 // next was looked at, and did not go beside the one before
       for (int k = 0;; ++k) {
         const int sl = k % TR_ITEMS;
         TRItem it;
         it.mode = End;
         it.qs = 0;
-        if (have || walk.pos < walk.end) {
-          it.part[0] = have ? next : piece();
-          have = false;
-          if (it.part[0].ntok > a.tok_per_tile) {
-            it.mode = Pair;
-          } else {
-            it.mode = Split;
-            if (walk.pos < walk.end) {
-              next = piece();
-              have = next.ntok > a.tok_per_tile || abs(it.part[0].nt - next.nt) > TR_DUAL_SLACK;
-              if (!have) it.mode = Dual;
-            }
+#pragma unroll 1
+        for (int x = 0; x < 2; ++x) {
+          if (!have) {
+            if (walk.pos >= walk.end) break;
+            next = piece();
+            have = true;
+          }
+          if (x == 0) {
+            it.part[0] = it.part[1] = next;
+            it.mode = next.ntok > a.tok_per_tile ? Pair : Split;
+            have = false;
+            if (it.mode == Pair) break;
+          } else if (next.ntok <= a.tok_per_tile && abs(it.part[0].nt - next.nt) <= TR_DUAL_SLACK) {
+            it.part[1] = next;
+            it.mode = Dual;
+            have = false;
           }
         }
         if (k >= TR_ITEMS && !tr_wait(&item_empty[sl], (uint32_t)((k / TR_ITEMS) - 1) & 1u, abort_flag, a)) break;
@@ -686,15 +710,10 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
         }
         qs = it.mode == Split ? qs ^ 1 : 1;
         it.qs = qs;
-        if (it.mode == Dual) {
-          it.part[1] = next;
-        } else {
-          it.part[1] = it.part[0];
-          if (it.mode == Split) {
-            it.part[0].nt = (it.part[0].nt + 1) >> 1;
-            it.part[1].nt >>= 1;
-            ++it.part[1].kt0;
-          }
+        if (it.mode == Split) {
+          it.part[0].nt = (it.part[0].nt + 1) >> 1;
+          it.part[1].nt >>= 1;
+          ++it.part[1].kt0;
         }
         if (lane == 0) {
           items[sl] = it;
@@ -725,6 +744,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
       }
       if (lane == 0) {
         a.cuts[blockIdx.x] = cut;
+#pragma unroll 1
         for (int s = 0; s < 2; ++s)
           if (((loaded >> s) & 1u) && !mbar_wait_bounded(&q_full[s], ((qn >> s) & 1u) ^ 1u)) record_error(a.err, INK_DEVERR_WAIT_TIMEOUT);
       }
@@ -903,14 +923,17 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
     __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.out);
 
     // sequences that see no key: zero rows, shared out over the CTAs; what is wrong with a sequence is told here
+#pragma unroll 1
     for (int b = (int)blockIdx.x; b < a.B; b += (int)gridDim.x) {
       TRSeq s;
       s.load(a, b);
       if (tid == 0 && s.bad) record_error(a.err, s.bad);
       if (s.tiles > 0 || s.n <= 0) continue;
+#pragma unroll 1
       for (long long x = tid; x < (long long)s.n * a.Hq * (D / 8); x += 256)
         reinterpret_cast<uint4*>(out + (size_t)s.c0 * a.Hq * D)[x] = make_uint4(0u, 0u, 0u, 0u);
       if (a.lse)
+#pragma unroll 1
         for (long long x = tid; x < (long long)s.n * a.Hq; x += 256) a.lse[(size_t)s.c0 * a.Hq + x] = -INFINITY;
     }
 
@@ -994,6 +1017,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
             b_row = row;
             const int n = min(d0 - (a.E - 1), KT);
             if (!(a.W > 0 && a.W <= a.E) && rv && n > 0) {
+#pragma unroll 1
               for (int c = 0; c < n; ++c) {
                 if (a.rel_bf16) reinterpret_cast<uint16_t*>(row)[KT - 1 - c] = (uint16_t)(__float_as_uint(rc) >> 16);
                 else reinterpret_cast<float*>(row)[KT - 1 - c] = rc;

@@ -5,12 +5,14 @@
 //     S_{s+1}(i) = S_s(i) + S_s(u_s(i)),   u_{s+1}(i) = u_s(u_s(i))
 // doubles the way covered in every step, so a tree of depth d takes log2(d) steps; the depth is |S| - 1.  A block takes a
 // sequence, its sets (a bit per token) and pointers twice in shared memory, read from one copy and
-// written to the other.  Latency bounds it: a launch and a chain of three loads.
+// written to the other.  Latency bounds it: a launch and a chain of three loads (one tree 2.9 us of GPU time alone, 128 trees of
+// up to 64 tokens 3.7).
 //
 // Commit: row path[j] of a sequence goes to row j, in place.  The path increases, so path[j] >= j, and what is
 // written while rows j0 .. j1 - 1 move lies below all that is read for rows from j1 on: a warp takes the rows in order,
 // a batch of loads, then the batch's stores.  Bytes bound it, read and written once in rows of 2 D bytes, but a path moves few of
-// them and the chain of loads in front of them (lengths, path, table) is longer.
+// them and the chain of loads in front of them (lengths, path, table) is longer (one pool 2.9 us of GPU time alone; 22 pools, 64
+// paths of up to 32 tokens of 8 heads of 128, 5.9 us).
 #include <algorithm>
 
 #include "tree_common.cuh"
