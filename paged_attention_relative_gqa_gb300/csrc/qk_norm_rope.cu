@@ -294,8 +294,9 @@ cudaError_t launch_qk_norm_rope(NormRopeArgs& a, int head_dim, bool interleaved,
   // wave, 20.7 in thirds, which is two, 24.4 in ninths).
   const long long resident = (long long)num_sms * NR_BLOCKS * (NR_THREADS / 32);
   long long best = 0;
-  a.chunk = a.passes;
-  for (int cut = 1; cut <= a.passes; ++cut) {
+  a.chunk = (long long)a.T * a.passes <= resident ? 1 : a.passes;   // (all of them at once: nothing to weigh)
+  const long long most = a.chunk == 1 ? 0 : std::min<long long>(a.passes, 2 * resident / std::max(a.T, 1));
+  for (int cut = 1; cut <= most; ++cut) {
     const int chunk = (a.passes + cut - 1) / cut, n = (a.passes + chunk - 1) / chunk;
     const long long cost = ((a.T * (long long)n + resident - 1) / resident) * (NR_START + chunk);
     if (cut > 1 && cost >= best) continue;
