@@ -713,7 +713,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
         if (it.mode == Split) {
           it.part[0].nt = (it.part[0].nt + 1) >> 1;
           it.part[1].nt >>= 1;
-          ++it.part[1].kt0;
+          if (it.part[1].nt > 0) ++it.part[1].kt0;   // (a part without a tile keeps a tile that is there: its table entries are read)
         }
         if (lane == 0) {
           items[sl] = it;

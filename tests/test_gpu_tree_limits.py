@@ -134,6 +134,28 @@ def test_the_last_key_there_is(cuda_device, tokens, page, window, bias, softcap,
     check(out, lse, ref, f"window {window}")
 
 
+@pytest.mark.parametrize("window", [20, 70, 250, 500])
+def test_the_last_tile_as_a_run_of_its_own(cuda_device, window):
+    """One KV head, pages smaller than a tile, a length of 2^31 less a page: runs are cut so that the last tile stands alone (the
+    other chain has no tile, and none would follow)."""
+    dev, page, heads, dim, tokens = cuda_device, 16, (8, 1), 128, 9
+    L = 2**31 - page
+    params, parents, table, (q, k, v, table_d, lens, cu) = at_the_end(dev, L, tokens, heads, dim, page, window, 37)
+    ints = lambda *s: torch.empty(*s, dtype=torch.int32, device=dev)
+    par, pos, anc = torch.tensor(parents, dtype=torch.int32, device=dev), ints(tokens), ints(tokens, 1)
+    ws = binding.alloc_tree_workspace(params, dev)
+    out, lse = torch.full_like(q, 7.0), torch.full(q.shape[:2], 7.0, device=dev)
+    binding.inkling_attn_tree_plan(params, cu, lens, par, pos, anc, ws)
+    binding.inkling_attn_tree(params, q, cu, k, v, table_d, lens, pos, anc, out, ws, lse=lse)
+    assert binding.inkling_attn_read_device_error(ws) == 0
+    at, seen = oracle.plan(parents, L - tokens, 1)
+    first = (table.shape[1] - 60) * page
+    ref = oracle.attention(num_q_heads=heads[0], num_kv_heads=heads[1], head_dim=dim, page_size=page, window=window,
+                           sm_scale=dim ** -0.5, cu_q=np.array([0, tokens]), seq_lens=np.array([L - first]), q_bits=bits(q),
+                           k_bits=bits(k), v_bits=bits(v), block_table=table[:, -60:].numpy(), positions=at - first, ancestors=seen)
+    check(out, lse, ref, f"window {window}")
+
+
 @pytest.mark.parametrize("tokens", [1, 20])
 def test_the_longest_history(cuda_device, tokens):
     """2^31 - 256 keys, all seen.  Keys of zeros weigh the same; values are powers of two, a channel each: sums of up to 2^23 of
