@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(CT_THREADS, ct_blocks(KS)) kv_conv_tree_kernel
         if (tell) record_error(a.err, INK_DEVERR_QLEN_EXCEEDS_KV);
       } else {
         const int key = L - n + t - c0, pi = key >> a.log2_page;
-        const int page_id = pi < a.max_pages ? __ldg(a.block_table + (size_t)b * a.max_pages + pi) : -1;
+        const int page_id = pi < a.max_pages ? __ldg(a.block_table + (size_t)b * a.max_pages + min(pi, a.max_pages - 1)) : -1;
         int node = t - c0, back = KS - 2;   // the state's newest row is the parent of a root
 #pragma unroll
         for (int i = 0; i < KS; ++i) {
@@ -168,7 +168,8 @@ __global__ void __launch_bounds__(CT_THREADS) kv_conv_state_tree_kernel(const Tr
       m = tree_path(path, __ldg(a.path_lens + b), a.max_path, c1 - c0, lane, a.err);
     }
     // row r of the new state is row m + r of the old one and the path's rows side by side
-    if (lane < KS - 1) from[lane] = m + lane < KS - 1 ? ~(b * (KS - 1) + m + lane) : c0 + __ldg(path + m + lane - (KS - 1));
+    if (lane < KS - 1) from[lane] = m + lane < KS - 1 ? ~(b * (KS - 1) + m + lane)
+                                                          : c0 + __ldg(path + max(m + lane - (KS - 1), 0));
   }
   __syncthreads();
   const int vec = blockIdx.y * CT_THREADS + threadIdx.x;

@@ -296,7 +296,8 @@ struct TRRow {
   bool cut;                       // the window may hide an ancestor
 
   __device__ __forceinline__ uint32_t word(const TreeArgs& a, int i) const {
-    return i == 0 ? w0 : i > 0 && i < a.words ? __ldg(bits + i) : 0u;
+    // (a load behind a select may be issued whatever the select says: every such address is one that is there)
+    return i == 0 ? w0 : i > 0 && i < a.words ? __ldg(bits + min(max(i, 0), a.words - 1)) : 0u;
   }
   __device__ __forceinline__ uint32_t sees(const TreeArgs& a, int base) const {
     const int x0 = max(lo - base, 0), x1 = min(hist - base, 32);
@@ -875,7 +876,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             const int kk = k0 + 32 * x + lane;
-            pk[x] = kk >= it.H && kk < it.hi ? max(__ldg(a.positions + it.c0 + kk - it.H), it.H) : kk;
+            pk[x] = kk >= it.H && kk < it.hi ? max(__ldg(a.positions + it.c0 + min(max(kk - it.H, 0), it.n - 1)), it.H) : kk;
           }
           // (all loads of a batch first, from rows that are there: what is not seen is masked)
           auto fill = [&](auto load) {
@@ -960,8 +961,10 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
         if (a.slopes) slope = __ldg(a.slopes + head);
         if (a.rel) {
           const size_t x = ((size_t)t * a.Hq + head + 1) * a.E - 1;
-          rc = a.rel_bf16 ? __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t*>(a.rel) + x) << 16)
-                          : __ldg(static_cast<const float*>(a.rel) + x);
+          const void* here = a.positions;   // (for the load of the other type)
+          const uint32_t two = __ldg(a.rel_bf16 ? static_cast<const uint16_t*>(a.rel) + x : static_cast<const uint16_t*>(here));
+          const float one = __ldg(a.rel_bf16 ? static_cast<const float*>(here) : static_cast<const float*>(a.rel) + x);
+          rc = a.rel_bf16 ? __uint_as_float(two << 16) : one;
         }
       }
       const size_t orow = (size_t)t * a.Hq + head;

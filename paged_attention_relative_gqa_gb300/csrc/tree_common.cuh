@@ -21,7 +21,7 @@ __device__ __forceinline__ int tree_path(const int32_t* path, int m, int max_pat
   bool ok = m >= 0 && m <= max_path;
   for (int j = lane; ok && j < m; j += 32) {
     const int i = __ldg(path + j);
-    ok = i < n && i > (j > 0 ? __ldg(path + j - 1) : -1);
+    ok = i < n && i > (j > 0 ? __ldg(path + max(j - 1, 0)) : -1);
   }
   ok = __all_sync(0xffffffffu, ok);
   if (!ok && lane == 0) record_error(err, INK_DEVERR_BAD_TREE);

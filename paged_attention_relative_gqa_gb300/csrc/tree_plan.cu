@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(TC_THREADS) tree_commit_kernel(const __grid_co
   // row of head 0 of a key (-1: not in the pool)
   auto row = [&](int key) -> long long {
     const int pi = key >> a.log2_page;
-    const int page = pi < a.max_pages ? __ldg(a.block_table + (size_t)b * a.max_pages + pi) : -1;
+    const int page = pi < a.max_pages ? __ldg(a.block_table + (size_t)b * a.max_pages + min(pi, a.max_pages - 1)) : -1;
     if (page < 0 || page >= a.num_pages) return -1;
     return ((long long)page * a.Hkv << a.log2_page) + (key & ((1 << a.log2_page) - 1));
   };
@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(TC_THREADS) tree_commit_kernel(const __grid_co
   uint16_t* base = a.pool[pool];
   const int lr = lane % LPR, rip = lane / LPR;
   for (int j0 = 0; j0 < m; j0 += 32) {
-    const int j = j0 + lane, i = j < m ? __ldg(path + j) : j;
+    const int j = j0 + lane, i = j < m ? __ldg(path + min(j, m - 1)) : j;
     long long src = -1, dst = -1;
     if (i != j) {
       src = row(H + i);
