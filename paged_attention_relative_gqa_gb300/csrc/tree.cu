@@ -7,8 +7,8 @@
 // A few tokens against a long history: the bytes of K and V, and of the bias rows where there is a bias tensor, bound
 // it, so they have to flow evenly over the SMs whatever the lengths are.  The rows of a tile of 128 (the M of an MMA) are (token,
 // query head) pairs of one sequence and KV head, tokens outermost; an item is up to two row tiles.  All tiles of 64 keys of all
-// items stand in one row, tiles of an item side by side, and every CTA takes an equal run of them, found on
-// the device from the lengths (a graph replays with other ones).  A run cuts two items at most; pieces of
+// items stand in one row, tiles of an item side by side, and every CTA takes a run of them that takes as long as the others', found
+// on the device from the lengths (a graph replays with other ones).  A run cuts two items at most; pieces of
 // a cut item leave O, maximum and sum in fp32, two places a CTA, and a second kernel joins them in order, spread over
 // all SMs (one CTA that joined the 20 pieces of an item of a single long sequence would take as long as six key tiles).
 //
@@ -60,7 +60,14 @@ constexpr int TR_BAD = 16;        // tiles whose unreadable keys are remembered 
 // one who waits: next to a chain's last tile its next is at most TR_DUAL_SLACK + 1 behind it (the other chain's longer
 // piece, or two items of one tile, whose Q tiles a chain without tiles waits for).
 constexpr int TR_TILES = 8;
-constexpr int TR_MIN_TILES = 4;   // least run of a CTA
+// What a tile takes, in units: for two row tiles (2,000 clocks; bound by its softmax), for one (1,150 to 1,500, by the softmax or by
+// memory); one whose bias rows have to be read takes twice as much.  TR_ENDS tiles more for an item's start, its last tile and its
+// output, TR_ENDS_BIAS with a bias tensor (10,000 clocks).  Runs of as many tiles each, against these: 4 trees of up to 61 tokens
+// against 64 K keys 281 -> 255 us (some CTAs had one row tile a tile, and were done after 330 of 560 thousand clocks), 16 of up to
+// 40 against 16 K with 2,048 distances 445 -> 375, of up to 16 with 4,096 221 -> 211, windows of 512 with a bias 137 -> 140.  With
+// 4 for both, windows with a bias take 149; with 15 for both, 16 trees of up to 40 without one 200 instead of 193.
+constexpr int TR_PAIR = 3, TR_ONE = 2, TR_ENDS = 4, TR_ENDS_BIAS = 15;
+constexpr int TR_MIN_RUN = 4 * TR_ONE;   // least run of a CTA; no tile but an item's last takes more
 constexpr int TR_DUAL_SLACK = 4;  // most tiles that two pieces may differ in to run side by side
 constexpr float TR_RESCALE_LOG2 = 8.f;
 
@@ -161,6 +168,7 @@ __device__ __forceinline__ long long tr_div(long long a, long long b) {
 // A sequence's rows and keys; tiles == 0: none of its rows sees a key (or it has none).
 struct TRSeq {
   int c0, n, L, lo, hi, tiles;
+  int plain;      // tiles, the first ones, of which no row needs more of its bias than the last value
   uint32_t bad;   // error bits; BAD_ROWS: its rows are not touched
 
   __device__ __forceinline__ void load(const TreeArgs& a, int b) {
@@ -168,7 +176,7 @@ struct TRSeq {
     const int c1 = __ldg(a.cu_q + b + 1);
     L = __ldg(a.seq_lens + b);
     n = c1 - c0;
-    lo = hi = tiles = 0;
+    lo = hi = tiles = plain = 0;
     bad = 0;
     if (c0 < 0 || c1 > a.T || c1 < c0) {
       bad = INK_DEVERR_BAD_ROWS;
@@ -185,26 +193,35 @@ struct TRSeq {
       hi = (int)min((long long)L, cap);
       lo = a.W > 0 ? max(0, L - n - a.W + 1) : 0;
       if (lo < hi) tiles = (hi - 1) / KT - lo / KT + 1;
+      plain = tiles;
+      if (a.rel) {   // (as tr_bias finds it)
+        const long long far = (long long)L - n - (KT - 1) - (a.E - 1);   // the last first key of such a tile
+        plain = far < 0 ? 0 : min(max((int)(far / KT) + 1 - lo / KT, 0), tiles);
+      }
     }
   }
 };
 
-// The row of tiles, walked by a whole warp: 32 sequences at a time in the lanes.  Divisions are made
-// once per run: later pieces begin with their item.
+// The row of tiles, walked by a whole warp: 32 sequences at a time in the lanes.  It is measured in units; a tile belongs to the run
+// in which it begins.  Divisions are made once per run: later pieces begin with their item.
 struct TRWalk {
-  long long base, incl, chunk, total;   // tiles before sequence cb; up to and with this lane's; of a run; of the 32
+  long long base, incl, chunk, total;   // units before sequence cb; up to and with this lane's; of a run; of the 32
   long long pos, end;                   // of this CTA's run
-  int cb, per, items, cta;
-  int src, groups, left;                // the sequence's lane; its items; of these not begun
+  long long units;                      // of all items of this lane's sequence for one head chunk
+  int items, last;                      // their number; units of a tile of the last one
+  int cb, per, cta, ends;
+  int src, left;                        // the sequence's lane; its items not begun
   int kvh, hc, item;                    // the next one
   TRSeq s;
 
   __device__ __forceinline__ void load(const TreeArgs& a, int lane) {
     const int b = cb + lane;
-    s.tiles = s.n = 0;
+    s.tiles = s.plain = s.n = 0;
     if (b < a.B) s.load(a, b);
     items = (s.n + 2 * a.tok_per_tile - 1) / (2 * a.tok_per_tile);
-    incl = (long long)s.tiles * items * per;
+    last = s.n - (items - 1) * 2 * a.tok_per_tile > a.tok_per_tile ? TR_PAIR : TR_ONE;
+    units = s.tiles > 0 ? (long long)(2 * s.tiles - s.plain + ends) * (TR_PAIR * (items - 1) + last) : 0;
+    incl = units * per;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long v = __shfl_up_sync(0xffffffffu, incl, o);
@@ -215,6 +232,7 @@ struct TRWalk {
 
   __device__ __forceinline__ void begin(const TreeArgs& a, int lane) {
     per = a.Hkv * a.head_chunks;
+    ends = a.rel ? TR_ENDS_BIAS : TR_ENDS;
     cta = (int)blockIdx.x;
     long long all = 0;
 #pragma unroll 1
@@ -225,43 +243,67 @@ struct TRWalk {
     cb = 0;
     base = 0;
     left = 0;
-    chunk = max(tr_div(all + gridDim.x - 1, gridDim.x), (long long)TR_MIN_TILES);
+    chunk = max(tr_div(all + gridDim.x - 1, gridDim.x), (long long)TR_MIN_RUN);
     pos = min(cta * chunk, all);
     end = min(pos + chunk, all);
   }
 
-  // The next piece of the run; first: the CTA where its item begins.
+  // The next piece of the run (pos < end), with no tile if there is none; first: the CTA where its item begins.
   __device__ __forceinline__ TRPart next(const TreeArgs& a, int lane, int& first) {
-    int x0 = 0;
-    first = cta;
-    if (left == 0) {   // of another sequence than the one before
-#pragma unroll 1
-      while (pos >= base + total) {
-        base += total;
-        cb += 32;
-        load(a, lane);
-      }
-      src = __ffs(__ballot_sync(0xffffffffu, pos < base + incl)) - 1;
-      const int ni = __shfl_sync(0xffffffffu, items, src), tiles = __shfl_sync(0xffffffffu, s.tiles, src);
-      groups = ni * per;
-      const long long off = pos - (base + __shfl_sync(0xffffffffu, incl - (long long)s.tiles * items * per, src));
-      int gi = 0;
-      if (off > 0) {   // the run begins within a sequence
-        gi = (int)tr_div(off, tiles);
-        x0 = (int)(off - (long long)gi * tiles);
-        first = (int)tr_div(pos - x0, chunk);
-      }
-      left = groups - gi;
-      const int hk = gi / ni;
-      item = gi - hk * ni;
-      kvh = hk / a.head_chunks;
-      hc = hk - kvh * a.head_chunks;
-    }
-    const int ni = __shfl_sync(0xffffffffu, items, src), tiles = __shfl_sync(0xffffffffu, s.tiles, src);
     TRPart w;
+    int x0 = 0, ni, tiles, plain, weight;
+    first = cta;
+    for (;;) {
+      long long off = 0;
+      if (left == 0) {   // of another sequence than the one before
+#pragma unroll 1
+        while (pos >= base + total) {
+          base += total;
+          cb += 32;
+          load(a, lane);
+        }
+        src = __ffs(__ballot_sync(0xffffffffu, pos < base + incl)) - 1;
+        off = pos - (base + __shfl_sync(0xffffffffu, incl - units * per, src));
+      }
+      w.n = __shfl_sync(0xffffffffu, s.n, src);
+      tiles = __shfl_sync(0xffffffffu, s.tiles, src);
+      plain = __shfl_sync(0xffffffffu, s.plain, src);
+      ni = __shfl_sync(0xffffffffu, items, src);
+      const int wl = __shfl_sync(0xffffffffu, last, src), size = 2 * tiles - plain + ends;
+      if (left == 0) {
+        int hk = 0;
+        item = 0;
+        if (off > 0) {   // the run begins within a sequence
+          const long long one = (long long)size * (TR_PAIR * (ni - 1) + wl);
+          hk = (int)tr_div(off, one);
+          off -= hk * one;
+          item = min((int)tr_div(off, (long long)size * TR_PAIR), ni - 1);
+          off -= (long long)item * size * TR_PAIR;
+        }
+        left = per * ni - (hk * ni + item);
+        kvh = hk / a.head_chunks;
+        hc = hk - kvh * a.head_chunks;
+      }
+      weight = item == ni - 1 ? wl : TR_PAIR;
+      if (off > 0) {       // and within an item
+        const int y = weight == TR_PAIR ? ((int)off + TR_PAIR - 1) / TR_PAIR : ((int)off + TR_ONE - 1) / TR_ONE;
+        first = (int)tr_div(pos - off, chunk);
+        x0 = y <= plain ? y : plain + (y - plain + 1) / 2;
+        pos += (long long)weight * (x0 >= tiles ? size : x0 <= plain ? x0 : 2 * x0 - plain) - off;
+        if (x0 >= tiles) { // in its last tile: the run begins with the next one
+          x0 = 0;
+          first = cta;
+          left = 0;
+          w.nt = 0;
+          if (pos >= end) return w;
+          continue;
+        }
+      }
+      break;
+    }
+    const long long start = pos - (long long)weight * (x0 <= plain ? x0 : 2 * x0 - plain);   // of the item
     w.b = cb + src;
     w.c0 = __shfl_sync(0xffffffffu, s.c0, src);
-    w.n = __shfl_sync(0xffffffffu, s.n, src);
     w.lo = __shfl_sync(0xffffffffu, s.lo, src);
     w.hi = __shfl_sync(0xffffffffu, s.hi, src);
     w.H = __shfl_sync(0xffffffffu, s.L, src) - w.n;
@@ -271,11 +313,18 @@ struct TRWalk {
     w.t0 = w.c0 + item * 2 * a.tok_per_tile;
     w.ntok = min(2 * a.tok_per_tile, w.n - item * 2 * a.tok_per_tile);
     w.kt0 = w.lo / KT + x0;
-    w.nt = (int)min((long long)(tiles - x0), end - pos);
-    const long long g1 = pos - x0 + tiles;
-    w.parts = (g1 <= end ? cta : (int)tr_div(g1 - 1, chunk)) - first + 1;
+    // the tiles that begin before the run's end
+    const long long room = end - start;
+    int x1 = tiles;
+    if (room < (long long)weight * (2 * tiles - plain + ends)) {
+      const int y = weight == TR_PAIR ? ((int)room + TR_PAIR - 1) / TR_PAIR : ((int)room + TR_ONE - 1) / TR_ONE;
+      x1 = min(y <= plain ? y : plain + (y - plain + 1) / 2, tiles);
+    }
+    w.nt = x1 - x0;
+    const long long last_tile = start + (long long)weight * (tiles - 1 <= plain ? tiles - 1 : 2 * (tiles - 1) - plain);
+    w.parts = (last_tile < end ? cta : (int)tr_div(last_tile, chunk)) - first + 1;
     w.place = 2 * cta + (cta == first ? 1 : 0);
-    pos += w.nt;
+    pos = start + (long long)weight * (x1 == tiles ? 2 * tiles - plain + ends : x1 <= plain ? x1 : 2 * x1 - plain);
     --left;
     if (++item == ni) {
       item = 0;
@@ -666,6 +715,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
       auto piece = [&]() {               // the next one of the run
         int first;
         TRPart w = walk.next(a, lane, first);
+        if (w.nt == 0) return w;
         if (w.parts > 1 && first == (int)blockIdx.x) cut = {w.parts, w.t0, w.ntok, w.h0, w.gh};
         // all rows see the keys from the largest first one on
         w.lo_max = 0;
@@ -688,6 +738,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
           if (!have) {
             if (walk.pos >= walk.end) break;
             next = piece();
+            if (next.nt == 0) break;
             have = true;
           }
           if (x == 0) {
