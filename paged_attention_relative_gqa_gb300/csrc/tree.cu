@@ -72,6 +72,7 @@ constexpr int TR_DUAL_SLACK = 4;  // most tiles that two pieces may differ in to
 constexpr float TR_RESCALE_LOG2 = 8.f;
 
 constexpr int KT = TILE_KEYS, KW = KT / 32;   // keys of a tile, words of 32
+constexpr int TR_ELEMENTS = KT + 1;           // words of a bias row that is filled element by element
 
 template <int D, bool CAP, bool BIAS>
 struct TRShape {
@@ -92,7 +93,6 @@ struct TRShape {
   // slots went by without one).
   static constexpr bool ROLL = CAP || BIAS;
   static constexpr uint32_t TQ = 128;              // with a bias: S_h at 64 h, Q_h at TQ + 64 h
-  static constexpr int ELEMENTS = KT + 1;          // words of a bias row that is filled element by element
   static constexpr uint32_t TO = 256;              // without: S_h at 128 h, two of them; O_h at TO + D h
   static constexpr uint32_t TS = BIAS ? 64 : 128;
 };
@@ -564,49 +564,50 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
           chunk_val[h] = __ldg(bt[h] + min(chunk_base[h] + lane, (hi[h] - 1) >> a.log2_page));
         }
         done_item(k);
-        for (int j = 0; j < longest && go; ++j)   // (the chains' tiles take turns)
+        for (int j = 0; j < longest && go; ++j) {   // (the chains' tiles take turns)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (!go || j >= nt[h]) continue;
-          if (((k0[h] + KT - 1) >> a.log2_page) >= chunk_base[h] + 32) {
-            chunk_base[h] = k0[h] >> a.log2_page;
-            chunk_val[h] = __ldg(bt[h] + min(chunk_base[h] + lane, (hi[h] - 1) >> a.log2_page));
-          }
-          const int ks = k0[h] + (wide ? 0 : lane * seg);   // lane < nseg takes one segment
-          const bool want = lane < nseg && ks < hi[h] && ks + seg > lo[h];
-          const int page = __shfl_sync(0xffffffffu, chunk_val[h], min(max((ks >> a.log2_page) - chunk_base[h], 0), 31));
-          const bool bad_seg = want && (page < 0 || page >= a.num_pages);
-          const bool load = want && !bad_seg;
-          const uint32_t bmask = __ballot_sync(0xffffffffu, bad_seg);
-          const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, load)) * (uint32_t)(seg * D * 2);
-          const int row = load ? ((page * a.Hkv + kvh[h]) << a.log2_page) + (ks & (P - 1)) : 0;
-          if (round > 0) go = tr_wait(&empty[st], (round - 1) & 1u, abort_flag, a);
-          if (!go) continue;
-          uint64_t* full = (kv ? v_full : k_full) + x % TR_TILES;
-          uint8_t* dst = smem + L_::ring + (size_t)st * S::TILE + (wide ? 0 : lane * seg * 128);
-          if (lane == 0) {
-            if (kv == 0) {   // keys of this tile whose page is outside the pool
-              uint64_t bad = 0;
-#pragma unroll 1
-              for (uint32_t mm = bmask; mm; mm &= mm - 1) bad |= (~0ull >> (64 - seg)) << ((__ffs(mm) - 1) * seg);
-              *reinterpret_cast<uint64_t*>(kbad + x % TR_BAD * KW) = bad;
-              if (bmask) record_error(a.err, INK_DEVERR_PAGE_OUT_OF_RANGE);
+          for (int h = 0; h < 2; ++h) {
+            if (!go || j >= nt[h]) continue;
+            if (((k0[h] + KT - 1) >> a.log2_page) >= chunk_base[h] + 32) {
+              chunk_base[h] = k0[h] >> a.log2_page;
+              chunk_val[h] = __ldg(bt[h] + min(chunk_base[h] + lane, (hi[h] - 1) >> a.log2_page));
             }
-            mbar_arrive_expect_tx(full, bytes);
-            if (wide && load) tma_load_3d(dst, kv ? &tmV : &tmK, 0, row, 0, full);
-          }
-          if (!wide && load) {
+            const int ks = k0[h] + (wide ? 0 : lane * seg);   // lane < nseg takes one segment
+            const bool want = lane < nseg && ks < hi[h] && ks + seg > lo[h];
+            const int page = __shfl_sync(0xffffffffu, chunk_val[h], min(max((ks >> a.log2_page) - chunk_base[h], 0), 31));
+            const bool bad_seg = want && (page < 0 || page >= a.num_pages);
+            const bool load = want && !bad_seg;
+            const uint32_t bmask = __ballot_sync(0xffffffffu, bad_seg);
+            const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, load)) * (uint32_t)(seg * D * 2);
+            const int row = load ? ((page * a.Hkv + kvh[h]) << a.log2_page) + (ks & (P - 1)) : 0;
+            if (round > 0) go = tr_wait(&empty[st], (round - 1) & 1u, abort_flag, a);
+            if (!go) continue;
+            uint64_t* full = (kv ? v_full : k_full) + x % TR_TILES;
+            uint8_t* dst = smem + L_::ring + (size_t)st * S::TILE + (wide ? 0 : lane * seg * 128);
+            if (lane == 0) {
+              if (kv == 0) {   // keys of this tile whose page is outside the pool
+                uint64_t bad = 0;
+#pragma unroll 1
+                for (uint32_t mm = bmask; mm; mm &= mm - 1) bad |= (~0ull >> (64 - seg)) << ((__ffs(mm) - 1) * seg);
+                *reinterpret_cast<uint64_t*>(kbad + x % TR_BAD * KW) = bad;
+                if (bmask) record_error(a.err, INK_DEVERR_PAGE_OUT_OF_RANGE);
+              }
+              mbar_arrive_expect_tx(full, bytes);
+              if (wide && load) tma_load_3d(dst, kv ? &tmV : &tmK, 0, row, 0, full);
+            }
+            if (!wide && load) {
 #pragma unroll
-            for (int cb = 0; cb < S::CB; ++cb)
-              tma_load_2d(dst + cb * S::SUB, kv ? &tmV : &tmK, cb * 64, row, full);
+              for (int cb = 0; cb < S::CB; ++cb)
+                tma_load_2d(dst + cb * S::SUB, kv ? &tmV : &tmK, cb * 64, row, full);
+            }
+            st += 2;
+            if (st >= NS) {
+              st = kv;
+              ++round;
+            }
+            ++x;
+            k0[h] += kstep;
           }
-          st += 2;
-          if (st >= NS) {
-            st = kv;
-            ++round;
-          }
-          ++x;
-          k0[h] += kstep;
         }
       }
       if (lane == 0) pp_drain_ring(kv ? v_full : k_full, TR_TILES, x, a.err);
@@ -807,67 +808,68 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
       for (int k = 0; go && next_item(k); ++k) {
         const TRItem& item = items[k % TR_ITEMS];
         const int longest = item.longest(), step = item.step();
-        for (int j = 0; j < longest && go; ++j)
-        for (int h = 0; h < (item.mode == Pair ? 1 : 2); ++h) {
-          const TRPart& it = item.part[h];
-          if (j >= it.nt) continue;
-          const int hist = min(it.H, it.hi), kt = it.kt0 + j * step;
-          const int st = (2 * g + 1) % NS;
-          // (what cannot be read comes with K)
-          go = tr_wait(&k_full[g % TR_TILES], (uint32_t)(g / TR_TILES) & 1u, abort_flag, a) &&
-               tr_wait(&v_full[g % TR_TILES], (uint32_t)(g / TR_TILES) & 1u, abort_flag, a);
-          if (!go) break;
-          const int k0 = kt * KT;
-          const uint32_t* badw = kbad + (g % TR_BAD) * KW;
-          uint32_t any = 0;
+        for (int j = 0; j < longest && go; ++j) {
+          for (int h = 0; h < (item.mode == Pair ? 1 : 2); ++h) {
+            const TRPart& it = item.part[h];
+            if (j >= it.nt) continue;
+            const int hist = min(it.H, it.hi), kt = it.kt0 + j * step;
+            const int st = (2 * g + 1) % NS;
+            // (what cannot be read comes with K)
+            go = tr_wait(&k_full[g % TR_TILES], (uint32_t)(g / TR_TILES) & 1u, abort_flag, a) &&
+                 tr_wait(&v_full[g % TR_TILES], (uint32_t)(g / TR_TILES) & 1u, abort_flag, a);
+            if (!go) break;
+            const int k0 = kt * KT;
+            const uint32_t* badw = kbad + (g % TR_BAD) * KW;
+            uint32_t any = 0;
 #pragma unroll
-          for (int x = 0; x < KW; ++x) any |= badw[x];
-          if (k0 < it.lo_max || hist - k0 < KT || any) {
-            uint8_t* vt = smem + L_::ring + (size_t)st * S::TILE;
-            bool found = false;
+            for (int x = 0; x < KW; ++x) any |= badw[x];
+            if (k0 < it.lo_max || hist - k0 < KT || any) {
+              uint8_t* vt = smem + L_::ring + (size_t)st * S::TILE;
+              bool found = false;
 #pragma unroll 1
-            for (int x = 0; x < KW; ++x) {
-              const int kk = k0 + 32 * x + lane;
-              uint4* row = reinterpret_cast<uint4*>(vt + (32 * x + lane) * 128);
-              const bool zero = kk < it.lo || kk >= it.hi || ((badw[x] >> lane) & 1u);
-              if (!zero && kk >= it.lo_max && kk < hist) continue;   // every row sees it
-              if (!zero) {   // exponents all ones carry into the sign places
-                uint32_t odd = 0;
+              for (int x = 0; x < KW; ++x) {
+                const int kk = k0 + 32 * x + lane;
+                uint4* row = reinterpret_cast<uint4*>(vt + (32 * x + lane) * 128);
+                const bool zero = kk < it.lo || kk >= it.hi || ((badw[x] >> lane) & 1u);
+                if (!zero && kk >= it.lo_max && kk < hist) continue;   // every row sees it
+                if (!zero) {   // exponents all ones carry into the sign places
+                  uint32_t odd = 0;
 #pragma unroll
-                for (int c = 0; c < S::CB; ++c)
+                  for (int c = 0; c < S::CB; ++c)
 #pragma unroll
-                  for (int y = 0; y < 8; ++y) {
-                    const uint4 w = row[c * (S::SUB / 16) + (y ^ (lane & 7))];
-                    odd |= ((w.x & 0x7F807F80u) + 0x00800080u) | ((w.y & 0x7F807F80u) + 0x00800080u) |
-                           ((w.z & 0x7F807F80u) + 0x00800080u) | ((w.w & 0x7F807F80u) + 0x00800080u);
-                  }
-                if (odd & 0x80008000u) {
-                  found = true;
-                  auto finite = [](uint32_t w) {   // infinities and NaN to zero, the other half as it is
-                    return w & ~(((((w & 0x7F807F80u) + 0x00800080u) >> 15) & 0x00010001u) * 0xFFFFu);
-                  };
+                    for (int y = 0; y < 8; ++y) {
+                      const uint4 w = row[c * (S::SUB / 16) + (y ^ (lane & 7))];
+                      odd |= ((w.x & 0x7F807F80u) + 0x00800080u) | ((w.y & 0x7F807F80u) + 0x00800080u) |
+                             ((w.z & 0x7F807F80u) + 0x00800080u) | ((w.w & 0x7F807F80u) + 0x00800080u);
+                    }
+                  if (odd & 0x80008000u) {
+                    found = true;
+                    auto finite = [](uint32_t w) {   // infinities and NaN to zero, the other half as it is
+                      return w & ~(((((w & 0x7F807F80u) + 0x00800080u) >> 15) & 0x00010001u) * 0xFFFFu);
+                    };
 #pragma unroll 1
-                  for (int y = 0; y < 8 * S::CB; ++y) {
-                    uint4& w = row[(y >> 3) * (S::SUB / 16) + ((y & 7) ^ (lane & 7))];
-                    w = make_uint4(finite(w.x), finite(w.y), finite(w.z), finite(w.w));
+                    for (int y = 0; y < 8 * S::CB; ++y) {
+                      uint4& w = row[(y >> 3) * (S::SUB / 16) + ((y & 7) ^ (lane & 7))];
+                      w = make_uint4(finite(w.x), finite(w.y), finite(w.z), finite(w.w));
+                    }
                   }
+                } else {
+#pragma unroll
+                  for (int c = 0; c < S::CB; ++c)
+#pragma unroll
+                    for (int y = 0; y < 8; ++y) row[c * (S::SUB / 16) + (y ^ (lane & 7))] = make_uint4(0u, 0u, 0u, 0u);
                 }
-              } else {
-#pragma unroll
-                for (int c = 0; c < S::CB; ++c)
-#pragma unroll
-                  for (int y = 0; y < 8; ++y) row[c * (S::SUB / 16) + (y ^ (lane & 7))] = make_uint4(0u, 0u, 0u, 0u);
               }
+              if (found) {
+                atomicMin(poison + 4 * (k % TR_ITEMS) + 2 * h, kt);
+                atomicMax(poison + 4 * (k % TR_ITEMS) + 2 * h + 1, kt);
+              }
+              asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             }
-            if (found) {
-              atomicMin(poison + 4 * (k % TR_ITEMS) + 2 * h, kt);
-              atomicMax(poison + 4 * (k % TR_ITEMS) + 2 * h + 1, kt);
-            }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&v_ok[g % TR_TILES]);
+            ++g;
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&v_ok[g % TR_TILES]);
-          ++g;
         }
         done_item(k);
       }
@@ -948,8 +950,8 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
               }
 #pragma unroll
               for (int y = 0; y < 8; ++y) {
-                buf[(r + y) * S::ELEMENTS + KT - 1 - lane] = v[y][0];
-                buf[(r + y) * S::ELEMENTS + KT - 33 - lane] = v[y][1];
+                buf[(r + y) * TR_ELEMENTS + KT - 1 - lane] = v[y][0];
+                buf[(r + y) * TR_ELEMENTS + KT - 33 - lane] = v[y][1];
               }
             }
           };
@@ -1079,7 +1081,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
               asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // (a copy may write here next)
             }
           } else {
-            b_row = bias + h * TREE_BIAS_BYTES + r * S::ELEMENTS * 4;
+            b_row = bias + h * TREE_BIAS_BYTES + r * TR_ELEMENTS * 4;
           }
         }
         // ---- scores and their maximum
