@@ -36,13 +36,13 @@
 // Behind the history distances have no order, and a bias warp brings them element by element, a lane a key.
 // Every wait is bounded; after a timeout the CTA records it, stops issuing, waits for what is in flight and exits.
 //
-// Measured (GPU time alone; 64 query heads, D = 128): 32 trees of up to 16 tokens against up to 16 K keys, 8 KV heads, 254 us
-// (6.5 TB/s), capped 275, with slopes 439, D = 64 190; 4 of up to 16 against 64 K 136 us (6.0 TB/s); 4 of up to 61 (two items that
-// read K and V each for themselves) 281 us, 0.90 PFLOP/s: 64 keys of both chains take 2,000 clocks, of which their softmax warps
-// are busy 1,850 and the tensor cores 1,050; 16 of up to 16 against 16 K with 4,096 fp32 distances 220 us (147 at the rate of a
-// copy); 64 of up to 8 in a window of 512 with 512 distances 137 us (49), without 75 (42): items of nine tiles, whose start, masks,
-// last tile and output run code that the instruction cache does not hold from one item to the next (17 % of its requests miss,
-// against 2 % on long histories).
+// Measured (GPU time alone; 64 query heads, D = 128): 32 trees of up to 16 tokens against up to 16 K keys, 8 KV heads, 255 us
+// (6.4 TB/s), capped 273, with slopes 436, D = 64 202; 4 of up to 16 against 64 K 136 us (6.0 TB/s); 4 of up to 61 (two items that
+// read K and V each for themselves) 254 us, 0.99 PFLOP/s: 64 keys of both chains take 2,000 clocks, of which their softmax warps
+// are busy 1,850 and the tensor cores 1,050; 16 of up to 16 against 16 K with 4,096 fp32 distances 210 us (147 at the rate of a
+// copy); 64 of up to 8 in a window of 512 with 512 distances 140 us (49), without 79 (42): items of nine tiles, whose start, masks,
+// last tile and output run code that the instruction cache does not hold from one item to the next (19 % of its requests miss,
+// against 2 % on long histories).  How the code happens to lie moves the two last by 5 to 8 %.
 #include <algorithm>
 #include <climits>
 
