@@ -64,6 +64,33 @@ def test_rotation_at_positions(cuda_device, heads, dim, page, n, history, rot, l
         assert np.array_equal(a, b)
 
 
+@pytest.mark.parametrize("heads,dim,n", [((64, 8), 128, [20] * 85), ((64, 8), 128, [30] * 110), ((8, 2), 64, [29] * 128),
+                                         ((64, 8), 128, [40] * 25), ((8, 2), 128, [41] * 100)])
+@pytest.mark.parametrize("layout,rot", [("half", 64), ("interleaved", 32)])
+def test_rows_do_not_depend_on_how_many_there_are(cuda_device, heads, dim, n, layout, rot):
+    """However a token's heads are shared out over warps: the call for all sequences gives the bits of calls for a few of them."""
+    step = Step(heads, dim, 64, n, [100 + i for i in range(len(n))], 34, cuda_device)
+    p = step.prob
+    q, k, v = rope_inputs(step, 35, cuda_device)
+    w, freq = torch.rand(dim, device=cuda_device) + 0.5, rotary.inv_freq(rot, device=cuda_device)[0]
+    ws = binding.alloc_tree_workspace(step.params, cuda_device)
+    outs = []
+    for most in (len(n), 3):
+        kc, vc, q_out = p.k_cache.clone(), p.v_cache.clone(), torch.zeros_like(p.q)
+        for b in range(0, len(n), most):
+            few = slice(b, min(b + most, len(n)))
+            t = slice(sum(n[: few.start]), sum(n[: few.stop]))
+            params = binding.params_of(p)
+            params.num_seqs = few.stop - few.start
+            binding.inkling_attn_qk_norm_rope_write(params, q[t], k[t], v[t], p.cu_q_lens[b: few.stop + 1] - t.start, p.seq_lens[few],
+                                                    p.block_table[few], q_out[t], kc, vc, ws, w_q=w, w_k=w, inv_freq=freq,
+                                                    layout=layout, positions=step.positions[t])
+        outs.append((q_out, kc, vc))
+    assert binding.inkling_attn_read_device_error(ws) == 0
+    assert all(torch.equal(x.view(torch.int16), y.view(torch.int16)) for x, y in zip(*outs))
+    assert all(outs[0][0].abs().sum(-1).flatten() > 0)
+
+
 def test_positions_of_the_slots_change_nothing(cuda_device):
     step = Step((8, 2), 128, 64, [33, 4], [100, 9], 32, cuda_device, "chain")
     p = step.prob
