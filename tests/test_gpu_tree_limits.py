@@ -80,6 +80,27 @@ def test_two_graphs_of_one_workspace_replayed_with_other_trees(cuda_device, bias
     assert bad and binding.inkling_attn_read_device_error(ws) == binding.DEVERR_PAGE_OUT_OF_RANGE
 
 
+def test_two_calls_at_once(cuda_device):
+    """Two streams, a workspace each: neither call sees the other."""
+    steps = [Step((64, 8), 128, 64, [61, 5], [3000, 900], 38, cuda_device),
+             Step((16, 4), 128, 16, [7] * 20, [600] * 20, 39, cuda_device, window=200, extent=200, bias=F32)]
+    streams = [torch.cuda.Stream() for _ in steps]
+    made = [binding.alloc_tree_workspace(x.params, cuda_device) for x in steps]
+    want = [x.call(workspace=ws)[:2] for x, ws in zip(steps, made)]
+    for x, got in zip(steps, want):
+        check(*got, x.reference(), "alone")
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(20):
+        for x, ws, stream in zip(steps, made, streams):
+            with torch.cuda.stream(stream):
+                outs.append(x.call(workspace=ws, stream=stream)[:2])
+    torch.cuda.synchronize()
+    for i, (out, lse) in enumerate(outs):
+        assert torch.equal(out, want[i % 2][0]) and torch.equal(lse, want[i % 2][1])
+    assert all(binding.inkling_attn_read_device_error(ws) == 0 for ws in made)
+
+
 def at_the_end(device, L, tokens, heads, dim, page, window, seed, kind="tree"):
     """One sequence that ends at key L and names few pages, all of them at the end."""
     width = (L + page - 1) // page
