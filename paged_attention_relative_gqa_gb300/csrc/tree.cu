@@ -58,7 +58,10 @@ constexpr int TR_ITEMS = 2;       // published items in flight
 constexpr int TR_BAD = 16;        // tiles whose unreadable keys are remembered (K is up to 8 ahead of a softmax)
 // Barriers of K and V tiles go by tile.  A chain waits for its own tiles only, so a barrier must not be two of its phases behind
 // one who waits: next to a chain's last tile its next is at most TR_DUAL_SLACK + 1 behind it (the other chain's longer
-// piece, or two items of one tile, whose Q tiles a chain without tiles waits for).
+// piece, or two items of one tile, whose Q tiles a chain without tiles waits for).  Nor may it be two phases ahead of one who waits.  A
+// chain frees a tile's slots after its own waits, but S, which frees K's, runs up to three tiles ahead of the one that the V check is
+// at: with 8 K slots (D = 64) K of the tile 11 further on may come before the check of the next ones.  So the V check frees K's
+// slots too, once it has seen K, and there are no more slots than barriers.
 constexpr int TR_TILES = 8;
 // What a tile takes, in units: for two row tiles (2,000 clocks; bound by its softmax), for one (1,150 to 1,500, by the softmax or by
 // memory); one whose bias rows have to be read takes twice as much.  TR_ENDS tiles more for an item's start, its last tile and its
@@ -83,6 +86,7 @@ struct TRShape {
   static constexpr int QTILE = CB * QSUB;
   // Ring slots, K and V tiles in turn: each kind has slots, and a producer, of its own.
   static constexpr int NS = D == 64 ? 16 : BIAS ? 8 : 10;
+  static_assert(NS / 2 <= TR_TILES, "a tile's barriers are used again before all who wait have seen it");
   static constexpr int V_WARP = BIAS ? 15 : 13;    // the producer of V
   static constexpr int THREADS = (V_WARP + 1) * 32;
   // S that a chain has at a time: the second one waits for no softmax.  A bias takes the room of Q in shared memory, and Q that of
@@ -476,7 +480,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
     return;
   }
   if (tid == 0) {
-    for (int x = 0; x < NS; ++x) mbar_init(&empty[x], 2);
+    for (int x = 0; x < NS; ++x) mbar_init(&empty[x], x & 1 ? 2 : 3);   // two products; K's wait for the V check too
     for (int x = 0; x < TR_TILES; ++x) {
       mbar_init(&k_full[x], 1);
       mbar_init(&v_full[x], 1);
@@ -815,8 +819,10 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
             const int hist = min(it.H, it.hi), kt = it.kt0 + j * step;
             const int st = (2 * g + 1) % NS;
             // (what cannot be read comes with K)
-            go = tr_wait(&k_full[g % TR_TILES], (uint32_t)(g / TR_TILES) & 1u, abort_flag, a) &&
-                 tr_wait(&v_full[g % TR_TILES], (uint32_t)(g / TR_TILES) & 1u, abort_flag, a);
+            go = tr_wait(&k_full[g % TR_TILES], (uint32_t)(g / TR_TILES) & 1u, abort_flag, a);
+            if (!go) break;
+            if (lane == 0) mbar_arrive(&empty[2 * g % NS]);
+            go = tr_wait(&v_full[g % TR_TILES], (uint32_t)(g / TR_TILES) & 1u, abort_flag, a);
             if (!go) break;
             const int k0 = kt * KT;
             const uint32_t* badw = kbad + (g % TR_BAD) * KW;
