@@ -397,12 +397,17 @@ __device__ __forceinline__ TRBias tr_bias(const TreeArgs& a, const TRPart& it, i
 }
 
 // Infinities and NaN of the keys that this row sees, in tiles first to last, into channels [c0, c1) of what it has stored: its
-// output, or its partial (channel c at float 4 (c / 4) rows + c % 4).
+// output, or its partial (channel c at float 4 (c / 4) rows + c % 4).  Tiles between the windows' beginnings and the history's
+// end are seen by every row and were left as they are: nothing of them is missing, and they are passed over (a look at each of
+// 300 K keys, channel by channel, took longer than 20 ms, the time of hundreds of calls).  A warp that shares the work among its lanes
+// needs registers that cost windows 6 %, called or not.
 __device__ __noinline__ void tr_infinite(const TreeArgs& a, const TRPart& it, const TRRow& row, int first, int last, int c0, int c1,
                                          __nv_bfloat16* out, float* part, int D) {
 #pragma unroll 1
-  for (int w = 0; w < (last + 1 - first) * KW; ++w) {
-    const int base = first * KT + 32 * w;
+  for (int w = first * KW; w < (last + 1) * KW; ++w) {
+    if (w * 32 >= it.lo_max && min(it.H, it.hi) - w * 32 >= KT) w = min(it.H, it.hi) / KT * KW;
+    if (w >= (last + 1) * KW) break;
+    const int base = w * 32;
 #pragma unroll 1
     for (uint32_t vis = row.sees(a, base); vis; vis &= vis - 1) {
       const int kk = base + __ffs(vis) - 1;
@@ -412,6 +417,14 @@ __device__ __noinline__ void tr_infinite(const TreeArgs& a, const TRPart& it, co
                           ((((size_t)page * a.Hkv + it.kvh) << a.log2_page) + (kk & ((1 << a.log2_page) - 1))) * D;
 #pragma unroll 1
       for (int c = c0; c < c1; ++c) {
+        if ((c & 7) == 0) {
+          const uint4 x = __ldg(reinterpret_cast<const uint4*>(v + c));
+          if (!((((x.x & 0x7F807F80u) + 0x00800080u) | ((x.y & 0x7F807F80u) + 0x00800080u) | ((x.z & 0x7F807F80u) + 0x00800080u) |
+                 ((x.w & 0x7F807F80u) + 0x00800080u)) & 0x80008000u)) {
+            c += 7;
+            continue;
+          }
+        }
         const uint32_t x = (uint32_t)__ldg(v + c) << 16;
         if ((x & 0x7F800000u) != 0x7F800000u) continue;
         if (out) {
