@@ -451,7 +451,9 @@ size_t inkling_attn_tree_workspace_bytes(const ink_attn_params_t* params);
  *   workspace  device, >= inkling_attn_tree_workspace_bytes(params), initialised once
  * One token per sequence with a bit of its own makes this a decode, so that a batch may mix sequences that
  * draft with sequences that do not.  What is written must overlap nothing else (INK_ERR_BAD_SHAPE).
- * Rounding, infinities and NaN, |V|: as for inkling_attn_prefill_masked.  A token that sees no key gets a zero row and
+ * Rounding, infinities and NaN, |V|: as for inkling_attn_prefill_masked.  Scores are held in fp32 whatever their size, so a row
+ * whose keys all carry a bias of the type's lowest value (a mask written that way) is the mean over those that share its largest
+ * score; a bias of -infinity takes a key's weight altogether.  A token that sees no key gets a zero row and
  * lse = -infinity; so do the tokens of a sequence with n_b > seq_lens[b] (INK_DEVERR_QLEN_EXCEEDS_KV) or
  * n_b > 32 * words (INK_DEVERR_QLEN_EXCEEDS_MAX).  A sequence whose rows lie outside [0, total_q) is skipped
  * (INK_DEVERR_BAD_ROWS).

@@ -73,6 +73,11 @@ constexpr int TR_PAIR = 3, TR_ONE = 2, TR_ENDS = 4, TR_ENDS_BIAS = 15;
 constexpr int TR_MIN_RUN = 4 * TR_ONE;   // least run of a CTA; no tile but an item's last takes more
 constexpr int TR_DUAL_SLACK = 4;  // most tiles that two pieces may differ in to run side by side
 constexpr float TR_RESCALE_LOG2 = 8.f;
+// With a bias a row's scores may all be as low as its type goes (a mask written that way), where a factor of log2(e) overflows and the
+// rounding of score times factor is more than an exponent holds.  Scores of TR_BIG and beyond are 16 apart or equal: of such rows only
+// the keys that share the maximum weigh anything, and 2^(s - max) says so.  Maxima are kept in units of which the exponent takes two,
+// s log2(e) / 2, and beyond TR_BIG as they are: one order, no overflow.
+constexpr float TR_BIG = 134217728.f;
 
 constexpr int KT = TILE_KEYS, KW = KT / 32;   // keys of a tile, words of 32
 constexpr int TR_ELEMENTS = KT + 1;           // words of a bias row that is filled element by element
@@ -446,6 +451,11 @@ __device__ __forceinline__ uint64_t tr_mul(uint64_t a, uint64_t b) {
 
 // An infinity or NaN of a part stays one, whatever the part's weight.
 __device__ __forceinline__ float tr_weigh(float w, float x) { return fabsf(x) <= 3.4028235e38f ? w * x : x; }
+
+// A maximum in natural units.
+__device__ __forceinline__ float tr_natural(float m, bool bias) {
+  return bias && fabsf(m) >= TR_BIG ? m : m * (bias ? 2.f * LN2 : LN2);
+}
 
 // CAP: capped scores, by a polynomial where all scores of a warp's tile allow it (as in the masked prefill).
 template <int D, bool CAP, bool BIAS>
@@ -1013,6 +1023,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
     const bool scaled = CAP || BIAS || !(a.scale_log2 > 0.f);
     // With a bias scores are kept in natural units until the exponent: what is added needs no factor.
     const float mul_ = BIAS ? LOG2E : scaled ? 1.f : a.scale_log2;
+    constexpr float UNIT = BIAS ? 2.f : 1.f;    // of a maximum, in the exponent
     const float pre = CAP ? LN2 : a.sm_scale;   // of the score to which a bias is added
     uint32_t c = 0, c_other = 0, bn = 0, mn = 0;   // tiles of this chain and of the other one so far
     int g = 0;
@@ -1039,6 +1050,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
           rc = a.rel_bf16 ? __uint_as_float(two << 16) : one;
         }
       }
+      const bool near0 = BIAS && __all_sync(0xffffffffu, fabsf(rc) < TR_BIG);   // (beyond, a score's own bits are lost beside it)
       const size_t orow = (size_t)t * a.Hq + head;
       if (BIAS && nt > 0) {   // Q straight into tensor memory, a row a thread (every product with the one before is done)
 #pragma unroll 1
@@ -1177,7 +1189,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
         uint32_t all[S::ROLL ? 32 : KT];
         float mul = mul_, off = 0.f;      // a score's factor in the exponent, and what is added to it
         // One value for a whole row changes no order: such scores stay as they are.
-        const bool lean = BIAS && !CAP && how == NoLoad && !part && !a.slopes && pre > 0.f;
+        const bool lean = BIAS && !CAP && how == NoLoad && !part && !a.slopes && pre > 0.f && near0;
         if (lean) {
           mul = a.scale_log2;
           off = rc * LOG2E;
@@ -1221,14 +1233,19 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
           }
         }
         // ---- running maximum, moved only when it grows by more than 2^8
-        mx = fmaf(mx, mul, off);
-        const bool mine = mx > m + TR_RESCALE_LOG2;
+        if constexpr (BIAS) {
+          const float s = lean ? fmaf(mx, pre, rc) : mx;
+          mx = fabsf(s) < TR_BIG ? 0.5f * fmaf(mx, mul, off) : s;
+        } else {
+          mx = fmaf(mx, mul, off);
+        }
+        const bool mine = mx > m + TR_RESCALE_LOG2 / UNIT;
         if (__any_sync(0xffffffffu, mine)) {
           if (j > 0) {   // (s_full came after all products into O_h but the last one)
             go = tr_wait(&o_done[2 * h + (buf ^ 1u)], ((c - 2) >> 1) & 1u, abort_flag, a);
             if (!go) break;
             tc_fence_after();
-            const float fr = mine ? fast_exp2(m - mx) : 1.f;
+            const float fr = mine ? fast_exp2(UNIT * (m - mx)) : 1.f;
 #pragma unroll 1
             for (int c2 = 0; c2 < D / 16; ++c2) {
               uint32_t ov[16];
@@ -1243,7 +1260,13 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
           if (mine) m = mx;
         }
         // ---- numerators
-        const float nm = off - (m == -INFINITY ? 0.f : m);
+        float nm = off - (m == -INFINITY ? 0.f : UNIT * m);
+        if constexpr (BIAS) {
+          if (fabsf(m) >= TR_BIG && m != -INFINITY) {
+            mul = lean ? pre : 1.f;
+            nm = (lean ? rc : 0.f) - m;
+          }
+        }
         const uint64_t mul2 = f2_pack(mul, mul), nm2 = f2_pack(nm, nm);
         uint64_t ls2[4] = {0ull, 0ull, 0ull, 0ull};
         auto numerators = [&](int w, uint32_t (&sr)[32]) {
@@ -1302,8 +1325,8 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
         if (!go) break;
         const float2 x0 = ml[r], x1 = both ? ml[TREE_ROWS + r] : make_float2(-INFINITY, 0.f);
         M = fmaxf(x0.x, x1.x);
-        f0 = x0.x == -INFINITY ? 0.f : fast_exp2(x0.x - M);
-        f1 = x1.x == -INFINITY ? 0.f : fast_exp2(x1.x - M);
+        f0 = x0.x == -INFINITY ? 0.f : fast_exp2(UNIT * (x0.x - M));
+        f1 = x1.x == -INFINITY ? 0.f : fast_exp2(UNIT * (x1.x - M));
         l = (x0.y == 0.f ? 0.f : x0.y * f0) + (x1.y == 0.f ? 0.f : x1.y * f1);
       }
       tc_fence_after();
@@ -1365,7 +1388,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
                     reinterpret_cast<float*>(part_o), D);
       if (!merge || h == 0) {
         if (!whole) __stcg(reinterpret_cast<float2*>(a.part_ml) + ((size_t)it.place * 2 + rt) * TREE_ROWS + r, make_float2(M, l));
-        else if (rv && a.lse) a.lse[orow] = nothing ? -INFINITY : M * LN2 + logf(l);
+        else if (rv && a.lse) a.lse[orow] = nothing ? -INFINITY : tr_natural(M, BIAS) + logf(l);
       }
       tc_fence_before();
       __syncwarp();
@@ -1395,6 +1418,7 @@ __global__ void __launch_bounds__(TREE_ROWS) tree_join_kernel(const TreeArgs a) 
   auto place = [&](int x) { return (size_t)(2 * ((int)blockIdx.x + x) + (x == 0 ? 1 : 0)) * 2 + rt; };
   const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + r;
   const float4* po = reinterpret_cast<const float4*>(a.part_o) + (size_t)c * 4 * TREE_ROWS + r;
+  const bool bias = a.rel || a.slopes;
   float M = -INFINITY;
 #pragma unroll 8
   for (int x = 0; x < cut.parts; ++x) M = fmaxf(M, __ldcg(ml + place(x) * TREE_ROWS).x);
@@ -1407,7 +1431,7 @@ __global__ void __launch_bounds__(TREE_ROWS) tree_join_kernel(const TreeArgs a) 
     float4 v[4];
 #pragma unroll
     for (int y = 0; y < 4; ++y) v[y] = __ldcg(po + (place(x) * (D / 4) + y) * TREE_ROWS);
-    const float w = p.x == -INFINITY ? 0.f : fast_exp2(p.x - M);
+    const float w = p.x == -INFINITY ? 0.f : fast_exp2((bias ? 2.f : 1.f) * (p.x - M));
     if (p.y != 0.f) l = fmaf(p.y, w, l);
 #pragma unroll
     for (int y = 0; y < 4; ++y) {
@@ -1426,7 +1450,7 @@ __global__ void __launch_bounds__(TREE_ROWS) tree_join_kernel(const TreeArgs a) 
   uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + row * D + c * 16);
   dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
   dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
-  if (c == 0 && a.lse) a.lse[row] = nothing ? -INFINITY : M * LN2 + logf(l);
+  if (c == 0 && a.lse) a.lse[row] = nothing ? -INFINITY : tr_natural(M, bias) + logf(l);
 }
 
 template <int D, bool CAP, bool BIAS>
