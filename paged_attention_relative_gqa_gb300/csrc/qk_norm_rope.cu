@@ -34,7 +34,7 @@ namespace {
 
 constexpr int NR_THREADS = 256;
 constexpr int NR_BLOCKS = 3;   // blocks an SM has registers for
-constexpr int NR_START = 40;   // passes that take as long as a warp's start
+constexpr int NR_START = 6;    // passes that weigh as much as a warp's start
 
 __device__ __forceinline__ void unpack_bf16x8(const uint4 r, float (&f)[8]) {
   const uint32_t w[4] = {r.x, r.y, r.z, r.w};
@@ -288,14 +288,16 @@ cudaError_t launch_t(const NormRopeArgs& a, int layout, cudaStream_t stream) {
 cudaError_t launch_qk_norm_rope(NormRopeArgs& a, int head_dim, bool interleaved, int num_sms, cudaStream_t stream) {
   const int rpp = 32 / (head_dim / 8);
   a.passes = (a.H[0] + rpp - 1) / rpp + 2 * ((a.H[1] + rpp - 1) / rpp);
-  // A token's passes are cut over several warps when there are few tokens, down to one pass each.  A warp's serial start takes
-  // as long as about NR_START passes, and a wave of warps that is not full as long as a full one: of all cuts the one with the
-  // shortest waves is taken (1,700 tokens of 64 + 2 x 8 heads of 128, 40 passes: 22.2 us uncut, 17.4 in halves, which is one
-  // wave, 20.7 in thirds, which is two, 24.4 in ninths).
+  // A token's passes are cut over several warps when there are few tokens, down to one pass each.  A warp's serial start weighs
+  // as much as about NR_START passes of a full wave, and a wave of warps that is not full takes nearly as long as a full one: of the
+  // cuts into at most four waves the one with the shortest waves is taken.  Against all cuts of 8 layouts (4 to 48 passes) and 28
+  // numbers of tokens it is 1 % off the best on average.  64 + 2 x 8 heads of 128 (40 passes): 1,700 tokens 23.8 us whole, 19.1 in
+  // halves (one wave), 22.7 in thirds (two); 3,800 tokens 46.7 whole (two waves), 40.9 in halves (three), 40.2 in thirds (four).  With 40
+  // for NR_START and two waves 3,800 tokens stayed whole.
   const long long resident = (long long)num_sms * NR_BLOCKS * (NR_THREADS / 32);
   long long best = 0;
   a.chunk = (long long)a.T * a.passes <= resident ? 1 : a.passes;   // (all of them at once: nothing to weigh)
-  const long long most = a.chunk == 1 ? 0 : std::min<long long>(a.passes, 2 * resident / std::max(a.T, 1));
+  const long long most = a.chunk == 1 ? 0 : std::min<long long>(a.passes, 4 * resident / std::max(a.T, 1));
   for (int cut = 1; cut <= most; ++cut) {
     const int chunk = (a.passes + cut - 1) / cut, n = (a.passes + chunk - 1) / chunk;
     const long long cost = ((a.T * (long long)n + resident - 1) / resident) * (NR_START + chunk);
