@@ -476,7 +476,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
   uint64_t* p_full = s_full + 4;        // [2 chains][2] P written
   uint64_t* o_done = p_full + 4;        // [2 chains][2] product of that P done
   uint64_t* q_full = o_done + 4;        // [2]
-  uint64_t* q_empty = q_full + 2;       // [2] the piece's last product with a Q tile done
+  uint64_t* q_empty = q_full + 2;       // [2] the piece's last product with a Q tile done, and all waits for it
   uint64_t* item_full = q_empty + 2;    // [ITEMS]
   uint64_t* item_empty = item_full + TR_ITEMS;
   uint64_t* o_free = item_empty + TR_ITEMS;   // both O of a Split item read
@@ -517,7 +517,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
       mbar_init(&o_done[2 * x], 1);
       mbar_init(&o_done[2 * x + 1], 1);
       mbar_init(&q_full[x], BIAS ? 4 : 1);
-      mbar_init(&q_empty[x], 2);
+      mbar_init(&q_empty[x], 3);   // last products, and a chain that has no part in them (Split: the first) is past its wait
       mbar_init(&drain[x], 1);
       if constexpr (BIAS) {
         mbar_init(&bias_full[x], 32);   // every lane of a warp
@@ -692,9 +692,10 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
           }
         } else {
           // (Every phase is waited for, of the other chain's Q tile and by a chain without a tile too: a parity tells a phase from
-          // its neighbours only.)
+          // its neighbours only.  A Q tile goes back when both chains are past that wait, too.)
           go = tr_wait(&q_full[qs], (qn >> qs) & 1u, abort_flag, a);
           if (go && !split) go = tr_wait(&q_full[h ^ 1], (qn >> (h ^ 1)) & 1u, abort_flag, a);
+          if (go && lane == 0 && (!split || h == 0)) mbar_arrive(&q_empty[split ? qs : h ^ 1]);
           qn ^= split ? 1u << qs : 3u;
         }
         if (!go) break;
