@@ -707,8 +707,9 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
           if (lane == 0) mbar_arrive(&q_empty[qs]);
           __syncwarp();
         }
-        // both O of a Split item have been read
-        if (go && merged) go = tr_wait(o_free, (merges - 1) & 1u, abort_flag, a);
+        // both O of a Split item have been read (a chain without a tile does not wait: the item may be over before it looks, and the
+        // one after would have the parity of the one before)
+        if (go && merged && nt > 0) go = tr_wait(o_free, (merges - 1) & 1u, abort_flag, a);
         for (int j = 0; j < nt && go; ++j) {
           const int x = g + j + min(j + h, beside);
           // (v_ok comes after v_full)

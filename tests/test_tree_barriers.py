@@ -13,7 +13,7 @@ import pytest
 TILES = 8       # barriers of K tiles, of V tiles and of checked V tiles
 LISTS = 16      # of a tile's keys that cannot be read
 SLACK = 4       # most tiles that two pieces may differ in to run side by side
-TIES = ("the V check frees K's slots", "each chain frees both Q tiles")
+TIES = ("the V check frees K's slots", "each chain frees both Q tiles", "a chain without a tile waits for no O")
 
 
 class Barrier:
@@ -32,7 +32,7 @@ class Model:
     def __init__(self, seed, slots, ahead, bias, short, ties):
         self.r = r = random.Random(seed)
         self.slots, self.ahead, self.bias = slots, ahead, bias
-        self.v_tie, self.q_tie = (t in ties for t in TIES)
+        self.v_tie, self.q_tie, self.o_tie = (t in ties for t in TIES)
         self.wrong, self.events, self.now = [], [], (0.0, 0)
         # items: mode, tiles of each chain, Q slot of a piece that both chains share
         self.items, slot = [], 1
@@ -165,7 +165,7 @@ class Model:
                     yield from scores(j)
             elif not self.bias:
                 self.q_empty[s].arrive()
-            if merged:
+            if merged and (n > 0 or not self.o_tie):
                 yield self.wait(who + ", O", self.o_free, merges - 1)
             yield self.late()
             for j in range(n):
@@ -286,13 +286,13 @@ SHAPES = [(8, 2, False), (5, 2, False), (8, 1, True), (4, 1, True)]
 
 
 @pytest.mark.parametrize("shape", SHAPES)
-@pytest.mark.parametrize("short", [False])
+@pytest.mark.parametrize("short", [False, True])
 def test_every_wait_ends_with_its_phase(shape, short):
     for seed in range(300):
         assert Model(seed, *shape, short, TIES).run() == "", seed
 
 
-@pytest.mark.parametrize("shape,tie", [((8, 2, False), 0), ((8, 1, True), 0), ((5, 2, False), 1)])
+@pytest.mark.parametrize("shape,tie", [((8, 2, False), 0), ((8, 1, True), 0), ((5, 2, False), 1), ((8, 2, False), 2), ((4, 1, True), 2)])
 def test_a_tie_that_is_missing_is_noticed(shape, tie):
     ties = [t for i, t in enumerate(TIES) if i != tie]
-    assert any(Model(seed, *shape, False, ties).run() for seed in range(300))
+    assert any(Model(seed, *shape, tie == 2, ties).run() for seed in range(1000))
