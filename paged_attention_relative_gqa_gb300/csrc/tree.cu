@@ -37,12 +37,12 @@
 // Every wait is bounded; after a timeout the CTA records it, stops issuing, waits for what is in flight and exits.
 //
 // Measured (GPU time alone; 64 query heads, D = 128): 32 trees of up to 16 tokens against up to 16 K keys, 8 KV heads, 255 us
-// (6.4 TB/s), capped 273, with slopes 436, D = 64 202; 4 of up to 16 against 64 K 136 us (6.0 TB/s); 4 of up to 61 (two items that
-// read K and V each for themselves) 254 us, 0.99 PFLOP/s: 64 keys of both chains take 2,000 clocks, of which their softmax warps
-// are busy 1,850 and the tensor cores 1,050; 16 of up to 16 against 16 K with 4,096 fp32 distances 210 us (147 at the rate of a
-// copy); 64 of up to 8 in a window of 512 with 512 distances 140 us (49), without 79 (42): items of nine tiles, whose start, masks,
-// last tile and output run code that the instruction cache does not hold from one item to the next (19 % of its requests miss,
-// against 2 % on long histories).  How the code happens to lie moves the two last by 5 to 8 %.
+// (6.4 TB/s), capped 273, with slopes 444, D = 64 206; 4 of up to 16 against 64 K 137 us (6.0 TB/s); 4 of up to 61 (two items that
+// read K and V each for themselves) 255 us, 0.99 PFLOP/s: 64 keys of both chains take 2,000 clocks, of which their softmax warps
+// are busy 1,850 and the tensor cores 1,050; 16 of up to 16 against 16 K with 4,096 fp32 distances 211 us (147 at the rate of a
+// copy), with 4,095, whose rows do not begin on 16 bytes, 829; 64 of up to 8 in a window of 512 with 512 distances 143 us (49), without 77 (42): items of nine tiles, whose start, masks,
+// last tile and output run code that the instruction cache does not hold from one item to the next (20 % of its requests miss,
+// against 2 % on long histories).  How the code happens to lie moves the two last by 5 to 8 % and D = 64 by 4 %.
 #include <algorithm>
 #include <climits>
 
@@ -68,7 +68,9 @@ constexpr int TR_TILES = 8;
 // output, TR_ENDS_BIAS with a bias tensor (10,000 clocks).  Runs of as many tiles each, against these: 4 trees of up to 61 tokens
 // against 64 K keys 281 -> 255 us (some CTAs had one row tile a tile, and were done after 330 of 560 thousand clocks), 16 of up to
 // 40 against 16 K with 2,048 distances 445 -> 375, of up to 16 with 4,096 221 -> 211, windows of 512 with a bias 137 -> 140.  With
-// 4 for both, windows with a bias take 149; with 15 for both, 16 trees of up to 40 without one 200 instead of 193.
+// 4 for both, windows with a bias take 149; with 15 for both, 16 trees of up to 40 without one 200 instead of 193.  Two row tiles at
+// 3 against 2 serve the other forms too: 4 trees of up to 61 tokens with D = 64 256 instead of 274, capped 369 (414), with slopes 635 (713); slopes
+// with 15 for the ends 500 instead of 474 (16 of up to 40).
 constexpr int TR_PAIR = 3, TR_ONE = 2, TR_ENDS = 4, TR_ENDS_BIAS = 15;
 constexpr int TR_MIN_RUN = 4 * TR_ONE;   // least run of a CTA; no tile but an item's last takes more
 constexpr int TR_DUAL_SLACK = 4;  // most tiles that two pieces may differ in to run side by side
@@ -392,7 +394,8 @@ __device__ __forceinline__ TRRow tr_row(const TreeArgs& a, const TRPart& it, int
 }
 
 // How the bias of a tile comes to the softmax.  Behind the history distances have no order.  Before it a row's are KT values
-// side by side, one copy a row where 16-byte boundaries can be kept inside the tensor; all of them at E - 1 or more are one value.
+// side by side, brought by a box a token where rows of the tensor begin on 16 bytes, else element by element (four times as long on
+// long histories); all of them at E - 1 or more are one value.
 enum TRBias { NoLoad, Boxes, Elements };
 
 __device__ __forceinline__ TRBias tr_bias(const TreeArgs& a, const TRPart& it, int k0) {
@@ -692,10 +695,9 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
           }
         } else {
           // (Every phase is waited for, of the other chain's Q tile and by a chain without a tile too: a parity tells a phase from
-          // its neighbours only.  A Q tile goes back when both chains are past that wait, too.)
+          // its neighbours only.  A Q tile goes back when both chains are past that wait: each tells so at its item's end.)
           go = tr_wait(&q_full[qs], (qn >> qs) & 1u, abort_flag, a);
           if (go && !split) go = tr_wait(&q_full[h ^ 1], (qn >> (h ^ 1)) & 1u, abort_flag, a);
-          if (go && lane == 0 && (!split || h == 0)) mbar_arrive(&q_empty[split ? qs : h ^ 1]);
           qn ^= split ? 1u << qs : 3u;
         }
         if (!go) break;
@@ -727,6 +729,8 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
           __syncwarp();
           if (j + S::AHEAD < nt) issue_s(j + S::AHEAD);   // (with two: over the P just read)
         }
+        // (the other chain's Q tile, seen above; at the wait itself it cost short items 5 to 10 %)
+        if (!BIAS && go && lane == 0 && (!split || h == 0)) mbar_arrive(&q_empty[split ? qs : h ^ 1]);
         merged = split;
         merges += split;
         g += all;
@@ -1261,7 +1265,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUt
           }
           if (mine) m = mx;
         }
-        // ---- numerators
+        // ---- numerators, rounded to bf16 (an operand of the product has V's type: off by 2^-8 of a weight; the sum is of unrounded ones)
         float nm = off - (m == -INFINITY ? 0.f : UNIT * m);
         if constexpr (BIAS) {
           if (fabsf(m) >= TR_BIG && m != -INFINITY) {

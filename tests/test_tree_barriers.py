@@ -141,9 +141,7 @@ class Model:
             if not self.bias and not split:
                 yield self.wait(who + ", the other Q", self.q_full[h ^ 1], qn[h ^ 1])
                 qn[h ^ 1] += 1
-            if not self.bias and self.q_tie and not (split and h == 1):
-                self.q_empty[s if split else h ^ 1].arrive()
-            yield self.late()
+                yield self.late()
 
             def scores(j):
                 nonlocal sc
@@ -181,6 +179,8 @@ class Model:
                 pc += 1
                 if j + self.ahead < n:
                     yield from scores(j + self.ahead)
+            if not self.bias and self.q_tie and not (split and h == 1):
+                self.q_empty[s if split else h ^ 1].arrive()
             merged = split
             merges += split
             self.end(k)
