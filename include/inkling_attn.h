@@ -429,7 +429,8 @@ typedef struct {
   float softcap;              /* in [1e-6, 1e6]: scores capped by a tanh; 0: not capped */
   const float* slopes;        /* device fp32 [Hq], or NULL: no bias linear in the distance */
   const void* rel_logits;     /* device [total_q, Hq, rel_extent], 4-byte (bf16: 2-byte) aligned, or NULL: no
-                                 bias tensor */
+                                 bias tensor.  Rows that begin on 16 bytes (rel_extent a multiple of 4, bf16: of 8)
+                                 are read up to four times as fast */
   int32_t rel_is_bf16;        /* rel_logits holds bf16 instead of fp32 */
 } ink_attn_tree_options_t;
 
@@ -516,7 +517,9 @@ ink_status_t inkling_attn_kv_conv_state_tree(const ink_attn_params_t* params, co
  * H_b + j, j < path_lens[b].  The rows behind them stay as they are.
  *   cu_q_lens, seq_lens, block_table   of the step (seq_lens with all drafted tokens)
  *   path       device, int32 [B, max_path]: places of the accepted tokens in their sequence, from the root on,
- *              so strictly increasing; entries from path_lens[b] on are not looked at
+ *              so strictly increasing; entries from path_lens[b] on are not looked at.  That each is a child of
+ *              the one before is the caller's to keep: the call has no parents to check it with, and K rows of
+ *              another way would stay rotated for other positions than those they move to
  *   path_lens  device, int32 [B], 0..max_path
  *   k_caches, v_caches   host arrays of num_pools device pointers (1..INK_TREE_MAX_POOLS): pools of the layers that share
  *              block_table and the geometry of params

@@ -195,7 +195,7 @@ cudaError_t launch_state_t(const TreeConvArgs& a, cudaStream_t stream) {
 template <int KS>
 cudaError_t launch_conv_t(const TreeConvArgs& a, int num_sms, cudaStream_t stream) {
   const int cols = (2 * a.nvec + CT_THREADS - 1) / CT_THREADS;
-  // as few tokens a block as one wave of CT_BLOCKS blocks an SM holds: they share the loads of the taps, but follow one another
+  // as few tokens a block as one wave of ct_blocks(KS) blocks an SM holds: they share the loads of the taps, but follow one another
   const long long fit = std::max(1ll, (long long)ct_blocks(KS) * num_sms / cols);
   const int tokens = (int)std::min<long long>(CT_TOKENS, (a.T + fit - 1) / fit);
   kv_conv_tree_kernel<KS><<<dim3((a.T + tokens - 1) / tokens, cols), CT_THREADS, 0, stream>>>(a, tokens);

@@ -6,13 +6,13 @@
 // doubles the way covered in every step, so a tree of depth d takes log2(d) steps; the depth is |S| - 1.  A block takes a
 // sequence, its sets (a bit per token) and pointers twice in shared memory, read from one copy and
 // written to the other.  Latency bounds it: a launch and a chain of three loads (one tree 2.9 us of GPU time alone, 128 trees of
-// up to 64 tokens 3.7).
+// up to 64 tokens 3.7; 32 of up to 512 take 43 us, chains of them 61: with 16 words a token lanes meet on two banks).
 //
 // Commit: row path[j] of a sequence goes to row j, in place.  The path increases, so path[j] >= j, and what is
 // written while rows j0 .. j1 - 1 move lies below all that is read for rows from j1 on: a warp takes the rows in order,
 // a batch of loads, then the batch's stores.  Bytes bound it, read and written once in rows of 2 D bytes, but a path moves few of
-// them and the chain of loads in front of them (lengths, path, table) is longer (one pool 2.9 us of GPU time alone; 22 pools, 64
-// paths of up to 32 tokens of 8 heads of 128, 5.9 us).
+// them and the chain of loads in front of them (lengths, path, table) is longer (one layer 3.0 us of GPU time alone; 11 layers, 64
+// paths in trees of up to 32 tokens, 8 heads of 128, 6.0 us).
 #include <algorithm>
 
 #include "tree_common.cuh"
