@@ -298,12 +298,14 @@ cudaError_t launch_qk_norm_rope(NormRopeArgs& a, int head_dim, bool interleaved,
   long long best = 0;
   a.chunk = (long long)a.T * a.passes <= resident ? 1 : a.passes;   // (all of them at once: nothing to weigh)
   const long long most = a.chunk == 1 ? 0 : std::min<long long>(a.passes, 4 * resident / std::max(a.T, 1));
-  for (int cut = 1; cut <= most; ++cut) {
-    const int chunk = (a.passes + cut - 1) / cut, n = (a.passes + chunk - 1) / chunk;
-    const long long cost = ((a.T * (long long)n + resident - 1) / resident) * (NR_START + chunk);
-    if (cut > 1 && cost >= best) continue;
-    best = cost;
-    a.chunk = chunk;
+  for (int cut = 1, chunk; cut <= most; cut = (a.passes + chunk - 2) / (chunk - 1)) {   // (the least cut into smaller chunks)
+    chunk = (a.passes + cut - 1) / cut;
+    const long long n = (a.passes + chunk - 1) / chunk, cost = ((a.T * n + resident - 1) / resident) * (NR_START + chunk);
+    if (cut == 1 || cost < best) {
+      best = cost;
+      a.chunk = chunk;
+    }
+    if (chunk == 1) break;
   }
   a.nchunks = (a.passes + a.chunk - 1) / a.chunk;
   const int layout = a.rot_dim == 0 ? 0 : interleaved ? 2 : 1;
