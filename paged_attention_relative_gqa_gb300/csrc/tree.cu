@@ -40,9 +40,10 @@
 // (6.4 TB/s), capped 273, with slopes 444, D = 64 206; 4 of up to 16 against 64 K 137 us (6.0 TB/s); 4 of up to 61 (two items that
 // read K and V each for themselves) 255 us, 0.99 PFLOP/s: 64 keys of both chains take 2,000 clocks, of which their softmax warps
 // are busy 1,850 and the tensor cores 1,050; 16 of up to 16 against 16 K with 4,096 fp32 distances 211 us (147 at the rate of a
-// copy), with 4,095, whose rows do not begin on 16 bytes, 829; 64 of up to 8 in a window of 512 with 512 distances 143 us (49), without 77 (42): items of nine tiles, whose start, masks,
-// last tile and output run code that the instruction cache does not hold from one item to the next (20 % of its requests miss,
-// against 2 % on long histories).  How the code happens to lie moves the two last by 5 to 8 % and D = 64 by 4 %.
+// copy), with 4,095, whose rows do not begin on 16 bytes, 829; 64 of up to 8 in a window of 512 with 512 distances 143 us (49),
+// without 77 (42): items of nine tiles, whose start, masks, last tile and output run code that the instruction cache does not hold
+// from one item to the next (20 % of its requests miss, against 2 % on long histories).  How the code happens to lie moves the two
+// last by 5 to 8 % and D = 64 by 4 %.
 #include <algorithm>
 #include <climits>
 
@@ -69,8 +70,8 @@ constexpr int TR_TILES = 8;
 // against 64 K keys 281 -> 255 us (some CTAs had one row tile a tile, and were done after 330 of 560 thousand clocks), 16 of up to
 // 40 against 16 K with 2,048 distances 445 -> 375, of up to 16 with 4,096 221 -> 211, windows of 512 with a bias 137 -> 140.  With
 // 4 for both, windows with a bias take 149; with 15 for both, 16 trees of up to 40 without one 200 instead of 193.  Two row tiles at
-// 3 against 2 serve the other forms too: 4 trees of up to 61 tokens with D = 64 256 instead of 274, capped 369 (414), with slopes 635 (713); slopes
-// with 15 for the ends 500 instead of 474 (16 of up to 40).
+// 3 against 2 serve the other forms too: 4 trees of up to 61 tokens with D = 64 256 instead of 274, capped 369 (414), with slopes
+// 635 (713); slopes with 15 for the ends 500 instead of 474 (16 of up to 40).
 constexpr int TR_PAIR = 3, TR_ONE = 2, TR_ENDS = 4, TR_ENDS_BIAS = 15;
 constexpr int TR_MIN_RUN = 4 * TR_ONE;   // least run of a CTA; no tile but an item's last takes more
 constexpr int TR_DUAL_SLACK = 4;  // most tiles that two pieces may differ in to run side by side
